@@ -42,7 +42,9 @@ EXPORTS = ("moe_cache_init", "moe_layer_forward", "moe_cache_sync", "moe_cache_s
            "moe_cache_timing",
            "moe_cache_probe_h2d", "moe_expert_bytes", "moe_cache_launch_count",
            "moe_cache_destroy", "moe_strerror", "moe_expert_ffn_static", "moe_cache_usage",
-           "moe_cache_state_size", "moe_cache_save_state", "moe_cache_load_state")
+           "moe_cache_state_size", "moe_cache_save_state", "moe_cache_load_state",
+           "moe_kv_page_bytes", "moe_kv_append", "moe_kv_read", "moe_kv_attention_workspace",
+           "moe_kv_attention")
 
 MOE_STATE_MAGIC = 0x53454F4D
 MOE_STATE_VERSION = 1
@@ -355,3 +357,19 @@ class MoECache:
 
     def launch_count(self) -> int:
         return int(lib().moe_cache_launch_count(self.handle))
+
+
+# ------------------------------------------------------- attention operators
+_ATTENTION = ("kv_append", "kv_read", "kv_attention", "kv_attention_workspace", "kv_pages", "kv_page_bytes",
+              "rope_table", "status_message", "MOE_KV_BAD_PAGE", "MOE_KV_BAD_LENGTH", "MOE_KV_BAD_POSITION",
+              "MOE_KV_TIMED_OUT")
+
+
+def __getattr__(name):
+    # loaded on first use: the rest of this module does without PyTorch
+    if name in _ATTENTION:
+        from . import attention
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,391 @@
+// Appending to the paged 4-bit cache, and reading it back.
+//
+// Append: rotation y_a = a c - b s, y_b = b c + a s of queries and keys, then per
+// 32 values of a key or value head m = the value of largest magnitude, d = m / -8,
+// q = min(15, trunc(x / d + 8.5)).  Rotation and quantisation keep every fp32
+// operation separately rounded (no contraction): a code is decided by a comparison
+// with a border, and the same border has to be met by any other implementation.
+//
+// Bound: memory (every value is read once and written once, a few dozen
+// instructions per 8 values); for a token or two, the latency of the chain cu ->
+// start -> table -> store.  Layout of the work: a thread takes 8 consecutive
+// values (one 16-byte load of a 16-bit type), so a head is D/8 lanes of one warp,
+// the rotation's other half sits in another lane of the same head (a shuffle), and
+// a quantisation block is 4 neighbouring lanes.  A warp stays on one token and
+// walks over its heads, so the token's cosines and sines, its sequence and its
+// page are found once and kept in registers.
+#include <algorithm>
+
+#include "attn_common.cuh"
+
+namespace moe {
+namespace {
+
+struct AppendJob {
+  moe_kv_cache c;
+  const int32_t *starts, *cu;
+  int n_tokens;
+  moe_tensor q, k, v;
+  int hq, hkv;
+  const float *cos, *sin;
+  int rot, n_pos, interleaved;
+  void *q_out, *k_out, *v_out;
+  int per_warp;  // heads (of q, k and v together) that one warp takes
+};
+
+constexpr int kAppendWarps = 8;
+
+// The sequence of token i: the last s with cu[s] <= i, by all lanes of a warp.
+__device__ __forceinline__ int find_seq(const int32_t *cu, int n_seqs, int i) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = n_seqs;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const bool le = at < n && __ldg(cu + lo + at) <= i;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, le));
+    const int skip = cnt > 0 ? (cnt - 1) * step : 0;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo;
+}
+
+struct TokenPlace {
+  int seq;
+  int64_t pos;    // -1: the offsets make no sense
+  int page;       // -1: none
+  int in_page;
+  int row;        // token within its tile
+};
+
+__device__ __forceinline__ TokenPlace place_token(const moe_kv_cache &c, const int32_t *starts, const int32_t *cu,
+                                                  int i) {
+  TokenPlace p;
+  p.seq = find_seq(cu, c.n_seqs, i);
+  p.pos = kv_position(i, __ldg(cu + p.seq), __ldg(cu + p.seq + 1), __ldg(starts + p.seq));
+  p.page = -1;
+  p.in_page = 0;
+  p.row = (int)(p.pos & 31);
+  if (p.pos >= 0)
+    p.page = kv_page(c.page_table + (int64_t)p.seq * c.table_stride, c.table_width, c.n_pages, c.page_size,
+                     p.pos / kKvTile, &p.in_page);
+  return p;
+}
+
+// 8 consecutive values to and from fp32.
+__device__ __forceinline__ void load8(const float *p, float x[8]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float x[8]) {
+  const uint4 v = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __half *p, float x[8]) {
+  const uint4 v = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void store8(float *p, const float x[8]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <typename T2, typename T>
+__device__ __forceinline__ void store8_16(T *p, const float x[8], T2 (*pack)(float, float)) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const T2 h = pack(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ __nv_bfloat162 pack_bf16(float a, float b) { return __floats2bfloat162_rn(a, b); }
+__device__ __forceinline__ __half2 pack_f16(float a, float b) { return __floats2half2_rn(a, b); }
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float x[8]) { store8_16<__nv_bfloat162>(p, x, pack_bf16); }
+__device__ __forceinline__ void store8(__half *p, const float x[8]) { store8_16<__half2>(p, x, pack_f16); }
+
+// Quantise the 32 values held by 4 neighbouring lanes (8 each) and store codes
+// and scale of one block.  Every lane of the warp calls it; `live` lanes store.
+__device__ __forceinline__ void quantise_store(const float x[8], uint8_t *tile, int D, int value, int block, int tok,
+                                               bool live) {
+  const int part = threadIdx.x & 3;
+  float hi = x[0], lo = x[0];
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    hi = fmaxf(hi, x[i]);
+    lo = fminf(lo, x[i]);
+    fine = fine && (fabsf(x[i]) <= 3.4028235e38f);  // false for NaN and infinities
+  }
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+  }
+  const uint32_t bad = __ballot_sync(0xffffffffu, !fine);
+  fine = ((bad >> (threadIdx.x & 28)) & 15u) == 0;
+  const float d = (hi >= -lo ? hi : lo) * -0.125f;
+  uint32_t q = 0;  // 8 codes, value i at bits 4 i
+  if (fine) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = d == 0.f ? 8.f : __fadd_rn(__fdiv_rn(x[i], d), 8.5f);
+      q |= (uint32_t)fminf(fmaxf(y, 0.f), 15.f) << (4 * i);
+    }
+  }
+  // byte j of the block = code j | code j + 16 << 4: lanes 0 and 1 hold codes 0..15, lanes 2 and 3 codes 16..31
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, q, 2);
+  if (!live) return;
+  if (part < 2) {
+    uint32_t w[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = (q >> (16 * z + 4 * i)) & 15u, b = (other >> (16 * z + 4 * i)) & 15u;
+        v |= (a | (b << 4)) << (8 * i);
+      }
+      w[z] = v;
+    }
+    *reinterpret_cast<uint2 *>(tile + kv_code_off(D, value, block, tok) + 8 * part) = make_uint2(w[0], w[1]);
+  } else if (part == 2) {
+    const __half h = fine ? __float2half_rn(fminf(fmaxf(d, -65504.f), 65504.f)) : __ushort_as_half(0x7E00);
+    *reinterpret_cast<__half *>(tile + kv_scale_off(D, value, block, tok)) = h;
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const AppendJob j) {
+  constexpr int L = D / 8;         // lanes of one head
+  constexpr int HPW = 32 / L;      // heads that a warp handles at once
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int total = j.hq + 2 * j.hkv, parts = (total + j.per_warp - 1) / j.per_warp;
+  const int64_t item = (int64_t)blockIdx.x * kAppendWarps + warp;
+  const int i = (int)(item / parts), part = (int)(item % parts);
+  if (i >= j.n_tokens) return;
+  const int sub = lane / L, dim = (lane % L) * 8;
+  const TokenPlace at = place_token(j.c, j.starts, j.cu, i);
+  const bool no_rot = j.rot > 0 && (at.pos < 0 || at.pos >= j.n_pos);
+  if (lane == 0 && j.c.status) {
+    const int bits = (at.pos < 0 ? MOE_KV_BAD_LENGTH : (at.page < 0 ? MOE_KV_BAD_PAGE : 0)) |
+                     (at.pos >= 0 && no_rot ? MOE_KV_BAD_POSITION : 0);
+    if (bits) atomicOr(j.c.status, bits);
+  }
+  const bool turned = dim < j.rot;
+  float c[8], s[8];  // of this thread's values; s carries the sign of the rotation's other term
+  int partner = lane;
+  if (turned) {
+    if (no_rot) {
+#pragma unroll
+      for (int z = 0; z < 8; ++z) c[z] = s[z] = __int_as_float(0x7fffffff);
+    } else {
+      const float *ct = j.cos + at.pos * (j.rot / 2), *st = j.sin + at.pos * (j.rot / 2);
+      if (j.interleaved) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(ct + dim / 2));
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(st + dim / 2));
+        const float cc[4] = {a.x, a.y, a.z, a.w}, ss[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          c[z] = cc[z / 2];
+          s[z] = (z & 1) ? ss[z / 2] : -ss[z / 2];
+        }
+      } else {
+        const int first = dim < j.rot / 2, o = first ? dim : dim - j.rot / 2;
+        float ss[8];
+        load8(ct + o, c);
+        load8(st + o, ss);
+#pragma unroll
+        for (int z = 0; z < 8; ++z) s[z] = first ? -ss[z] : ss[z];
+        partner = first ? lane + j.rot / 16 : lane - j.rot / 16;
+      }
+    }
+  }
+  const bool writes = at.page >= 0 && !no_rot;
+  const int h0 = part * j.per_warp, h1 = min(h0 + j.per_warp, total);
+#pragma unroll 2
+  for (int hb = h0; hb < h1; hb += HPW) {
+    const int h = hb + sub;
+    const bool live = h < h1;
+    const int hc = live ? h : h1 - 1;
+    const int kind = hc < j.hq ? 0 : (hc < j.hq + j.hkv ? 1 : 2);
+    const int hh = kind == 0 ? hc : (kind == 1 ? hc - j.hq : hc - j.hq - j.hkv);
+    const moe_tensor &src = kind == 0 ? j.q : (kind == 1 ? j.k : j.v);
+    float x[8], y[8];
+    load8(static_cast<const T *>(src.data) + i * src.token_stride + hh * src.head_stride + dim, x);
+    // every lane takes part in the shuffles; a pair is (z, z ^ 1) of this thread, or the partner lane's value z
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      const float far = __shfl_sync(0xffffffffu, x[z], partner);
+      const float o = j.interleaved ? x[z ^ 1] : far;
+      y[z] = turned && kind < 2 ? __fadd_rn(__fmul_rn(x[z], c[z]), __fmul_rn(o, s[z])) : x[z];
+    }
+    if (live && kind == 0)
+      store8(static_cast<T *>(j.q_out) + ((int64_t)i * j.hq + hh) * D + dim, y);
+    if (live && kind == 1 && j.k_out)
+      store8(static_cast<T *>(j.k_out) + ((int64_t)i * j.hkv + hh) * D + dim, y);
+    if (hb + HPW > j.hq) {  // warp-uniform: some lane holds a key or value head
+      uint8_t *tile = static_cast<uint8_t *>(j.c.pages) + (int64_t)(at.page < 0 ? 0 : at.page) * j.c.page_stride +
+                      kv_tile_off(D, j.c.page_size, hh, at.in_page);
+      quantise_store(y, tile, D, kind == 2, dim / 32, at.row, live && writes && kind > 0);
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kAppendWarps) kv_read_kernel(const AppendJob j) {
+  constexpr int L = D / 8, HPW = 32 / L;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int total = 2 * j.hkv, parts = (total + j.per_warp - 1) / j.per_warp;
+  const int64_t item = (int64_t)blockIdx.x * kAppendWarps + warp;
+  const int i = (int)(item / parts), part = (int)(item % parts);
+  if (i >= j.n_tokens) return;
+  const int sub = lane / L, dim = (lane % L) * 8;
+  const TokenPlace at = place_token(j.c, j.starts, j.cu, i);
+  if (lane == 0 && j.c.status && at.page < 0)
+    atomicOr(j.c.status, at.pos < 0 ? MOE_KV_BAD_LENGTH : MOE_KV_BAD_PAGE);
+  const int h0 = part * j.per_warp, h1 = min(h0 + j.per_warp, total);
+  const uint8_t *page = static_cast<const uint8_t *>(j.c.pages) + (int64_t)(at.page < 0 ? 0 : at.page) * j.c.page_stride;
+#pragma unroll 4
+  for (int h = h0 + sub; h < h1; h += HPW) {
+    const int value = h >= j.hkv, hh = value ? h - j.hkv : h;
+    T *out = static_cast<T *>(value ? j.v_out : j.k_out);
+    if (!out) continue;
+    float y[8];
+    if (at.page < 0) {
+#pragma unroll
+      for (int z = 0; z < 8; ++z) y[z] = __int_as_float(0x7fffffff);
+    } else {
+      const uint8_t *tile = page + kv_tile_off(D, j.c.page_size, hh, at.in_page);
+      const uint2 w = *reinterpret_cast<const uint2 *>(tile + kv_code_off(D, value, dim / 32, at.row) + (dim & 8));
+      const float d = __half2float(*reinterpret_cast<const __half *>(tile + kv_scale_off(D, value, dim / 32, at.row)));
+      const int sh = (dim & 16) ? 4 : 0;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        const int q = (int)(((z < 4 ? w.x : w.y) >> (8 * (z & 3) + sh)) & 15u) - 8;
+        y[z] = (float)q * d;
+      }
+    }
+    store8(out + ((int64_t)i * j.hkv + hh) * D + dim, y);
+  }
+}
+
+// Heads per warp: as many as leave about two warps per scheduler slot of the GPU,
+// in whole turns of the warp; with fewer tokens a warp takes a single turn.
+int heads_per_warp(int n_tokens, int total, int per_turn) {
+  const int64_t warps = 152 * 32;
+  const int64_t turns = (total + per_turn - 1) / per_turn;
+  const int64_t want = std::min<int64_t>(turns, std::max<int64_t>(1, (int64_t)n_tokens * turns / warps));
+  return (int)want * per_turn;
+}
+
+template <template <typename, int> class Launch>
+int by_type(const AppendJob &j, int dtype, cudaStream_t st) {
+  const int D = j.c.head_dim;
+#define MOE_BY_D(T)                                     \
+  (D == 64 ? Launch<T, 64>::go(j, st) : D == 128 ? Launch<T, 128>::go(j, st) : Launch<T, 256>::go(j, st))
+  switch (dtype) {
+    case MOE_F32: return MOE_BY_D(float);
+    case MOE_BF16: return MOE_BY_D(__nv_bfloat16);
+    default: return MOE_BY_D(__half);
+  }
+#undef MOE_BY_D
+}
+
+template <typename T, int D>
+struct LaunchAppend {
+  static int go(AppendJob j, cudaStream_t st) {
+    const int total = j.hq + 2 * j.hkv;
+    j.per_warp = heads_per_warp(j.n_tokens, total, 256 / D);
+    const int64_t items = (int64_t)j.n_tokens * ((total + j.per_warp - 1) / j.per_warp);
+    kv_append_kernel<T, D><<<(unsigned)((items + kAppendWarps - 1) / kAppendWarps), 32 * kAppendWarps, 0, st>>>(j);
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+};
+template <typename T, int D>
+struct LaunchRead {
+  static int go(AppendJob j, cudaStream_t st) {
+    const int total = 2 * j.hkv;
+    j.per_warp = heads_per_warp(j.n_tokens, total, 256 / D);
+    const int64_t items = (int64_t)j.n_tokens * ((total + j.per_warp - 1) / j.per_warp);
+    kv_read_kernel<T, D><<<(unsigned)((items + kAppendWarps - 1) / kAppendWarps), 32 * kAppendWarps, 0, st>>>(j);
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+};
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API int64_t moe_kv_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_size) {
+  if (!kv_sizes_ok(n_kv_heads, head_dim, page_size)) return 0;
+  return (int64_t)n_kv_heads * (page_size / kKvTile) * kv_tile_bytes(head_dim);
+}
+
+MOE_API int moe_kv_append(const moe_kv_cache *c, const int32_t *starts, const int32_t *cu_tokens, int32_t n_tokens,
+                          const moe_tensor *q, int32_t n_q_heads, const moe_tensor *k, const moe_tensor *v,
+                          const float *cos, const float *sin, int32_t rot_dim, int32_t n_positions,
+                          int32_t interleaved, void *q_out, void *k_out, int32_t dtype, void *cuda_stream) {
+  if (const int rc = check_cache(c)) return rc;
+  if (n_tokens < 0 || !k || !v || dtype < MOE_F32 || dtype > MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (n_tokens == 0) return MOE_OK;
+  const int size = dtype == MOE_F32 ? 4 : 2;
+  const bool has_q = q && q->data;
+  if (!starts || !cu_tokens || rot_dim < 0 || rot_dim > c->head_dim || rot_dim % 16) return MOE_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!cos || !sin || n_positions <= 0 || (uintptr_t)cos % 16 || (uintptr_t)sin % 16))
+    return MOE_ERR_INVALID_ARG;
+  if (has_q && (n_q_heads <= 0 || n_q_heads > kMaxAttnHeads || !q_out)) return MOE_ERR_INVALID_ARG;
+  if (const int rc = check_tensor(k, size)) return rc;
+  if (const int rc = check_tensor(v, size)) return rc;
+  if (has_q)
+    if (const int rc = check_tensor(q, size)) return rc;
+  if ((uintptr_t)q_out % 16 || (uintptr_t)k_out % 16) return MOE_ERR_INVALID_ARG;
+  AppendJob j = {};
+  j.c = *c;
+  j.starts = starts;
+  j.cu = cu_tokens;
+  j.n_tokens = n_tokens;
+  if (has_q) j.q = *q;
+  j.k = *k;
+  j.v = *v;
+  j.hq = has_q ? n_q_heads : 0;
+  j.hkv = c->n_kv_heads;
+  j.cos = cos;
+  j.sin = sin;
+  j.rot = rot_dim;
+  j.n_pos = n_positions;
+  j.interleaved = interleaved != 0;
+  j.q_out = q_out;
+  j.k_out = k_out;
+  return by_type<LaunchAppend>(j, dtype, (cudaStream_t)cuda_stream);
+}
+
+MOE_API int moe_kv_read(const moe_kv_cache *c, const int32_t *starts, const int32_t *cu_tokens, int32_t n_tokens,
+                        void *k_out, void *v_out, int32_t dtype, void *cuda_stream) {
+  if (const int rc = check_cache(c)) return rc;
+  if (n_tokens < 0 || dtype < MOE_F32 || dtype > MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (n_tokens == 0 || (!k_out && !v_out)) return MOE_OK;
+  if (!starts || !cu_tokens || (uintptr_t)k_out % 16 || (uintptr_t)v_out % 16) return MOE_ERR_INVALID_ARG;
+  AppendJob j = {};
+  j.c = *c;
+  j.starts = starts;
+  j.cu = cu_tokens;
+  j.n_tokens = n_tokens;
+  j.hkv = c->n_kv_heads;
+  j.k_out = k_out;
+  j.v_out = v_out;
+  return by_type<LaunchRead>(j, dtype, (cudaStream_t)cuda_stream);
+}

@@ -1,0 +1,66 @@
+// Index arithmetic of the paged 4-bit key/value cache: plain C++ that the
+// kernels and the host share, with every check of device-side numbers (page
+// table entries, lengths, positions) that stands between them and an access.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define KV_HD __host__ __device__ inline
+#else
+#define KV_HD inline
+#endif
+
+namespace moe {
+
+constexpr int kKvTile = 32;  // tokens of one tile
+
+// Bytes of one tile (32 tokens of one head of width D): codes and scales of keys, then of values.
+KV_HD int kv_tile_bytes(int D) { return 36 * D; }
+// Offsets inside a tile.
+KV_HD int kv_code_off(int D, int value, int block, int tok) { return value * 18 * D + (block * 32 + tok) * 16; }
+KV_HD int kv_scale_off(int D, int value, int block, int tok) {
+  return value * 18 * D + 16 * D + (tok * (D / 32) + block) * 2;
+}
+// Byte offset of a tile from the start of its page.
+KV_HD int64_t kv_tile_off(int D, int page_size, int head, int tile_in_page) {
+  return ((int64_t)head * (page_size / kKvTile) + tile_in_page) * kv_tile_bytes(D);
+}
+
+// Page of the 32-token tile `tile` of a sequence, or -1 when the table has no
+// such entry or its entry is out of range.  row: the sequence's table row.
+KV_HD int kv_page(const int32_t *row, int table_width, int n_pages, int page_size, int64_t tile, int *in_page) {
+  const int per = page_size / kKvTile;
+  const int64_t i = tile / per;
+  *in_page = (int)(tile - i * per);
+  if (tile < 0 || i >= table_width) return -1;
+  const int32_t p = row[i];
+  return (p >= 0 && p < n_pages) ? p : -1;
+}
+
+// Position of token i of a call in its sequence, or -1 when the offsets or the
+// start make no sense: lo = cu[s], hi = cu[s + 1].
+KV_HD int64_t kv_position(int64_t i, int64_t lo, int64_t hi, int64_t start) {
+  if (i < lo || i >= hi || start < 0) return -1;
+  return start + (i - lo);
+}
+
+// Range of keys [lo, hi) that row j of a sequence's q_tokens sees.
+KV_HD void kv_visible(int64_t len, int q_tokens, int j, int window, int64_t *lo, int64_t *hi) {
+  const int64_t h = len - q_tokens + j + 1;
+  *hi = h < 0 ? 0 : h;
+  *lo = (window > 0 && h > window) ? h - window : 0;
+}
+
+// Tiles [first, first + count) that hold what any row of a sequence sees; -1 when the
+// length is not one that the page table can hold.
+KV_HD int64_t kv_tiles(int64_t len, int q_tokens, int window, int table_width, int page_size, int64_t *first) {
+  *first = 0;
+  if (len < 0 || len > (int64_t)table_width * page_size) return -1;
+  int64_t lo, hi;
+  kv_visible(len, q_tokens, 0, window, &lo, &hi);
+  *first = lo / kKvTile;
+  return (len + kKvTile - 1) / kKvTile - *first;
+}
+
+}  // namespace moe
