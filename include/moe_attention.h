@@ -116,7 +116,7 @@ int moe_kv_read(const moe_kv_cache *c, const int32_t *starts, const int32_t *cu_
  * of n_kv_heads; query head h reads key/value head h / (n_q_heads / n_kv_heads)).
  * Token j of a sequence of n tokens stands at position p = n - q_tokens + j and
  * sees the positions [max(0, p - window + 1), p], or [0, p] when window == 0; a
- * row that sees nothing gives 0 (and lse -inf).
+ * row that sees nothing gives 0 (and lse -inf).  scale: positive and finite.
  * out: [n_seqs * q_tokens][n_q_heads][head_dim] contiguous, in dtype (MOE_BF16
  * or MOE_F16, q's too).  lse: fp32 [n_seqs * q_tokens][n_q_heads], the natural
  * logarithm of the sum of exponentials, or NULL.
@@ -129,6 +129,28 @@ int64_t moe_kv_attention_workspace(int32_t n_q_heads, int32_t n_kv_heads, int32_
 int moe_kv_attention(const moe_kv_cache *c, const int32_t *seq_lens, const moe_tensor *q, int32_t n_q_heads,
                      int32_t q_tokens, float scale, int32_t window, void *out, float *lse, int32_t dtype,
                      void *workspace, int64_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Causal attention over whole prompts, packed one after another.
+ * Queries [cu_q[s], cu_q[s+1]) and keys [cu_k[s], cu_k[s+1]) are sequence s's
+ * (device int32 [n_seqs + 1], increasing, from 0 to the tensors' tokens).  A
+ * sequence's queries stand at its last positions (keys before them: tokens that
+ * an earlier call has seen): query i of n_q, with n_k keys, stands at p = n_k -
+ * n_q + i and sees the keys [max(0, p - window + 1), p], or [0, p] when window
+ * == 0; a row that sees nothing gives 0 (and lse -inf).  scale: positive and finite.
+ * q [n_q_tokens][n_q_heads][head_dim]; k, v [n_k_tokens][n_kv_heads][head_dim];
+ * n_q_heads a multiple of n_kv_heads, at most 64 times it.  out: contiguous, q's
+ * shape; lse: fp32 [n_q_tokens][n_q_heads], the natural logarithm of the sum of
+ * exponentials, or NULL.  dtype: MOE_BF16 or MOE_F16, of q, k, v and out; weights
+ * are rounded to it before they meet the values, sums are fp32.  Strides are not 0.
+ * A NaN or infinity that a row does not see does not reach it.
+ * status: as above (bad offsets: a sequence whose cu_q makes no sense is skipped,
+ * one whose cu_k makes none gives NaN), or NULL.
+ */
+int moe_prompt_attention(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads, const moe_tensor *k,
+                         const moe_tensor *v, int32_t n_k_tokens, int32_t n_kv_heads, int32_t head_dim,
+                         const int32_t *cu_q, const int32_t *cu_k, int32_t n_seqs, float scale, int32_t window,
+                         void *out, float *lse, int32_t dtype, int32_t *status, void *cuda_stream);
 
 #ifdef __cplusplus
 }

@@ -56,6 +56,7 @@ def _lib():
         L.moe_kv_attention_workspace.restype = i64
         L.moe_kv_attention_workspace.argtypes = [i32, i32, i32, i32]
         L.moe_kv_attention.argtypes = [pc, vp, pt, i32, i32, f32, i32, vp, vp, i32, vp, i64, vp]
+        L.moe_prompt_attention.argtypes = [pt, i32, i32, pt, pt, i32, i32, i32, vp, vp, i32, f32, i32, vp, vp, i32, vp, vp]
         _bound = L
     return _bound
 
@@ -259,6 +260,38 @@ def kv_attention(q, pages, page_table, seq_lens, *, page_size, n_kv_heads, q_tok
                                            1.0 / math.sqrt(d) if scale is None else scale, window, out.data_ptr(),
                                            lse.data_ptr() if return_lse else None, _DTYPES[q.dtype], ws.data_ptr(),
                                            ws.numel(), h), "moe_kv_attention")
+    return (out, lse) if return_lse else out
+
+
+def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_lse=False, out=None, status=None,
+                     stream=None):
+    """Causal attention over packed prompts (moe_prompt_attention).
+
+    q [n_q_tokens, n_q_heads, head_dim], k and v [n_k_tokens, n_kv_heads, head_dim], bfloat16 or float16;
+    cu_q, cu_k int32 [n_seqs + 1] (cu_k None: cu_q).  With more keys than queries a sequence's queries are its
+    last tokens.  window > 0: a token sees itself and the window - 1 tokens before it.  Returns q's shape, and
+    the log of the sums of exponentials (fp32 [n_q_tokens, n_q_heads]) with return_lse."""
+    dev = _device(q)
+    if q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16):
+        _refuse("q must be bfloat16 or float16 [tokens, heads, head_dim]", MOE_ERR_UNSUPPORTED)
+    n, hq, d = q.shape
+    tq, tk = _tokens(q, "q", n, hq, d, q.dtype, dev), _tokens(k, "k", None, None, d, q.dtype, dev)
+    tv = _tokens(v, "v", k.shape[0], k.shape[1], d, q.dtype, dev)
+    cu_k = cu_q if cu_k is None else cu_k
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        _refuse("cu_q must hold n_seqs + 1 offsets")
+    n_cu = cu_q.shape[0]
+    pq, pk = _index(cu_q, "cu_q", n_cu, dev), _index(cu_k, "cu_k", n_cu, dev)
+    if status is not None and (status.dtype != torch.int32 or status.numel() != 1 or status.device != dev):
+        _refuse("status must be one int32 on the GPU")
+    with _On(stream) as h:
+        out = _output(out, "out", (n, hq, d), q.dtype, dev)
+        lse = torch.empty((n, hq), dtype=torch.float32, device=dev) if return_lse else None
+        _check(_lib().moe_prompt_attention(ctypes.byref(tq), n, hq, ctypes.byref(tk), ctypes.byref(tv), k.shape[0],
+                                           k.shape[1], d, pq, pk, n_cu - 1, 1.0 / math.sqrt(d) if scale is None else scale,
+                                           window, out.data_ptr(), lse.data_ptr() if return_lse else None,
+                                           _DTYPES[q.dtype], None if status is None else status.data_ptr(), h),
+               "moe_prompt_attention")
     return (out, lse) if return_lse else out
 
 

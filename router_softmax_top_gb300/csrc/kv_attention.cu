@@ -693,7 +693,8 @@ MOE_API int moe_kv_attention(const moe_kv_cache *c, const int32_t *seq_lens, con
                              void *workspace, int64_t workspace_bytes, void *cuda_stream) {
   if (c && c->n_seqs == 0) return MOE_OK;
   if (const int rc = check_cache(c)) return rc;
-  if (!seq_lens || !out || n_q_heads <= 0 || n_q_heads % c->n_kv_heads || q_tokens <= 0 || window < 0)
+  if (!seq_lens || !out || n_q_heads <= 0 || n_q_heads % c->n_kv_heads || q_tokens <= 0 || window < 0 ||
+      !(scale > 0.f && scale <= 3.4e38f))
     return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
   if (n_q_heads > kMaxAttnHeads || q_tokens > 1024) return MOE_ERR_UNSUPPORTED;

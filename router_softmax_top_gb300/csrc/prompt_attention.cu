@@ -1,0 +1,682 @@
+// Causal attention over whole prompts, packed one after another, on the 5th-gen
+// tensor cores.
+//
+// o_i = sum_j 2^(t_ij - r_i) v_j / sum_j 2^(t_ij - r_i), t = scale log2(e) q_i . k_j,
+// over the keys that row i sees, in one pass over the keys; the reference r_i moves
+// only when a score exceeds it by more than 2^8, and the sums then scale.
+//
+// Bound: the tensor cores, 4 D flops per (query, key) pair and head; beside them an
+// exponential per pair and head, which the same SM does at about the rate that the
+// matrices allow.  So both have to run at once:
+//  * A CTA works on NQ tiles of 128 rows (two where tensor memory holds two score
+//    tiles and two outputs, D <= 128).  While one tile's scores are turned into
+//    weights by its own four warps, the other tile's products run.  At D = 256 one
+//    tile with two score buffers takes turns.
+//  * A row is (token, head): the heads that share a key head are rows of the same
+//    tile, 128 / group tokens of each, so keys and values are loaded once for all of
+//    them and the diagonal cuts off at most that many tokens' worth of work.
+//  * Q K^T: both operands K-major in shared memory (TMA, 128-byte swizzle), scores in
+//    tensor memory.  A thread owns a row: it loads its scores, takes maximum and sum
+//    in registers without any shuffle, and writes the weights (16 bits) over them.
+//  * P V: weights from tensor memory, values from shared memory as the TMA left them
+//    (the contraction runs across their rows: an MN-major operand), output
+//    accumulated in tensor memory across all key blocks.
+//  * One thread issues all matrix instructions in an order in which every product of
+//    one tile has the other tile's exponentials behind it; one thread loads.
+// Blocks of keys that no row of a tile sees are skipped; only blocks that a row sees in
+// part are masked.  A masked weight is an exact 0; since 0 x infinity and 0 x NaN are not,
+// a row whose result is not finite although its sum is gets its result again from the
+// keys it sees, one by one (never in ordinary data).
+// Every wait is bounded; when one gives up all roles stop, rows become NaN and the
+// status word says so.
+#include <algorithm>
+
+#include "attn_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.f;
+constexpr int kTileRows = 128;
+
+struct PromptMaps {
+  CUtensorMap q, k, v;
+};
+
+struct PromptJob {
+  moe_tensor q, k, v;
+  const int32_t *cu_q, *cu_k;
+  int n_q, n_k, n_seqs, hq, hkv, group, tile_tokens, window;
+  float scale;
+  void *out;
+  float *lse;
+  int32_t *status;
+};
+
+template <int D>
+struct PromptCfg {
+  static constexpr int kNQ = D == 256 ? 1 : 2;         // row tiles
+  static constexpr int kBuf = 2;                       // score buffers (one per tile, or two of the one tile)
+  static constexpr int kBK = D == 256 ? 64 : 128;      // keys of a block
+  static constexpr int kStages = D == 64 ? 4 : 2;      // of keys, and of values
+  static constexpr uint32_t kQBytes = kTileRows * D * 2, kKBytes = kBK * D * 2;
+  static constexpr uint32_t kQOff = 0, kKOff = kNQ * kQBytes, kVOff = kKOff + kStages * kKBytes;
+  static constexpr size_t kSmem = kVOff + kStages * kKBytes + 1024;
+  // tensor memory: score buffers, then outputs
+  static constexpr uint32_t kOCol = kBuf * kBK;
+  static constexpr int kSoftWarps = 4 * kNQ, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+  static constexpr int kThreads = 32 * (kSoftWarps + 2);
+  static_assert(kOCol + kNQ * D <= 512, "tensor memory");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+template <typename T>
+constexpr uint32_t kFmt = 0;  // fp16
+template <>
+constexpr uint32_t kFmt<__nv_bfloat16> = 1;
+
+// Instruction descriptor, kind::f16, fp32 accumulate, both operands of type T; b_mn: B is MN-major.
+template <typename T>
+__host__ __device__ constexpr uint32_t p_idesc(int N, bool b_mn) {
+  return (1u << 4) | (kFmt<T> << 7) | (kFmt<T> << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(kTileRows >> 4) << 24);
+}
+// Shared-memory descriptors, 128-byte swizzle.  K-major: groups of 8 rows 1024 bytes
+// apart.  MN-major: groups of 8 contraction rows 1024 bytes apart, next 64 columns `lbo` bytes on.
+__device__ __forceinline__ uint64_t p_desc_k(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFF) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t p_desc_mn(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)(lbo >> 4) << 16) | (64ull << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+__device__ __forceinline__ void p_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void p_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+          d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void p_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(a_smem(bar))
+               : "memory");
+}
+__device__ __forceinline__ void p_ld32(uint32_t addr, float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void p_st32(uint32_t addr, const float *v) {
+  const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void p_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void p_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void p_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void p_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void p_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void p_tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(a_smem(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float p_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float p_float(__half x) { return __half2float(x); }
+
+// What one CTA works on: tiles of one sequence's rows.
+struct PromptWork {
+  int seq;                 // -1: nothing
+  int q0, n_q, k0, n_k;    // tokens of the sequence
+  int bad_k;               // the key offsets make no sense
+  int first_token;         // of tile 0, within the sequence
+};
+
+// Key blocks [jb, je) that a tile's rows see, and the range [whole_lo, whole_hi) that all its rows see.
+struct TileRange {
+  int jb, je, whole_lo, whole_hi;
+};
+template <int BK>
+__device__ __forceinline__ TileRange tile_range(const PromptJob &j, const PromptWork &w, int tile) {
+  TileRange r = {0, 0, 0, 0};
+  const int a = w.first_token + tile * j.tile_tokens, b = min(w.n_q, a + j.tile_tokens) - 1;
+  if (a > b || w.bad_k) return r;
+  const int off = w.n_k - w.n_q, hi = off + b + 1;  // n_k, n_q < 2^30
+  if (hi <= 0) return r;
+  r.whole_hi = max(0, off + a + 1);
+  int lo = 0;
+  if (j.window > 0) {
+    lo = max(0, off + a + 1 - j.window);
+    r.whole_lo = max(0, off + b + 1 - j.window);
+  }
+  r.jb = lo / BK;
+  r.je = (hi + BK - 1) / BK;
+  return r;
+}
+
+// One row's output from the keys it sees, one by one: the warp's lanes hold D / 32 values each.
+template <int D, typename T>
+__device__ __noinline__ void row_by_keys(const PromptJob &j, int q_tok, int head, int64_t k0, int lo, int hi, float ref,
+                                         T *out) {
+  const int lane = threadIdx.x & 31, kvh = head / j.group;
+  constexpr int N = D / 32;
+  float q[N], acc[N], sum = 0.f;
+  const T *qp = static_cast<const T *>(j.q.data) + q_tok * j.q.token_stride + head * j.q.head_stride + lane * N;
+  for (int i = 0; i < N; ++i) {
+    q[i] = p_float(qp[i]);
+    acc[i] = 0.f;
+  }
+  for (int key = lo; key < hi; ++key) {
+    const T *kp = static_cast<const T *>(j.k.data) + (k0 + key) * j.k.token_stride + kvh * j.k.head_stride + lane * N;
+    const T *vp = static_cast<const T *>(j.v.data) + (k0 + key) * j.v.token_stride + kvh * j.v.head_stride + lane * N;
+    float s = 0.f;
+    for (int i = 0; i < N; ++i) s = fmaf(q[i], p_float(kp[i]), s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float p = a_exp2(s * (j.scale * kLog2e) - ref);
+    sum += p;
+    for (int i = 0; i < N; ++i) acc[i] = fmaf(p, p_float(vp[i]), acc[i]);
+  }
+  for (int i = 0; i < N; ++i) out[lane * N + i] = T(acc[i] / sum);
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ PromptMaps maps, const PromptJob j) {
+  using C = PromptCfg<D>;
+  constexpr int NQ = C::kNQ, BK = C::kBK, ST = C::kStages, DC = D / 64;
+  extern __shared__ __align__(1024) unsigned char sm_raw[];
+  __shared__ uint64_t q_full, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], pv_done[NQ], done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_fail;
+  __shared__ PromptWork s_work;
+  const uint32_t sm = (a_smem(sm_raw) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    s_fail = 0;
+    a_mbar_init(&q_full, 1);
+    for (int i = 0; i < ST; ++i) {
+      a_mbar_init(&k_full[i], 1);
+      a_mbar_init(&k_empty[i], 1);
+      a_mbar_init(&v_full[i], 1);
+      a_mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      a_mbar_init(&s_full[i], 1);
+      a_mbar_init(&p_full[i], 128);
+    }
+    for (int i = 0; i < NQ; ++i) a_mbar_init(&pv_done[i], 1);
+    a_mbar_init(&done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 0) {
+    // the sequence and tiles of this CTA: tiles are counted along the sequences, a sequence's last ones
+    // (the longest) first
+    const int per = NQ * j.tile_tokens;
+    int before = 0;
+    PromptWork w = {-1, 0, 0, 0, 0, 0, 0};
+    const int mine = (int)(blockIdx.x / j.hkv);
+    for (int base = 0; base < j.n_seqs; base += 32) {
+      const int s = base + lane;
+      int n = 0, a = 0, b = 0;
+      if (s < j.n_seqs) {
+        a = __ldg(j.cu_q + s);
+        b = __ldg(j.cu_q + s + 1);
+        if (a < 0 || b < a || b > j.n_q) {
+          if (blockIdx.x == 0 && j.status) atomicOr(j.status, MOE_KV_BAD_LENGTH);
+          a = b = 0;
+        }
+        n = (b - a + per - 1) / per;
+      }
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const bool hit = mine >= before + inc - n && mine < before + inc;
+      const uint32_t who = __ballot_sync(0xffffffffu, hit);
+      if (who) {
+        if (hit) {
+          w.seq = s;
+          w.q0 = a;
+          w.n_q = b - a;
+          w.first_token = (n - 1 - (mine - (before + inc - n))) * per;
+          const int c = __ldg(j.cu_k + s), d = __ldg(j.cu_k + s + 1);
+          w.bad_k = c < 0 || d < c || d > j.n_k;
+          w.k0 = w.bad_k ? 0 : c;
+          w.n_k = w.bad_k ? 0 : d - c;
+          if (w.bad_k && j.status) atomicOr(j.status, MOE_KV_BAD_LENGTH);
+          s_work = w;
+        }
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+      if (base + 32 >= j.n_seqs && lane == 0) s_work = w;
+    }
+  }
+  if (warp == C::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(a_smem(&s_tmem)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  p_fence_before();
+  __syncthreads();
+  p_fence_after();
+  const uint32_t tmem = s_tmem;
+  const PromptWork w = s_work;
+  const int kvh = (int)(blockIdx.x % j.hkv);
+
+  TileRange tr[NQ];
+  int J0 = 0x7fffffff, J1 = 0;
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) {
+    tr[t] = w.seq < 0 ? TileRange{0, 0, 0, 0} : tile_range<BK>(j, w, t);
+    if (tr[t].je > tr[t].jb) {
+      J0 = min(J0, tr[t].jb);
+      J1 = max(J1, tr[t].je);
+    }
+  }
+  const int n_blocks = max(0, J1 - J0);
+
+  if (warp == C::kLoadWarp) {
+    if (lane == 0 && n_blocks > 0) {
+      int issued = 0;
+      bool ok = true;
+      const uint32_t q_rows_bytes = (uint32_t)(j.group * j.tile_tokens) * 128u;
+      uint32_t q_bytes = 0;
+#pragma unroll
+      for (int t = 0; t < NQ; ++t)
+        if (tr[t].je > tr[t].jb) q_bytes += DC * q_rows_bytes;
+      a_expect_tx(&q_full, q_bytes);
+#pragma unroll
+      for (int t = 0; t < NQ; ++t)
+        if (tr[t].je > tr[t].jb)
+          for (int c = 0; c < DC; ++c)
+            p_tma_3d(sm + C::kQOff + t * C::kQBytes + c * kTileRows * 128, &maps.q, 64 * c, kvh * j.group,
+                     w.q0 + w.first_token + t * j.tile_tokens, &q_full);
+      for (int i = 0; i < n_blocks && ok; ++i) {
+        const int st = i % ST;
+        const uint32_t ph = (uint32_t)(i / ST - 1) & 1u;
+        const int row = w.k0 + (J0 + i) * BK;
+        if (i >= ST && !a_mbar_wait(&k_empty[st], ph, &s_fail)) { ok = false; break; }
+        a_expect_tx(&k_full[st], C::kKBytes);
+        for (int c = 0; c < DC; ++c)
+          p_tma_3d(sm + C::kKOff + st * C::kKBytes + c * BK * 128, &maps.k, 64 * c, kvh, row, &k_full[st]);
+        if (i >= ST && !a_mbar_wait(&v_empty[st], ph, &s_fail)) { ok = false; }
+        if (ok) {
+          a_expect_tx(&v_full[st], C::kKBytes);
+          for (int c = 0; c < DC; ++c)
+            p_tma_3d(sm + C::kVOff + st * C::kKBytes + c * BK * 128, &maps.v, 64 * c, kvh, row, &v_full[st]);
+          issued = i + 1;
+        } else {
+          (void)a_mbar_wait(&k_full[st], (uint32_t)(i / ST) & 1u);
+        }
+      }
+      if (!ok) s_fail = 1;
+      // no copy may be in flight when the CTA leaves
+      if (*(volatile int *)&s_fail) (void)a_mbar_wait(&q_full, 0);
+      for (int i = issued < ST ? 0 : issued - ST; i < issued; ++i) {
+        (void)a_mbar_wait(&k_full[i % ST], (uint32_t)(i / ST) & 1u);
+        (void)a_mbar_wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u);
+      }
+    }
+  } else if (warp == C::kMmaWarp) {
+    if (lane == 0 && n_blocks > 0) {
+      constexpr uint32_t id_qk = p_idesc<T>(BK, false), id_pv = p_idesc<T>(D, true);
+      auto qk = [&](int t, int buf, int i) {
+        const uint64_t a0 = p_desc_k(sm + C::kQOff + t * C::kQBytes);
+        const uint64_t b0 = p_desc_k(sm + C::kKOff + (i % ST) * C::kKBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          p_mma_ss(tmem + buf * BK, a0 + (kk / 4) * (kTileRows * 128 / 16) + (kk % 4) * 2,
+                   b0 + (kk / 4) * (BK * 128 / 16) + (kk % 4) * 2, id_qk, kk > 0);
+        p_commit(&s_full[buf]);
+      };
+      auto pv = [&](int t, int buf, int i, bool first) {
+        const uint64_t b0 = p_desc_mn(sm + C::kVOff + (i % ST) * C::kKBytes, BK * 128);
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          p_mma_ts(tmem + C::kOCol + t * D, tmem + buf * BK + kk * 8, b0 + kk * (2048 / 16), id_pv, !first || kk > 0);
+        p_commit(&pv_done[t]);
+      };
+      bool ok = a_mbar_wait(&q_full, 0, &s_fail) && a_mbar_wait(&k_full[0], 0, &s_fail);
+      if (ok) {
+        p_fence_after();
+#pragma unroll
+        for (int t = 0; t < NQ; ++t)
+          if (J0 >= tr[t].jb && J0 < tr[t].je) qk(t, t, 0);
+        p_commit(&k_empty[0]);
+      }
+      for (int i = 0; i < n_blocks && ok; ++i) {
+        const int jj = J0 + i;
+        const bool more = i + 1 < n_blocks;
+        if (more && !(ok = a_mbar_wait(&k_full[(i + 1) % ST], (uint32_t)((i + 1) / ST) & 1u, &s_fail))) break;
+        if (NQ == 1 && more) {
+          p_fence_after();
+          qk(0, (i + 1) & 1, i + 1);
+          p_commit(&k_empty[(i + 1) % ST]);
+        }
+        if (!(ok = a_mbar_wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u, &s_fail))) break;
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          const int buf = NQ == 1 ? (i & 1) : t;
+          if (jj >= tr[t].jb && jj < tr[t].je) {
+            const int n = jj - tr[t].jb;
+            const uint32_t ph = (uint32_t)(NQ == 1 ? n >> 1 : n) & 1u;
+            if (!(ok = a_mbar_wait(&p_full[buf], ph, &s_fail))) break;
+            p_fence_after();
+            pv(t, buf, i, jj == tr[t].jb);
+          }
+          if (NQ == 2 && more && jj + 1 >= tr[t].jb && jj + 1 < tr[t].je) qk(t, t, i + 1);
+        }
+        if (!ok) break;
+        if (NQ == 2 && more) p_commit(&k_empty[(i + 1) % ST]);
+        p_commit(&v_empty[i % ST]);
+      }
+      if (!ok) s_fail = 1;
+      p_commit(&done);
+      (void)a_mbar_wait(&done, 0);
+    }
+  } else {
+    // ---- softmax: thread = row of tile t
+    const int t = warp / 4, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 (warp % 4) in the lane field
+    const TileRange range = NQ == 1 ? tr[0] : (t == 0 ? tr[0] : tr[NQ - 1]);
+    const int tok = w.first_token + t * j.tile_tokens + r / j.group, head = kvh * j.group + r % j.group;
+    const bool live = w.seq >= 0 && r < j.group * j.tile_tokens && tok < w.n_q;
+    const int hi = live ? max(0, w.n_k - w.n_q + tok + 1) : 0;
+    const int lo = j.window > 0 ? max(0, hi - j.window) : 0;
+    const float c = j.scale * kLog2e;
+    float m = -a_inf(), l = 0.f;  // reference (log2 units) and sum
+    bool ok = true;
+    const uint32_t o_col = tmem + lanes + C::kOCol + t * D;
+    for (int jj = range.jb; jj < range.je; ++jj) {
+      const int n = jj - range.jb, buf = NQ == 1 ? (n & 1) : t;
+      const uint32_t ph = (uint32_t)(NQ == 1 ? n >> 1 : n) & 1u;
+      ok = __all_sync(0xffffffffu, a_mbar_wait(&s_full[buf], ph, &s_fail));
+      if (!ok) break;
+      p_fence_after();
+      const uint32_t s_col = tmem + lanes + buf * BK;
+      float s[BK];
+#pragma unroll
+      for (int x = 0; x < BK; x += 32) p_ld32(s_col + x, s + x);
+      p_ld_wait();
+      const int key0 = jj * BK;
+      if (key0 < range.whole_lo || key0 + BK > range.whole_hi) {
+#pragma unroll
+        for (int x = 0; x < BK; ++x)
+          if (key0 + x < lo || key0 + x >= hi) s[x] = -a_inf();
+      }
+      float top[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) top[z] = -a_inf();
+#pragma unroll
+      for (int x = 0; x < BK; x += 8)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) top[z] = fmaxf(top[z], fmaxf(s[x + z], s[x + 4 + z]));
+      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;  // c > 0
+      const bool over = mx > m + kLazy;
+      if (__any_sync(0xffffffffu, over)) {
+        const float m_new = fmaxf(m, mx);
+        const float a = m == -a_inf() ? 0.f : a_exp2(m - m_new);
+        m = m_new;
+        l *= a;
+        if (n > 0) {
+          ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)(n - 1) & 1u, &s_fail));
+          if (!ok) break;
+          p_fence_after();
+#pragma unroll 1
+          for (int x = 0; x < D; x += 32) {
+            float o[32];
+            p_ld32(o_col + x, o);
+            p_ld_wait();
+#pragma unroll
+            for (int z = 0; z < 32; ++z) o[z] *= a;
+            p_st32(o_col + x, o);
+          }
+          p_st_wait();
+        }
+      }
+      const float ref = m == -a_inf() ? 0.f : m;
+      const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(-ref, -ref);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int x = 0; x < BK; x += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int z = 0; z < 16; ++z) {
+          float a, b;
+          f2_unpack(f2_fma(f2_pack(s[x + 2 * z], s[x + 2 * z + 1]), c2, r2), a, b);
+          a = a_exp2(a);
+          b = a_exp2(b);
+          sum[z & 1] = f2_add(sum[z & 1], f2_pack(a, b));
+          p[z] = pack16<T>(a, b);
+        }
+        p_st16(s_col + x / 2, p);
+      }
+      p_st_wait();
+      p_fence_before();
+      a_mbar_arrive(&p_full[buf]);
+      float a, b;
+      f2_unpack(f2_add(sum[0], sum[1]), a, b);
+      l += a + b;
+    }
+    // ---- the rows' results
+    const int n_mine = range.je - range.jb;
+    if (ok && n_mine > 0)
+      ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)(n_mine - 1) & 1u, &s_fail));
+    if (!ok) s_fail = 1;
+    p_fence_after();
+    if (w.seq >= 0) {
+      const int64_t at = (int64_t)(w.q0 + tok) * j.hq + head;
+      T *out = static_cast<T *>(j.out) + at * D;
+      if (!ok || w.bad_k) l = a_nan();
+      const bool some = n_mine > 0 && ok;
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      bool finite = true;
+#pragma unroll 1
+      for (int x = 0; x < D; x += 32) {
+        float o[32];
+        if (some) {
+          p_ld32(o_col + x, o);
+          p_ld_wait();
+        } else {
+#pragma unroll
+          for (int z = 0; z < 32; ++z) o[z] = 0.f;
+        }
+        uint32_t p[16];
+#pragma unroll
+        for (int z = 0; z < 16; ++z) {
+          finite = finite && fabsf(o[2 * z]) < a_inf() && fabsf(o[2 * z + 1]) < a_inf();
+          // a row that sees nothing is 0 even where its accumulator took a 0 x infinity
+          p[z] = l == 0.f ? 0u : pack16<T>(o[2 * z] * inv, o[2 * z + 1] * inv);
+        }
+        if (live)
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            *reinterpret_cast<uint4 *>(out + x + 8 * z) = make_uint4(p[4 * z], p[4 * z + 1], p[4 * z + 2], p[4 * z + 3]);
+      }
+      if (live && j.lse) j.lse[at] = l == 0.f ? -a_inf() : (m + log2f(l)) * kLn2;
+      // a product of a zero weight with a value that is not finite: once more, without the unseen keys
+      uint32_t again = __ballot_sync(0xffffffffu, live && some && !finite && l > 0.f && l < a_inf());
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        const int rtok = __shfl_sync(0xffffffffu, tok, src), rhead = __shfl_sync(0xffffffffu, head, src);
+        const int rlo = __shfl_sync(0xffffffffu, lo, src), rhi = __shfl_sync(0xffffffffu, hi, src);
+        const float rm = __shfl_sync(0xffffffffu, m, src);
+        __syncwarp();
+        row_by_keys<D, T>(j, w.q0 + rtok, rhead, w.k0, rlo, rhi, rm,
+                          static_cast<T *>(j.out) + ((int64_t)(w.q0 + rtok) * j.hq + rhead) * D);
+      }
+    }
+  }
+  p_fence_before();
+  __syncthreads();
+  if (s_fail && tid == 0 && j.status) atomicOr(j.status, MOE_KV_TIMED_OUT);
+  if (warp == C::kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  static EncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// Tensor [tokens][heads][D] as boxes of 64 values x box_heads heads x box_tokens tokens, 128-byte swizzle.
+bool encode_map(CUtensorMap *m, const moe_tensor &t, int tokens, int heads, int D, int box_heads, int box_tokens,
+                int dtype) {
+  const EncodeFn fn = encoder();
+  if (!fn) return false;
+  // with one head its stride is never used, but has to be one that the encoder takes
+  const uint64_t hs = heads > 1 ? (uint64_t)t.head_stride * 2 : (uint64_t)D * 2;
+  const uint64_t ts = tokens > 1 ? (uint64_t)t.token_stride * 2 : (uint64_t)heads * D * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens}, strides[2] = {hs, ts};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, elem[3] = {1, 1, 1};
+  return fn(m, dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void *>(t.data), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, typename T>
+int launch_prompt(PromptJob j, int dtype, cudaStream_t st) {
+  using C = PromptCfg<D>;
+  static DynSmemLimit limit;
+  if (ensure_dyn_smem(prompt_attention_kernel<D, T>, C::kSmem, limit) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  PromptMaps maps;
+  if (!encode_map(&maps.q, j.q, j.n_q, j.hq, D, j.group, j.tile_tokens, dtype) ||
+      !encode_map(&maps.k, j.k, std::max(1, j.n_k), j.hkv, D, 1, C::kBK, dtype) ||
+      !encode_map(&maps.v, j.v, std::max(1, j.n_k), j.hkv, D, 1, C::kBK, dtype))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t per = (int64_t)C::kNQ * j.tile_tokens;
+  // at most this many tile groups: a sequence's last one may be partly filled
+  const int64_t groups = j.n_q / per + std::min<int64_t>(j.n_seqs, j.n_q);
+  if (groups * j.hkv > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  prompt_attention_kernel<D, T><<<(unsigned)(groups * j.hkv), C::kThreads, C::kSmem, st>>>(maps, j);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API int moe_prompt_attention(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads, const moe_tensor *k,
+                                 const moe_tensor *v, int32_t n_k_tokens, int32_t n_kv_heads, int32_t head_dim,
+                                 const int32_t *cu_q, const int32_t *cu_k, int32_t n_seqs, float scale, int32_t window,
+                                 void *out, float *lse, int32_t dtype, int32_t *status, void *cuda_stream) {
+  if (n_q_tokens < 0 || n_k_tokens < 0 || n_seqs < 0 || n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads ||
+      window < 0 || !(scale > 0.f && scale <= 3.4e38f))
+    return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
+  const int group = n_q_heads / n_kv_heads;
+  if (!kv_sizes_ok(n_kv_heads, head_dim, kKvTile) || n_q_heads > kMaxAttnHeads || group > 64 ||
+      n_q_tokens > (1 << 29) || n_k_tokens > (1 << 29))
+    return MOE_ERR_UNSUPPORTED;
+  if (n_q_tokens == 0 || n_seqs == 0) return MOE_OK;
+  if (!cu_q || !cu_k || !out || (uintptr_t)out % 16 || (uintptr_t)lse % 4) return MOE_ERR_INVALID_ARG;
+  if (const int rc = check_tensor(q, 2)) return rc;
+  if (n_k_tokens > 0) {
+    if (const int rc = check_tensor(k, 2)) return rc;
+    if (const int rc = check_tensor(v, 2)) return rc;
+  }
+  PromptJob j = {};
+  j.q = *q;
+  // without keys nothing is loaded, but the maps want an address
+  j.k = n_k_tokens > 0 ? *k : moe_tensor{q->data, head_dim, head_dim};
+  j.v = n_k_tokens > 0 ? *v : j.k;
+  j.cu_q = cu_q;
+  j.cu_k = cu_k;
+  j.n_q = n_q_tokens;
+  j.n_k = n_k_tokens;
+  j.n_seqs = n_seqs;
+  j.hq = n_q_heads;
+  j.hkv = n_kv_heads;
+  j.group = group;
+  j.tile_tokens = kTileRows / group;
+  j.window = window;
+  j.scale = scale;
+  j.out = out;
+  j.lse = lse;
+  j.status = status;
+  cudaStream_t st = (cudaStream_t)cuda_stream;
+  if (dtype == MOE_BF16)
+    return head_dim == 64    ? launch_prompt<64, __nv_bfloat16>(j, dtype, st)
+           : head_dim == 128 ? launch_prompt<128, __nv_bfloat16>(j, dtype, st)
+                             : launch_prompt<256, __nv_bfloat16>(j, dtype, st);
+  return head_dim == 64    ? launch_prompt<64, __half>(j, dtype, st)
+         : head_dim == 128 ? launch_prompt<128, __half>(j, dtype, st)
+                           : launch_prompt<256, __half>(j, dtype, st);
+}

@@ -183,6 +183,8 @@ def test_append_of_nothing_is_a_no_op(lib):
 
 @pytest.mark.parametrize("change,code", [
     (dict(hq=12), moe.MOE_ERR_INVALID_ARG), (dict(hq=0), moe.MOE_ERR_INVALID_ARG), (dict(qt=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(scale=0.0), moe.MOE_ERR_INVALID_ARG), (dict(scale=-0.1), moe.MOE_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), moe.MOE_ERR_INVALID_ARG), (dict(scale=float("inf")), moe.MOE_ERR_INVALID_ARG),
     (dict(window=-1), moe.MOE_ERR_INVALID_ARG), (dict(dtype=0), moe.MOE_ERR_UNSUPPORTED), (dict(lens=0), moe.MOE_ERR_INVALID_ARG),
     (dict(out=0), moe.MOE_ERR_INVALID_ARG), (dict(ws=0), moe.MOE_ERR_INVALID_ARG), (dict(ws=(1 << 20) + 16), moe.MOE_ERR_INVALID_ARG),
     (dict(ws_bytes=4096), moe.MOE_ERR_INVALID_ARG), (dict(qt=1025), moe.MOE_ERR_UNSUPPORTED),
@@ -190,11 +192,41 @@ def test_append_of_nothing_is_a_no_op(lib):
     (dict(q=A.MoeTensor(0, 2048, 128)), moe.MOE_ERR_INVALID_ARG)])
 def test_bad_attention_calls_are_refused(lib, change, code):
     a = dict(lens=1 << 20, q=A.MoeTensor(1 << 20, 2048, 128), hq=16, qt=1, window=0, out=1 << 20, dtype=1, ws=1 << 20,
-             ws_bytes=1 << 30)
+             ws_bytes=1 << 30, scale=1.0)
     a.update(change)
-    rc = lib.moe_kv_attention(ctypes.byref(_cache()), a["lens"], ctypes.byref(a["q"]), a["hq"], a["qt"], 1.0, a["window"],
+    rc = lib.moe_kv_attention(ctypes.byref(_cache()), a["lens"], ctypes.byref(a["q"]), a["hq"], a["qt"], a["scale"], a["window"],
                               a["out"], None, a["dtype"], a["ws"], a["ws_bytes"], None)
     assert rc == code
+
+
+def _prompt(lib, **kw):
+    a = dict(q=A.MoeTensor(1 << 20, 2048, 128), nq=5, hq=16, k=A.MoeTensor(1 << 20, 1024, 128),
+             v=A.MoeTensor(1 << 20, 1024, 128), nk=5, hkv=8, d=128, cq=1 << 20, ck=1 << 20, n=2, scale=0.1, window=0,
+             out=1 << 20, dtype=1)
+    a.update(kw)
+    return lib.moe_prompt_attention(ctypes.byref(a["q"]), a["nq"], a["hq"], ctypes.byref(a["k"]), ctypes.byref(a["v"]),
+                                    a["nk"], a["hkv"], a["d"], a["cq"], a["ck"], a["n"], a["scale"], a["window"], a["out"],
+                                    None, a["dtype"], None, None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(hq=12), moe.MOE_ERR_INVALID_ARG), (dict(hkv=0), moe.MOE_ERR_INVALID_ARG), (dict(d=96), moe.MOE_ERR_UNSUPPORTED),
+    (dict(nq=-1), moe.MOE_ERR_INVALID_ARG), (dict(nk=-1), moe.MOE_ERR_INVALID_ARG), (dict(n=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(window=-1), moe.MOE_ERR_INVALID_ARG), (dict(dtype=0), moe.MOE_ERR_UNSUPPORTED),
+    (dict(scale=0.0), moe.MOE_ERR_INVALID_ARG), (dict(scale=-1.0), moe.MOE_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), moe.MOE_ERR_INVALID_ARG), (dict(scale=float("inf")), moe.MOE_ERR_INVALID_ARG),
+    (dict(cq=0), moe.MOE_ERR_INVALID_ARG), (dict(ck=0), moe.MOE_ERR_INVALID_ARG), (dict(out=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(out=(1 << 20) + 2), moe.MOE_ERR_INVALID_ARG), (dict(hq=65, hkv=1), moe.MOE_ERR_UNSUPPORTED),
+    (dict(nq=1 << 30), moe.MOE_ERR_UNSUPPORTED), (dict(q=A.MoeTensor((1 << 20) + 2, 2048, 128)), moe.MOE_ERR_UNSUPPORTED),
+    (dict(k=A.MoeTensor(1 << 20, 1025, 128)), moe.MOE_ERR_UNSUPPORTED),
+    (dict(v=A.MoeTensor(0, 1024, 128)), moe.MOE_ERR_INVALID_ARG)])
+def test_bad_prompt_calls_are_refused(lib, change, code):
+    assert _prompt(lib, **change) == code
+
+
+def test_prompt_of_nothing_is_a_no_op(lib):
+    assert _prompt(lib, nq=0) == moe.MOE_OK
+    assert _prompt(lib, n=0) == moe.MOE_OK
 
 
 def test_sizes(lib):
