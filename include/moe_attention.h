@@ -52,6 +52,8 @@ extern "C" {
 #define MOE_KV_BAD_POSITION 4  /* a position past the rotation table                     */
 #define MOE_KV_TIMED_OUT 8     /* a bounded device wait gave up                          */
 
+#define MOE_KV_COUNTER_BYTES 4096
+
 #define MOE_F32 0
 #define MOE_BF16 1
 #define MOE_F16 2
@@ -121,8 +123,8 @@ int moe_kv_read(const moe_kv_cache *c, const int32_t *starts, const int32_t *cu_
  * or MOE_F16, q's too).  lse: fp32 [n_seqs * q_tokens][n_q_heads], the natural
  * logarithm of the sum of exponentials, or NULL.
  * workspace: device memory of moe_kv_attention_workspace bytes, 256-byte
- * aligned, all zero before its first use; every call leaves it ready for the
- * next one on the same stream.
+ * aligned, its first MOE_KV_COUNTER_BYTES zero before its first use; every call
+ * leaves it ready for the next one on the same stream.
  * A NaN or infinity that a row does not see does not reach it.
  */
 int64_t moe_kv_attention_workspace(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t q_tokens);

@@ -23,6 +23,7 @@ MOE_KV_BAD_PAGE = 1
 MOE_KV_BAD_LENGTH = 2
 MOE_KV_BAD_POSITION = 4
 MOE_KV_TIMED_OUT = 8
+MOE_KV_COUNTER_BYTES = 4096
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
@@ -219,7 +220,9 @@ def kv_attention_workspace(n_q_heads, n_kv_heads, head_dim, q_tokens=1, device="
     n = int(_lib().moe_kv_attention_workspace(n_q_heads, n_kv_heads, head_dim, q_tokens))
     if n <= 0:
         _refuse("kv_attention_workspace: unsupported sizes", MOE_ERR_UNSUPPORTED)
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:MOE_KV_COUNTER_BYTES].zero_()
+    return ws
 
 
 def _workspace(hq, hkv, d, q_tokens, handle, dev):

@@ -26,14 +26,16 @@
 //    p d stays inside fp16 whatever the scales are.
 //  * Rows in the matrix's N: 8 of them (heads sharing a key head x query tokens).
 //
-// Work: the 32-token tiles of all (sequence, key head) pairs in a row are split evenly
-// over the CTAs (a sequence's length does not matter), and the tiles of a CTA's piece
-// of one pair go round its warps.  Each warp copies its own tiles (one bulk copy per
-// tile, as the layout keeps a tile contiguous) into a ring of its own, running ahead
-// across pieces, so no CTA barrier stands in the loop.  Pieces are merged over the
-// warps in shared memory; a pair that several CTAs share is merged by the last of
-// them from partial results in the workspace, in the order of the CTAs, so results do
-// not depend on timing.
+// Work: the 32-token tiles of all (sequence, key head) pairs in a row, plus a few
+// tiles' worth per pair for its set-up and result, are split evenly over all warps of
+// the grid, so neither a sequence's length nor its place matters.  A warp walks its
+// share alone: it copies its own tiles (one bulk copy per tile, as the layout keeps a
+// tile contiguous) into a ring of its own, running ahead across pairs, and writes the
+// result of every pair that it has whole; no barrier stands in the loop.  At the end the
+// CTA merges, in shared memory, the pairs that its warps share, and a pair that several
+// CTAs share is merged by the last of them from partial results in the workspace, always
+// in the order of the keys, so results do not depend on timing.  Few short pairs
+// instead take a CTA each, whose warps share its tiles: nothing is merged across CTAs.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -53,9 +55,8 @@ struct DecodeJob {
   float scale;
   void *out;
   float *lse;
-  float *part;        // [grid][2][kRows][D + 2]: partial sums, reference and weight sum per row
-  uint32_t *count;    // [grid]: pieces done of the pair whose first piece that CTA has
-  int min_share;      // fewest tiles of one CTA
+  float *part;        // [grid][2][kPart]: partial results of the pairs that a CTA shares with the one before or after
+  uint32_t *count;    // [grid]: CTAs done with the pair whose first tiles that CTA has
 };
 
 template <int D>
@@ -63,12 +64,24 @@ struct DecodeCfg {
   static constexpr int kWarps = 8;
   static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kTile = 36 * D;
-  static constexpr int kOut = kRows * D;  // values of one merged result
+  // a partial result: accumulators as the matrix unit leaves them, [D/16][32 lanes][4], then per t of a lane the
+  // references and weight sums of rows 2t and 2t + 1
+  static constexpr int kOut = kRows * D, kPart = kOut + 16;
   static constexpr size_t kRing = (size_t)kWarps * kStages * kTile;
-  static constexpr size_t kSmem = kRing + (size_t)(kWarps / 2) * (kOut + 2 * kRows) * sizeof(float);
+  static constexpr size_t kSmem = kRing + (size_t)kWarps * kPart * sizeof(float);
   static constexpr int kCtas = D == 256 ? 1 : 2;  // resident per SM
+  static_assert((size_t)kStages * kTile >= kPart * sizeof(float), "a warp's ring holds its last partial result");
 };
 
+// d = a b + c
+__device__ __forceinline__ void mma16816_from(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+// c += a b
 __device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -94,10 +107,16 @@ __device__ __forceinline__ void store_pair(__half *p, float a, float b) {
   *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b);
 }
 
-// A walk over the pieces of a CTA's range of units.  Units are ordered by
-// sequence, then key head and row tile, then tile.
+// What a pair costs beside its tiles, in tiles (its queries' set-up and its result): measured, see below.
+constexpr int kPairCost = 4;
+// A pair of at most this many tiles may take a CTA of its own when there are CTAs for all pairs.
+constexpr int kAloneTiles = 64;
+
+// A walk over the pieces (tiles of one pair) of a warp's share.  Pairs are ordered by sequence, then key head
+// and row tile; a pair of n tiles takes kPairCost + n places, its tiles the last n of them.
 struct Walk {
-  int64_t left;   // units not yet walked
+  int64_t left;   // places of the share not yet walked
+  int64_t pair0;  // the current pair's first place
   int seq, hr;    // current pair: sequence, key head * row_tiles + row tile
   int first;      // first tile of what the sequence's rows see
   int n;          // tiles of the pair
@@ -111,23 +130,70 @@ __device__ __forceinline__ int seq_tiles(const DecodeJob &j, int s, int *first) 
   return n < 0 ? 0 : (int)n;
 }
 
-__device__ __forceinline__ void walk_clip(Walk &w) {
-  w.end = (int)(w.left < (int64_t)(w.n - w.at) ? w.at + w.left : w.n);
-  w.left -= w.end - w.at;
+// The piece of the current pair from its place `off` on; false when the share holds none of its tiles.
+__device__ __forceinline__ bool walk_clip(Walk &w, int64_t off) {
+  const int64_t take = min(w.left, (int64_t)(w.n + kPairCost) - off);
+  w.at = (int)max((int64_t)0, off - kPairCost);
+  w.end = (int)max((int64_t)w.at, off + take - kPairCost);
+  w.left -= take;
+  return w.end > w.at;
 }
-// Next piece; false when the range is done.
+// Next piece; false when the share is done.
 __device__ __forceinline__ bool walk_next(const DecodeJob &j, Walk &w) {
-  if (w.left <= 0) return false;
-  if (++w.hr == j.c.n_kv_heads * j.row_tiles) {
-    w.hr = 0;
-    do {
-      if (++w.seq >= j.c.n_seqs) return false;
-      w.n = seq_tiles(j, w.seq, &w.first);
-    } while (w.n == 0);
-  }
-  w.at = 0;
-  walk_clip(w);
+  const int heads = j.c.n_kv_heads * j.row_tiles;
+  do {
+    if (w.left <= 0) return false;
+    w.pair0 += w.n + kPairCost;
+    if (++w.hr == heads) {
+      w.hr = 0;
+      do {
+        if (++w.seq >= j.c.n_seqs) return false;
+        w.n = seq_tiles(j, w.seq, &w.first);
+      } while (w.n == 0);
+    }
+  } while (!walk_clip(w, 0));
   return true;
+}
+
+// A partial result that a warp leaves for the merge.
+struct PartMeta {
+  int64_t pair0;
+  int seq, hr, n;
+  int valid;
+};
+
+// Merges partial results, in order, for the four values of accumulator word f: rows 2t and 2t + 1 of a lane.
+// Own: parts in shared memory; otherwise in the workspace, written by other CTAs (read past L1).
+template <bool Own, typename V>
+__device__ __forceinline__ V part_load(const float *p) {
+  if constexpr (Own) return *reinterpret_cast<const V *>(p);
+  else return __ldcg(reinterpret_cast<const V *>(p));
+}
+template <bool Own, typename Ptr>
+__device__ __forceinline__ float4 merge_parts(int f, int out_floats, int parts, Ptr ptr, float r[2], float l[2]) {
+  const int t = f & 3;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  r[0] = r[1] = -a_inf();
+  for (int i = 0; i < parts; ++i) {
+    const float2 x = part_load<Own, float2>(ptr(i) + out_floats + 4 * t);
+    r[0] = fmaxf(r[0], x.x);
+    r[1] = fmaxf(r[1], x.y);
+  }
+  l[0] = l[1] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float4 x = part_load<Own, float4>(ptr(i) + out_floats + 4 * t);
+    const float4 v = part_load<Own, float4>(ptr(i) + 4 * f);
+    const float w0 = x.x == -a_inf() ? 0.f : a_exp2(x.x - r[0]), w1 = x.y == -a_inf() ? 0.f : a_exp2(x.y - r[1]);
+    a.x += v.x * w0;
+    a.z += v.z * w0;
+    a.y += v.y * w1;
+    a.w += v.w * w1;
+    // a poisoned part may hold no weight: its NaN must not be multiplied away
+    l[0] += x.z != x.z ? x.z : x.z * w0;
+    l[1] += x.w != x.w ? x.w : x.w * w1;
+  }
+  return a;
 }
 
 template <int D, typename T>
@@ -136,159 +202,172 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   constexpr int W = C::kWarps, S = C::kStages, NB = D / 32, kThreads = 32 * W;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ uint64_t bars[W][S];
-  __shared__ int64_t scan[W], sh_off;
-  __shared__ int sh_seq, sh_last;
-  float *merge = reinterpret_cast<float *>(sm + C::kRing);
+  __shared__ PartMeta meta[2 * W];  // per warp: of its first piece, of its last one
+  __shared__ Walk loads[W];         // per warp: the piece that its copies are at
+  __shared__ int sh_last;
+  float *heads_mem = reinterpret_cast<float *>(sm + C::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int heads = j.c.n_kv_heads * j.row_tiles;
+  const int64_t n_rows_all = (int64_t)j.q_tokens * j.hq;
+  const int n_rows = j.group * j.q_tokens;
   uint64_t *bar = bars[warp];
+  unsigned char *ring = sm + (size_t)warp * S * C::kTile;
   if (lane == 0) {
 #pragma unroll
     for (int s = 0; s < S; ++s) a_mbar_init(&bar[s], 1);
+    meta[2 * warp].valid = meta[2 * warp + 1].valid = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
 
-  // ---- this CTA's share of the units
-  int64_t mine = 0;
-  for (int s = tid; s < j.c.n_seqs; s += kThreads) {
-    int first;
-    mine += seq_tiles(j, s, &first);
-  }
-  int64_t sum = mine;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) scan[warp] = sum;
-  if (tid == 0) sh_seq = -1;
-  __syncthreads();
-  int64_t units = 0;
-  for (int w = 0; w < W; ++w) units += scan[w];
-  units *= heads;
-  int64_t share = (units + gridDim.x - 1) / gridDim.x;
-  if (share < j.min_share) share = j.min_share;
-  const int64_t u0 = share * blockIdx.x;
-
-  // ---- sequences without tiles (empty, or a length the table cannot hold): their rows
-  for (int s = blockIdx.x; s < j.c.n_seqs; s += gridDim.x) {
-    const int len = __ldg(j.lens + s);
-    int first;
-    if (seq_tiles(j, s, &first) > 0) continue;
-    const bool bad = len != 0;
-    if (bad && tid == 0 && j.c.status) atomicOr(j.c.status, MOE_KV_BAD_LENGTH);
-    const float fill = bad ? a_nan() : 0.f;
-    const int64_t n = (int64_t)j.q_tokens * j.hq;
-    T *o = static_cast<T *>(j.out) + (int64_t)s * n * D;
-    for (int64_t i = tid; i < n * D / 2; i += kThreads) store_pair(o + 2 * i, fill, fill);
-    if (j.lse)
-      for (int64_t i = tid; i < n; i += kThreads) j.lse[(int64_t)s * n + i] = bad ? a_nan() : -a_inf();
-  }
-  if (u0 >= units) return;
-
-  // ---- where the share begins
-  Walk walk;
-  {
-    int64_t run = 0;
-    __syncthreads();
-    for (int base = 0; base < j.c.n_seqs; base += kThreads) {
-      const int s = base + tid;
-      int first = 0;
-      const int64_t n = s < j.c.n_seqs ? (int64_t)seq_tiles(j, s, &first) * heads : 0;
-      int64_t inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (lane == 31) scan[warp] = inc;
-      __syncthreads();
-      int64_t before = run, all = run;
-      for (int w = 0; w < W; ++w) {
-        if (w < warp) before += scan[w];
-        all += scan[w];
-      }
-      if (u0 >= before + inc - n && u0 < before + inc) {
-        sh_seq = s;
-        sh_off = u0 - (before + inc - n);
-      }
-      __syncthreads();
-      run = all;
-      if (sh_seq >= 0) break;
+  // ---- this warp's share of the places
+  int64_t total = 0;
+  int most = 0;
+  for (int base = 0; base < j.c.n_seqs; base += 32) {
+    int first, n = 0;
+    const bool in = base + lane < j.c.n_seqs;
+    if (in) n = seq_tiles(j, base + lane, &first);
+    total += n ? n + kPairCost : 0;
+    most = max(most, n);
+    // sequences without tiles (empty, or of a length that the table cannot hold): their rows
+    uint32_t none = __ballot_sync(0xffffffffu, in && n == 0);
+    while (none) {
+      const int s = base + __ffs(none) - 1;
+      none &= none - 1;
+      if (s % (int)(gridDim.x * W) != (int)(warp * gridDim.x + blockIdx.x)) continue;
+      const bool bad = __ldg(j.lens + s) != 0;
+      if (bad && lane == 0 && j.c.status) atomicOr(j.c.status, MOE_KV_BAD_LENGTH);
+      const float fill = bad ? a_nan() : 0.f;
+      T *o = static_cast<T *>(j.out) + (int64_t)s * n_rows_all * D;
+      for (int64_t i = lane; i < n_rows_all * D / 2; i += 32) store_pair(o + 2 * i, fill, fill);
+      if (j.lse)
+        for (int64_t i = lane; i < n_rows_all; i += 32) j.lse[(int64_t)s * n_rows_all + i] = bad ? a_nan() : -a_inf();
     }
-    walk.seq = sh_seq;
-    walk.n = seq_tiles(j, walk.seq, &walk.first);
-    walk.hr = (int)(sh_off / walk.n);
-    walk.at = (int)(sh_off % walk.n);
-    walk.left = min(share, units - u0);
-    walk_clip(walk);
   }
-  // unit index of the current pair's first tile
-  int64_t pair0 = u0 - walk.at;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  total *= heads;
+  const int64_t pairs = (int64_t)j.c.n_seqs * heads;
+  const bool alone = most <= kAloneTiles && pairs <= (int64_t)gridDim.x;  // a CTA per pair
+  const int64_t share = (total + (int64_t)gridDim.x * W - 1) / ((int64_t)gridDim.x * W);
+  Walk walk = {0, 0, 0, 0, 0, 0, 0, 0};
+  bool work;
+  if (alone) {
+    work = blockIdx.x < pairs;
+    if (work) {
+      walk.seq = blockIdx.x / heads;
+      walk.hr = blockIdx.x % heads;
+      walk.n = seq_tiles(j, walk.seq, &walk.first);
+      walk.at = walk.n * warp / W;
+      walk.end = walk.n * (warp + 1) / W;
+      work = walk.end > walk.at;
+    }
+  } else {
+    const int64_t u0 = share * ((int64_t)blockIdx.x * W + warp);
+    work = u0 < total;
+    if (work) {
+      int64_t run = 0;
+      for (int base = 0; base < j.c.n_seqs; base += 32) {
+        int first = 0, n = 0;
+        if (base + lane < j.c.n_seqs) n = seq_tiles(j, base + lane, &first);
+        const int64_t cost = n ? (int64_t)(n + kPairCost) * heads : 0;
+        int64_t inc = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const int64_t begin = run + inc - cost;
+        const uint32_t who = __ballot_sync(0xffffffffu, u0 >= begin && u0 < begin + cost);
+        run += __shfl_sync(0xffffffffu, inc, 31);
+        if (who) {
+          const int src = __ffs(who) - 1;
+          walk.seq = base + src;
+          walk.n = __shfl_sync(0xffffffffu, n, src);
+          walk.first = __shfl_sync(0xffffffffu, first, src);
+          walk.pair0 = __shfl_sync(0xffffffffu, begin, src);
+          break;
+        }
+      }
+      const int64_t off = u0 - walk.pair0;
+      walk.hr = (int)(off / (walk.n + kPairCost));
+      walk.pair0 += (int64_t)walk.hr * (walk.n + kPairCost);
+      walk.left = min(share, total - u0);
+      work = walk_clip(walk, off % (walk.n + kPairCost)) || walk_next(j, walk);
+    }
+  }
 
   // ---- this warp's copies: a second walk that runs up to S tiles ahead
-  unsigned char *ring = sm + (size_t)warp * S * C::kTile;
-  Walk load = walk;
-  int load_tile = load.at + warp;  // next tile to copy
-  bool load_more = true;
+  Walk &load = loads[warp];
+  if (lane == 0) load = walk;
+  __syncwarp();
+  int load_tile = walk.at, load_end = walk.end;  // next tile to copy, and the end of its piece
+  bool load_more = work;
   uint32_t issued = 0, used = 0;
-  int pages = 0, pages_at = -1, pages_seq = -1;  // page numbers of the next tiles, one per lane
-  uint32_t bad_mask = 0;  // of the last 32 copies, by (issued & 31): a tile without a page
+  int64_t src_off = -1;     // offset of tile src_at + lane in the cache, -1: the tile has no page
+  int src_at = 0, src_end = 0;
+  uint32_t bad_mask = 0;    // by (issued & 31): a tile without a page
 
   auto issue = [&]() {
-    // the next tile of this warp, or nothing
-    while (load_more && load_tile >= load.end) {
-      load_more = walk_next(j, load);
-      load_tile = load.at + warp;
-    }
     if (!load_more) return;
-    if (pages_seq != load.seq || load_tile < pages_at || load_tile >= pages_at + 32 * W ||
-        (load_tile - pages_at) % W != 0) {
-      pages_seq = load.seq;
-      pages_at = load_tile;
-      const int tile = load_tile + lane * W;
-      int in_page = 0, p = -1;
-      if (tile < load.n)
-        p = kv_page(j.c.page_table + (int64_t)load.seq * j.c.table_stride, j.c.table_width, j.c.n_pages,
-                    j.c.page_size, load.first + tile, &in_page);
-      pages = p;
+    if (load_tile >= load_end) {
+      Walk next = load;
+      load_more = walk_next(j, next);
+      if (!load_more) return;
+      load_tile = next.at;
+      load_end = next.end;
+      src_end = 0;
+      __syncwarp();
+      if (lane == 0) load = next;
+      __syncwarp();
     }
-    const int page = __shfl_sync(0xffffffffu, pages, (load_tile - pages_at) / W);
+    if (load_tile >= src_end) {
+      src_at = load_tile;
+      src_end = load_tile + 32;
+      const int tile = load_tile + lane;
+      src_off = -1;
+      if (tile < load_end) {
+        int in_page = 0;
+        const int p = kv_page(j.c.page_table + (int64_t)load.seq * j.c.table_stride, j.c.table_width, j.c.n_pages,
+                              j.c.page_size, load.first + tile, &in_page);
+        if (p >= 0)
+          src_off = (int64_t)p * j.c.page_stride + kv_tile_off(D, j.c.page_size, load.hr / j.row_tiles, in_page);
+      }
+    }
+    const int64_t off = __shfl_sync(0xffffffffu, src_off, load_tile - src_at);
     const int st = issued % S;
-    const int per = j.c.page_size / kKvTile;
-    const int in_page = (load.first + load_tile) % per;
     bad_mask &= ~(1u << (issued & 31));
-    if (page < 0) {
+    if (off < 0) {
       bad_mask |= 1u << (issued & 31);
       if (lane == 0) a_mbar_arrive(&bar[st]);
     } else if (lane == 0) {
       a_expect_tx(&bar[st], C::kTile);
-      a_bulk_load(ring + (size_t)st * C::kTile,
-                  static_cast<const uint8_t *>(j.c.pages) + (int64_t)page * j.c.page_stride +
-                      kv_tile_off(D, j.c.page_size, load.hr / j.row_tiles, in_page),
-                  C::kTile, &bar[st]);
+      a_bulk_load(ring + (size_t)st * C::kTile, static_cast<const uint8_t *>(j.c.pages) + off, C::kTile, &bar[st]);
     }
     ++issued;
-    load_tile += W;
+    ++load_tile;
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) issue();
 
   bool dead = false;  // a wait gave up: nothing more is copied or read
-  do {
+  bool first_piece = true;
+  while (work) {
     const int kvh = walk.hr / j.row_tiles, rt = walk.hr % j.row_tiles;
-    const int64_t len = __ldg(j.lens + walk.seq);
-    const int n_rows = j.group * j.q_tokens;
+    const int len = __ldg(j.lens + walk.seq);
     // ---- the rows' queries: lane (g, t) holds row g's values 4t.. of each half block
     uint32_t qf[NB][4];
     float qinit[NB][2], f[2];
-    int lo[2], hi[2], all_lo = 0, all_hi = 0x7fffffff;
+    int lo[2], hi[2], all_lo, all_hi;
     {
       const int r = rt * kRows + g;
-      float x[NB][8];
+      uint2 raw[NB][2];
       float top = 0.f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int z = 0; z < 8; ++z) x[b][z] = 0.f;
+      for (int b = 0; b < NB; ++b) raw[b][0] = raw[b][1] = make_uint2(0u, 0u);
       if (r < n_rows) {
         const T *src = static_cast<const T *>(j.q.data) +
                        ((int64_t)walk.seq * j.q_tokens + r / j.group) * j.q.token_stride +
@@ -296,16 +375,14 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint2 raw = *reinterpret_cast<const uint2 *>(src + 32 * b + 16 * half + 4 * t);
-            const T *e = reinterpret_cast<const T *>(&raw);
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              x[b][4 * half + z] = to_float(e[z]);
-              top = fmaxf(top, fabsf(x[b][4 * half + z]));
-            }
-          }
+          for (int half = 0; half < 2; ++half)
+            raw[b][half] = *reinterpret_cast<const uint2 *>(src + 32 * b + 16 * half + 4 * t);
       }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int z = 0; z < 8; ++z)
+          top = fmaxf(top, fabsf(to_float(reinterpret_cast<const T *>(&raw[b][z / 4])[z % 4])));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // 2^e with the row's largest value below 2^13 after it (an infinity or NaN stays what it is)
@@ -315,41 +392,41 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        float total = 0.f;
+        float sum = 0.f;
         __half h[8];
 #pragma unroll
         for (int z = 0; z < 8; ++z) {
           // high nibbles are 2^4 too large as fp16: their query values are 2^-4
-          h[z] = __float2half_rn(x[b][z] * up * (z < 4 ? 1.f : 0.0625f));
-          total += __half2float(h[z]) * (z < 4 ? 1.f : 16.f);
+          h[z] = __float2half_rn(to_float(reinterpret_cast<const T *>(&raw[b][z / 4])[z % 4]) * up *
+                                 (z < 4 ? 1.f : 0.0625f));
+          sum += __half2float(h[z]) * (z < 4 ? 1.f : 16.f);
         }
         qf[b][0] = h2_bits(__halves2half2(h[0], h[2]));
         qf[b][1] = h2_bits(__halves2half2(h[1], h[3]));
         qf[b][2] = h2_bits(__halves2half2(h[4], h[6]));
         qf[b][3] = h2_bits(__halves2half2(h[5], h[7]));
-        total += __shfl_xor_sync(0xffffffffu, total, 1);
-        total += __shfl_xor_sync(0xffffffffu, total, 2);
-        total *= -8.f * 5.9604644775390625e-08f;  // -8 x 2^-24
-        qinit[b][0] = __shfl_sync(0xffffffffu, total, 8 * t);
-        qinit[b][1] = __shfl_sync(0xffffffffu, total, 8 * t + 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= -8.f * 5.9604644775390625e-08f;  // -8 x 2^-24
+        qinit[b][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+        qinit[b][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
       }
       const float mine_f = j.scale * kLog2e * down * 16777216.f;
+      int64_t a, b;
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         f[z] = __shfl_sync(0xffffffffu, mine_f, 8 * t + 4 * z);
         const int rr = rt * kRows + 2 * t + z;
-        int64_t l = 0, h = 0;
-        if (rr < n_rows) kv_visible(len, j.q_tokens, rr / j.group, j.window, &l, &h);
-        lo[z] = (int)l;
-        hi[z] = (int)h;
+        a = b = 0;
+        if (rr < n_rows) kv_visible(len, j.q_tokens, rr / j.group, j.window, &a, &b);
+        lo[z] = (int)a;
+        hi[z] = (int)b;
       }
       // a tile inside [all_lo, all_hi) is seen whole by every row
-      const int last = min(n_rows, (rt + 1) * kRows) - 1;
-      int64_t l, h;
-      kv_visible(len, j.q_tokens, last / j.group, j.window, &l, &h);
-      all_lo = (int)l;
-      kv_visible(len, j.q_tokens, rt * kRows / j.group, j.window, &l, &h);
-      all_hi = (int)h;
+      kv_visible(len, j.q_tokens, (min(n_rows, (rt + 1) * kRows) - 1) / j.group, j.window, &a, &b);
+      all_lo = (int)a;
+      kv_visible(len, j.q_tokens, rt * kRows / j.group, j.window, &a, &b);
+      all_hi = (int)b;
     }
     // ---- this warp's tiles of the piece
     float acc[NB][2][4];
@@ -360,11 +437,12 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
 #pragma unroll
         for (int z = 0; z < 4; ++z) acc[b][h][z] = 0.f;
     float m[2] = {-a_inf(), -a_inf()}, l[2] = {0.f, 0.f};
-    float dtop = 0.f;   // largest value scale seen
-    float shift = -7.f; // reference = m + shift
+    float dtop = 0.f;                           // bound of the value scales seen
+    __half2 dtop2 = __float2half2_rn(0.f);
+    float shift = -7.f;                         // reference = m + shift
     bool poison = false;
 
-    for (int tile = walk.at + warp; tile < walk.end; tile += W) {
+    for (int tile = walk.at; tile < walk.end; ++tile) {
       const int st = used % S;
       const bool bad = (bad_mask >> (used & 31)) & 1u;
       if (!dead) dead = !__all_sync(0xffffffffu, a_mbar_wait(&bar[st], (used / S) & 1u));
@@ -401,70 +479,66 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
           }
         }
 #pragma unroll
-        for (int z = 0; z < 4; ++z) s[mt][z] = 0.f;
-#pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint32_t wa = *reinterpret_cast<const uint32_t *>(tp + (b * 32 + ra) * 16 + 4 * t);
           const uint32_t wb = *reinterpret_cast<const uint32_t *>(tp + (b * 32 + ra + 8) * 16 + 4 * t);
           const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
-          float c[4] = {qinit[b][0], qinit[b][1], qinit[b][0], qinit[b][1]};
-          mma16816(c, wa & 0x000F000Fu, wb & 0x000F000Fu, wa8 & 0x000F000Fu, wb8 & 0x000F000Fu, qf[b][0], qf[b][1]);
+          float c[4];
+          mma16816_from(c, wa & 0x000F000Fu, wb & 0x000F000Fu, wa8 & 0x000F000Fu, wb8 & 0x000F000Fu, qf[b][0], qf[b][1],
+                        qinit[b][0], qinit[b][1], qinit[b][0], qinit[b][1]);
           mma16816(c, wa & 0x00F000F0u, wb & 0x00F000F0u, wa8 & 0x00F000F0u, wb8 & 0x00F000F0u, qf[b][2], qf[b][3]);
           const float2 da = __half22float2(ka[b / 2]), db = __half22float2(kb[b / 2]);
           const float fa = (b & 1) ? da.y : da.x, fb = (b & 1) ? db.y : db.x;
-          s[mt][0] = fmaf(c[0], fa, s[mt][0]);
-          s[mt][1] = fmaf(c[1], fa, s[mt][1]);
-          s[mt][2] = fmaf(c[2], fb, s[mt][2]);
-          s[mt][3] = fmaf(c[3], fb, s[mt][3]);
+          s[mt][0] = b ? fmaf(c[0], fa, s[mt][0]) : c[0] * fa;
+          s[mt][1] = b ? fmaf(c[1], fa, s[mt][1]) : c[1] * fa;
+          s[mt][2] = b ? fmaf(c[2], fb, s[mt][2]) : c[2] * fb;
+          s[mt][3] = b ? fmaf(c[3], fb, s[mt][3]) : c[3] * fb;
         }
       }
-      // ---- scores in log2 units; what a row does not see is -inf
-      bool over = false;
+      // ---- what a row does not see scores -inf
+      if (!whole) {
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          s[mt][z] *= f[z & 1];
-          if (!whole) {
+          for (int z = 0; z < 4; ++z) {
             const int key = tok0 + mt * 16 + (z >= 2 ? 8 : 0) + pg;
             if (key < lo[z & 1] || key >= hi[z & 1]) s[mt][z] = -a_inf();
           }
-          over |= s[mt][z] > m[z & 1] + kLazy;
-        }
-      // ---- the largest value scale of the tile (those of tokens past the sequence count as 0)
+      }
+      float mx[2];  // log2 units; f > 0
+#pragma unroll
+      for (int z = 0; z < 2; ++z) mx[z] = fmaxf(fmaxf(s[0][z], s[0][z + 2]), fmaxf(s[1][z], s[1][z + 2])) * f[z];
+      // ---- the largest value scale of the tile (those of tokens past the sequence count as 0, NaN as none)
       const unsigned char *vs = tp + 34 * D;
-      uint32_t dmax = 0;
+      __half2 dmax = __float2half2_rn(0.f);
 #pragma unroll
       for (int z = 0; z < D / 64; ++z) {
         const int off = (z * 32 + lane) * 4;  // two scales of one token
-        uint32_t w = *reinterpret_cast<const uint32_t *>(vs + off) & 0x7FFF7FFFu;
-        if (!whole && tok0 + off / (D / 16) >= (int)len) w = 0;
-        dmax = __vmaxu2(dmax, w & ~__vcmpgtu2(w, 0x7BFF7BFFu));  // a NaN is no scale to make room for
+        __half2 w = *reinterpret_cast<const __half2 *>(vs + off);
+        if (!whole && tok0 + off / (D / 16) >= len) w = __float2half2_rn(0.f);
+        dmax = __hmax2(dmax, __habs2(w));
       }
-      const float dlane = fmaxf(__low2float(*reinterpret_cast<__half2 *>(&dmax)),
-                                __high2float(*reinterpret_cast<__half2 *>(&dmax)));
-      over |= dlane > dtop;
+      const bool over = mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy || !__hble2(dmax, dtop2);
       if (__any_sync(0xffffffffu, over)) {
-        float dn = dlane, mn[2];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) mn[z] = fmaxf(fmaxf(s[0][z], s[0][z + 2]), fmaxf(s[1][z], s[1][z + 2]));
+        float dn = fmaxf(__low2float(dmax), __high2float(dmax));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
-          mn[0] = fmaxf(mn[0], __shfl_xor_sync(0xffffffffu, mn[0], o));
-          mn[1] = fmaxf(mn[1], __shfl_xor_sync(0xffffffffu, mn[1], o));
+          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) dn = fmaxf(dn, __shfl_xor_sync(0xffffffffu, dn, o));
         float shift_n = shift;
         if (dn > dtop) {
-          // the new bound leaves room for scales up to twice the largest one; 2^(8 - shift) dtop < 2^16
-          dtop = fminf(dn, 65504.f) * 2.f;
+          // the bound leaves room for scales up to twice the largest one; 2^(8 - shift) dtop < 2^16
+          dtop = fminf(dn * 2.f, 65504.f);
+          dtop2 = __float2half2_rn(dtop);
           const int ex = (int)((__float_as_uint(dtop) >> 23) & 255) - 126;  // dtop < 2^ex
           shift_n = fmaxf((float)ex - 6.f, -7.f);
         }
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          const float m_new = fmaxf(m[z], mn[z]);
+          const float m_new = fmaxf(m[z], mx[z]);
           const float a = m[z] == -a_inf() ? 0.f : a_exp2((m[z] - m_new) + (shift - shift_n));
           m[z] = m_new;
           l[z] *= a;
@@ -478,11 +552,11 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
         }
         shift = shift_n;
       }
-      const float r0 = m[0] == -a_inf() ? 0.f : m[0] + shift, r1 = m[1] == -a_inf() ? 0.f : m[1] + shift;
+      const float r0 = m[0] == -a_inf() ? 0.f : -(m[0] + shift), r1 = m[1] == -a_inf() ? 0.f : -(m[1] + shift);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const float p0 = a_exp2(s[mt][0] - r0), p1 = a_exp2(s[mt][1] - r1);
-        const float p2 = a_exp2(s[mt][2] - r0), p3 = a_exp2(s[mt][3] - r1);
+        const float p0 = a_exp2(fmaf(s[mt][0], f[0], r0)), p1 = a_exp2(fmaf(s[mt][1], f[1], r1));
+        const float p2 = a_exp2(fmaf(s[mt][2], f[0], r0)), p3 = a_exp2(fmaf(s[mt][3], f[1], r1));
         l[0] += p0 + p2;
         l[1] += p1 + p3;
         const uint32_t b0 = transpose8x8(h2_bits(__floats2half2_rn(p0, p1)));  // row g, tokens t and t + 4
@@ -503,17 +577,17 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
             }
           }
         }
+        uint32_t unseen0 = 0, unseen1 = 0;
+        if (!whole) {
+          // a weight of 0 contributes 0 even where the scale is not finite: such a token may be unseen
+          unseen0 = __vcmpeq2(b0, 0u);
+          unseen1 = __vcmpeq2(b1, 0u);
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint32_t sel = (b & 1) ? 0x7632u : 0x5410u;
-          uint32_t e0 = mul_h2(b0, __byte_perm(d[0][b / 2], d[1][b / 2], sel));
-          uint32_t e1 = mul_h2(b1, __byte_perm(d[2][b / 2], d[3][b / 2], sel));
-          if (!whole) {
-            // a weight of 0 contributes 0 even where the scale is not finite: such a token may be unseen
-            const uint32_t z0 = __vcmpeq2(b0, 0u), z1 = __vcmpeq2(b1, 0u);
-            e0 &= ~z0;
-            e1 &= ~z1;
-          }
+          const uint32_t e0 = mul_h2(b0, __byte_perm(d[0][b / 2], d[1][b / 2], sel)) & ~unseen0;
+          const uint32_t e1 = mul_h2(b1, __byte_perm(d[2][b / 2], d[3][b / 2], sel)) & ~unseen1;
           const unsigned char *cp = tp + 18 * D + (b * 32 + k0) * 16 + 2 * g;
           const uint32_t v0 = *reinterpret_cast<const uint16_t *>(cp), v1 = *reinterpret_cast<const uint16_t *>(cp + 64);
           const uint32_t v2 = *reinterpret_cast<const uint16_t *>(cp + 128),
@@ -530,7 +604,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       __syncwarp();
       issue();
     }
-    // ---- merge the warps: l over the lanes that share a row, then pairwise over the warps
+    // ---- the piece: l over the lanes that share a row; accumulators without the nibbles' factors
     if (__any_sync(0xffffffffu, poison)) l[0] = l[1] = a_nan();
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
@@ -540,124 +614,122 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     float r[2];
 #pragma unroll
     for (int z = 0; z < 2; ++z) r[z] = m[z] == -a_inf() ? -a_inf() : m[z] + shift;
-    constexpr int kSlot = C::kOut + 2 * kRows;
-#pragma unroll 1
-    for (int half = W / 2; half > 0; half >>= 1) {
-      __syncthreads();
-      if (warp >= half && warp < 2 * half) {
-        float *o = merge + (size_t)(warp - half) * kSlot;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float4 *>(o + ((b * 2 + h) * 32 + lane) * 4) =
-                make_float4(acc[b][h][0], acc[b][h][1], acc[b][h][2], acc[b][h][3]);
-        if (g == 0)
-          *reinterpret_cast<float4 *>(o + C::kOut + 4 * t) = make_float4(r[0], r[1], l[0], l[1]);
-      }
-      __syncthreads();
-      if (warp < half) {
-        const float *o = merge + (size_t)warp * kSlot;
-        const float4 w = *reinterpret_cast<const float4 *>(o + C::kOut + 4 * t);
-        const float ro[2] = {w.x, w.y}, lo2[2] = {w.z, w.w};
-        float wa[2], wb[2];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const float top = fmaxf(r[z], ro[z]);
-          wa[z] = r[z] == -a_inf() ? 0.f : a_exp2(r[z] - top);
-          wb[z] = ro[z] == -a_inf() ? 0.f : a_exp2(ro[z] - top);
-          // a poisoned warp may hold no weight: its NaN must not be multiplied away
-          l[z] = (l[z] != l[z] || lo2[z] != lo2[z]) ? a_nan() : l[z] * wa[z] + lo2[z] * wb[z];
-          r[z] = top;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 v = *reinterpret_cast<const float4 *>(o + ((b * 2 + h) * 32 + lane) * 4);
-            acc[b][h][0] = acc[b][h][0] * wa[0] + v.x * wb[0];
-            acc[b][h][1] = acc[b][h][1] * wa[1] + v.y * wb[1];
-            acc[b][h][2] = acc[b][h][2] * wa[0] + v.z * wb[0];
-            acc[b][h][3] = acc[b][h][3] * wa[1] + v.w * wb[1];
-          }
-      }
-    }
-    // ---- the piece's result, or its part of the pair's
-    const int64_t first_cta = pair0 / share, last_cta = (pair0 + walk.n - 1) / share;
-    const bool alone = first_cta == last_cta;
-    const int64_t tok = (int64_t)walk.seq * j.q_tokens;
-    if (warp == 0) {
+        for (int z = 0; z < 4; ++z) acc[b][h][z] *= z < 2 ? 16777216.f : 1048576.f;
+    if (walk.at == 0 && walk.end == walk.n) {
+      // all of the pair: its result
+      const int64_t tok = (int64_t)walk.seq * j.q_tokens;
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
-        const int row = 2 * t + z, rr = rt * kRows + row;
-        float *po = j.part + ((size_t)(blockIdx.x * 2 + (blockIdx.x == first_cta ? 1 : 0)) * kRows + row) * (D + 2);
+        const int rr = rt * kRows + 2 * t + z;
+        if (rr >= n_rows) continue;
         const float inv = l[z] > 0.f || l[z] != l[z] ? 1.f / l[z] : 0.f;
-        const bool live = rr < n_rows;
         const int64_t at = (tok + rr / j.group) * j.hq + kvh * j.group + rr % j.group;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float k = half ? 1048576.f : 16777216.f;
-            const float a = acc[b][0][z + 2 * half] * k, c = acc[b][1][z + 2 * half] * k;
-            const int dim = 32 * b + 16 * half + 2 * g;
-            if (alone) {
-              if (live) store_pair(static_cast<T *>(j.out) + at * D + dim, a * inv, c * inv);
-            } else {
-              *reinterpret_cast<float2 *>(po + dim) = make_float2(a, c);
-            }
-          }
-        if (g == 0) {
-          if (!alone) *reinterpret_cast<float2 *>(po + D) = make_float2(r[z], l[z]);
-          else if (live && j.lse) j.lse[at] = l[z] == 0.f ? -a_inf() : (r[z] + log2f(l[z])) * kLn2;
-        }
+          for (int half = 0; half < 2; ++half)
+            store_pair(static_cast<T *>(j.out) + at * D + 32 * b + 16 * half + 2 * g, acc[b][0][z + 2 * half] * inv,
+                       acc[b][1][z + 2 * half] * inv);
+        if (g == 0 && j.lse) j.lse[at] = l[z] == 0.f ? -a_inf() : (r[z] + log2f(l[z])) * kLn2;
       }
+    } else {
+      // a part: the first piece waits beside the ring, the last one in the ring (every copy has been used by then)
+      const bool begins = walk.at == 0;
+      float *o = first_piece && !begins ? heads_mem + (size_t)warp * C::kPart : reinterpret_cast<float *>(ring);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float4 *>(o + ((b * 2 + h) * 32 + lane) * 4) =
+              make_float4(acc[b][h][0], acc[b][h][1], acc[b][h][2], acc[b][h][3]);
+      if (g == 0) *reinterpret_cast<float4 *>(o + C::kOut + 4 * t) = make_float4(r[0], r[1], l[0], l[1]);
+      if (lane == 0) meta[2 * warp + (first_piece && !begins ? 0 : 1)] = {walk.pair0, walk.seq, walk.hr, walk.n, 1};
     }
-    if (!alone) {
-      __threadfence();
-      __syncthreads();
-      const int parts = (int)(last_cta - first_cta) + 1;
-      if (tid == 0) {
-        __threadfence();
-        sh_last = atomicAdd(j.count + first_cta, 1u) == (uint32_t)(parts - 1);
-      }
-      __syncthreads();
-      if (sh_last) {
-        __threadfence();
-        if (tid == 0) j.count[first_cta] = 0;
-        auto piece = [&](int i) {
-          return j.part + (size_t)((first_cta + i) * 2 + (i == 0 ? 1 : 0)) * kRows * (D + 2);
-        };
-        for (int x = tid; x < kRows * D / 2; x += kThreads) {
-          const int row = x / (D / 2), dim = (x % (D / 2)) * 2, rr = rt * kRows + row;
-          if (rr >= n_rows) continue;
-          float top = -a_inf();
-          for (int i = 0; i < parts; ++i) top = fmaxf(top, __ldcg(piece(i) + row * (D + 2) + D));
-          float a = 0.f, c = 0.f, sum_l = 0.f;
-          for (int i = 0; i < parts; ++i) {
-            const float *p = piece(i) + row * (D + 2);
-            const float2 rl = __ldcg(reinterpret_cast<const float2 *>(p + D));
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(p + dim));
-            if (rl.y != rl.y) sum_l = a_nan();
-            if (rl.x == -a_inf()) continue;
-            const float w = a_exp2(rl.x - top);
-            a += v.x * w;
-            c += v.y * w;
-            sum_l += rl.y * w;
-          }
-          const float inv = sum_l > 0.f || sum_l != sum_l ? 1.f / sum_l : 0.f;
-          const int64_t at = (tok + rr / j.group) * j.hq + kvh * j.group + rr % j.group;
-          store_pair(static_cast<T *>(j.out) + at * D + dim, a * inv, c * inv);
-          if (dim == 0 && j.lse) j.lse[at] = sum_l == 0.f ? -a_inf() : (top + log2f(sum_l)) * kLn2;
-        }
-      }
-    }
-    // ---- next piece
-    pair0 += walk.n;
-  } while (walk_next(j, walk));
+    first_piece = false;
+    work = walk_next(j, walk);
+  }
   // copies that a wait gave up on, or that came after it, must have landed before the CTA's memory is gone
   if (dead)
     for (uint32_t i = issued > S ? issued - S : 0; i < issued; ++i) (void)a_mbar_wait(&bar[i % S], (i / S) & 1u);
+
+  // ---- pairs that warps share
+  __syncthreads();
+  for (int i = 0; i < 2 * W;) {
+    if (!meta[i].valid) {
+      ++i;
+      continue;
+    }
+    const PartMeta pm = meta[i];
+    int parts = 0;
+    uint64_t list = 0;  // the parts' places in meta, 4 bits each
+    for (; i < 2 * W && (!meta[i].valid || meta[i].pair0 == pm.pair0); ++i)
+      if (meta[i].valid) {
+        list |= (uint64_t)i << (4 * parts);
+        ++parts;
+      }
+    auto own_part = [&](int k) {
+      const int at = (int)(list >> (4 * k)) & 15;
+      return (at & 1) ? reinterpret_cast<const float *>(sm + (size_t)(at / 2) * S * C::kTile)
+                      : heads_mem + (size_t)(at / 2) * C::kPart;
+    };
+    // CTAs that hold tiles of the pair
+    int64_t cta0 = blockIdx.x, cta1 = blockIdx.x;
+    if (!alone) {
+      cta0 = (pm.pair0 + kPairCost) / (share * W);
+      cta1 = (pm.pair0 + kPairCost + pm.n - 1) / (share * W);
+    }
+    const int kvh = pm.hr / j.row_tiles, rt = pm.hr % j.row_tiles;
+    auto result = [&](int f, const float4 v, const float r[2], const float l[2]) {
+      const int ln = f & 31, dim = 32 * (f / 64) + 2 * (ln >> 2) + ((f >> 5) & 1);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int rr = rt * kRows + 2 * (ln & 3) + z;
+        if (rr >= n_rows) continue;
+        const float inv = l[z] > 0.f || l[z] != l[z] ? 1.f / l[z] : 0.f;
+        const int64_t at = ((int64_t)pm.seq * j.q_tokens + rr / j.group) * j.hq + kvh * j.group + rr % j.group;
+        T *o = static_cast<T *>(j.out) + at * D + dim;
+        o[0] = T((z ? v.y : v.x) * inv);
+        o[16] = T((z ? v.w : v.z) * inv);
+        if (f < 4 && j.lse) j.lse[at] = l[z] == 0.f ? -a_inf() : (r[z] + log2f(l[z])) * kLn2;
+      }
+    };
+    if (cta0 == cta1) {
+      for (int f = tid; f < C::kOut / 4; f += kThreads) {
+        float r[2], l[2];
+        const float4 v = merge_parts<true>(f, C::kOut, parts, own_part, r, l);
+        result(f, v, r, l);
+      }
+      continue;
+    }
+    float *mine = j.part + (size_t)(blockIdx.x * 2 + (blockIdx.x == cta0 ? 1 : 0)) * C::kPart;
+    for (int f = tid; f < C::kOut / 4; f += kThreads) {
+      float r[2], l[2];
+      const float4 v = merge_parts<true>(f, C::kOut, parts, own_part, r, l);
+      *reinterpret_cast<float4 *>(mine + 4 * f) = v;
+      if (f < 4) *reinterpret_cast<float4 *>(mine + C::kOut + 4 * f) = make_float4(r[0], r[1], l[0], l[1]);
+    }
+    __threadfence();
+    __syncthreads();
+    const int ctas = (int)(cta1 - cta0) + 1;
+    if (tid == 0) sh_last = atomicAdd(j.count + cta0, 1u) == (uint32_t)(ctas - 1);
+    __syncthreads();
+    if (sh_last) {
+      __threadfence();
+      if (tid == 0) j.count[cta0] = 0;
+      auto cta_part = [&](int k) { return j.part + (size_t)((cta0 + k) * 2 + (k == 0 ? 1 : 0)) * C::kPart; };
+      for (int f = tid; f < C::kOut / 4; f += kThreads) {
+        float r[2], l[2];
+        const float4 v = merge_parts<false>(f, C::kOut, ctas, cta_part, r, l);
+        result(f, v, r, l);
+      }
+    }
+    __syncthreads();  // sh_last is read by all before the next pair's
+  }
 }
 
 constexpr int kDecodeSms = 152;
@@ -675,7 +747,8 @@ int launch_decode(const DecodeJob &j, int grid, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-constexpr int64_t kCountBytes = 4096;  // counters at the head of the workspace
+constexpr int64_t kCountBytes = MOE_KV_COUNTER_BYTES;  // counters at the head of the workspace
+static_assert(kDecodeSms * 2 * 4 <= kCountBytes, "a counter per CTA");
 
 }  // namespace
 }  // namespace moe
@@ -685,7 +758,7 @@ using namespace moe;
 MOE_API int64_t moe_kv_attention_workspace(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t q_tokens) {
   if (n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads || q_tokens <= 0 || !kv_sizes_ok(n_kv_heads, head_dim, 32))
     return 0;
-  return kCountBytes + (int64_t)decode_grid_cap(head_dim) * 2 * kRows * (head_dim + 2) * 4;
+  return kCountBytes + (int64_t)decode_grid_cap(head_dim) * 2 * (kRows * head_dim + 16) * 4;
 }
 
 MOE_API int moe_kv_attention(const moe_kv_cache *c, const int32_t *seq_lens, const moe_tensor *q, int32_t n_q_heads,
@@ -717,11 +790,10 @@ MOE_API int moe_kv_attention(const moe_kv_cache *c, const int32_t *seq_lens, con
   j.lse = lse;
   j.count = static_cast<uint32_t *>(workspace);
   j.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCountBytes);
-  j.min_share = 16;
-  // no more CTAs than there can be shares
-  const int64_t tiles = (int64_t)c->n_seqs * c->n_kv_heads * j.row_tiles *
-                        std::max<int64_t>(1, (int64_t)c->table_width * (c->page_size / kKvTile));
-  const int64_t most = std::max<int64_t>(1, (tiles + j.min_share - 1) / j.min_share);
+  // no more CTAs than there are tiles for their warps, unless pairs can have one each
+  const int64_t pairs = (int64_t)c->n_seqs * c->n_kv_heads * j.row_tiles;
+  const int64_t tiles = pairs * std::max<int64_t>(1, (int64_t)c->table_width * (c->page_size / kKvTile));
+  const int64_t most = std::max<int64_t>(pairs, (tiles + 7) / 8);
   const int grid = (int)std::min<int64_t>(most, decode_grid_cap(c->head_dim));
   cudaStream_t st = (cudaStream_t)cuda_stream;
   const int D = c->head_dim;
