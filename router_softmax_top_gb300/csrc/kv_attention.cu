@@ -37,6 +37,7 @@
 // in the order of the keys, so results do not depend on timing.  Few short pairs
 // instead take a CTA each, whose warps share its tiles: nothing is merged across CTAs.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.cuh"
 
@@ -45,6 +46,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;  // log2 by which a score may exceed its row's reference
+constexpr int kDecodeWarps = 8;
 constexpr int kRows = 8;      // rows (heads x query tokens) of one work unit
 
 struct DecodeJob {
@@ -55,20 +57,23 @@ struct DecodeJob {
   float scale;
   void *out;
   float *lse;
-  float *part;        // [grid][2][kPart]: partial results of the pairs that a CTA shares with the one before or after
+  float *part;        // [grid][2 + kWarps][kPart]: partial results of the pairs that a CTA shares with the one before
+                      // or after, then those of the first pieces of its warps
   uint32_t *count;    // [grid]: CTAs done with the pair whose first tiles that CTA has
 };
 
 template <int D>
 struct DecodeCfg {
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = kDecodeWarps;
   static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kTile = 36 * D;
   // a partial result: accumulators as the matrix unit leaves them, [D/16][32 lanes][4], then per t of a lane the
   // references and weight sums of rows 2t and 2t + 1
   static constexpr int kOut = kRows * D, kPart = kOut + 16;
   static constexpr size_t kRing = (size_t)kWarps * kStages * kTile;
-  static constexpr size_t kSmem = kRing + (size_t)kWarps * kPart * sizeof(float);
+  // per warp and block: the query operand (16 bytes per lane), and the accumulators' start (16 bytes per t)
+  static constexpr int kQuery = (D / 32) * (32 + 4) * 16;
+  static constexpr size_t kSmem = kRing + (size_t)kWarps * kQuery;
   static constexpr int kCtas = D == 256 ? 1 : 2;  // resident per SM
   static_assert((size_t)kStages * kTile >= kPart * sizeof(float), "a warp's ring holds its last partial result");
 };
@@ -76,7 +81,7 @@ struct DecodeCfg {
 // d = a b + c
 __device__ __forceinline__ void mma16816_from(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
@@ -84,14 +89,14 @@ __device__ __forceinline__ void mma16816_from(float d[4], uint32_t a0, uint32_t 
 // c += a b
 __device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
@@ -163,7 +168,7 @@ struct PartMeta {
 };
 
 // Merges partial results, in order, for the four values of accumulator word f: rows 2t and 2t + 1 of a lane.
-// Own: parts in shared memory; otherwise in the workspace, written by other CTAs (read past L1).
+// Own: parts of this CTA's warps, in shared memory or the workspace; otherwise other CTAs' (read past L1).
 template <bool Own, typename V>
 __device__ __forceinline__ V part_load(const float *p) {
   if constexpr (Own) return *reinterpret_cast<const V *>(p);
@@ -205,7 +210,9 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   __shared__ PartMeta meta[2 * W];  // per warp: of its first piece, of its last one
   __shared__ Walk loads[W];         // per warp: the piece that its copies are at
   __shared__ int sh_last;
-  float *heads_mem = reinterpret_cast<float *>(sm + C::kRing);
+  float *heads_mem = j.part + ((size_t)blockIdx.x * (2 + W) + 2) * C::kPart;
+  uint4 *q_mem = reinterpret_cast<uint4 *>(sm + C::kRing + (size_t)(threadIdx.x >> 5) * C::kQuery);  // [NB][32]
+  float4 *q_start = reinterpret_cast<float4 *>(q_mem + D);                                          // [NB][4]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int heads = j.c.n_kv_heads * j.row_tiles;
   const int64_t n_rows_all = (int64_t)j.q_tokens * j.hq;
@@ -312,21 +319,20 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   uint32_t bad_mask = 0;    // by (issued & 31): a tile without a page
 
   auto issue = [&]() {
-    if (!load_more) return;
-    if (load_tile >= load_end) {
-      Walk next = load;
-      load_more = walk_next(j, next);
-      if (!load_more) return;
-      load_tile = next.at;
-      load_end = next.end;
-      src_end = 0;
-      __syncwarp();
-      if (lane == 0) load = next;
-      __syncwarp();
-    }
-    if (load_tile >= src_end) {
+    if (load_tile >= src_end) {  // page numbers of the next tiles, one per lane
+      if (load_tile >= load_end) {
+        if (!load_more) return;
+        Walk next = load;
+        load_more = walk_next(j, next);
+        if (!load_more) return;
+        load_tile = next.at;
+        load_end = next.end;
+        __syncwarp();
+        if (lane == 0) load = next;
+        __syncwarp();
+      }
       src_at = load_tile;
-      src_end = load_tile + 32;
+      src_end = min(load_end, load_tile + 32);
       const int tile = load_tile + lane;
       src_off = -1;
       if (tile < load_end) {
@@ -353,14 +359,19 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
 #pragma unroll
   for (int s = 0; s < S; ++s) issue();
 
+  // -8 as fp16 pairs: -8 2^-24 for the low nibbles' rows, -8 2^-20 for the high ones'.  Four registers that the
+  // compiler cannot see through: it would build the operand anew, move by move, for every instruction.
+  uint32_t eight[4];
+  asm volatile("mov.b32 %0, 0x80088008;\n mov.b32 %1, 0x80808080;\n mov.b32 %2, 0x80088008;\n mov.b32 %3, 0x80808080;"
+               : "=r"(eight[0]), "=r"(eight[1]), "=r"(eight[2]), "=r"(eight[3]));
+
   bool dead = false;  // a wait gave up: nothing more is copied or read
   bool first_piece = true;
   while (work) {
     const int kvh = walk.hr / j.row_tiles, rt = walk.hr % j.row_tiles;
     const int len = __ldg(j.lens + walk.seq);
     // ---- the rows' queries: lane (g, t) holds row g's values 4t.. of each half block
-    uint32_t qf[NB][4];
-    float qinit[NB][2], f[2];
+    float f[2];
     int lo[2], hi[2], all_lo, all_hi;
     {
       const int r = rt * kRows + g;
@@ -401,16 +412,15 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
                                  (z < 4 ? 1.f : 0.0625f));
           sum += __half2float(h[z]) * (z < 4 ? 1.f : 16.f);
         }
-        qf[b][0] = h2_bits(__halves2half2(h[0], h[2]));
-        qf[b][1] = h2_bits(__halves2half2(h[1], h[3]));
-        qf[b][2] = h2_bits(__halves2half2(h[4], h[6]));
-        qf[b][3] = h2_bits(__halves2half2(h[5], h[7]));
+        q_mem[b * 32 + lane] = make_uint4(h2_bits(__halves2half2(h[0], h[2])), h2_bits(__halves2half2(h[1], h[3])),
+                                          h2_bits(__halves2half2(h[4], h[6])), h2_bits(__halves2half2(h[5], h[7])));
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         sum *= -8.f * 5.9604644775390625e-08f;  // -8 x 2^-24
-        qinit[b][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-        qinit[b][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        const float s0 = __shfl_sync(0xffffffffu, sum, 8 * t), s1 = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        if (g == 0) q_start[b * 4 + t] = make_float4(s0, s1, s0, s1);
       }
+      __syncwarp();
       const float mine_f = j.scale * kLog2e * down * 16777216.f;
       int64_t a, b;
 #pragma unroll
@@ -442,57 +452,47 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     float shift = -7.f;                         // reference = m + shift
     bool poison = false;
 
-    for (int tile = walk.at; tile < walk.end; ++tile) {
-      const int st = used % S;
-      const bool bad = (bad_mask >> (used & 31)) & 1u;
-      if (!dead) dead = !__all_sync(0xffffffffu, a_mbar_wait(&bar[st], (used / S) & 1u));
-      ++used;
-      if (dead || bad) {
-        poison = true;
-        if (lane == 0 && j.c.status) atomicOr(j.c.status, dead ? MOE_KV_TIMED_OUT : MOE_KV_BAD_PAGE);
-        __syncwarp();
-        if (!dead) issue();
-        continue;
-      }
-      const unsigned char *tp = ring + (size_t)st * C::kTile;
-      const int tok0 = (walk.first + tile) * kKvTile;
-      const bool whole = tok0 >= all_lo && tok0 + kKvTile <= all_hi;
+    // One tile.  Whole: every row sees all of it.
+    auto compute = [&](const unsigned char *tp, const int tok0, auto is_whole) {
+      constexpr bool whole = decltype(is_whole)::value;
       // key k of the matrix (of 8) is token perm(k) = k / 2 + 4 (k odd), so that the value operand's
       // pairs (2t, 2t + 1) are tokens t and t + 4 and a load covers neighbouring tokens
       const int pg = (g >> 1) + ((g & 1) << 2);
       float s[2][4];
+      __half2 kd[2][2][NB / 2];  // key scales of tokens 16 mt + pg and 8 more
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const int ra = mt * 16 + pg;
-        __half2 ka[NB / 2], kb[NB / 2];
-        {
-          const unsigned char *sa = tp + 16 * D + ra * (D / 16), *sb = sa + 8 * (D / 16);
-          if constexpr (NB == 2) {
-            ka[0] = *reinterpret_cast<const __half2 *>(sa);
-            kb[0] = *reinterpret_cast<const __half2 *>(sb);
-          } else {
+      for (int x = 0; x < 4; ++x) {
+        const unsigned char *sa = tp + 16 * D + (8 * x + pg) * (D / 16);
+        if constexpr (NB == 2) {
+          kd[x / 2][x % 2][0] = *reinterpret_cast<const __half2 *>(sa);
+        } else {
 #pragma unroll
-            for (int z = 0; z < NB / 4; ++z) {
-              *reinterpret_cast<uint2 *>(&ka[2 * z]) = *reinterpret_cast<const uint2 *>(sa + 8 * z);
-              *reinterpret_cast<uint2 *>(&kb[2 * z]) = *reinterpret_cast<const uint2 *>(sb + 8 * z);
-            }
-          }
+          for (int z = 0; z < NB / 4; ++z)
+            *reinterpret_cast<uint2 *>(&kd[x / 2][x % 2][2 * z]) = *reinterpret_cast<const uint2 *>(sa + 8 * z);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float c[2][4];
+        const uint4 qf = q_mem[b * 32 + lane];
+        const float4 start = q_start[b * 4 + t];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const unsigned char *kp = tp + (b * 32 + mt * 16 + pg) * 16 + 4 * t;
+          const uint32_t wa = *reinterpret_cast<const uint32_t *>(kp), wb = *reinterpret_cast<const uint32_t *>(kp + 128);
+          const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
+          mma16816_from(c[mt], wa & 0x000F000Fu, wb & 0x000F000Fu, wa8 & 0x000F000Fu, wb8 & 0x000F000Fu, qf.x, qf.y,
+                        start.x, start.y, start.z, start.w);
+          mma16816(c[mt], wa & 0x00F000F0u, wb & 0x00F000F0u, wa8 & 0x00F000F0u, wb8 & 0x00F000F0u, qf.z, qf.w);
         }
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint32_t wa = *reinterpret_cast<const uint32_t *>(tp + (b * 32 + ra) * 16 + 4 * t);
-          const uint32_t wb = *reinterpret_cast<const uint32_t *>(tp + (b * 32 + ra + 8) * 16 + 4 * t);
-          const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
-          float c[4];
-          mma16816_from(c, wa & 0x000F000Fu, wb & 0x000F000Fu, wa8 & 0x000F000Fu, wb8 & 0x000F000Fu, qf[b][0], qf[b][1],
-                        qinit[b][0], qinit[b][1], qinit[b][0], qinit[b][1]);
-          mma16816(c, wa & 0x00F000F0u, wb & 0x00F000F0u, wa8 & 0x00F000F0u, wb8 & 0x00F000F0u, qf[b][2], qf[b][3]);
-          const float2 da = __half22float2(ka[b / 2]), db = __half22float2(kb[b / 2]);
-          const float fa = (b & 1) ? da.y : da.x, fb = (b & 1) ? db.y : db.x;
-          s[mt][0] = b ? fmaf(c[0], fa, s[mt][0]) : c[0] * fa;
-          s[mt][1] = b ? fmaf(c[1], fa, s[mt][1]) : c[1] * fa;
-          s[mt][2] = b ? fmaf(c[2], fb, s[mt][2]) : c[2] * fb;
-          s[mt][3] = b ? fmaf(c[3], fb, s[mt][3]) : c[3] * fb;
+        for (int mt = 0; mt < 2; ++mt) {
+          const float fa = (b & 1) ? __high2float(kd[mt][0][b / 2]) : __low2float(kd[mt][0][b / 2]);
+          const float fb = (b & 1) ? __high2float(kd[mt][1][b / 2]) : __low2float(kd[mt][1][b / 2]);
+          s[mt][0] = b ? fmaf(c[mt][0], fa, s[mt][0]) : c[mt][0] * fa;
+          s[mt][1] = b ? fmaf(c[mt][1], fa, s[mt][1]) : c[mt][1] * fa;
+          s[mt][2] = b ? fmaf(c[mt][2], fb, s[mt][2]) : c[mt][2] * fb;
+          s[mt][3] = b ? fmaf(c[mt][3], fb, s[mt][3]) : c[mt][3] * fb;
         }
       }
       // ---- what a row does not see scores -inf
@@ -586,8 +586,12 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint32_t sel = (b & 1) ? 0x7632u : 0x5410u;
-          const uint32_t e0 = mul_h2(b0, __byte_perm(d[0][b / 2], d[1][b / 2], sel)) & ~unseen0;
-          const uint32_t e1 = mul_h2(b1, __byte_perm(d[2][b / 2], d[3][b / 2], sel)) & ~unseen1;
+          uint32_t e0 = mul_h2(b0, __byte_perm(d[0][b / 2], d[1][b / 2], sel));
+          uint32_t e1 = mul_h2(b1, __byte_perm(d[2][b / 2], d[3][b / 2], sel));
+          if (!whole) {
+            e0 &= ~unseen0;
+            e1 &= ~unseen1;
+          }
           const unsigned char *cp = tp + 18 * D + (b * 32 + k0) * 16 + 2 * g;
           const uint32_t v0 = *reinterpret_cast<const uint16_t *>(cp), v1 = *reinterpret_cast<const uint16_t *>(cp + 64);
           const uint32_t v2 = *reinterpret_cast<const uint16_t *>(cp + 128),
@@ -596,13 +600,36 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
           const uint32_t x8 = x >> 8, y8 = y >> 8;
           mma16816(acc[b][0], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, e0, e1);
           mma16816(acc[b][1], x8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x000F000Fu, y8 & 0x00F000F0u, e0, e1);
-          // -8: as fp16, -8 2^-24 for the low nibbles' rows and -8 2^-20 for the high ones'
-          mma16816(acc[b][0], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, e0, e1);
-          mma16816(acc[b][1], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, e0, e1);
+          mma16816(acc[b][0], eight[0], eight[1], eight[2], eight[3], e0, e1);
+          mma16816(acc[b][1], eight[0], eight[1], eight[2], eight[3], e0, e1);
         }
       }
-      __syncwarp();
-      issue();
+    };
+    auto tiles = [&](int from, int to, auto is_whole) {
+#pragma unroll 1
+      for (int tile = from; tile < to; ++tile) {
+        const int st = used % S;
+        const uint32_t ph = (used / S) & 1u, bit = 1u << (used & 31);
+        ++used;
+        if (!__all_sync(0xffffffffu, a_mbar_try(&bar[st], ph)))  // not there yet
+          dead = dead || !__all_sync(0xffffffffu, a_mbar_wait(&bar[st], ph));
+        if (dead || (bad_mask & bit)) {
+          poison = true;
+          if (lane == 0 && j.c.status) atomicOr(j.c.status, dead ? MOE_KV_TIMED_OUT : MOE_KV_BAD_PAGE);
+        } else {
+          compute(ring + (size_t)st * C::kTile, (walk.first + tile) * kKvTile, is_whole);
+        }
+        __syncwarp();
+        if (!dead) issue();
+      }
+    };
+    // tiles that some row sees in part, tiles that all rows see whole, and again those in part
+    const int w0 = min(max((all_lo + kKvTile - 1) / kKvTile - walk.first, walk.at), walk.end);
+    const int w1 = min(max(all_hi / kKvTile - walk.first, w0), walk.end);
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      tiles(pass ? w1 : walk.at, pass ? walk.end : w0, std::false_type());
+      if (pass == 0) tiles(w0, w1, std::true_type());
     }
     // ---- the piece: l over the lanes that share a row; accumulators without the nibbles' factors
     if (__any_sync(0xffffffffu, poison)) l[0] = l[1] = a_nan();
@@ -638,7 +665,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
         if (g == 0 && j.lse) j.lse[at] = l[z] == 0.f ? -a_inf() : (r[z] + log2f(l[z])) * kLn2;
       }
     } else {
-      // a part: the first piece waits beside the ring, the last one in the ring (every copy has been used by then)
+      // a part: the first piece waits in the workspace, the last one in the ring (every copy has been used by then)
       const bool begins = walk.at == 0;
       float *o = first_piece && !begins ? heads_mem + (size_t)warp * C::kPart : reinterpret_cast<float *>(ring);
 #pragma unroll
@@ -675,7 +702,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     auto own_part = [&](int k) {
       const int at = (int)(list >> (4 * k)) & 15;
       return (at & 1) ? reinterpret_cast<const float *>(sm + (size_t)(at / 2) * S * C::kTile)
-                      : heads_mem + (size_t)(at / 2) * C::kPart;
+                      : static_cast<const float *>(heads_mem + (size_t)(at / 2) * C::kPart);
     };
     // CTAs that hold tiles of the pair
     int64_t cta0 = blockIdx.x, cta1 = blockIdx.x;
@@ -706,7 +733,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       }
       continue;
     }
-    float *mine = j.part + (size_t)(blockIdx.x * 2 + (blockIdx.x == cta0 ? 1 : 0)) * C::kPart;
+    float *mine = j.part + ((size_t)blockIdx.x * (2 + W) + (blockIdx.x == cta0 ? 1 : 0)) * C::kPart;
     for (int f = tid; f < C::kOut / 4; f += kThreads) {
       float r[2], l[2];
       const float4 v = merge_parts<true>(f, C::kOut, parts, own_part, r, l);
@@ -721,7 +748,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     if (sh_last) {
       __threadfence();
       if (tid == 0) j.count[cta0] = 0;
-      auto cta_part = [&](int k) { return j.part + (size_t)((cta0 + k) * 2 + (k == 0 ? 1 : 0)) * C::kPart; };
+      auto cta_part = [&](int k) { return j.part + ((size_t)(cta0 + k) * (2 + W) + (k == 0 ? 1 : 0)) * C::kPart; };
       for (int f = tid; f < C::kOut / 4; f += kThreads) {
         float r[2], l[2];
         const float4 v = merge_parts<false>(f, C::kOut, ctas, cta_part, r, l);
@@ -758,7 +785,7 @@ using namespace moe;
 MOE_API int64_t moe_kv_attention_workspace(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t q_tokens) {
   if (n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads || q_tokens <= 0 || !kv_sizes_ok(n_kv_heads, head_dim, 32))
     return 0;
-  return kCountBytes + (int64_t)decode_grid_cap(head_dim) * 2 * (kRows * head_dim + 16) * 4;
+  return kCountBytes + (int64_t)decode_grid_cap(head_dim) * (2 + kDecodeWarps) * (kRows * head_dim + 16) * 4;
 }
 
 MOE_API int moe_kv_attention(const moe_kv_cache *c, const int32_t *seq_lens, const moe_tensor *q, int32_t n_q_heads,
