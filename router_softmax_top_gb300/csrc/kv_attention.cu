@@ -208,7 +208,9 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ uint64_t bars[W][S];
   __shared__ PartMeta meta[2 * W];  // per warp: of its first piece, of its last one
-  __shared__ Walk loads[W];         // per warp: the piece that its copies are at
+  __shared__ Walk walks[W][2];      // per warp: the piece that it computes, and the one that its copies are at
+  __shared__ int load_tile[W];      // per warp: the first tile of that piece whose page is not looked up yet
+  __shared__ int no_page[W][8];     // per warp and piece (its number & 7; copies run at most 4 pieces ahead): a tile has no page
   __shared__ int sh_last;
   float *heads_mem = j.part + ((size_t)blockIdx.x * (2 + W) + 2) * C::kPart;
   uint4 *q_mem = reinterpret_cast<uint4 *>(sm + C::kRing + (size_t)(threadIdx.x >> 5) * C::kQuery);  // [NB][32]
@@ -307,57 +309,74 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     }
   }
 
-  // ---- this warp's copies: a second walk that runs up to S tiles ahead
-  Walk &load = loads[warp];
-  if (lane == 0) load = walk;
+  // ---- this warp's copies: a second walk that runs up to S tiles ahead.  The walks live in shared memory: they
+  // change once per piece, and registers are what bounds the tile's code.
+  if (lane == 0) {
+    walks[warp][0] = walks[warp][1] = walk;
+    load_tile[warp] = walk.at;
+    no_page[warp][0] = 0;
+  }
   __syncwarp();
-  int load_tile = walk.at, load_end = walk.end;  // next tile to copy, and the end of its piece
-  bool load_more = work;
-  uint32_t issued = 0, used = 0;
-  int64_t src_off = -1;     // offset of tile src_at + lane in the cache, -1: the tile has no page
-  int src_at = 0, src_end = 0;
-  uint32_t bad_mask = 0;    // by (issued & 31): a tile without a page
+  uint32_t used = 0;            // tiles consumed: tile x is in stage x % S
+  int64_t src_off = -1;         // per lane: where one of the next tiles is in the cache, -1: the tile has no page
+  int src_next = 0, src_n = 0;  // next lane's turn, and lanes in use
+  uint32_t load_piece = 0;      // number of the copies' piece; ~0: no more
 
-  auto issue = [&]() {
-    if (load_tile >= src_end) {  // page numbers of the next tiles, one per lane
-      if (load_tile >= load_end) {
-        if (!load_more) return;
-        Walk next = load;
-        load_more = walk_next(j, next);
-        if (!load_more) return;
-        load_tile = next.at;
-        load_end = next.end;
-        __syncwarp();
-        if (lane == 0) load = next;
-        __syncwarp();
+  auto refill = [&]() {
+    if (load_piece == ~0u) return;
+    Walk w = walks[warp][1];
+    int tile = load_tile[warp];
+    __syncwarp();
+    if (tile >= w.end) {
+      if (!walk_next(j, w)) {
+        load_piece = ~0u;
+        return;
       }
-      src_at = load_tile;
-      src_end = min(load_end, load_tile + 32);
-      const int tile = load_tile + lane;
-      src_off = -1;
-      if (tile < load_end) {
-        int in_page = 0;
-        const int p = kv_page(j.c.page_table + (int64_t)load.seq * j.c.table_stride, j.c.table_width, j.c.n_pages,
-                              j.c.page_size, load.first + tile, &in_page);
-        if (p >= 0)
-          src_off = (int64_t)p * j.c.page_stride + kv_tile_off(D, j.c.page_size, load.hr / j.row_tiles, in_page);
+      ++load_piece;
+      tile = w.at;
+      if (lane == 0) {
+        walks[warp][1] = w;
+        no_page[warp][load_piece & 7] = 0;
       }
     }
-    const int64_t off = __shfl_sync(0xffffffffu, src_off, load_tile - src_at);
-    const int st = issued % S;
-    bad_mask &= ~(1u << (issued & 31));
-    if (off < 0) {
-      bad_mask |= 1u << (issued & 31);
-      if (lane == 0) a_mbar_arrive(&bar[st]);
-    } else if (lane == 0) {
-      a_expect_tx(&bar[st], C::kTile);
-      a_bulk_load(ring + (size_t)st * C::kTile, static_cast<const uint8_t *>(j.c.pages) + off, C::kTile, &bar[st]);
+    src_next = 0;
+    src_n = min(32, w.end - tile);
+    src_off = -1;
+    if (lane < src_n) {
+      int in_page = 0;
+      const int p = kv_page(j.c.page_table + (int64_t)w.seq * j.c.table_stride, j.c.table_width, j.c.n_pages,
+                            j.c.page_size, w.first + tile + lane, &in_page);
+      if (p >= 0)
+        src_off = (int64_t)p * j.c.page_stride + kv_tile_off(D, j.c.page_size, w.hr / j.row_tiles, in_page);
     }
-    ++issued;
-    ++load_tile;
+    const bool missing = __any_sync(0xffffffffu, lane < src_n && src_off < 0);
+    if (lane == 0) {
+      load_tile[warp] = tile + src_n;
+      if (missing) no_page[warp][load_piece & 7] = 1;
+    }
+    __syncwarp();
   };
-#pragma unroll
-  for (int s = 0; s < S; ++s) issue();
+  // Copies the share's tile x, if there is one, into its stage.
+  auto issue = [&](uint32_t x) {
+    if (src_next == src_n) {
+      src_next = src_n = 0;
+      refill();
+      if (src_n == 0) return;
+    }
+    const int64_t off = __shfl_sync(0xffffffffu, src_off, src_next++);
+    if (lane == 0) {
+      uint64_t *b = bar + x % S;
+      if (off < 0) {
+        a_mbar_arrive(b);
+      } else {
+        a_expect_tx(b, C::kTile);
+        a_bulk_load(ring + (x % S) * C::kTile, static_cast<const uint8_t *>(j.c.pages) + off, C::kTile, b);
+      }
+    }
+  };
+  if (work)
+#pragma unroll 1
+    for (int x = 0; x < S; ++x) issue(x);
 
   // -8 as fp16 pairs: -8 2^-24 for the low nibbles' rows, -8 2^-20 for the high ones'.  Four registers that the
   // compiler cannot see through: it would build the operand anew, move by move, for every instruction.
@@ -365,14 +384,15 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   asm volatile("mov.b32 %0, 0x80088008;\n mov.b32 %1, 0x80808080;\n mov.b32 %2, 0x80088008;\n mov.b32 %3, 0x80808080;"
                : "=r"(eight[0]), "=r"(eight[1]), "=r"(eight[2]), "=r"(eight[3]));
 
-  bool dead = false;  // a wait gave up: nothing more is copied or read
-  bool first_piece = true;
-  while (work) {
+  bool dead = false;  // a wait gave up: later ones do not wait
+  for (uint32_t piece = 0; work; ++piece) {
+    __syncwarp();
+    const Walk &walk = walks[warp][0];
     const int kvh = walk.hr / j.row_tiles, rt = walk.hr % j.row_tiles;
     const int len = __ldg(j.lens + walk.seq);
     // ---- the rows' queries: lane (g, t) holds row g's values 4t.. of each half block
     float f[2];
-    int lo[2], hi[2], all_lo, all_hi;
+    int w0, w1;  // tiles [w0, w1) of the piece are seen whole by every row
     {
       const int r = rt * kRows + g;
       uint2 raw[NB][2];
@@ -422,21 +442,13 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       }
       __syncwarp();
       const float mine_f = j.scale * kLog2e * down * 16777216.f;
-      int64_t a, b;
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        f[z] = __shfl_sync(0xffffffffu, mine_f, 8 * t + 4 * z);
-        const int rr = rt * kRows + 2 * t + z;
-        a = b = 0;
-        if (rr < n_rows) kv_visible(len, j.q_tokens, rr / j.group, j.window, &a, &b);
-        lo[z] = (int)a;
-        hi[z] = (int)b;
-      }
-      // a tile inside [all_lo, all_hi) is seen whole by every row
-      kv_visible(len, j.q_tokens, (min(n_rows, (rt + 1) * kRows) - 1) / j.group, j.window, &a, &b);
-      all_lo = (int)a;
-      kv_visible(len, j.q_tokens, rt * kRows / j.group, j.window, &a, &b);
-      all_hi = (int)b;
+      for (int z = 0; z < 2; ++z) f[z] = __shfl_sync(0xffffffffu, mine_f, 8 * t + 4 * z);
+      int64_t a, b, lo, hi;
+      kv_visible(len, j.q_tokens, (min(n_rows, (rt + 1) * kRows) - 1) / j.group, j.window, &lo, &b);
+      kv_visible(len, j.q_tokens, rt * kRows / j.group, j.window, &a, &hi);
+      w0 = min(max((int)((lo + kKvTile - 1) / kKvTile) - walk.first, walk.at), walk.end);
+      w1 = min(max((int)(hi / kKvTile) - walk.first, w0), walk.end);
     }
     // ---- this warp's tiles of the piece
     float acc[NB][2][4];
@@ -450,7 +462,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     float dtop = 0.f;                           // bound of the value scales seen
     __half2 dtop2 = __float2half2_rn(0.f);
     float shift = -7.f;                         // reference = m + shift
-    bool poison = false;
+    int poison = 0;                             // status bits: what the piece's result is worth
 
     // One tile.  Whole: every row sees all of it.
     auto compute = [&](const unsigned char *tp, const int tok0, auto is_whole) {
@@ -498,12 +510,16 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       // ---- what a row does not see scores -inf
       if (!whole) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int z = 0; z < 2; ++z) {
+          const int rr = rt * kRows + 2 * t + z;
+          int64_t lo = 0, hi = 0;
+          if (rr < n_rows) kv_visible(len, j.q_tokens, rr / j.group, j.window, &lo, &hi);
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int key = tok0 + mt * 16 + (z >= 2 ? 8 : 0) + pg;
-            if (key < lo[z & 1] || key >= hi[z & 1]) s[mt][z] = -a_inf();
+          for (int x = 0; x < 4; ++x) {
+            const int key = tok0 + 8 * x + pg;
+            if (key < lo || key >= hi) s[x / 2][2 * (x % 2) + z] = -a_inf();
           }
+        }
       }
       float mx[2];  // log2 units; f > 0
 #pragma unroll
@@ -608,31 +624,29 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     auto tiles = [&](int from, int to, auto is_whole) {
 #pragma unroll 1
       for (int tile = from; tile < to; ++tile) {
-        const int st = used % S;
-        const uint32_t ph = (used / S) & 1u, bit = 1u << (used & 31);
-        ++used;
-        if (!__all_sync(0xffffffffu, a_mbar_try(&bar[st], ph)))  // not there yet
-          dead = dead || !__all_sync(0xffffffffu, a_mbar_wait(&bar[st], ph));
-        if (dead || (bad_mask & bit)) {
-          poison = true;
-          if (lane == 0 && j.c.status) atomicOr(j.c.status, dead ? MOE_KV_TIMED_OUT : MOE_KV_BAD_PAGE);
-        } else {
-          compute(ring + (size_t)st * C::kTile, (walk.first + tile) * kKvTile, is_whole);
+        const uint32_t x = used++;
+        if (!__all_sync(0xffffffffu, a_mbar_try(&bar[x % S], (x / S) & 1u))) {  // not there yet
+          if (!dead) dead = !__all_sync(0xffffffffu, a_mbar_wait(&bar[x % S], (x / S) & 1u));
+          // a tile that never came is computed on as it lies there: the result is NaN
+          if (dead) poison |= MOE_KV_TIMED_OUT;
         }
+        compute(ring + (x % S) * C::kTile, (walk.first + tile) * kKvTile, is_whole);
         __syncwarp();
-        if (!dead) issue();
+        issue(x + S);
       }
     };
     // tiles that some row sees in part, tiles that all rows see whole, and again those in part
-    const int w0 = min(max((all_lo + kKvTile - 1) / kKvTile - walk.first, walk.at), walk.end);
-    const int w1 = min(max(all_hi / kKvTile - walk.first, w0), walk.end);
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
       tiles(pass ? w1 : walk.at, pass ? walk.end : w0, std::false_type());
       if (pass == 0) tiles(w0, w1, std::true_type());
     }
     // ---- the piece: l over the lanes that share a row; accumulators without the nibbles' factors
-    if (__any_sync(0xffffffffu, poison)) l[0] = l[1] = a_nan();
+    if (no_page[warp][piece & 7]) poison |= MOE_KV_BAD_PAGE;
+    if (poison) {
+      l[0] = l[1] = a_nan();
+      if (lane == 0 && j.c.status) atomicOr(j.c.status, poison);
+    }
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     } else {
       // a part: the first piece waits in the workspace, the last one in the ring (every copy has been used by then)
       const bool begins = walk.at == 0;
-      float *o = first_piece && !begins ? heads_mem + (size_t)warp * C::kPart : reinterpret_cast<float *>(ring);
+      float *o = piece == 0 && !begins ? heads_mem + (size_t)warp * C::kPart : reinterpret_cast<float *>(ring);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -675,14 +689,16 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
           *reinterpret_cast<float4 *>(o + ((b * 2 + h) * 32 + lane) * 4) =
               make_float4(acc[b][h][0], acc[b][h][1], acc[b][h][2], acc[b][h][3]);
       if (g == 0) *reinterpret_cast<float4 *>(o + C::kOut + 4 * t) = make_float4(r[0], r[1], l[0], l[1]);
-      if (lane == 0) meta[2 * warp + (first_piece && !begins ? 0 : 1)] = {walk.pair0, walk.seq, walk.hr, walk.n, 1};
+      if (lane == 0) meta[2 * warp + (piece == 0 && !begins ? 0 : 1)] = {walk.pair0, walk.seq, walk.hr, walk.n, 1};
     }
-    first_piece = false;
-    work = walk_next(j, walk);
+    Walk next = walk;
+    work = walk_next(j, next);
+    __syncwarp();
+    if (lane == 0) walks[warp][0] = next;
   }
   // copies that a wait gave up on, or that came after it, must have landed before the CTA's memory is gone
   if (dead)
-    for (uint32_t i = issued > S ? issued - S : 0; i < issued; ++i) (void)a_mbar_wait(&bar[i % S], (i / S) & 1u);
+    for (uint32_t x = used > S ? used - S : 0; x < used; ++x) (void)a_mbar_wait(&bar[x % S], (x / S) & 1u);
 
   // ---- pairs that warps share
   __syncthreads();
