@@ -47,6 +47,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;  // log2 by which a score may exceed its row's reference
 constexpr int kDecodeWarps = 8;
+constexpr int kDecodeSms = 152, kDecodeCtasMost = 2 * kDecodeSms;  // CTAs of a launch at most
 constexpr int kRows = 8;      // rows (heads x query tokens) of one work unit
 
 struct DecodeJob {
@@ -76,6 +77,7 @@ struct DecodeCfg {
   static constexpr size_t kSmem = kRing + (size_t)kWarps * kQuery;
   static constexpr int kCtas = D == 256 ? 1 : 2;  // resident per SM
   static_assert((size_t)kStages * kTile >= kPart * sizeof(float), "a warp's ring holds its last partial result");
+  static_assert(kRing >= (kDecodeCtasMost + 2) * kRows * sizeof(float), "the rings hold the weights of all CTAs' parts");
 };
 
 // d = a b + c
@@ -160,58 +162,218 @@ __device__ __forceinline__ bool walk_next(const DecodeJob &j, Walk &w) {
   return true;
 }
 
-// A partial result that a warp leaves for the merge.
-struct PartMeta {
+// A pair that several warps share.
+struct SharedPair {
   int64_t pair0;
   int seq, hr, n;
-  int valid;
+  int wa, wb;  // the warps of this CTA that hold parts of it
 };
 
-// Merges partial results, in order, for the four values of accumulator word f: rows 2t and 2t + 1 of a lane.
-// Own: parts of this CTA's warps, in shared memory or the workspace; otherwise other CTAs' (read past L1).
-template <bool Own, typename V>
-__device__ __forceinline__ V part_load(const float *p) {
-  if constexpr (Own) return *reinterpret_cast<const V *>(p);
-  else return __ldcg(reinterpret_cast<const V *>(p));
+// The part that warp w of this CTA holds of a pair: its last piece, in its ring, or, for the pair's last warp if it
+// goes on with other pairs, its first piece, in the workspace.
+template <int D>
+__device__ __forceinline__ const float *warp_part(const DecodeJob &j, const SharedPair &sp, unsigned char *sm,
+                                                  const int *in_heads, int w) {
+  using C = DecodeCfg<D>;
+  return w == sp.wb && in_heads[w] ? j.part + ((size_t)blockIdx.x * (2 + C::kWarps) + 2 + w) * C::kPart
+                                   : reinterpret_cast<const float *>(sm + (size_t)w * C::kStages * C::kTile);
 }
-template <bool Own, typename Ptr>
-__device__ __forceinline__ float4 merge_parts(int f, int out_floats, int parts, Ptr ptr, float r[2], float l[2]) {
-  const int t = f & 3;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  r[0] = r[1] = -a_inf();
-  for (int i = 0; i < parts; ++i) {
-    const float2 x = part_load<Own, float2>(ptr(i) + out_floats + 4 * t);
-    r[0] = fmaxf(r[0], x.x);
-    r[1] = fmaxf(r[1], x.y);
+
+// Weight of a part with reference r under the reference `top`, and its weight sum l under it.
+__device__ __forceinline__ float part_weight(float r, float top) { return r == -a_inf() ? 0.f : a_exp2(r - top); }
+// a poisoned part may hold no weight: its NaN must not be multiplied away
+__device__ __forceinline__ float part_sum(float l, float w) { return l != l ? l : l * w; }
+__device__ __forceinline__ float part_inverse(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
+__device__ __forceinline__ float part_lse(float r, float l) { return l == 0.f ? -a_inf() : (r + log2f(l)) * kLn2; }
+
+// Element of the output's rows: query token and head of row rr of a pair.
+__device__ __forceinline__ int64_t row_at(const DecodeJob &j, int seq, int hr, int rr) {
+  return ((int64_t)seq * j.q_tokens + rr / j.group) * j.hq + hr / j.row_tiles * j.group + rr % j.group;
+}
+
+// A pair whose tiles are all in this CTA, in some of its warps: merged by the one warp that is done last.
+template <int D, typename T>
+__device__ __noinline__ void merge_by_warp(const DecodeJob &j, const SharedPair &sp, unsigned char *sm,
+                                           const int *in_heads) {
+  using C = DecodeCfg<D>;
+  constexpr int N = C::kOut / 128;  // accumulator words (of 4) per lane
+  const int lane = threadIdx.x & 31, t = lane & 3;
+  float top[2] = {-a_inf(), -a_inf()}, l[2] = {0.f, 0.f};
+  for (int w = sp.wa; w <= sp.wb; ++w) {
+    const float4 x = *reinterpret_cast<const float4 *>(warp_part<D>(j, sp, sm, in_heads, w) + C::kOut + 4 * t);
+    top[0] = fmaxf(top[0], x.x);
+    top[1] = fmaxf(top[1], x.y);
   }
-  l[0] = l[1] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const float4 x = part_load<Own, float4>(ptr(i) + out_floats + 4 * t);
-    const float4 v = part_load<Own, float4>(ptr(i) + 4 * f);
-    const float w0 = x.x == -a_inf() ? 0.f : a_exp2(x.x - r[0]), w1 = x.y == -a_inf() ? 0.f : a_exp2(x.y - r[1]);
-    a.x += v.x * w0;
-    a.z += v.z * w0;
-    a.y += v.y * w1;
-    a.w += v.w * w1;
-    // a poisoned part may hold no weight: its NaN must not be multiplied away
-    l[0] += x.z != x.z ? x.z : x.z * w0;
-    l[1] += x.w != x.w ? x.w : x.w * w1;
+  float4 a[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int w = sp.wa; w <= sp.wb; ++w) {
+    const float *p = warp_part<D>(j, sp, sm, in_heads, w);
+    const float4 x = *reinterpret_cast<const float4 *>(p + C::kOut + 4 * t);
+    const float w0 = part_weight(x.x, top[0]), w1 = part_weight(x.y, top[1]);
+    l[0] += part_sum(x.z, w0);
+    l[1] += part_sum(x.w, w1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4 v = *reinterpret_cast<const float4 *>(p + 4 * (32 * i + lane));
+      a[i].x += v.x * w0;
+      a[i].y += v.y * w1;
+      a[i].z += v.z * w0;
+      a[i].w += v.w * w1;
+    }
   }
-  return a;
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    const int rr = sp.hr % j.row_tiles * kRows + 2 * t + z;
+    if (rr >= j.group * j.q_tokens) continue;
+    const float inv = part_inverse(l[z]);
+    const int64_t at = row_at(j, sp.seq, sp.hr, rr);
+    T *o = static_cast<T *>(j.out) + at * D + 2 * (lane >> 2);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      store_pair(o + 16 * i, (z ? a[i].y : a[i].x) * inv, (z ? a[i + 1].y : a[i + 1].x) * inv);
+      store_pair(o + 16 * i + 16, (z ? a[i].w : a[i].z) * inv, (z ? a[i + 1].w : a[i + 1].z) * inv);
+    }
+    if (lane < 4 && j.lse) j.lse[at] = part_lse(top[z], l[z]);
+  }
+}
+
+// Pairs that the whole CTA merges once its warps are done: the one that warps of earlier CTAs hold tiles of too (or
+// that all of this CTA's warps hold parts of), and the one that goes on in later CTAs.  The last CTA to be done with a
+// pair merges the CTAs' results.
+template <int D, typename T>
+__device__ __noinline__ void merge_by_cta(const DecodeJob &j, const SharedPair *sps, const int *has, unsigned char *sm,
+                                          const int *in_heads, int64_t share, bool alone, int *is_last) {
+  using C = DecodeCfg<D>;
+  constexpr int W = C::kWarps, kThreads = 32 * W;
+  const int tid = threadIdx.x, lane = tid & 31, t = lane & 3;
+  auto result = [&](const SharedPair &sp, int f, const float4 v, const float r[2], const float l[2]) {
+    const int dim = 32 * (f / 64) + 2 * (lane >> 2) + ((f >> 5) & 1);
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {  // rows 2t and 2t + 1
+      const int rr = sp.hr % j.row_tiles * kRows + 2 * t + z;
+      if (rr >= j.group * j.q_tokens) continue;
+      const int64_t at = row_at(j, sp.seq, sp.hr, rr);
+      const float inv = part_inverse(l[z]);
+      T *o = static_cast<T *>(j.out) + at * D + dim;
+      o[0] = T((z ? v.y : v.x) * inv);
+      o[16] = T((z ? v.w : v.z) * inv);
+      if (f < 4 && j.lse) j.lse[at] = part_lse(r[z], l[z]);
+    }
+  };
+  int64_t cta0[2], cta1[2];  // CTAs that hold tiles of the pair
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    if (!has[x]) continue;
+    const SharedPair &sp = sps[x];
+    cta0[x] = alone ? blockIdx.x : (sp.pair0 + kPairCost) / (share * W);
+    cta1[x] = alone ? blockIdx.x : (sp.pair0 + kPairCost + sp.n - 1) / (share * W);
+    float *mine = j.part + ((size_t)blockIdx.x * (2 + W) + (blockIdx.x == cta0[x] ? 1 : 0)) * C::kPart;
+    for (int f = tid; f < C::kOut / 4; f += kThreads) {
+      float r[2] = {-a_inf(), -a_inf()}, l[2] = {0.f, 0.f};
+      for (int w = sp.wa; w <= sp.wb; ++w) {
+        const float2 y = *reinterpret_cast<const float2 *>(warp_part<D>(j, sp, sm, in_heads, w) + C::kOut + 4 * t);
+        r[0] = fmaxf(r[0], y.x);
+        r[1] = fmaxf(r[1], y.y);
+      }
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = sp.wa; w <= sp.wb; ++w) {
+        const float *p = warp_part<D>(j, sp, sm, in_heads, w);
+        const float4 y = *reinterpret_cast<const float4 *>(p + C::kOut + 4 * t);
+        const float4 v = *reinterpret_cast<const float4 *>(p + 4 * f);
+        const float w0 = part_weight(y.x, r[0]), w1 = part_weight(y.y, r[1]);
+        l[0] += part_sum(y.z, w0);
+        l[1] += part_sum(y.w, w1);
+        a.x += v.x * w0;
+        a.y += v.y * w1;
+        a.z += v.z * w0;
+        a.w += v.w * w1;
+      }
+      if (cta0[x] == cta1[x]) {
+        result(sp, f, a, r, l);
+      } else {
+        *reinterpret_cast<float4 *>(mine + 4 * f) = a;
+        if (f < 4) *reinterpret_cast<float4 *>(mine + C::kOut + 4 * f) = make_float4(r[0], r[1], l[0], l[1]);
+      }
+    }
+  }
+  const bool shared0 = has[0] && cta0[0] != cta1[0], shared1 = has[1] && cta0[1] != cta1[1];
+  if (!shared0 && !shared1) return;
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    const bool mine = tid ? shared1 : shared0;
+    const int64_t c0 = tid ? cta0[1] : cta0[0], c1 = tid ? cta1[1] : cta1[0];
+    is_last[tid] = mine && atomicAdd(j.count + c0, 1u) == (uint32_t)(c1 - c0);
+    if (is_last[tid]) j.count[c0] = 0;
+  }
+  __syncthreads();
+  __threadfence();
+#pragma unroll 1
+  for (int x = 0; x < 2; ++x) {
+    if (!is_last[x]) continue;
+    const SharedPair &sp = sps[x];
+    const int ctas = (int)(cta1[x] - cta0[x]) + 1;
+    const int64_t first = cta0[x];
+    auto part = [&](int k) { return j.part + ((size_t)(first + k) * (2 + W) + (k == 0 ? 1 : 0)) * C::kPart; };
+    // the parts' weights, a warp per row, in the rings' memory (the warps' parts have been used)
+    float *wt = reinterpret_cast<float *>(sm), *head = wt + kDecodeCtasMost * kRows;  // [ctas][kRows]; [2][kRows]
+    for (int row = tid >> 5; row < kRows; row += W) {
+      // part's meta data: per t the references of rows 2t, 2t + 1, then their sums
+      const int at = C::kOut + 4 * (row >> 1) + (row & 1);
+      float top = -a_inf(), sum = 0.f;
+      for (int k = lane; k < ctas; k += 32) {
+        const float r = __ldcg(part(k) + at);
+        wt[k * kRows + row] = r;
+        top = fmaxf(top, r);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int k = lane; k < ctas; k += 32) {
+        const float w = part_weight(wt[k * kRows + row], top);
+        sum += part_sum(__ldcg(part(k) + at + 2), w);
+        wt[k * kRows + row] = w;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) {
+        head[row] = top;
+        head[kRows + row] = sum;
+      }
+    }
+    __syncthreads();
+    for (int f = tid; f < C::kOut / 4; f += kThreads) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int k = 0; k < ctas; ++k) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(k) + 4 * f));
+        const float2 w = *reinterpret_cast<const float2 *>(wt + k * kRows + 2 * t);
+        a.x += v.x * w.x;
+        a.y += v.y * w.y;
+        a.z += v.z * w.x;
+        a.w += v.w * w.y;
+      }
+      const float r[2] = {head[2 * t], head[2 * t + 1]}, l[2] = {head[kRows + 2 * t], head[kRows + 2 * t + 1]};
+      result(sp, f, a, r, l);
+    }
+    __syncthreads();
+  }
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas) kv_attention_kernel(const DecodeJob j) {
   using C = DecodeCfg<D>;
-  constexpr int W = C::kWarps, S = C::kStages, NB = D / 32, kThreads = 32 * W;
+  constexpr int W = C::kWarps, S = C::kStages, NB = D / 32;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ uint64_t bars[W][S];
-  __shared__ PartMeta meta[2 * W];  // per warp: of its first piece, of its last one
+  __shared__ SharedPair cta_pairs[2];  // pairs that the whole CTA merges
+  __shared__ int has_pair[2], sh_last[2];
+  __shared__ int parts_done[W];     // per pair that only warps of this CTA share, by its first warp
+  __shared__ int in_heads[W];       // per warp: its first piece is a part in the workspace
   __shared__ Walk walks[W][2];      // per warp: the piece that it computes, and the one that its copies are at
   __shared__ int load_tile[W];      // per warp: the first tile of that piece whose page is not looked up yet
   __shared__ int no_page[W][8];     // per warp and piece (its number & 7; copies run at most 4 pieces ahead): a tile has no page
-  __shared__ int sh_last;
   float *heads_mem = j.part + ((size_t)blockIdx.x * (2 + W) + 2) * C::kPart;
   uint4 *q_mem = reinterpret_cast<uint4 *>(sm + C::kRing + (size_t)(threadIdx.x >> 5) * C::kQuery);  // [NB][32]
   float4 *q_start = reinterpret_cast<float4 *>(q_mem + D);                                          // [NB][4]
@@ -224,26 +386,31 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   if (lane == 0) {
 #pragma unroll
     for (int s = 0; s < S; ++s) a_mbar_init(&bar[s], 1);
-    meta[2 * warp].valid = meta[2 * warp + 1].valid = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    parts_done[warp] = in_heads[warp] = 0;
+    if (warp == 0) has_pair[0] = has_pair[1] = 0;
   }
-  __syncwarp();
+  __syncthreads();
 
-  // ---- this warp's share of the places
+  // ---- this warp's share of the places: a lane counts `per` consecutive sequences
+  const int per = (j.c.n_seqs + 31) / 32;
   int64_t total = 0;
   int most = 0;
-  for (int base = 0; base < j.c.n_seqs; base += 32) {
+  bool some_empty = false;
+#pragma unroll 4
+  for (int k = 0; k < per; ++k) {
+    const int s = lane * per + k;
     int first, n = 0;
-    const bool in = base + lane < j.c.n_seqs;
-    if (in) n = seq_tiles(j, base + lane, &first);
+    if (s < j.c.n_seqs) n = seq_tiles(j, s, &first);
+    some_empty |= s < j.c.n_seqs && n == 0;
     total += n ? n + kPairCost : 0;
     most = max(most, n);
-    // sequences without tiles (empty, or of a length that the table cannot hold): their rows
-    uint32_t none = __ballot_sync(0xffffffffu, in && n == 0);
-    while (none) {
-      const int s = base + __ffs(none) - 1;
-      none &= none - 1;
-      if (s % (int)(gridDim.x * W) != (int)(warp * gridDim.x + blockIdx.x)) continue;
+  }
+  // sequences without tiles (empty, or of a length that the table cannot hold): their rows
+  if (__any_sync(0xffffffffu, some_empty))
+    for (int s = warp * gridDim.x + blockIdx.x; s < j.c.n_seqs; s += gridDim.x * W) {
+      int first;
+      if (seq_tiles(j, s, &first) > 0) continue;
       const bool bad = __ldg(j.lens + s) != 0;
       if (bad && lane == 0 && j.c.status) atomicOr(j.c.status, MOE_KV_BAD_LENGTH);
       const float fill = bad ? a_nan() : 0.f;
@@ -252,13 +419,16 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       if (j.lse)
         for (int64_t i = lane; i < n_rows_all; i += 32) j.lse[(int64_t)s * n_rows_all + i] = bad ? a_nan() : -a_inf();
     }
-  }
+  const int64_t mine = total * heads;
+  int64_t before = mine;  // sums over the lanes before, in places
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
     most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
-  total *= heads;
+  total = __shfl_sync(0xffffffffu, before, 31);
+  before -= mine;
   const int64_t pairs = (int64_t)j.c.n_seqs * heads;
   const bool alone = most <= kAloneTiles && pairs <= (int64_t)gridDim.x;  // a CTA per pair
   const int64_t share = (total + (int64_t)gridDim.x * W - 1) / ((int64_t)gridDim.x * W);
@@ -270,18 +440,21 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       walk.seq = blockIdx.x / heads;
       walk.hr = blockIdx.x % heads;
       walk.n = seq_tiles(j, walk.seq, &walk.first);
-      walk.at = walk.n * warp / W;
-      walk.end = walk.n * (warp + 1) / W;
+      const int n = max(walk.n, W);  // fewer tiles than warps: one each
+      walk.at = min(n * warp / W, walk.n);
+      walk.end = min(n * (warp + 1) / W, walk.n);
       work = walk.end > walk.at;
     }
   } else {
     const int64_t u0 = share * ((int64_t)blockIdx.x * W + warp);
     work = u0 < total;
     if (work) {
-      int64_t run = 0;
-      for (int base = 0; base < j.c.n_seqs; base += 32) {
+      const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= before && u0 < before + mine)) - 1;
+      int64_t run = __shfl_sync(0xffffffffu, before, src);
+      for (int base = 0; base < per; base += 32) {
+        const int k = base + lane, s = src * per + k;
         int first = 0, n = 0;
-        if (base + lane < j.c.n_seqs) n = seq_tiles(j, base + lane, &first);
+        if (k < per && s < j.c.n_seqs) n = seq_tiles(j, s, &first);
         const int64_t cost = n ? (int64_t)(n + kPairCost) * heads : 0;
         int64_t inc = cost;
 #pragma unroll
@@ -293,21 +466,38 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
         const uint32_t who = __ballot_sync(0xffffffffu, u0 >= begin && u0 < begin + cost);
         run += __shfl_sync(0xffffffffu, inc, 31);
         if (who) {
-          const int src = __ffs(who) - 1;
-          walk.seq = base + src;
-          walk.n = __shfl_sync(0xffffffffu, n, src);
-          walk.first = __shfl_sync(0xffffffffu, first, src);
-          walk.pair0 = __shfl_sync(0xffffffffu, begin, src);
+          const int at = __ffs(who) - 1;
+          walk.seq = src * per + base + at;
+          walk.n = __shfl_sync(0xffffffffu, n, at);
+          walk.first = __shfl_sync(0xffffffffu, first, at);
+          walk.pair0 = __shfl_sync(0xffffffffu, begin, at);
           break;
         }
       }
-      const int64_t off = u0 - walk.pair0;
-      walk.hr = (int)(off / (walk.n + kPairCost));
+      walk.hr = (int)((u0 - walk.pair0) / (walk.n + kPairCost));
       walk.pair0 += (int64_t)walk.hr * (walk.n + kPairCost);
       walk.left = min(share, total - u0);
-      work = walk_clip(walk, off % (walk.n + kPairCost)) || walk_next(j, walk);
+      work = walk_clip(walk, u0 - walk.pair0) || walk_next(j, walk);
     }
   }
+  // ---- the rows' queries, as they are: lane (g, t) holds row g's values 4t.. of each half block.  Asked for before
+  // the copies, behind which they would queue.
+  uint2 raw[NB][2];
+  auto load_q = [&](const Walk &w) {
+    const int kvh = w.hr / j.row_tiles, r = w.hr % j.row_tiles * kRows + g;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) raw[b][0] = raw[b][1] = make_uint2(0u, 0u);
+    if (r < n_rows) {
+      const T *src = static_cast<const T *>(j.q.data) + ((int64_t)w.seq * j.q_tokens + r / j.group) * j.q.token_stride +
+                     (int64_t)(kvh * j.group + r % j.group) * j.q.head_stride;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          raw[b][half] = *reinterpret_cast<const uint2 *>(src + 32 * b + 16 * half + 4 * t);
+    }
+  };
+  if (work) load_q(walk);
 
   // ---- this warp's copies: a second walk that runs up to S tiles ahead.  The walks live in shared memory: they
   // change once per piece, and registers are what bounds the tile's code.
@@ -390,25 +580,11 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     const Walk &walk = walks[warp][0];
     const int kvh = walk.hr / j.row_tiles, rt = walk.hr % j.row_tiles;
     const int len = __ldg(j.lens + walk.seq);
-    // ---- the rows' queries: lane (g, t) holds row g's values 4t.. of each half block
+    // ---- the rows' queries as matrix operands
     float f[2];
     int w0, w1;  // tiles [w0, w1) of the piece are seen whole by every row
     {
-      const int r = rt * kRows + g;
-      uint2 raw[NB][2];
       float top = 0.f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) raw[b][0] = raw[b][1] = make_uint2(0u, 0u);
-      if (r < n_rows) {
-        const T *src = static_cast<const T *>(j.q.data) +
-                       ((int64_t)walk.seq * j.q_tokens + r / j.group) * j.q.token_stride +
-                       (int64_t)(kvh * j.group + r % j.group) * j.q.head_stride;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            raw[b][half] = *reinterpret_cast<const uint2 *>(src + 32 * b + 16 * half + 4 * t);
-      }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -661,6 +837,9 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int z = 0; z < 4; ++z) acc[b][h][z] *= z < 2 ? 16777216.f : 1048576.f;
+    Walk next = walk;
+    const bool more = walk_next(j, next);
+    if (more) load_q(next);
     if (walk.at == 0 && walk.end == walk.n) {
       // all of the pair: its result
       const int64_t tok = (int64_t)walk.seq * j.q_tokens;
@@ -679,9 +858,9 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
         if (g == 0 && j.lse) j.lse[at] = l[z] == 0.f ? -a_inf() : (r[z] + log2f(l[z])) * kLn2;
       }
     } else {
-      // a part: the first piece waits in the workspace, the last one in the ring (every copy has been used by then)
-      const bool begins = walk.at == 0;
-      float *o = piece == 0 && !begins ? heads_mem + (size_t)warp * C::kPart : reinterpret_cast<float *>(ring);
+      // a part: a last piece waits in the ring (every copy has been used by then), a first one that others follow
+      // in the workspace
+      float *o = more ? heads_mem + (size_t)warp * C::kPart : reinterpret_cast<float *>(ring);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -689,93 +868,44 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
           *reinterpret_cast<float4 *>(o + ((b * 2 + h) * 32 + lane) * 4) =
               make_float4(acc[b][h][0], acc[b][h][1], acc[b][h][2], acc[b][h][3]);
       if (g == 0) *reinterpret_cast<float4 *>(o + C::kOut + 4 * t) = make_float4(r[0], r[1], l[0], l[1]);
-      if (lane == 0) meta[2 * warp + (piece == 0 && !begins ? 0 : 1)] = {walk.pair0, walk.seq, walk.hr, walk.n, 1};
+      if (more && lane == 0) in_heads[warp] = 1;
+      SharedPair sp = {walk.pair0, walk.seq, walk.hr, walk.n, 0, min(W, walk.n) - 1};
+      bool begun = false, goes_on = false;  // tiles of the pair in an earlier CTA, in a later one
+      if (!alone) {
+        const int64_t p0 = (sp.pair0 + kPairCost) / share - (int64_t)blockIdx.x * W;
+        const int64_t p1 = (sp.pair0 + kPairCost + sp.n - 1) / share - (int64_t)blockIdx.x * W;
+        begun = p0 < 0;
+        goes_on = p1 >= W;
+        sp.wa = (int)max((int64_t)0, p0);
+        sp.wb = (int)min((int64_t)(W - 1), p1);
+      }
+      if (begun || goes_on || sp.wb - sp.wa == W - 1) {
+        // (one that all warps hold is the only such pair, or shares no side with another)
+        if (lane == 0) {
+          cta_pairs[goes_on && !begun] = sp;
+          has_pair[goes_on && !begun] = 1;
+        }
+      } else {
+        __threadfence_block();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) last = atomicAdd(&parts_done[sp.wa], 1) == sp.wb - sp.wa;
+        last = __shfl_sync(0xffffffffu, last, 0);
+        __threadfence_block();
+        if (last) merge_by_warp<D, T>(j, sp, sm, in_heads);
+      }
     }
-    Walk next = walk;
-    work = walk_next(j, next);
+    work = more;
     __syncwarp();
     if (lane == 0) walks[warp][0] = next;
   }
-  // copies that a wait gave up on, or that came after it, must have landed before the CTA's memory is gone
+  // copies that a wait gave up on must have landed before the CTA's memory is gone
   if (dead)
     for (uint32_t x = used > S ? used - S : 0; x < used; ++x) (void)a_mbar_wait(&bar[x % S], (x / S) & 1u);
-
-  // ---- pairs that warps share
   __syncthreads();
-  for (int i = 0; i < 2 * W;) {
-    if (!meta[i].valid) {
-      ++i;
-      continue;
-    }
-    const PartMeta pm = meta[i];
-    int parts = 0;
-    uint64_t list = 0;  // the parts' places in meta, 4 bits each
-    for (; i < 2 * W && (!meta[i].valid || meta[i].pair0 == pm.pair0); ++i)
-      if (meta[i].valid) {
-        list |= (uint64_t)i << (4 * parts);
-        ++parts;
-      }
-    auto own_part = [&](int k) {
-      const int at = (int)(list >> (4 * k)) & 15;
-      return (at & 1) ? reinterpret_cast<const float *>(sm + (size_t)(at / 2) * S * C::kTile)
-                      : static_cast<const float *>(heads_mem + (size_t)(at / 2) * C::kPart);
-    };
-    // CTAs that hold tiles of the pair
-    int64_t cta0 = blockIdx.x, cta1 = blockIdx.x;
-    if (!alone) {
-      cta0 = (pm.pair0 + kPairCost) / (share * W);
-      cta1 = (pm.pair0 + kPairCost + pm.n - 1) / (share * W);
-    }
-    const int kvh = pm.hr / j.row_tiles, rt = pm.hr % j.row_tiles;
-    auto result = [&](int f, const float4 v, const float r[2], const float l[2]) {
-      const int ln = f & 31, dim = 32 * (f / 64) + 2 * (ln >> 2) + ((f >> 5) & 1);
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int rr = rt * kRows + 2 * (ln & 3) + z;
-        if (rr >= n_rows) continue;
-        const float inv = l[z] > 0.f || l[z] != l[z] ? 1.f / l[z] : 0.f;
-        const int64_t at = ((int64_t)pm.seq * j.q_tokens + rr / j.group) * j.hq + kvh * j.group + rr % j.group;
-        T *o = static_cast<T *>(j.out) + at * D + dim;
-        o[0] = T((z ? v.y : v.x) * inv);
-        o[16] = T((z ? v.w : v.z) * inv);
-        if (f < 4 && j.lse) j.lse[at] = l[z] == 0.f ? -a_inf() : (r[z] + log2f(l[z])) * kLn2;
-      }
-    };
-    if (cta0 == cta1) {
-      for (int f = tid; f < C::kOut / 4; f += kThreads) {
-        float r[2], l[2];
-        const float4 v = merge_parts<true>(f, C::kOut, parts, own_part, r, l);
-        result(f, v, r, l);
-      }
-      continue;
-    }
-    float *mine = j.part + ((size_t)blockIdx.x * (2 + W) + (blockIdx.x == cta0 ? 1 : 0)) * C::kPart;
-    for (int f = tid; f < C::kOut / 4; f += kThreads) {
-      float r[2], l[2];
-      const float4 v = merge_parts<true>(f, C::kOut, parts, own_part, r, l);
-      *reinterpret_cast<float4 *>(mine + 4 * f) = v;
-      if (f < 4) *reinterpret_cast<float4 *>(mine + C::kOut + 4 * f) = make_float4(r[0], r[1], l[0], l[1]);
-    }
-    __threadfence();
-    __syncthreads();
-    const int ctas = (int)(cta1 - cta0) + 1;
-    if (tid == 0) sh_last = atomicAdd(j.count + cta0, 1u) == (uint32_t)(ctas - 1);
-    __syncthreads();
-    if (sh_last) {
-      __threadfence();
-      if (tid == 0) j.count[cta0] = 0;
-      auto cta_part = [&](int k) { return j.part + ((size_t)(cta0 + k) * (2 + W) + (k == 0 ? 1 : 0)) * C::kPart; };
-      for (int f = tid; f < C::kOut / 4; f += kThreads) {
-        float r[2], l[2];
-        const float4 v = merge_parts<false>(f, C::kOut, ctas, cta_part, r, l);
-        result(f, v, r, l);
-      }
-    }
-    __syncthreads();  // sh_last is read by all before the next pair's
-  }
+  if (has_pair[0] || has_pair[1])
+    merge_by_cta<D, T>(j, cta_pairs, has_pair, sm, in_heads, share, alone, sh_last);
 }
-
-constexpr int kDecodeSms = 152;
 
 int decode_grid_cap(int D) { return kDecodeSms * (D == 256 ? 1 : 2); }
 
@@ -791,7 +921,7 @@ int launch_decode(const DecodeJob &j, int grid, cudaStream_t st) {
 }
 
 constexpr int64_t kCountBytes = MOE_KV_COUNTER_BYTES;  // counters at the head of the workspace
-static_assert(kDecodeSms * 2 * 4 <= kCountBytes, "a counter per CTA");
+static_assert(kDecodeCtasMost * 4 <= kCountBytes, "a counter per CTA");
 
 }  // namespace
 }  // namespace moe
