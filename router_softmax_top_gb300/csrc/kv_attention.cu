@@ -77,7 +77,6 @@ struct DecodeCfg {
   static constexpr size_t kSmem = kRing + (size_t)kWarps * kQuery;
   static constexpr int kCtas = D == 256 ? 1 : 2;  // resident per SM
   static_assert((size_t)kStages * kTile >= kPart * sizeof(float), "a warp's ring holds its last partial result");
-  static_assert(kRing >= (kDecodeCtasMost + 2) * kRows * sizeof(float), "the rings hold the weights of all CTAs' parts");
 };
 
 // d = a b + c
@@ -164,9 +163,9 @@ __device__ __forceinline__ bool walk_next(const DecodeJob &j, Walk &w) {
 
 // A pair that several warps share.
 struct SharedPair {
-  int64_t pair0;
-  int seq, hr, n;
-  int wa, wb;  // the warps of this CTA that hold parts of it
+  int seq, hr;
+  int wa, wb;      // the warps of this CTA that hold parts of it
+  int cta0, cta1;  // the CTAs that hold tiles of it
 };
 
 // The part that warp w of this CTA holds of a pair: its last piece, in its ring, or, for the pair's last warp if it
@@ -188,6 +187,7 @@ __device__ __forceinline__ float part_lse(float r, float l) { return l == 0.f ? 
 
 // Element of the output's rows: query token and head of row rr of a pair.
 __device__ __forceinline__ int64_t row_at(const DecodeJob &j, int seq, int hr, int rr) {
+  if (j.q_tokens == 1 && j.row_tiles == 1) return (int64_t)seq * j.hq + hr * j.group + rr;  // the usual one, without divisions
   return ((int64_t)seq * j.q_tokens + rr / j.group) * j.hq + hr / j.row_tiles * j.group + rr % j.group;
 }
 
@@ -244,7 +244,7 @@ __device__ __noinline__ void merge_by_warp(const DecodeJob &j, const SharedPair 
 // pair merges the CTAs' results.
 template <int D, typename T>
 __device__ __noinline__ void merge_by_cta(const DecodeJob &j, const SharedPair *sps, const int *has, unsigned char *sm,
-                                          const int *in_heads, int64_t share, bool alone, int *is_last) {
+                                          const int *in_heads, int *is_last) {
   using C = DecodeCfg<D>;
   constexpr int W = C::kWarps, kThreads = 32 * W;
   const int tid = threadIdx.x, lane = tid & 31, t = lane & 3;
@@ -262,14 +262,11 @@ __device__ __noinline__ void merge_by_cta(const DecodeJob &j, const SharedPair *
       if (f < 4 && j.lse) j.lse[at] = part_lse(r[z], l[z]);
     }
   };
-  int64_t cta0[2], cta1[2];  // CTAs that hold tiles of the pair
-#pragma unroll
+#pragma unroll 1
   for (int x = 0; x < 2; ++x) {
     if (!has[x]) continue;
     const SharedPair &sp = sps[x];
-    cta0[x] = alone ? blockIdx.x : (sp.pair0 + kPairCost) / (share * W);
-    cta1[x] = alone ? blockIdx.x : (sp.pair0 + kPairCost + sp.n - 1) / (share * W);
-    float *mine = j.part + ((size_t)blockIdx.x * (2 + W) + (blockIdx.x == cta0[x] ? 1 : 0)) * C::kPart;
+    float *mine = j.part + ((size_t)blockIdx.x * (2 + W) + ((int)blockIdx.x == sp.cta0 ? 1 : 0)) * C::kPart;
     for (int f = tid; f < C::kOut / 4; f += kThreads) {
       float r[2] = {-a_inf(), -a_inf()}, l[2] = {0.f, 0.f};
       for (int w = sp.wa; w <= sp.wb; ++w) {
@@ -290,7 +287,7 @@ __device__ __noinline__ void merge_by_cta(const DecodeJob &j, const SharedPair *
         a.z += v.z * w0;
         a.w += v.w * w1;
       }
-      if (cta0[x] == cta1[x]) {
+      if (sp.cta0 == sp.cta1) {
         result(sp, f, a, r, l);
       } else {
         *reinterpret_cast<float4 *>(mine + 4 * f) = a;
@@ -298,15 +295,15 @@ __device__ __noinline__ void merge_by_cta(const DecodeJob &j, const SharedPair *
       }
     }
   }
-  const bool shared0 = has[0] && cta0[0] != cta1[0], shared1 = has[1] && cta0[1] != cta1[1];
+  const bool shared0 = has[0] && sps[0].cta0 != sps[0].cta1, shared1 = has[1] && sps[1].cta0 != sps[1].cta1;
   if (!shared0 && !shared1) return;
   __threadfence();
   __syncthreads();
   if (tid < 2) {
     const bool mine = tid ? shared1 : shared0;
-    const int64_t c0 = tid ? cta0[1] : cta0[0], c1 = tid ? cta1[1] : cta1[0];
-    is_last[tid] = mine && atomicAdd(j.count + c0, 1u) == (uint32_t)(c1 - c0);
-    if (is_last[tid]) j.count[c0] = 0;
+    const SharedPair &sp = sps[tid];
+    is_last[tid] = mine && atomicAdd(j.count + sp.cta0, 1u) == (uint32_t)(sp.cta1 - sp.cta0);
+    if (is_last[tid]) j.count[sp.cta0] = 0;
   }
   __syncthreads();
   __threadfence();
@@ -314,50 +311,50 @@ __device__ __noinline__ void merge_by_cta(const DecodeJob &j, const SharedPair *
   for (int x = 0; x < 2; ++x) {
     if (!is_last[x]) continue;
     const SharedPair &sp = sps[x];
-    const int ctas = (int)(cta1[x] - cta0[x]) + 1;
-    const int64_t first = cta0[x];
-    auto part = [&](int k) { return j.part + ((size_t)(first + k) * (2 + W) + (k == 0 ? 1 : 0)) * C::kPart; };
-    // the parts' weights, a warp per row, in the rings' memory (the warps' parts have been used)
-    float *wt = reinterpret_cast<float *>(sm), *head = wt + kDecodeCtasMost * kRows;  // [ctas][kRows]; [2][kRows]
-    for (int row = tid >> 5; row < kRows; row += W) {
-      // part's meta data: per t the references of rows 2t, 2t + 1, then their sums
-      const int at = C::kOut + 4 * (row >> 1) + (row & 1);
-      float top = -a_inf(), sum = 0.f;
-      for (int k = lane; k < ctas; k += 32) {
-        const float r = __ldcg(part(k) + at);
-        wt[k * kRows + row] = r;
-        top = fmaxf(top, r);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      for (int k = lane; k < ctas; k += 32) {
-        const float w = part_weight(wt[k * kRows + row], top);
-        sum += part_sum(__ldcg(part(k) + at + 2), w);
-        wt[k * kRows + row] = w;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) {
-        head[row] = top;
-        head[kRows + row] = sum;
-      }
-    }
-    __syncthreads();
+    const int ctas = sp.cta1 - sp.cta0 + 1;
+    auto part = [&](int k) { return j.part + ((size_t)(sp.cta0 + k) * (2 + W) + (k == 0 ? 1 : 0)) * C::kPart; };
     for (int f = tid; f < C::kOut / 4; f += kThreads) {
+      // eight parts at a time, all asked for before the first is used: each takes a trip to the L2
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int k = 0; k < ctas; ++k) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(k) + 4 * f));
-        const float2 w = *reinterpret_cast<const float2 *>(wt + k * kRows + 2 * t);
-        a.x += v.x * w.x;
-        a.y += v.y * w.y;
-        a.z += v.z * w.x;
-        a.w += v.w * w.y;
+      float top[2] = {-a_inf(), -a_inf()}, l[2] = {0.f, 0.f};
+#pragma unroll 1
+      for (int k0 = 0; k0 < ctas; k0 += 8) {
+        float4 v[8], y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float *p = part(min(k0 + k, ctas - 1));
+          y[k] = __ldcg(reinterpret_cast<const float4 *>(p + C::kOut + 4 * t));
+          v[k] = __ldcg(reinterpret_cast<const float4 *>(p + 4 * f));
+          if (k0 + k >= ctas) y[k] = make_float4(-a_inf(), -a_inf(), 0.f, 0.f);
+        }
+        float n0 = top[0], n1 = top[1];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          n0 = fmaxf(n0, y[k].x);
+          n1 = fmaxf(n1, y[k].y);
+        }
+        const float s0 = part_weight(top[0], n0), s1 = part_weight(top[1], n1);
+        top[0] = n0;
+        top[1] = n1;
+        a.x *= s0;
+        a.y *= s1;
+        a.z *= s0;
+        a.w *= s1;
+        l[0] *= s0;
+        l[1] *= s1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float w0 = part_weight(y[k].x, n0), w1 = part_weight(y[k].y, n1);
+          l[0] += part_sum(y[k].z, w0);
+          l[1] += part_sum(y[k].w, w1);
+          a.x += v[k].x * w0;
+          a.y += v[k].y * w1;
+          a.z += v[k].z * w0;
+          a.w += v[k].w * w1;
+        }
       }
-      const float r[2] = {head[2 * t], head[2 * t + 1]}, l[2] = {head[kRows + 2 * t], head[kRows + 2 * t + 1]};
-      result(sp, f, a, r, l);
+      result(sp, f, a, top, l);
     }
-    __syncthreads();
   }
 }
 
@@ -431,7 +428,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   before -= mine;
   const int64_t pairs = (int64_t)j.c.n_seqs * heads;
   const bool alone = most <= kAloneTiles && pairs <= (int64_t)gridDim.x;  // a CTA per pair
-  const int64_t share = (total + (int64_t)gridDim.x * W - 1) / ((int64_t)gridDim.x * W);
+  const int64_t share = kv_div(total + (int64_t)gridDim.x * W - 1, (int64_t)gridDim.x * W);
   Walk walk = {0, 0, 0, 0, 0, 0, 0, 0};
   bool work;
   if (alone) {
@@ -474,7 +471,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
           break;
         }
       }
-      walk.hr = (int)((u0 - walk.pair0) / (walk.n + kPairCost));
+      walk.hr = (int)kv_div(u0 - walk.pair0, walk.n + kPairCost);
       walk.pair0 += (int64_t)walk.hr * (walk.n + kPairCost);
       walk.left = min(share, total - u0);
       work = walk_clip(walk, u0 - walk.pair0) || walk_next(j, walk);
@@ -869,15 +866,17 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
               make_float4(acc[b][h][0], acc[b][h][1], acc[b][h][2], acc[b][h][3]);
       if (g == 0) *reinterpret_cast<float4 *>(o + C::kOut + 4 * t) = make_float4(r[0], r[1], l[0], l[1]);
       if (more && lane == 0) in_heads[warp] = 1;
-      SharedPair sp = {walk.pair0, walk.seq, walk.hr, walk.n, 0, min(W, walk.n) - 1};
+      SharedPair sp = {walk.seq, walk.hr, 0, min(W, walk.n) - 1, (int)blockIdx.x, (int)blockIdx.x};
       bool begun = false, goes_on = false;  // tiles of the pair in an earlier CTA, in a later one
       if (!alone) {
-        const int64_t p0 = (sp.pair0 + kPairCost) / share - (int64_t)blockIdx.x * W;
-        const int64_t p1 = (sp.pair0 + kPairCost + sp.n - 1) / share - (int64_t)blockIdx.x * W;
-        begun = p0 < 0;
-        goes_on = p1 >= W;
-        sp.wa = (int)max((int64_t)0, p0);
-        sp.wb = (int)min((int64_t)(W - 1), p1);
+        // warps of the grid that hold the pair's first and last tiles
+        const int64_t g0 = kv_div(walk.pair0 + kPairCost, share), g1 = kv_div(walk.pair0 + kPairCost + walk.n - 1, share);
+        sp.cta0 = (int)(g0 / W);
+        sp.cta1 = (int)(g1 / W);
+        begun = sp.cta0 < (int)blockIdx.x;
+        goes_on = sp.cta1 > (int)blockIdx.x;
+        sp.wa = begun ? 0 : (int)(g0 % W);
+        sp.wb = goes_on ? W - 1 : (int)(g1 % W);
       }
       if (begun || goes_on || sp.wb - sp.wa == W - 1) {
         // (one that all warps hold is the only such pair, or shares no side with another)
@@ -904,7 +903,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     for (uint32_t x = used > S ? used - S : 0; x < used; ++x) (void)a_mbar_wait(&bar[x % S], (x / S) & 1u);
   __syncthreads();
   if (has_pair[0] || has_pair[1])
-    merge_by_cta<D, T>(j, cta_pairs, has_pair, sm, in_heads, share, alone, sh_last);
+    merge_by_cta<D, T>(j, cta_pairs, has_pair, sm, in_heads, sh_last);
 }
 
 int decode_grid_cap(int D) { return kDecodeSms * (D == 256 ? 1 : 2); }

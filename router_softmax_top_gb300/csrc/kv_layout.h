@@ -15,6 +15,12 @@ namespace moe {
 
 constexpr int kKvTile = 32;  // tokens of one tile
 
+// a / b for 0 <= a, 0 < b: 64-bit division is a long sequence of instructions, and rarely needed.
+KV_HD int64_t kv_div(int64_t a, int64_t b) {
+  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // Bytes of one tile (32 tokens of one head of width D): codes and scales of keys, then of values.
 KV_HD int kv_tile_bytes(int D) { return 36 * D; }
 // Offsets inside a tile.
@@ -31,9 +37,11 @@ KV_HD int64_t kv_tile_off(int D, int page_size, int head, int tile_in_page) {
 // such entry or its entry is out of range.  row: the sequence's table row.
 KV_HD int kv_page(const int32_t *row, int table_width, int n_pages, int page_size, int64_t tile, int *in_page) {
   const int per = page_size / kKvTile;
-  const int64_t i = tile / per;
+  *in_page = 0;
+  if (tile < 0) return -1;
+  const int64_t i = kv_div(tile, per);
   *in_page = (int)(tile - i * per);
-  if (tile < 0 || i >= table_width) return -1;
+  if (i >= table_width) return -1;
   const int32_t p = row[i];
   return (p >= 0 && p < n_pages) ? p : -1;
 }
