@@ -13,7 +13,7 @@ their contents are checked by the kernels: see ``status_message``.
 from __future__ import annotations
 
 import ctypes
-import math
+import struct
 
 import torch
 
@@ -41,6 +41,10 @@ class MoeTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+# the same, packed: a call builds them for itself, and a Structure instance takes several times as long
+_CACHE = struct.Struct("@qqqqqiiiiii")
+_TENSOR = struct.Struct("@qqq")
+
 _bound = None
 
 
@@ -49,74 +53,79 @@ def _lib():
     if _bound is None:
         L = lib()
         vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-        pc, pt = ctypes.POINTER(MoeKvCache), ctypes.POINTER(MoeTensor)
         L.moe_kv_page_bytes.restype = i64
         L.moe_kv_page_bytes.argtypes = [i32, i32, i32]
-        L.moe_kv_append.argtypes = [pc, vp, vp, i32, pt, i32, pt, pt, vp, vp, i32, i32, i32, vp, vp, i32, vp]
-        L.moe_kv_read.argtypes = [pc, vp, vp, i32, vp, vp, i32, vp]
+        L.moe_kv_append.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp]
+        L.moe_kv_read.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp]
         L.moe_kv_attention_workspace.restype = i64
         L.moe_kv_attention_workspace.argtypes = [i32, i32, i32, i32]
-        L.moe_kv_attention.argtypes = [pc, vp, pt, i32, i32, f32, i32, vp, vp, i32, vp, i64, vp]
-        L.moe_prompt_attention.argtypes = [pt, i32, i32, pt, pt, i32, i32, i32, vp, vp, i32, f32, i32, vp, vp, i32, vp, vp]
+        L.moe_kv_attention.argtypes = [vp, vp, vp, i32, i32, f32, i32, vp, vp, i32, vp, i64, vp]
+        L.moe_prompt_attention.argtypes = [vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, i32, f32, i32, vp, vp, i32, vp, vp]
         _bound = L
     return _bound
 
 
 def _refuse(what: str, code: int = MOE_ERR_INVALID_ARG):
-    err = MoeError(code, what)
-    raise err
+    raise MoeError(code, what)
 
 
-def _index(t, name, n, device):
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        _refuse(f"{name} must be a contiguous int32 tensor of {n} entries on {device}")
+def _index(t, name, n, dev):
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous int32 tensor of {n} entries on the GPU")
     return t.data_ptr()
 
 
-def _tokens(t, name, n, heads, dim, dtype, device):
-    if t.dim() != 3 or t.dtype != dtype or t.device != device or t.stride(2) != 1 or t.shape[2] != dim \
-            or (heads is not None and t.shape[1] != heads) or (n is not None and t.shape[0] != n):
-        _refuse(f"{name} must be {dtype} [{n if n is not None else 'tokens'}, {heads or 'heads'}, {dim}] on {device} "
+def _tokens(t, name, n, heads, dim, dtype, dev):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or t.dtype is not dtype or t.get_device() != dev or stride[2] != 1 or shape[2] != dim \
+            or (heads is not None and shape[1] != heads) or (n is not None and shape[0] != n):
+        _refuse(f"{name} must be {dtype} [{n if n is not None else 'tokens'}, {heads or 'heads'}, {dim}] on the GPU "
                 "with a contiguous last dimension")
-    return MoeTensor(t.data_ptr(), t.stride(0), t.stride(1))
+    # a dimension of one has no stride to speak of
+    return _TENSOR.pack(t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
 
 
-def _output(t, name, shape, dtype, device):
+def _output(t, name, shape, dtype, dev):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+        return torch.empty(shape, dtype=dtype, device=_cuda(dev))
+    if tuple(t.shape) != tuple(shape) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the GPU")
     return t
 
 
+def _word(t, dev):
+    if t is None:
+        return 0
+    if t.dtype is not torch.int32 or t.numel() != 1 or t.get_device() != dev:
+        _refuse("status must be one int32 on the GPU")
+    return t.data_ptr()
+
+
 def _device(t):
-    d = t.device
-    if d.type != "cuda" or d.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         _refuse("tensors must be on the current CUDA device")
+    return dev
+
+
+_cuda_devices = {}
+
+
+def _cuda(dev):
+    d = _cuda_devices.get(dev)
+    if d is None:
+        d = _cuda_devices[dev] = torch.device("cuda", dev)
     return d
 
 
-class _On:
-    """The stream of a call as a handle; outputs are allocated for that stream."""
-
-    def __init__(self, stream):
-        self.ctx = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream().cuda_stream
-            return
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        self.handle = stream.cuda_stream
-        self.ctx = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+def _call(stream, dev, run):
+    """run(handle of the stream), its outputs allocated for that stream."""
+    if stream is None:
+        return run(torch._C._cuda_getCurrentRawStream(dev))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return run(stream.cuda_stream)
 
 
 def kv_page_bytes(n_kv_heads: int, head_dim: int, page_size: int) -> int:
@@ -141,20 +150,19 @@ def rope_table(n_positions: int, rot_dim: int, theta: float = 10000.0, device="c
     return a.cos().float(), a.sin().float()
 
 
-def _cache(pages, page_table, page_size, n_kv_heads, head_dim, status, device):
-    if pages.dtype != torch.uint8 or pages.dim() != 2 or pages.device != device or pages.stride(1) != 1:
+def _cache(pages, page_table, page_size, n_kv_heads, head_dim, status, dev):
+    shape, table, stride = pages.shape, page_table.shape, page_table.stride()
+    if pages.dtype is not torch.uint8 or len(shape) != 2 or pages.get_device() != dev or pages.stride(1) != 1:
         _refuse("pages must be uint8 [n_pages, page_bytes] on the GPU, rows contiguous")
-    if pages.shape[1] < kv_page_bytes(n_kv_heads, head_dim, page_size):
+    if shape[1] < n_kv_heads * page_size * head_dim * 9 // 8:
         _refuse("a row of pages is shorter than a page")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != device \
-            or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    if page_table.dtype is not torch.int32 or len(table) != 2 or page_table.get_device() != dev \
+            or (table[1] > 1 and stride[1] != 1):
         _refuse("page_table must be int32 [n_seqs, width] on the GPU, rows contiguous")
-    if status is not None and (status.dtype != torch.int32 or status.numel() != 1 or status.device != device):
-        _refuse("status must be one int32 on the GPU")
-    width = page_table.shape[1]
-    return MoeKvCache(pages.data_ptr(), pages.stride(0), page_table.data_ptr(), max(page_table.stride(0), width),
-                      0 if status is None else status.data_ptr(), pages.shape[0], page_size, n_kv_heads, head_dim,
-                      page_table.shape[0], width)
+    n, width = table
+    return _CACHE.pack(pages.data_ptr(), pages.stride(0) if shape[0] > 1 else shape[1], page_table.data_ptr(),
+                       stride[0] if n > 1 else width, 0 if status is None else _word(status, dev), shape[0], page_size,
+                       n_kv_heads, head_dim, n, width), n
 
 
 def kv_append(pages, page_table, starts, cu_tokens, k, v, *, page_size, q=None, cos=None, sin=None,
@@ -165,34 +173,34 @@ def kv_append(pages, page_table, starts, cu_tokens, k, v, *, page_size, q=None, 
     cos, sin [n_positions, rot_dim / 2] (``rope_table``); None: no rotation.  Returns the rotated queries
     (None without q) and the rotated keys, both contiguous in the inputs' type; the cache holds the keys
     quantised from their fp32 values."""
-    dev = _device(k)
-    if k.dtype not in _DTYPES or k.dim() != 3:
+    dev, dtype = _device(k), k.dtype
+    if dtype not in _DTYPES or k.dim() != 3:
         _refuse("k must be float32, bfloat16 or float16 [tokens, heads, head_dim]")
     T, hkv, d = k.shape
-    c = _cache(pages, page_table, page_size, hkv, d, status, dev)
-    tk, tv = _tokens(k, "k", T, hkv, d, k.dtype, dev), _tokens(v, "v", T, hkv, d, k.dtype, dev)
-    ps, pc = _index(starts, "starts", c.n_seqs, dev), _index(cu_tokens, "cu_tokens", c.n_seqs + 1, dev)
-    rot = n_pos = 0
-    cp = sp = None
+    c, n_seqs = _cache(pages, page_table, page_size, hkv, d, status, dev)
+    tk, tv = _tokens(k, "k", T, hkv, d, dtype, dev), _tokens(v, "v", T, hkv, d, dtype, dev)
+    ps, pc = _index(starts, "starts", n_seqs, dev), _index(cu_tokens, "cu_tokens", n_seqs + 1, dev)
+    tq, hq, rot, n_pos, cp, sp = None, 0, 0, 0, None, None
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        tq = _tokens(q, "q", T, None, d, dtype, dev)
     if cos is not None or sin is not None:
-        if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 \
-                or sin.dtype != torch.float32 or cos.device != dev or sin.device != dev \
+        if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape or cos.dtype is not torch.float32 \
+                or sin.dtype is not torch.float32 or cos.get_device() != dev or sin.get_device() != dev \
                 or not cos.is_contiguous() or not sin.is_contiguous():
             _refuse("cos and sin must be contiguous float32 [n_positions, rot_dim / 2] on the GPU")
         n_pos, rot = cos.shape[0], 2 * cos.shape[1]
         cp, sp = cos.data_ptr(), sin.data_ptr()
-    with _On(stream) as h:
-        tq, hq = None, 0
-        if q is not None:
-            tq = _tokens(q, "q", T, None, d, k.dtype, dev)
-            hq = q.shape[1]
-            q_out = _output(q_out, "q_out", (T, hq, d), k.dtype, dev)
-        k_out = _output(k_out, "k_out", (T, hkv, d), k.dtype, dev)
-        _check(_lib().moe_kv_append(ctypes.byref(c), ps, pc, T, None if tq is None else ctypes.byref(tq), hq,
-                                    ctypes.byref(tk), ctypes.byref(tv), cp, sp, rot, n_pos, int(interleaved),
-                                    None if q is None else q_out.data_ptr(), k_out.data_ptr(), _DTYPES[k.dtype], h),
-               "moe_kv_append")
-    return (None if q is None else q_out), k_out
+
+    def run(handle):
+        qo = None if tq is None else _output(q_out, "q_out", (T, hq, d), dtype, dev)
+        ko = _output(k_out, "k_out", (T, hkv, d), dtype, dev)
+        rc = _lib().moe_kv_append(c, ps, pc, T, tq, hq, tk, tv, cp, sp, rot, n_pos, int(interleaved),
+                                  None if qo is None else qo.data_ptr(), ko.data_ptr(), _DTYPES[dtype], handle)
+        if rc:
+            _check(rc, "moe_kv_append")
+        return qo, ko
+    return _call(stream, dev, run)
 
 
 def kv_read(pages, page_table, starts, cu_tokens, n_tokens, *, page_size, n_kv_heads, head_dim,
@@ -200,16 +208,19 @@ def kv_read(pages, page_table, starts, cu_tokens, n_tokens, *, page_size, n_kv_h
     """The values of cached tokens starts[s] + (i - cu_tokens[s]): keys and values [n_tokens, n_kv_heads,
     head_dim] (moe_kv_read)."""
     dev = _device(pages)
-    if dtype not in _DTYPES:
-        _refuse("dtype must be float32, bfloat16 or float16")
-    c = _cache(pages, page_table, page_size, n_kv_heads, head_dim, status, dev)
-    ps, pc = _index(starts, "starts", c.n_seqs, dev), _index(cu_tokens, "cu_tokens", c.n_seqs + 1, dev)
-    with _On(stream) as h:
-        k = torch.empty((n_tokens, n_kv_heads, head_dim), dtype=dtype, device=dev)
-        v = torch.empty_like(k)
-        _check(_lib().moe_kv_read(ctypes.byref(c), ps, pc, n_tokens, k.data_ptr(), v.data_ptr(), _DTYPES[dtype], h),
-               "moe_kv_read")
-    return k, v
+    if dtype not in _DTYPES or n_tokens < 0:
+        _refuse("dtype must be float32, bfloat16 or float16, and n_tokens not negative")
+    c, n_seqs = _cache(pages, page_table, page_size, n_kv_heads, head_dim, status, dev)
+    ps, pc = _index(starts, "starts", n_seqs, dev), _index(cu_tokens, "cu_tokens", n_seqs + 1, dev)
+
+    def run(handle):
+        shape = (n_tokens, n_kv_heads, head_dim)
+        k, v = _output(None, "k", shape, dtype, dev), _output(None, "v", shape, dtype, dev)
+        rc = _lib().moe_kv_read(c, ps, pc, n_tokens, k.data_ptr(), v.data_ptr(), _DTYPES[dtype], handle)
+        if rc:
+            _check(rc, "moe_kv_read")
+        return k, v
+    return _call(stream, dev, run)
 
 
 _workspaces = {}
@@ -228,11 +239,10 @@ def kv_attention_workspace(n_q_heads, n_kv_heads, head_dim, q_tokens=1, device="
 def _workspace(hq, hkv, d, q_tokens, handle, dev):
     # one per stream, as calls on one stream follow each other; a capture gets its own, which its graph keeps
     if torch.cuda.is_current_stream_capturing():
-        return kv_attention_workspace(hq, hkv, d, q_tokens, dev)
-    key = (dev.index, handle, d)
-    ws = _workspaces.get(key)
+        return kv_attention_workspace(hq, hkv, d, q_tokens, _cuda(dev))
+    ws = _workspaces.get((dev, handle, d))
     if ws is None:
-        ws = _workspaces[key] = kv_attention_workspace(hq, hkv, d, q_tokens, dev)
+        ws = _workspaces[dev, handle, d] = kv_attention_workspace(hq, hkv, d, q_tokens, _cuda(dev))
     return ws
 
 
@@ -245,25 +255,31 @@ def kv_attention(q, pages, page_table, seq_lens, *, page_size, n_kv_heads, q_tok
     Returns [n_seqs * q_tokens, n_q_heads, head_dim], and the log of the sums of exponentials (fp32) with
     return_lse.  Without `workspace` a module-level one per stream is used (inside a graph capture: one of the
     capture's own); graphs that may run at the same time need their own."""
-    dev = _device(q)
-    if q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16):
+    dev, dtype = _device(q), q.dtype
+    if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
         _refuse("q must be bfloat16 or float16 [tokens, heads, head_dim]", MOE_ERR_UNSUPPORTED)
-    n, hq, d = q.shape
-    c = _cache(pages, page_table, page_size, n_kv_heads, d, status, dev)
-    if n != c.n_seqs * q_tokens or hq % n_kv_heads:
+    shape = q.shape
+    n, hq, d = shape
+    c, n_seqs = _cache(pages, page_table, page_size, n_kv_heads, d, status, dev)
+    if n != n_seqs * q_tokens or n_kv_heads <= 0 or hq % n_kv_heads:
         _refuse("q must hold q_tokens tokens of every sequence, its heads a multiple of n_kv_heads")
-    tq = _tokens(q, "q", n, hq, d, q.dtype, dev)
-    pl = _index(seq_lens, "seq_lens", c.n_seqs, dev)
-    with _On(stream) as h:
-        out = _output(out, "out", (n, hq, d), q.dtype, dev)
-        lse = torch.empty((n, hq), dtype=torch.float32, device=dev) if return_lse else None
+    tq = _tokens(q, "q", n, hq, d, dtype, dev)
+    pl = _index(seq_lens, "seq_lens", n_seqs, dev)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        _refuse("workspace must be a contiguous tensor on the GPU")
+
+    def run(handle):
+        o = _output(out, "out", shape, dtype, dev)
+        lse = torch.empty((n, hq), dtype=torch.float32, device=_cuda(dev)) if return_lse else None
         if n:
-            ws = _workspace(hq, n_kv_heads, d, q_tokens, h, dev) if workspace is None else workspace
-            _check(_lib().moe_kv_attention(ctypes.byref(c), pl, ctypes.byref(tq), hq, q_tokens,
-                                           1.0 / math.sqrt(d) if scale is None else scale, window, out.data_ptr(),
-                                           lse.data_ptr() if return_lse else None, _DTYPES[q.dtype], ws.data_ptr(),
-                                           ws.numel(), h), "moe_kv_attention")
-    return (out, lse) if return_lse else out
+            ws = _workspace(hq, n_kv_heads, d, q_tokens, handle, dev) if workspace is None else workspace
+            rc = _lib().moe_kv_attention(c, pl, tq, hq, q_tokens, d ** -0.5 if scale is None else scale, window,
+                                         o.data_ptr(), lse.data_ptr() if return_lse else None, _DTYPES[dtype],
+                                         ws.data_ptr(), ws.numel() * ws.element_size(), handle)
+            if rc:
+                _check(rc, "moe_kv_attention")
+        return (o, lse) if return_lse else o
+    return _call(stream, dev, run)
 
 
 def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_lse=False, out=None, status=None,
@@ -274,28 +290,31 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_l
     cu_q, cu_k int32 [n_seqs + 1] (cu_k None: cu_q).  With more keys than queries a sequence's queries are its
     last tokens.  window > 0: a token sees itself and the window - 1 tokens before it.  Returns q's shape, and
     the log of the sums of exponentials (fp32 [n_q_tokens, n_q_heads]) with return_lse."""
-    dev = _device(q)
-    if q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16):
+    dev, dtype = _device(q), q.dtype
+    if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
         _refuse("q must be bfloat16 or float16 [tokens, heads, head_dim]", MOE_ERR_UNSUPPORTED)
-    n, hq, d = q.shape
-    tq, tk = _tokens(q, "q", n, hq, d, q.dtype, dev), _tokens(k, "k", None, None, d, q.dtype, dev)
-    tv = _tokens(v, "v", k.shape[0], k.shape[1], d, q.dtype, dev)
-    cu_k = cu_q if cu_k is None else cu_k
+    shape = q.shape
+    n, hq, d = shape
+    tq, tk = _tokens(q, "q", n, hq, d, dtype, dev), _tokens(k, "k", None, None, d, dtype, dev)
+    nk, hkv = k.shape[0], k.shape[1]
+    tv = _tokens(v, "v", nk, hkv, d, dtype, dev)
     if cu_q.dim() != 1 or cu_q.shape[0] < 1:
         _refuse("cu_q must hold n_seqs + 1 offsets")
     n_cu = cu_q.shape[0]
-    pq, pk = _index(cu_q, "cu_q", n_cu, dev), _index(cu_k, "cu_k", n_cu, dev)
-    if status is not None and (status.dtype != torch.int32 or status.numel() != 1 or status.device != dev):
-        _refuse("status must be one int32 on the GPU")
-    with _On(stream) as h:
-        out = _output(out, "out", (n, hq, d), q.dtype, dev)
-        lse = torch.empty((n, hq), dtype=torch.float32, device=dev) if return_lse else None
-        _check(_lib().moe_prompt_attention(ctypes.byref(tq), n, hq, ctypes.byref(tk), ctypes.byref(tv), k.shape[0],
-                                           k.shape[1], d, pq, pk, n_cu - 1, 1.0 / math.sqrt(d) if scale is None else scale,
-                                           window, out.data_ptr(), lse.data_ptr() if return_lse else None,
-                                           _DTYPES[q.dtype], None if status is None else status.data_ptr(), h),
-               "moe_prompt_attention")
-    return (out, lse) if return_lse else out
+    pq = _index(cu_q, "cu_q", n_cu, dev)
+    pk = pq if cu_k is None else _index(cu_k, "cu_k", n_cu, dev)
+    word = _word(status, dev)
+
+    def run(handle):
+        o = _output(out, "out", shape, dtype, dev)
+        lse = torch.empty((n, hq), dtype=torch.float32, device=_cuda(dev)) if return_lse else None
+        rc = _lib().moe_prompt_attention(tq, n, hq, tk, tv, nk, hkv, d, pq, pk, n_cu - 1,
+                                         d ** -0.5 if scale is None else scale, window, o.data_ptr(),
+                                         lse.data_ptr() if return_lse else None, _DTYPES[dtype], word, handle)
+        if rc:
+            _check(rc, "moe_prompt_attention")
+        return (o, lse) if return_lse else o
+    return _call(stream, dev, run)
 
 
 def status_message(status) -> str:
