@@ -33,7 +33,7 @@ struct AppendJob {
   int per_warp;  // heads (of q, k and v together) that one warp takes
 };
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4, kAppendCtas = 8;  // warps of a CTA, and CTAs that registers leave room for on an SM
 
 // The sequence of token i: the last s with cu[s] <= i, by all lanes of a warp.
 __device__ __forceinline__ int find_seq(const int32_t *cu, int n_seqs, int i) {
@@ -72,24 +72,33 @@ __device__ __forceinline__ TokenPlace place_token(const moe_kv_cache &c, const i
   return p;
 }
 
-// 8 consecutive values to and from fp32.
-__device__ __forceinline__ void load8(const float *p, float x[8]) {
-  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// 8 consecutive values as loaded, and to and from fp32.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T *p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+  return r;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float x[8]) {
-  const uint4 v = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void expand8(const Raw8<float> &r, float x[8]) {
+  const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void expand8(const Raw8<__nv_bfloat16> &r, float x[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load8(const __half *p, float x[8]) {
-  const uint4 v = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void expand8(const Raw8<__half> &r, float x[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
@@ -138,13 +147,25 @@ __device__ __forceinline__ void quantise_store(const float x[8], uint8_t *tile, 
   fine = ((bad >> (threadIdx.x & 28)) & 15u) == 0;
   const float d = (hi >= -lo ? hi : lo) * -0.125f;
   uint32_t q = 0;  // 8 codes, value i at bits 4 i
-  if (fine) {
+  if (fabsf(d) > 1e-30f) {
+    // x / d, correctly rounded, by Markstein's method: with r the rounded reciprocal, a quotient corrected once by
+    // its remainder is the rounded one.  (A quotient so small that the remainder underflows changes nothing: 8.5 is
+    // added to it.)  x / d >= -8, so the code is not negative; floor by rounding down at 2^23.
+    const float r = __frcp_rn(d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float y = d == 0.f ? 8.f : __fadd_rn(__fdiv_rn(x[i], d), 8.5f);
-      q |= (uint32_t)fminf(fmaxf(y, 0.f), 15.f) << (4 * i);
+      const float q0 = __fmul_rn(x[i], r), q1 = __fmaf_rn(__fmaf_rn(-q0, d, x[i]), r, q0);
+      const float y = fminf(__fadd_rn(q1, 8.5f), 15.5f);
+      q |= (__float_as_uint(__fadd_rd(y, 8388608.f)) & 15u) << (4 * i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = d == 0.f ? 8.f : fminf(__fadd_rn(__fdiv_rn(x[i], d), 8.5f), 15.5f);
+      q |= (uint32_t)y << (4 * i);
     }
   }
+  if (!fine) q = 0;
   // byte j of the block = code j | code j + 16 << 4: lanes 0 and 1 hold codes 0..15, lanes 2 and 3 codes 16..31
   const uint32_t other = __shfl_xor_sync(0xffffffffu, q, 2);
   if (!live) return;
@@ -168,15 +189,35 @@ __device__ __forceinline__ void quantise_store(const float x[8], uint8_t *tile, 
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const AppendJob j) {
+__global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) kv_append_kernel(const AppendJob j) {
   constexpr int L = D / 8;         // lanes of one head
   constexpr int HPW = 32 / L;      // heads that a warp handles at once
+  constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int total = j.hq + 2 * j.hkv, parts = (total + j.per_warp - 1) / j.per_warp;
   const int64_t item = (int64_t)blockIdx.x * kAppendWarps + warp;
   const int i = (int)(item / parts), part = (int)(item % parts);
   if (i >= j.n_tokens) return;
   const int sub = lane / L, dim = (lane % L) * 8;
+  const int h0 = part * j.per_warp, h1 = min(h0 + j.per_warp, total);
+  // this lane's values of the turn that begins at head hb (past the last head: that head's again)
+  const T *const q_in = static_cast<const T *>(j.q.data) + i * j.q.token_stride + dim;
+  const T *const k_in = static_cast<const T *>(j.k.data) + i * j.k.token_stride + dim;
+  const T *const v_in = static_cast<const T *>(j.v.data) + i * j.v.token_stride + dim;
+  const int first_k = j.hq, first_v = j.hq + j.hkv;  // in the list of q, k and v heads
+  auto fetch = [&](int hb) {
+    const int h = min(hb + sub, h1 - 1);
+    return load_raw(h < first_k ? q_in + h * j.q.head_stride
+                                : h < first_v ? k_in + (h - first_k) * j.k.head_stride
+                                              : v_in + (h - first_v) * j.v.head_stride);
+  };
+  // kAhead turns are asked for before the first is used, and before the token's place, which is a chain of loads.
+  // (Two, at 32 warps per SM: 18432 tokens of 48 heads of 128 take 135 us with the read; four turns at 16 warps 146 to
+  // 165, one turn at 40 warps 145.)
+  Raw8<T> next[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (h0 + u * HPW < h1) next[u] = fetch(h0 + u * HPW);
   const TokenPlace at = place_token(j.c, j.starts, j.cu, i);
   const bool no_rot = j.rot > 0 && (at.pos < 0 || at.pos >= j.n_pos);
   if (lane == 0 && j.c.status) {
@@ -205,8 +246,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
       } else {
         const int first = dim < j.rot / 2, o = first ? dim : dim - j.rot / 2;
         float ss[8];
-        load8(ct + o, c);
-        load8(st + o, ss);
+        expand8(load_raw(ct + o), c);
+        expand8(load_raw(st + o), ss);
 #pragma unroll
         for (int z = 0; z < 8; ++z) s[z] = first ? -ss[z] : ss[z];
         partner = first ? lane + j.rot / 16 : lane - j.rot / 16;
@@ -214,33 +255,48 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
     }
   }
   const bool writes = at.page >= 0 && !no_rot;
-  const int h0 = part * j.per_warp, h1 = min(h0 + j.per_warp, total);
-#pragma unroll 2
+  T *const q_to = static_cast<T *>(j.q_out) + (int64_t)i * j.hq * D + dim;
+  T *const k_to = static_cast<T *>(j.k_out) + (int64_t)i * j.hkv * D + dim;
+  uint8_t *const tiles = static_cast<uint8_t *>(j.c.pages) + (int64_t)(at.page < 0 ? 0 : at.page) * j.c.page_stride +
+                         kv_tile_off(D, j.c.page_size, 0, at.in_page);
+  const int64_t tile_stride = kv_tile_off(D, j.c.page_size, 1, 0);  // from head to head
+  // (one copy of the turn's code: for a token or two, fetching it is a good part of the time)
+#pragma unroll 1
   for (int hb = h0; hb < h1; hb += HPW) {
-    const int h = hb + sub;
-    const bool live = h < h1;
-    const int hc = live ? h : h1 - 1;
-    const int kind = hc < j.hq ? 0 : (hc < j.hq + j.hkv ? 1 : 2);
-    const int hh = kind == 0 ? hc : (kind == 1 ? hc - j.hq : hc - j.hq - j.hkv);
-    const moe_tensor &src = kind == 0 ? j.q : (kind == 1 ? j.k : j.v);
-    float x[8], y[8];
-    load8(static_cast<const T *>(src.data) + i * src.token_stride + hh * src.head_stride + dim, x);
-    // every lane takes part in the shuffles; a pair is (z, z ^ 1) of this thread, or the partner lane's value z
+    const Raw8<T> now = next[0];
 #pragma unroll
-    for (int z = 0; z < 8; ++z) {
-      const float far = __shfl_sync(0xffffffffu, x[z], partner);
-      const float o = j.interleaved ? x[z ^ 1] : far;
-      y[z] = turned && kind < 2 ? __fadd_rn(__fmul_rn(x[z], c[z]), __fmul_rn(o, s[z])) : x[z];
+    for (int u = 0; u + 1 < kAhead; ++u) next[u] = next[u + 1];
+    if (hb + kAhead * HPW < h1) next[kAhead - 1] = fetch(hb + kAhead * HPW);
+    const int h = min(hb + sub, h1 - 1);
+    const bool live = hb + sub < h1;
+    const int hh = h < first_v ? h - first_k : h - first_v;  // key or value head
+    float x[8];
+    expand8(now, x);
+    if (j.rot > 0 && hb < first_v) {  // warp-uniform: some lane holds a query or key head
+      // a pair is (z, z ^ 1) of this thread, or the partner lane's value z
+      float o[8];
+      if (j.interleaved) {
+#pragma unroll
+        for (int z = 0; z < 8; ++z) o[z] = x[z ^ 1];
+      } else {
+        Raw8<T> far;
+#pragma unroll
+        for (int z = 0; z < (int)sizeof(T) / 2; ++z)
+          far.w[z] = make_uint4(__shfl_sync(0xffffffffu, now.w[z].x, partner), __shfl_sync(0xffffffffu, now.w[z].y, partner),
+                                __shfl_sync(0xffffffffu, now.w[z].z, partner), __shfl_sync(0xffffffffu, now.w[z].w, partner));
+        expand8(far, o);
+      }
+      if (turned && h < first_v)
+#pragma unroll
+        for (int z = 0; z < 8; ++z) x[z] = __fadd_rn(__fmul_rn(x[z], c[z]), __fmul_rn(o[z], s[z]));
+      if (live && h < first_k) store8(q_to + h * D, x);
+      else if (live && h < first_v && j.k_out) store8(k_to + hh * D, x);
+    } else if (live && h < first_v) {
+      if (h < first_k) store8(q_to + h * D, x);
+      else if (j.k_out) store8(k_to + hh * D, x);
     }
-    if (live && kind == 0)
-      store8(static_cast<T *>(j.q_out) + ((int64_t)i * j.hq + hh) * D + dim, y);
-    if (live && kind == 1 && j.k_out)
-      store8(static_cast<T *>(j.k_out) + ((int64_t)i * j.hkv + hh) * D + dim, y);
-    if (hb + HPW > j.hq) {  // warp-uniform: some lane holds a key or value head
-      uint8_t *tile = static_cast<uint8_t *>(j.c.pages) + (int64_t)(at.page < 0 ? 0 : at.page) * j.c.page_stride +
-                      kv_tile_off(D, j.c.page_size, hh, at.in_page);
-      quantise_store(y, tile, D, kind == 2, dim / 32, at.row, live && writes && kind > 0);
-    }
+    if (hb + HPW > first_k)  // warp-uniform: some lane holds a key or value head
+      quantise_store(x, tiles + hh * tile_stride, D, h >= first_v, dim / 32, at.row, live && writes && h >= first_k);
   }
 }
 

@@ -11,6 +11,12 @@ import router_softmax_top_gb300 as moe
 from tests import attention_ref as R
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _seeded():
+    torch.manual_seed(21)
+
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
 
 
