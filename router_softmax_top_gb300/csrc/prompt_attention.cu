@@ -523,8 +523,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     }
     // ---- the rows' results
     const int n_mine = range.je - range.jb;
-    if (ok && n_mine > 0)
-      ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)(n_mine - 1) & 1u, &s_fail));
+    // A parity tells a phase from the next one only: with two score buffers the last scores come before the last
+    // product but one is done, so that one has to be waited for first.
+    for (int n = max(0, n_mine - 2); n < n_mine && ok; ++n)
+      ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)n & 1u, &s_fail));
     if (!ok) s_fail = 1;
     p_fence_after();
     if (w.seq >= 0) {
