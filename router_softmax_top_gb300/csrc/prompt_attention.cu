@@ -515,6 +515,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         p_st16(s_col + x / 2, p);
       }
       p_st_wait();
+      // The final wait below tells the last product's phase by its parity, so the one before has to be over by then.
+      // With a tile per score buffer it is (its scores were asked for after it); with two buffers of one tile it is
+      // waited for here, before the last product can run.
+      if (NQ == 1 && n > 0 && jj + 1 == range.je) {
+        ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)(n - 1) & 1u, &s_fail));
+        if (!ok) break;
+      }
       p_fence_before();
       a_mbar_arrive(&p_full[buf]);
       float a, b;
@@ -523,10 +530,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     }
     // ---- the rows' results
     const int n_mine = range.je - range.jb;
-    // A parity tells a phase from the next one only: with two score buffers the last scores come before the last
-    // product but one is done, so that one has to be waited for first.
-    for (int n = max(0, n_mine - 2); n < n_mine && ok; ++n)
-      ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)n & 1u, &s_fail));
+    if (ok && n_mine > 0)
+      ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)(n_mine - 1) & 1u, &s_fail));
     if (!ok) s_fail = 1;
     p_fence_after();
     if (w.seq >= 0) {
