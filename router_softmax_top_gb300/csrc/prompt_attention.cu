@@ -102,6 +102,11 @@ __device__ __forceinline__ void p_mma_ts(uint32_t d, uint32_t a, uint64_t b, uin
           d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void p_commit(uint64_t *bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(a_smem(bar))
                : "memory");
@@ -381,61 +386,75 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       }
     }
   } else if (warp == C::kMmaWarp) {
-    if (lane == 0 && n_blocks > 0) {
+    // The whole warp walks through the blocks and one elected lane issues: descriptors then stay in uniform registers,
+    // where the instructions want them.
+    if (n_blocks > 0) {
+      const bool one = elect_one();
       constexpr uint32_t id_qk = p_idesc<T>(BK, false), id_pv = p_idesc<T>(D, true);
       auto qk = [&](int t, int buf, int i) {
         const uint64_t a0 = p_desc_k(sm + C::kQOff + t * C::kQBytes);
         const uint64_t b0 = p_desc_k(sm + C::kKOff + (i % ST) * C::kKBytes);
+        if (one) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          p_mma_ss(tmem + buf * BK, a0 + (kk / 4) * (kTileRows * 128 / 16) + (kk % 4) * 2,
+          for (int kk = 0; kk < D / 16; ++kk)
+            p_mma_ss(tmem + buf * BK, a0 + (kk / 4) * (kTileRows * 128 / 16) + (kk % 4) * 2,
                    b0 + (kk / 4) * (BK * 128 / 16) + (kk % 4) * 2, id_qk, kk > 0);
-        p_commit(&s_full[buf]);
+          p_commit(&s_full[buf]);
+        }
+        __syncwarp();
       };
       auto pv = [&](int t, int buf, int i, bool first) {
         const uint64_t b0 = p_desc_mn(sm + C::kVOff + (i % ST) * C::kKBytes, BK * 128);
+        if (one) {
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          p_mma_ts(tmem + C::kOCol + t * D, tmem + buf * BK + kk * 8, b0 + kk * (2048 / 16), id_pv, !first || kk > 0);
-        p_commit(&pv_done[t]);
+          for (int kk = 0; kk < BK / 16; ++kk)
+            p_mma_ts(tmem + C::kOCol + t * D, tmem + buf * BK + kk * 8, b0 + kk * (2048 / 16), id_pv, !first || kk > 0);
+          p_commit(&pv_done[t]);
+        }
+        __syncwarp();
       };
-      bool ok = a_mbar_wait(&q_full, 0, &s_fail) && a_mbar_wait(&k_full[0], 0, &s_fail);
+      auto commit = [&](uint64_t *bar) {
+        if (one) p_commit(bar);
+        __syncwarp();
+      };
+      auto wait = [&](uint64_t *bar, uint32_t ph) { return __all_sync(0xffffffffu, a_mbar_wait(bar, ph, &s_fail)) != 0; };
+      bool ok = wait(&q_full, 0) && wait(&k_full[0], 0);
       if (ok) {
         p_fence_after();
 #pragma unroll
         for (int t = 0; t < NQ; ++t)
           if (J0 >= tr[t].jb && J0 < tr[t].je) qk(t, t, 0);
-        p_commit(&k_empty[0]);
+        commit(&k_empty[0]);
       }
       for (int i = 0; i < n_blocks && ok; ++i) {
         const int jj = J0 + i;
         const bool more = i + 1 < n_blocks;
-        if (more && !(ok = a_mbar_wait(&k_full[(i + 1) % ST], (uint32_t)((i + 1) / ST) & 1u, &s_fail))) break;
+        if (more && !(ok = wait(&k_full[(i + 1) % ST], (uint32_t)((i + 1) / ST) & 1u))) break;
         if (NQ == 1 && more) {
           p_fence_after();
           qk(0, (i + 1) & 1, i + 1);
-          p_commit(&k_empty[(i + 1) % ST]);
+          commit(&k_empty[(i + 1) % ST]);
         }
-        if (!(ok = a_mbar_wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u, &s_fail))) break;
+        if (!(ok = wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u))) break;
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
           const int buf = NQ == 1 ? (i & 1) : t;
           if (jj >= tr[t].jb && jj < tr[t].je) {
             const int n = jj - tr[t].jb;
             const uint32_t ph = (uint32_t)(NQ == 1 ? n >> 1 : n) & 1u;
-            if (!(ok = a_mbar_wait(&p_full[buf], ph, &s_fail))) break;
+            if (!(ok = wait(&p_full[buf], ph))) break;
             p_fence_after();
             pv(t, buf, i, jj == tr[t].jb);
           }
           if (NQ == 2 && more && jj + 1 >= tr[t].jb && jj + 1 < tr[t].je) qk(t, t, i + 1);
         }
         if (!ok) break;
-        if (NQ == 2 && more) p_commit(&k_empty[(i + 1) % ST]);
-        p_commit(&v_empty[i % ST]);
+        if (NQ == 2 && more) commit(&k_empty[(i + 1) % ST]);
+        commit(&v_empty[i % ST]);
       }
       if (!ok) s_fail = 1;
-      p_commit(&done);
-      (void)a_mbar_wait(&done, 0);
+      commit(&done);
+      (void)wait(&done, 0);
     }
   } else {
     // ---- softmax: thread = row of tile t
