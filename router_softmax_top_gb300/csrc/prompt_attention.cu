@@ -2,8 +2,10 @@
 // tensor cores.
 //
 // o_i = sum_j 2^(t_ij - r_i) v_j / sum_j 2^(t_ij - r_i), t = scale log2(e) q_i . k_j,
-// over the keys that row i sees, in one pass over the keys; the reference r_i moves
-// only when a score exceeds it by more than 2^8, and the sums then scale.
+// over the keys that row i sees, in one pass over the keys.  A block's weights are formed
+// with the reference as it stands; only if their sum exceeds 2^8 (no weight of a smaller
+// sum is larger) is the block's largest score looked for and the reference moved to it,
+// and the sums so far scale.
 //
 // Bound: the tensor cores, 4 D flops per (query, key) pair and head; beside them an
 // exponential per pair and head, which the same SM does at about the rate that the
@@ -37,7 +39,6 @@ namespace moe {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.f;
 constexpr int kTileRows = 128;
 
 struct PromptMaps {
@@ -66,7 +67,12 @@ struct PromptCfg {
   // tensor memory: score buffers, then outputs
   static constexpr uint32_t kOCol = kBuf * kBK;
   static constexpr int kSoftWarps = 4 * kNQ, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-  static constexpr int kThreads = 32 * (kSoftWarps + 2);
+  // a warpgroup for the two (a register split goes by warpgroups); its other warps have nothing to do
+  static constexpr int kThreads = 32 * (kSoftWarps + 4);
+  // registers per thread: what 384 threads can have at launch, then split; 256 threads need no split
+  static constexpr int kRegLaunch = 168, kRegSoft = 224, kRegRest = 56;
+  static constexpr bool kSplit = kNQ == 2;
+  static_assert(!kSplit || 2 * kRegSoft + kRegRest <= 3 * kRegLaunch, "a split draws on what the launch has");
   static_assert(kOCol + kNQ * D <= 512, "tensor memory");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -343,6 +349,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   }
   const int n_blocks = max(0, J1 - J0);
 
+  // (each role takes its registers in its own branch: the compiler allocates by them from there on)
+  if (warp >= C::kSoftWarps) {
+  if (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegRest));
   if (warp == C::kLoadWarp) {
     if (lane == 0 && n_blocks > 0) {
       int issued = 0;
@@ -456,7 +465,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       commit(&done);
       (void)wait(&done, 0);
     }
+  }
   } else {
+    if (C::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
     // ---- softmax: thread = row of tile t
     const int t = warp / 4, r = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 (warp % 4) in the lane field
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     const int hi = live ? max(0, w.n_k - w.n_q + tok + 1) : 0;
     const int lo = j.window > 0 ? max(0, hi - j.window) : 0;
     const float c = j.scale * kLog2e;
-    float m = -a_inf(), l = 0.f;  // reference (log2 units) and sum
+    float m = live ? -a_inf() : 0.f, l = 0.f;  // reference (log2 units) and sum
     bool ok = true;
     const uint32_t o_col = tmem + lanes + C::kOCol + t * D;
     for (int jj = range.jb; jj < range.je; ++jj) {
@@ -486,17 +497,44 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         for (int x = 0; x < BK; ++x)
           if (key0 + x < lo || key0 + x >= hi) s[x] = -a_inf();
       }
-      float top[4];
+      // Weights of 32 columns from x on, over the scores' first half; their sum.
+      auto weights = [&](int x, float ref) {
+        const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(-ref, -ref);
+        uint64_t sum[2] = {0, 0};
+        uint32_t p[16];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) top[z] = -a_inf();
+        for (int z = 0; z < 16; ++z) {
+          float a, b;
+          f2_unpack(f2_fma(f2_pack(s[x + 2 * z], s[x + 2 * z + 1]), c2, r2), a, b);
+          a = a_exp2(a);
+          b = a_exp2(b);
+          sum[z & 1] = f2_add(sum[z & 1], f2_pack(a, b));
+          p[z] = pack16<T>(a, b);
+        }
+        p_st16(s_col + x / 2, p);
+        float a, b;
+        f2_unpack(f2_add(sum[0], sum[1]), a, b);
+        return a + b;
+      };
+      // The old reference first, without looking for the largest score: a sum of at most 2^8 says that no weight of it
+      // was larger.
+      float sum = 0.f, ref = m == -a_inf() ? 0.f : m;
+      bool again = n == 0;
+      if (!again) {
 #pragma unroll
-      for (int x = 0; x < BK; x += 8)
+        for (int x = 0; x < BK; x += 32) sum += weights(x, ref);
+        again = __any_sync(0xffffffffu, live && (m == -a_inf() || !(sum <= 256.f)));
+      }
+      if (again) {
+        float top[4];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) top[z] = fmaxf(top[z], fmaxf(s[x + z], s[x + 4 + z]));
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;  // c > 0
-      const bool over = mx > m + kLazy;
-      if (__any_sync(0xffffffffu, over)) {
-        const float m_new = fmaxf(m, mx);
+        for (int z = 0; z < 4; ++z) top[z] = -a_inf();
+#pragma unroll
+        for (int x = 0; x < BK; x += 8)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) top[z] = fmaxf(top[z], fmaxf(s[x + z], s[x + 4 + z]));
+        const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c);  // c > 0
+        p_st_wait();  // of the weights that are written again
         const float a = m == -a_inf() ? 0.f : a_exp2(m - m_new);
         m = m_new;
         l *= a;
@@ -515,24 +553,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           }
           p_st_wait();
         }
-      }
-      const float ref = m == -a_inf() ? 0.f : m;
-      const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(-ref, -ref);
-      uint64_t sum[2] = {0, 0};
+        ref = m == -a_inf() ? 0.f : m;
+        sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < BK; x += 32) {
-        uint32_t p[16];
-#pragma unroll
-        for (int z = 0; z < 16; ++z) {
-          float a, b;
-          f2_unpack(f2_fma(f2_pack(s[x + 2 * z], s[x + 2 * z + 1]), c2, r2), a, b);
-          a = a_exp2(a);
-          b = a_exp2(b);
-          sum[z & 1] = f2_add(sum[z & 1], f2_pack(a, b));
-          p[z] = pack16<T>(a, b);
-        }
-        p_st16(s_col + x / 2, p);
+        for (int x = 0; x < BK; x += 32) sum += weights(x, ref);
       }
+      l += sum;
       p_st_wait();
       // The final wait below tells the last product's phase by its parity, so the one before has to be over by then.
       // With a tile per score buffer it is (its scores were asked for after it); with two buffers of one tile it is
@@ -543,9 +569,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       }
       p_fence_before();
       a_mbar_arrive(&p_full[buf]);
-      float a, b;
-      f2_unpack(f2_add(sum[0], sum[1]), a, b);
-      l += a + b;
     }
     // ---- the rows' results
     const int n_mine = range.je - range.jb;
