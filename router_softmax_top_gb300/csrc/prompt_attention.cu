@@ -59,7 +59,7 @@ template <int D>
 struct PromptCfg {
   static constexpr int kNQ = D == 256 ? 1 : 2;         // row tiles
   static constexpr int kBuf = 2;                       // score buffers (one per tile, or two of the one tile)
-  static constexpr int kBK = D == 256 ? 64 : 128;      // keys of a block
+  static constexpr int kBK = D == 128 ? 128 : 64;      // keys of a block
   static constexpr int kStages = D == 64 ? 4 : 2;      // of keys, and of values
   static constexpr uint32_t kQBytes = kTileRows * D * 2, kKBytes = kBK * D * 2;
   static constexpr uint32_t kQOff = 0, kKOff = kNQ * kQBytes, kVOff = kKOff + kStages * kKBytes;
@@ -70,11 +70,13 @@ struct PromptCfg {
   // a warpgroup for the two (a register split goes by warpgroups); its other warps have nothing to do
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
   // registers per thread: what 384 threads can have at launch, then split; 256 threads need no split
-  static constexpr int kRegLaunch = 168, kRegSoft = 224, kRegRest = 56;
+  static constexpr int kCtas = D == 64 ? 2 : 1;  // on an SM: what one CTA waits for at its ends, the other hides
+  static constexpr int kRegLaunch = D == 64 ? 80 : 168, kRegSoft = D == 64 ? 104 : 224, kRegRest = D == 64 ? 32 : 56;
+  static constexpr uint32_t kTmemCols = D == 64 ? 256 : 512;
   static constexpr bool kSplit = kNQ == 2;
   static_assert(!kSplit || 2 * kRegSoft + kRegRest <= 3 * kRegLaunch, "a split draws on what the launch has");
-  static_assert(kOCol + kNQ * D <= 512, "tensor memory");
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kOCol + kNQ * D <= kTmemCols, "tensor memory");
+  static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "shared memory");
 };
 
 template <typename T>
@@ -250,7 +252,7 @@ __device__ __noinline__ void row_by_keys(const PromptJob &j, int q_tok, int head
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     prompt_attention_kernel(const __grid_constant__ PromptMaps maps, const PromptJob j) {
   using C = PromptCfg<D>;
   constexpr int NQ = C::kNQ, BK = C::kBK, ST = C::kStages, DC = D / 64;
@@ -262,6 +264,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   const uint32_t sm = (a_smem(sm_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if (warp == C::kLoadWarp && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v)));
   if (tid == 0) {
     s_fail = 0;
     a_mbar_init(&q_full, 1);
@@ -289,10 +293,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     const int mine = (int)(blockIdx.x / j.hkv);
     for (int base = 0; base < j.n_seqs; base += 32) {
       const int s = base + lane;
-      int n = 0, a = 0, b = 0;
+      int n = 0, a = 0, b = 0, c = 0, d = 0;
       if (s < j.n_seqs) {
         a = __ldg(j.cu_q + s);
         b = __ldg(j.cu_q + s + 1);
+        c = __ldg(j.cu_k + s);  // with the others: a trip to memory less
+        d = __ldg(j.cu_k + s + 1);
         if (a < 0 || b < a || b > j.n_q) {
           if (blockIdx.x == 0 && j.status) atomicOr(j.status, MOE_KV_BAD_LENGTH);
           a = b = 0;
@@ -313,7 +319,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           w.q0 = a;
           w.n_q = b - a;
           w.first_token = (n - 1 - (mine - (before + inc - n))) * per;
-          const int c = __ldg(j.cu_k + s), d = __ldg(j.cu_k + s + 1);
           w.bad_k = c < 0 || d < c || d > j.n_k;
           w.k0 = w.bad_k ? 0 : c;
           w.n_k = w.bad_k ? 0 : d - c;
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     }
   }
   if (warp == C::kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(a_smem(&s_tmem)), "r"(512u));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(a_smem(&s_tmem)), "r"(C::kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   p_fence_before();
@@ -624,7 +629,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   __syncthreads();
   if (s_fail && tid == 0 && j.status) atomicOr(j.status, MOE_KV_TIMED_OUT);
   if (warp == C::kMmaWarp)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
