@@ -66,7 +66,8 @@ struct PromptCfg {
   static constexpr size_t kSmem = kVOff + kStages * kKBytes + 1024;
   // tensor memory: score buffers, then outputs
   static constexpr uint32_t kOCol = kBuf * kBK;
-  static constexpr int kSoftWarps = 4 * kNQ, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+  static constexpr int kSoftWarps = 4 * kNQ, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1,
+                       kReadyWarp = kSoftWarps + 2;  // (two tiles only)
   // a warpgroup for the two (a register split goes by warpgroups); its other warps have nothing to do
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
   // registers per thread: what 384 threads can have at launch, then split; 256 threads need no split
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
   using C = PromptCfg<D>;
   constexpr int NQ = C::kNQ, BK = C::kBK, ST = C::kStages, DC = D / 64;
   extern __shared__ __align__(1024) unsigned char sm_raw[];
-  __shared__ uint64_t q_full, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], pv_done[NQ], done;
+  __shared__ uint64_t q_full, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], pv_done[NQ], k_first, done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   __shared__ PromptWork s_work;
@@ -277,9 +278,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     }
     for (int i = 0; i < 2; ++i) {
       a_mbar_init(&s_full[i], 1);
-      a_mbar_init(&p_full[i], 128);
+      a_mbar_init(&p_full[i], NQ == 2 ? 129 : 128);
     }
     for (int i = 0; i < NQ; ++i) a_mbar_init(&pv_done[i], 1);
+    a_mbar_init(&k_first, 1);
     a_mbar_init(&done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -359,7 +361,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
   if (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegRest));
   if (warp == C::kLoadWarp) {
     if (lane == 0 && n_blocks > 0) {
-      int issued = 0;
       bool ok = true;
       const uint32_t q_rows_bytes = (uint32_t)(j.group * j.tile_tokens) * 128u;
       uint32_t q_bytes = 0;
@@ -373,31 +374,39 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
           for (int c = 0; c < DC; ++c)
             p_tma_3d(sm + C::kQOff + t * C::kQBytes + c * kTileRows * 128, &maps.q, 64 * c, kvh * j.group,
                      w.q0 + w.first_token + t * j.tile_tokens, &q_full);
-      for (int i = 0; i < n_blocks && ok; ++i) {
+      // block i's keys or values into their stage; keys go a block ahead of values, as they are used
+      auto load = [&](const CUtensorMap *map, uint32_t off, uint64_t *full, int i, int &count) {
         const int st = i % ST;
-        const uint32_t ph = (uint32_t)(i / ST - 1) & 1u;
-        const int row = w.k0 + (J0 + i) * BK;
-        if (i >= ST && !a_mbar_wait(&k_empty[st], ph, &s_fail)) { ok = false; break; }
-        a_expect_tx(&k_full[st], C::kKBytes);
+        a_expect_tx(&full[st], C::kKBytes);
         for (int c = 0; c < DC; ++c)
-          p_tma_3d(sm + C::kKOff + st * C::kKBytes + c * BK * 128, &maps.k, 64 * c, kvh, row, &k_full[st]);
-        if (i >= ST && !a_mbar_wait(&v_empty[st], ph, &s_fail)) { ok = false; }
-        if (ok) {
-          a_expect_tx(&v_full[st], C::kKBytes);
-          for (int c = 0; c < DC; ++c)
-            p_tma_3d(sm + C::kVOff + st * C::kKBytes + c * BK * 128, &maps.v, 64 * c, kvh, row, &v_full[st]);
-          issued = i + 1;
-        } else {
-          (void)a_mbar_wait(&k_full[st], (uint32_t)(i / ST) & 1u);
+          p_tma_3d(sm + off + st * C::kKBytes + c * BK * 128, map, 64 * c, kvh, w.k0 + (J0 + i) * BK, &full[st]);
+        count = i + 1;
+      };
+      auto free_from = [&](uint64_t *empty, int i) {  // the stage's use `i` (0, 1, ... over all stages) is over
+        return a_mbar_wait(&empty[i % ST], (uint32_t)(i / ST) & 1u, &s_fail);
+      };
+      int k_loaded = 0, v_loaded = 0;
+      load(&maps.k, C::kKOff, k_full, 0, k_loaded);
+      for (int i = 0; i < n_blocks; ++i) {
+        const int x = i + 1;
+        if (x >= ST && x <= n_blocks) {
+          if (NQ == 2) {
+            // one signal for the values of block i - ST and the keys of the block after it
+            ok = x == ST ? x == n_blocks || a_mbar_wait(&k_first, 0, &s_fail) : free_from(v_empty, x - ST - 1);
+          } else if (x < n_blocks) {
+            ok = free_from(k_empty, x - ST);
+          }
+          if (!ok) break;
         }
+        if (x < n_blocks) load(&maps.k, C::kKOff, k_full, x, k_loaded);
+        if (NQ == 1 && i >= ST && !(ok = free_from(v_empty, i - ST))) break;
+        load(&maps.v, C::kVOff, v_full, i, v_loaded);
       }
       if (!ok) s_fail = 1;
       // no copy may be in flight when the CTA leaves
       if (*(volatile int *)&s_fail) (void)a_mbar_wait(&q_full, 0);
-      for (int i = issued < ST ? 0 : issued - ST; i < issued; ++i) {
-        (void)a_mbar_wait(&k_full[i % ST], (uint32_t)(i / ST) & 1u);
-        (void)a_mbar_wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u);
-      }
+      for (int i = max(0, k_loaded - ST); i < k_loaded; ++i) (void)a_mbar_wait(&k_full[i % ST], (uint32_t)(i / ST) & 1u);
+      for (int i = max(0, v_loaded - ST); i < v_loaded; ++i) (void)a_mbar_wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u);
     }
   } else if (warp == C::kMmaWarp) {
     // The whole warp walks through the blocks and one elected lane issues: descriptors then stay in uniform registers,
@@ -417,13 +426,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         }
         __syncwarp();
       };
-      auto pv = [&](int t, int buf, int i, bool first) {
+      auto pv = [&](int t, int buf, int i, bool first, bool last) {
         const uint64_t b0 = p_desc_mn(sm + C::kVOff + (i % ST) * C::kKBytes, BK * 128);
         if (one) {
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
             p_mma_ts(tmem + C::kOCol + t * D, tmem + buf * BK + kk * 8, b0 + kk * (2048 / 16), id_pv, !first || kk > 0);
-          p_commit(&pv_done[t]);
+          // (of two tiles, the scores of the next block, asked for later, tell that this is done)
+          if (NQ == 1 || last) p_commit(&pv_done[t]);
         }
         __syncwarp();
       };
@@ -438,37 +448,69 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
 #pragma unroll
         for (int t = 0; t < NQ; ++t)
           if (J0 >= tr[t].jb && J0 < tr[t].je) qk(t, t, 0);
-        commit(&k_empty[0]);
+        commit(NQ == 2 ? &k_first : &k_empty[0]);
       }
       for (int i = 0; i < n_blocks && ok; ++i) {
         const int jj = J0 + i;
         const bool more = i + 1 < n_blocks;
-        if (more && !(ok = wait(&k_full[(i + 1) % ST], (uint32_t)((i + 1) / ST) & 1u))) break;
-        if (NQ == 1 && more) {
-          p_fence_after();
-          qk(0, (i + 1) & 1, i + 1);
-          commit(&k_empty[(i + 1) % ST]);
-        }
-        if (!(ok = wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u))) break;
+        if constexpr (NQ == 2) {
+          // A wait costs this warp a few hundred cycles even where there is nothing to wait for, and the tensor cores
+          // run dry meanwhile: so the weights' barrier also stands for block i's values and block i + 1's keys (another
+          // warp waits for them), and one commit frees both stages.
 #pragma unroll
-        for (int t = 0; t < NQ; ++t) {
-          const int buf = NQ == 1 ? (i & 1) : t;
-          if (jj >= tr[t].jb && jj < tr[t].je) {
-            const int n = jj - tr[t].jb;
-            const uint32_t ph = (uint32_t)(NQ == 1 ? n >> 1 : n) & 1u;
-            if (!(ok = wait(&p_full[buf], ph))) break;
-            p_fence_after();
-            pv(t, buf, i, jj == tr[t].jb);
+          for (int t = 0; t < 2; ++t) {
+            const bool now = jj >= tr[t].jb && jj < tr[t].je, next = more && jj + 1 >= tr[t].jb && jj + 1 < tr[t].je;
+            if (now) {
+              if (!(ok = wait(&p_full[t], (uint32_t)(jj - tr[t].jb) & 1u))) break;
+              p_fence_after();
+              pv(t, t, i, jj == tr[t].jb, jj + 1 == tr[t].je);
+            } else if (next) {
+              if (!(ok = wait(&k_full[(i + 1) % ST], (uint32_t)((i + 1) / ST) & 1u))) break;
+              p_fence_after();
+            }
+            // (the weights that these scores overwrite have been read by then: one thread's instructions run in order)
+            if (next) qk(t, t, i + 1);
           }
-          if (NQ == 2 && more && jj + 1 >= tr[t].jb && jj + 1 < tr[t].je) qk(t, t, i + 1);
+          if (!ok) break;
+          commit(&v_empty[i % ST]);
+        } else {
+          if (more && !(ok = wait(&k_full[(i + 1) % ST], (uint32_t)((i + 1) / ST) & 1u))) break;
+          if (more) {
+            p_fence_after();
+            qk(0, (i + 1) & 1, i + 1);
+            commit(&k_empty[(i + 1) % ST]);
+          }
+          if (!(ok = wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u))) break;
+          if (!(ok = wait(&p_full[i & 1], (uint32_t)(i >> 1) & 1u))) break;
+          p_fence_after();
+          pv(0, i & 1, i, i == 0, false);
+          commit(&v_empty[i % ST]);
         }
-        if (!ok) break;
-        if (NQ == 2 && more) commit(&k_empty[(i + 1) % ST]);
-        commit(&v_empty[i % ST]);
       }
       if (!ok) s_fail = 1;
       commit(&done);
       (void)wait(&done, 0);
+    }
+  } else if (NQ == 2 && warp == C::kReadyWarp) {
+    // block i's values and block i + 1's keys are there: one more arrival for the weights of block i
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0; i < n_blocks && ok; ++i) {
+        // Not before the weights of the block before are complete: an arrival that comes early would count for them, and
+        // a stage's barrier might not have seen its block before, whose parity is that of the next.
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          const int n = J0 + i - 1 - tr[t].jb;
+          if (ok && i > 0 && n >= 0 && J0 + i - 1 < tr[t].je) ok = a_mbar_wait(&p_full[t], (uint32_t)n & 1u, &s_fail);
+        }
+        ok = ok && (i + 1 == n_blocks || a_mbar_wait(&k_full[(i + 1) % ST], (uint32_t)((i + 1) / ST) & 1u, &s_fail)) &&
+             a_mbar_wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u, &s_fail);
+        if (!ok) break;
+#pragma unroll
+        for (int t = 0; t < NQ; ++t)
+          if (J0 + i >= tr[t].jb && J0 + i < tr[t].je) a_mbar_arrive(&p_full[t]);
+      }
+      if (!ok) s_fail = 1;
     }
   }
   } else {
@@ -544,7 +586,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         m = m_new;
         l *= a;
         if (n > 0) {
-          ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)(n - 1) & 1u, &s_fail));
+          // the products so far: of two tiles, these scores were asked for after them
+          if (NQ == 1) ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)(n - 1) & 1u, &s_fail));
           if (!ok) break;
           p_fence_after();
 #pragma unroll 1
@@ -578,7 +621,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     // ---- the rows' results
     const int n_mine = range.je - range.jb;
     if (ok && n_mine > 0)
-      ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], (uint32_t)(n_mine - 1) & 1u, &s_fail));
+      ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], NQ == 1 ? (uint32_t)(n_mine - 1) & 1u : 0u, &s_fail));
     if (!ok) s_fail = 1;
     p_fence_after();
     if (w.seq >= 0) {
