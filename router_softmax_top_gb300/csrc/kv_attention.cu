@@ -168,13 +168,14 @@ struct SharedPair {
   int cta0, cta1;  // the CTAs that hold tiles of it
 };
 
-// The part that warp w of this CTA holds of a pair: its last piece, in its ring, or, for the pair's last warp if it
-// goes on with other pairs, its first piece, in the workspace.
+// The part that warp w of this CTA holds of a pair: its last piece, in its ring, or, where the pair did not begin in w
+// and w goes on with other pairs, its first piece, in the workspace.
 template <int D>
 __device__ __forceinline__ const float *warp_part(const DecodeJob &j, const SharedPair &sp, unsigned char *sm,
                                                   const int *in_heads, int w) {
   using C = DecodeCfg<D>;
-  return w == sp.wb && in_heads[w] ? j.part + ((size_t)blockIdx.x * (2 + C::kWarps) + 2 + w) * C::kPart
+  const bool began_here = w == sp.wa && sp.cta0 == (int)blockIdx.x;
+  return !began_here && in_heads[w] ? j.part + ((size_t)blockIdx.x * (2 + C::kWarps) + 2 + w) * C::kPart
                                    : reinterpret_cast<const float *>(sm + (size_t)w * C::kStages * C::kTile);
 }
 
@@ -239,9 +240,9 @@ __device__ __noinline__ void merge_by_warp(const DecodeJob &j, const SharedPair 
   }
 }
 
-// Pairs that the whole CTA merges once its warps are done: the one that warps of earlier CTAs hold tiles of too (or
-// that all of this CTA's warps hold parts of), and the one that goes on in later CTAs.  The last CTA to be done with a
-// pair merges the CTAs' results.
+// Pairs that the whole CTA merges once its warps are done, up to three: [0] one that warps of earlier CTAs hold tiles
+// of too, [1] one that goes on in later CTAs (and began here), [2] one of this CTA alone that all its warps hold parts
+// of.  The last CTA to be done with a pair merges the CTAs' results.
 template <int D, typename T>
 __device__ __noinline__ void merge_by_cta(const DecodeJob &j, const SharedPair *sps, const int *has, unsigned char *sm,
                                           const int *in_heads, int *is_last) {
@@ -263,7 +264,7 @@ __device__ __noinline__ void merge_by_cta(const DecodeJob &j, const SharedPair *
     }
   };
 #pragma unroll 1
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 0; x < 3; ++x) {
     if (!has[x]) continue;
     const SharedPair &sp = sps[x];
     float *mine = j.part + ((size_t)blockIdx.x * (2 + W) + ((int)blockIdx.x == sp.cta0 ? 1 : 0)) * C::kPart;
@@ -364,8 +365,8 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   constexpr int W = C::kWarps, S = C::kStages, NB = D / 32;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ uint64_t bars[W][S];
-  __shared__ SharedPair cta_pairs[2];  // pairs that the whole CTA merges
-  __shared__ int has_pair[2], sh_last[2];
+  __shared__ SharedPair cta_pairs[3];  // pairs that the whole CTA merges
+  __shared__ int has_pair[3], sh_last[2];
   __shared__ int parts_done[W];     // per pair that only warps of this CTA share, by its first warp
   __shared__ int in_heads[W];       // per warp: its first piece is a part in the workspace
   __shared__ Walk walks[W][2];      // per warp: the piece that it computes, and the one that its copies are at
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     for (int s = 0; s < S; ++s) a_mbar_init(&bar[s], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     parts_done[warp] = in_heads[warp] = 0;
-    if (warp == 0) has_pair[0] = has_pair[1] = 0;
+    if (warp == 0) has_pair[0] = has_pair[1] = has_pair[2] = 0;
   }
   __syncthreads();
 
@@ -879,10 +880,10 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
         sp.wb = goes_on ? W - 1 : (int)(g1 % W);
       }
       if (begun || goes_on || sp.wb - sp.wa == W - 1) {
-        // (one that all warps hold is the only such pair, or shares no side with another)
+        const int x = begun ? 0 : goes_on ? 1 : 2;
         if (lane == 0) {
-          cta_pairs[goes_on && !begun] = sp;
-          has_pair[goes_on && !begun] = 1;
+          cta_pairs[x] = sp;
+          has_pair[x] = 1;
         }
       } else {
         __threadfence_block();
@@ -902,7 +903,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   if (dead)
     for (uint32_t x = used > S ? used - S : 0; x < used; ++x) (void)a_mbar_wait(&bar[x % S], (x / S) & 1u);
   __syncthreads();
-  if (has_pair[0] || has_pair[1])
+  if (has_pair[0] || has_pair[1] || has_pair[2])
     merge_by_cta<D, T>(j, cta_pairs, has_pair, sm, in_heads, sh_last);
 }
 

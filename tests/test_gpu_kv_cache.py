@@ -252,6 +252,30 @@ def test_attention_split_over_ctas(lens):
         assert torch.equal(a, b) and torch.equal(la, lb)
 
 
+@pytest.mark.parametrize("d,hq,hkv,q_tokens", [(64, 8, 8, 1), (128, 16, 8, 1), (256, 16, 8, 2), (128, 24, 2, 1)])
+@pytest.mark.parametrize("n,longest", [(2, 9000), (9, 8000), (70, 5000), (200, 700)])
+def test_attention_of_ragged_batches(d, hq, hkv, q_tokens, n, longest):
+    # pairs that begin, end and go on anywhere in the warps' and CTAs' shares; every row, against 64 bits on the GPU
+    g = torch.Generator().manual_seed(n + d)
+    lens = [int(x) for x in torch.randint(0, longest, (n,), generator=g)]
+    lens[n // 2] = longest
+    pages, table = filled(lens, 64, hkv, d, n)
+    td, q = table.cuda(), torch.randn(n * q_tokens, hq, d, device="cuda").half()
+    out = moe.kv_attention(q, pages, td, i32(lens), page_size=64, n_kv_heads=hkv, q_tokens=q_tokens)
+    for s, m in enumerate(lens):
+        k, v = [x.double().repeat_interleave(hq // hkv, 1) for x in moe.kv_read(
+            pages, td[s:s + 1], i32([0]), i32([0, m]), m, page_size=64, n_kv_heads=hkv, head_dim=d, dtype=torch.float32)]
+        rows = slice(s * q_tokens, (s + 1) * q_tokens)
+        z = torch.einsum("rhd,nhd->hrn", q[rows].double(), k) * d ** -0.5
+        at = m - q_tokens + torch.arange(q_tokens, device="cuda")
+        z.masked_fill_(torch.arange(m, device="cuda") > at[None, :, None], -float("inf"))
+        w = torch.nan_to_num(torch.softmax(z, -1)) if m else z
+        ref, mag = torch.einsum("hrn,nhd->rhd", w, v), torch.einsum("hrn,nhd->rhd", w, v.abs())
+        size = (torch.einsum("rhd,nhd->hrn", q[rows].double().abs(), k.abs()) * d ** -0.5).amax(-1).T[..., None] if m else 0.0
+        tol = mag * (2.0 ** -10 + 2.0 ** -12 + 2.0 ** -17 * size) + R.EPS[q.dtype] * ref.abs() + 1e-30
+        assert bool(((out[rows].double() - ref).abs() <= tol).all()), (s, m)
+
+
 @pytest.mark.parametrize("v_size", [1e-5, 1e-3, 300.0, 3e5])
 @pytest.mark.parametrize("q_size", [1e-6, 1.0, 1e4])
 def test_attention_over_far_apart_sizes(v_size, q_size):
