@@ -22,7 +22,7 @@
 //    2^-24 of the row's largest value).
 //  * Values: O^T = V^T P^T, P^T from the scores by an 8x8 transpose, multiplied by the
 //    value's scale per block (fp16: p and p d are each off by at most 2^-11 of
-//    themselves; sums are fp32).  The reference r includes the largest scale seen, so
+//    themselves, for fp16 results p d alone; sums are fp32).  The reference r includes the largest scale seen, so
 //    p d stays inside fp16 whatever the scales are.
 //  * Rows in the matrix's N: 8 of them (heads sharing a key head x query tokens).
 //
@@ -103,6 +103,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
   return h2_bits(__hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b)));
+}
+__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
+  return h2_bits(__hfma2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b),
+                         *reinterpret_cast<__half2 *>(&c)));
 }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
@@ -363,6 +367,9 @@ template <int D, typename T>
 __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas) kv_attention_kernel(const DecodeJob j) {
   using C = DecodeCfg<D>;
   constexpr int W = C::kWarps, S = C::kStages, NB = D / 32;
+  // fp16 results show a weight's second rounding (3.5e-4 of the result against 2.9e-4): their weights are carried in two
+  // halves, so that p d is rounded once.  bf16 results do not.
+  constexpr bool kExactWeights = std::is_same<T, __half>::value;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ uint64_t bars[W][S];
   __shared__ SharedPair cta_pairs[3];  // pairs that the whole CTA merges
@@ -749,8 +756,14 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
         const float p2 = a_exp2(fmaf(s[mt][2], f[0], r0)), p3 = a_exp2(fmaf(s[mt][3], f[1], r1));
         l[0] += p0 + p2;
         l[1] += p1 + p3;
-        const uint32_t b0 = transpose8x8(h2_bits(__floats2half2_rn(p0, p1)));  // row g, tokens t and t + 4
-        const uint32_t b1 = transpose8x8(h2_bits(__floats2half2_rn(p2, p3)));  // row g, tokens t + 8 and t + 12
+        const __half2 ha = __floats2half2_rn(p0, p1), hb = __floats2half2_rn(p2, p3);
+        const uint32_t b0 = transpose8x8(h2_bits(ha));  // row g, tokens t and t + 4
+        const uint32_t b1 = transpose8x8(h2_bits(hb));  // row g, tokens t + 8 and t + 12
+        uint32_t b0_rest = 0, b1_rest = 0;
+        if (kExactWeights) {
+          b0_rest = transpose8x8(h2_bits(__floats2half2_rn(p0 - __low2float(ha), p1 - __high2float(ha))));
+          b1_rest = transpose8x8(h2_bits(__floats2half2_rn(p2 - __low2float(hb), p3 - __high2float(hb))));
+        }
         const int k0 = mt * 16 + t;
         uint32_t d[4][NB / 2];  // scales of tokens t, t + 4, t + 8, t + 12
 #pragma unroll
@@ -776,8 +789,9 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint32_t sel = (b & 1) ? 0x7632u : 0x5410u;
-          uint32_t e0 = mul_h2(b0, __byte_perm(d[0][b / 2], d[1][b / 2], sel));
-          uint32_t e1 = mul_h2(b1, __byte_perm(d[2][b / 2], d[3][b / 2], sel));
+          const uint32_t d0 = __byte_perm(d[0][b / 2], d[1][b / 2], sel), d1 = __byte_perm(d[2][b / 2], d[3][b / 2], sel);
+          uint32_t e0 = kExactWeights ? fma_h2(b0, d0, mul_h2(b0_rest, d0)) : mul_h2(b0, d0);
+          uint32_t e1 = kExactWeights ? fma_h2(b1, d1, mul_h2(b1_rest, d1)) : mul_h2(b1, d1);
           if (!whole) {
             e0 &= ~unseen0;
             e1 &= ~unseen1;
