@@ -78,6 +78,14 @@ struct Raw8 {
   uint4 w[sizeof(T) / 2];
 };
 template <typename T>
+__device__ __forceinline__ void copy_raw(Raw8<T> *to, const T *from) {  // asynchronous, into shared memory
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a_smem(&to->w[i])),
+                 "l"(reinterpret_cast<const uint4 *>(from) + i)
+                 : "memory");
+}
+template <typename T>
 __device__ __forceinline__ Raw8<T> load_raw(const T *p) {
   Raw8<T> r;
 #pragma unroll
@@ -192,7 +200,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) kv_append_kernel(const AppendJob j) {
   constexpr int L = D / 8;         // lanes of one head
   constexpr int HPW = 32 / L;      // heads that a warp handles at once
-  constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;
+  constexpr int kAhead = 4;        // turns on their way (six or eight are no faster)
+  __shared__ Raw8<T> ring[kAppendWarps][kAhead][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int total = j.hq + 2 * j.hkv, parts = (total + j.per_warp - 1) / j.per_warp;
   const int64_t item = (int64_t)blockIdx.x * kAppendWarps + warp;
@@ -205,19 +214,20 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) kv_append_kern
   const T *const k_in = static_cast<const T *>(j.k.data) + i * j.k.token_stride + dim;
   const T *const v_in = static_cast<const T *>(j.v.data) + i * j.v.token_stride + dim;
   const int first_k = j.hq, first_v = j.hq + j.hkv;  // in the list of q, k and v heads
-  auto fetch = [&](int hb) {
+  Raw8<T>(*const mine)[32] = ring[warp];
+  auto fetch = [&](int hb, int slot) {
     const int h = min(hb + sub, h1 - 1);
-    return load_raw(h < first_k ? q_in + h * j.q.head_stride
-                                : h < first_v ? k_in + (h - first_k) * j.k.head_stride
-                                              : v_in + (h - first_v) * j.v.head_stride);
+    if (hb < h1)
+      copy_raw(&mine[slot][lane], h < first_k ? q_in + h * j.q.head_stride
+                                              : h < first_v ? k_in + (h - first_k) * j.k.head_stride
+                                                            : v_in + (h - first_v) * j.v.head_stride);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // kAhead turns are asked for before the first is used, and before the token's place, which is a chain of loads.
-  // (Two, at 32 warps per SM: 18432 tokens of 48 heads of 128 take 135 us with the read; four turns at 16 warps 146 to
-  // 165, one turn at 40 warps 145.)
-  Raw8<T> next[kAhead];
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u)
-    if (h0 + u * HPW < h1) next[u] = fetch(h0 + u * HPW);
+  // The values come through shared memory, kAhead turns before they are used: enough bytes on their way without
+  // holding registers, which are what limits the warps.  The first ones are asked for before the token's place, which is
+  // a chain of loads.
+#pragma unroll 1
+  for (int u = 0; u < kAhead; ++u) fetch(h0 + u * HPW, u);
   const TokenPlace at = place_token(j.c, j.starts, j.cu, i);
   const bool no_rot = j.rot > 0 && (at.pos < 0 || at.pos >= j.n_pos);
   if (lane == 0 && j.c.status) {
@@ -261,12 +271,15 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) kv_append_kern
                          kv_tile_off(D, j.c.page_size, 0, at.in_page);
   const int64_t tile_stride = kv_tile_off(D, j.c.page_size, 1, 0);  // from head to head
   // (one copy of the turn's code: for a token or two, fetching it is a good part of the time)
+  int slot = 0;
 #pragma unroll 1
   for (int hb = h0; hb < h1; hb += HPW) {
-    const Raw8<T> now = next[0];
-#pragma unroll
-    for (int u = 0; u + 1 < kAhead; ++u) next[u] = next[u + 1];
-    if (hb + kAhead * HPW < h1) next[kAhead - 1] = fetch(hb + kAhead * HPW);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    __syncwarp();
+    const Raw8<T> now = mine[slot][lane], far = mine[slot][partner];
+    __syncwarp();
+    fetch(hb + kAhead * HPW, slot);
+    slot = (slot + 1) % kAhead;
     const int h = min(hb + sub, h1 - 1);
     const bool live = hb + sub < h1;
     const int hh = h < first_v ? h - first_k : h - first_v;  // key or value head
@@ -279,11 +292,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) kv_append_kern
 #pragma unroll
         for (int z = 0; z < 8; ++z) o[z] = x[z ^ 1];
       } else {
-        Raw8<T> far;
-#pragma unroll
-        for (int z = 0; z < (int)sizeof(T) / 2; ++z)
-          far.w[z] = make_uint4(__shfl_sync(0xffffffffu, now.w[z].x, partner), __shfl_sync(0xffffffffu, now.w[z].y, partner),
-                                __shfl_sync(0xffffffffu, now.w[z].z, partner), __shfl_sync(0xffffffffu, now.w[z].w, partner));
         expand8(far, o);
       }
       if (turned && h < first_v)
@@ -314,27 +322,34 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_read_kernel(const Append
     atomicOr(j.c.status, at.pos < 0 ? MOE_KV_BAD_LENGTH : MOE_KV_BAD_PAGE);
   const int h0 = part * j.per_warp, h1 = min(h0 + j.per_warp, total);
   const uint8_t *page = static_cast<const uint8_t *>(j.c.pages) + (int64_t)(at.page < 0 ? 0 : at.page) * j.c.page_stride;
-#pragma unroll 4
-  for (int h = h0 + sub; h < h1; h += HPW) {
-    const int value = h >= j.hkv, hh = value ? h - j.hkv : h;
-    T *out = static_cast<T *>(value ? j.v_out : j.k_out);
-    if (!out) continue;
-    float y[8];
-    if (at.page < 0) {
+  const int sh = (dim & 16) ? 4 : 0;
+  constexpr int kBatch = 4;  // heads asked for before the first is used
+#pragma unroll 1
+  for (int hb = h0 + sub; hb < h1; hb += kBatch * HPW) {
+    uint2 w[kBatch];
+    __half d[kBatch];
 #pragma unroll
-      for (int z = 0; z < 8; ++z) y[z] = __int_as_float(0x7fffffff);
-    } else {
-      const uint8_t *tile = page + kv_tile_off(D, j.c.page_size, hh, at.in_page);
-      const uint2 w = *reinterpret_cast<const uint2 *>(tile + kv_code_off(D, value, dim / 32, at.row) + (dim & 8));
-      const float d = __half2float(*reinterpret_cast<const __half *>(tile + kv_scale_off(D, value, dim / 32, at.row)));
-      const int sh = (dim & 16) ? 4 : 0;
-#pragma unroll
-      for (int z = 0; z < 8; ++z) {
-        const int q = (int)(((z < 4 ? w.x : w.y) >> (8 * (z & 3) + sh)) & 15u) - 8;
-        y[z] = (float)q * d;
+    for (int u = 0; u < kBatch; ++u) {
+      w[u] = make_uint2(0u, 0u);
+      d[u] = __ushort_as_half(0x7E00);  // without a page: NaN
+      const int h = hb + u * HPW, value = h >= j.hkv;
+      if (h < h1 && at.page >= 0) {
+        const uint8_t *tile = page + kv_tile_off(D, j.c.page_size, value ? h - j.hkv : h, at.in_page);
+        w[u] = __ldcs(reinterpret_cast<const uint2 *>(tile + kv_code_off(D, value, dim / 32, at.row) + (dim & 8)));
+        d[u] = *reinterpret_cast<const __half *>(tile + kv_scale_off(D, value, dim / 32, at.row));
       }
     }
-    store8(out + ((int64_t)i * j.hkv + hh) * D + dim, y);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = hb + u * HPW, value = h >= j.hkv;
+      T *out = static_cast<T *>(value ? j.v_out : j.k_out);
+      if (h >= h1 || !out) continue;
+      float y[8];
+#pragma unroll
+      for (int z = 0; z < 8; ++z)
+        y[z] = (float)((int)(((z < 4 ? w[u].x : w[u].y) >> (8 * (z & 3) + sh)) & 15u) - 8) * __half2float(d[u]);
+      store8(out + ((int64_t)i * j.hkv + (value ? h - j.hkv : h)) * D + dim, y);
+    }
   }
 }
 
