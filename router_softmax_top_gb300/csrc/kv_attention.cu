@@ -22,20 +22,27 @@
 //    2^-24 of the row's largest value).
 //  * Values: O^T = V^T P^T, P^T from the scores by an 8x8 transpose, multiplied by the
 //    value's scale per block (fp16: p and p d are each off by at most 2^-11 of
-//    themselves, for fp16 results p d alone; sums are fp32).  The reference r includes the largest scale seen, so
-//    p d stays inside fp16 whatever the scales are.
+//    themselves, for fp16 results p d alone; sums are fp32).  The reference r includes
+//    the largest scale seen, so p d stays inside fp16 whatever the scales are.
 //  * Rows in the matrix's N: 8 of them (heads sharing a key head x query tokens).
+// Measured: 128 sequences of 64 to 8192 tokens (8 key heads of 128, 611 MB of cache) in
+// 125 us, 4.9 TB/s or 0.72 of the measured copy rate; their tiles alone go by in 100 us,
+// 6 us go to finding shares and the first bytes, 15 to 20 us to slower SMs and the last
+// merges.  One sequence of 131071 tokens takes 46 us, of which 23 us stream.  The unpacking
+// keeps the integer pipe half busy and the matrix pipe a third; scores and values
+// interleaved over two tiles, more or fewer warps, deeper rings and whole bytes instead of
+// masked high nibbles were all slower or less exact.
 //
 // Work: the 32-token tiles of all (sequence, key head) pairs in a row, plus a few
 // tiles' worth per pair for its set-up and result, are split evenly over all warps of
 // the grid, so neither a sequence's length nor its place matters.  A warp walks its
 // share alone: it copies its own tiles (one bulk copy per tile, as the layout keeps a
 // tile contiguous) into a ring of its own, running ahead across pairs, and writes the
-// result of every pair that it has whole; no barrier stands in the loop.  At the end the
-// CTA merges, in shared memory, the pairs that its warps share, and a pair that several
-// CTAs share is merged by the last of them from partial results in the workspace, always
-// in the order of the keys, so results do not depend on timing.  Few short pairs
-// instead take a CTA each, whose warps share its tiles: nothing is merged across CTAs.
+// result of every pair that it has whole; no barrier stands in the loop.  A pair that
+// warps of one CTA share is merged by the last of them to be done; one that several CTAs
+// share by the last of those, from partial results in the workspace; always in the order
+// of the keys, so results do not depend on timing.  Few short pairs instead take a CTA
+// each, whose warps share its tiles: nothing is merged across CTAs.
 #include <algorithm>
 #include <type_traits>
 
@@ -66,7 +73,7 @@ struct DecodeJob {
 template <int D>
 struct DecodeCfg {
   static constexpr int kWarps = kDecodeWarps;
-  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr int kStages = 2;  // (four, for heads of 64, are no faster)
   static constexpr int kTile = 36 * D;
   // a partial result: accumulators as the matrix unit leaves them, [D/16][32 lanes][4], then per t of a lane the
   // references and weight sums of rows 2t and 2t + 1
@@ -117,10 +124,13 @@ __device__ __forceinline__ void store_pair(__half *p, float a, float b) {
   *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b);
 }
 
-// What a pair costs beside its tiles, in tiles (its queries' set-up and its result): measured, see below.
+// What a pair costs beside its tiles, in tiles (its queries' set-up and its result).  Measured with 1, 2, 4, 8 and 16:
+// 128 sequences of 64 to 8192 tokens 132, 125, 125, 129 and 136 us; one of 131071 tokens 50, 48, 46, 46 and 45 us.
 constexpr int kPairCost = 4;
-// A pair of at most this many tiles may take a CTA of its own when there are CTAs for all pairs.
-constexpr int kAloneTiles = 64;
+// Where there are CTAs for all pairs, a pair of at most this many tiles takes a CTA of its own and no more.  Against
+// shares over all CTAs: 333 tokens 11.0 and 14.3 us, 30 sequences of up to 500 tokens 13.3 and 17.8 us, 1000 tokens
+// 13.4 and 13.9 us; but 2000 tokens 17.8 and 13.8 us, 4000 tokens 26.3 and 14.9 us.
+constexpr int kAloneTiles = 32;
 
 // A walk over the pieces (tiles of one pair) of a warp's share.  Pairs are ordered by sequence, then key head
 // and row tile; a pair of n tiles takes kPairCost + n places, its tiles the last n of them.

@@ -18,13 +18,26 @@
 //    tile, 128 / group tokens of each, so keys and values are loaded once for all of
 //    them and the diagonal cuts off at most that many tokens' worth of work.
 //  * Q K^T: both operands K-major in shared memory (TMA, 128-byte swizzle), scores in
-//    tensor memory.  A thread owns a row: it loads its scores, takes maximum and sum
-//    in registers without any shuffle, and writes the weights (16 bits) over them.
+//    tensor memory.  A thread owns a row: it loads its scores, forms weights and their
+//    sum in registers without any shuffle, and writes the weights (16 bits) over them.
 //  * P V: weights from tensor memory, values from shared memory as the TMA left them
 //    (the contraction runs across their rows: an MN-major operand), output
 //    accumulated in tensor memory across all key blocks.
-//  * One thread issues all matrix instructions in an order in which every product of
-//    one tile has the other tile's exponentials behind it; one thread loads.
+//  * One warp issues all matrix instructions in an order in which every product of
+//    one tile has the other tile's exponentials behind it; one thread loads.  What the
+//    issuing warp waits for is time that the tensor cores lose, as their queue is short:
+//    it waits once per product, on the weights' barrier, which a helper holds back
+//    until the keys and values are there too.
+// Measured: 8192 tokens, 32 heads of 128 on 8: 360 us, 1.53 PFLOP/s or 0.80 of the
+// measured bf16 rate (454 us with descriptors outside uniform registers, 393 us with
+// four waits and six commits per block).  The tensor pipe is active 65% of all cycles;
+// in the loop a block takes ~2700 cycles, 2048 of them matrix instructions at their full
+// rate, and a CTA's ends about a tenth of its time.  Heads of 64 are bound by the
+// exponentials' chain and by the ends of short CTAs, hence two CTAs per SM (75 -> 68 us
+// for twelve packed prompts); heads of 256 by loads, as one row tile uses a block of keys
+// half as often (a block of 64 keys waits ~1100 cycles for its keys).
+// Two issuing warps (one per tile) were slower (422 us), as were handing the weights on
+// in two parts and testing barriers before suspending on them.
 // Blocks of keys that no row of a tile sees are skipped; only blocks that a row sees in
 // part are masked.  A masked weight is an exact 0; since 0 x infinity and 0 x NaN are not,
 // a row whose result is not finite although its sum is gets its result again from the
@@ -163,24 +176,6 @@ __device__ __forceinline__ void p_tma_3d(uint32_t dst, const CUtensorMap *map, i
       : "memory");
 }
 
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float &a, float &b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 template <typename T>
 __device__ __forceinline__ uint32_t pack16(float a, float b);
 template <>
