@@ -127,10 +127,12 @@ __device__ __forceinline__ void store_pair(__half *p, float a, float b) {
 // What a pair costs beside its tiles, in tiles (its queries' set-up and its result).  Measured with 1, 2, 4, 8 and 16:
 // 128 sequences of 64 to 8192 tokens 132, 125, 125, 129 and 136 us; one of 131071 tokens 50, 48, 46, 46 and 45 us.
 constexpr int kPairCost = 4;
-// Where there are CTAs for all pairs, a pair of at most this many tiles takes a CTA of its own and no more.  Against
-// shares over all CTAs: 333 tokens 11.0 and 14.3 us, 30 sequences of up to 500 tokens 13.3 and 17.8 us, 1000 tokens
-// 13.4 and 13.9 us; but 2000 tokens 17.8 and 13.8 us, 4000 tokens 26.3 and 14.9 us.
-constexpr int kAloneTiles = 32;
+// Where there are CTAs for all pairs, a pair takes a CTA of its own and no more if its longest warp then has at most
+// this many tiles more than with even shares, which the merges across CTAs cost.  A CTA per pair against shares: 333
+// tokens 11.0 and 14.3 us, 1000 tokens 13.4 and 13.9 us, 32 sequences of 1024 tokens of 64 (256 pairs) 13.2 and 17.5 us,
+// 8 of 1000 (64 pairs) 13.9 and 15.4 us, 8 of 2000 18.3 and 18.2 us; but one of 2000 17.8 and 13.8 us, of 4000 26.3 and
+// 14.9 us.
+constexpr int kAloneMore = 4;
 
 // A walk over the pieces (tiles of one pair) of a warp's share.  Pairs are ordered by sequence, then key head
 // and row tile; a pair of n tiles takes kPairCost + n places, its tiles the last n of them.
@@ -445,8 +447,8 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   total = __shfl_sync(0xffffffffu, before, 31);
   before -= mine;
   const int64_t pairs = (int64_t)j.c.n_seqs * heads;
-  const bool alone = most <= kAloneTiles && pairs <= (int64_t)gridDim.x;  // a CTA per pair
   const int64_t share = kv_div(total + (int64_t)gridDim.x * W - 1, (int64_t)gridDim.x * W);
+  const bool alone = pairs <= (int64_t)gridDim.x && most <= W * (share + kAloneMore);  // a CTA per pair
   Walk walk = {0, 0, 0, 0, 0, 0, 0, 0};
   bool work;
   if (alone) {
