@@ -285,24 +285,31 @@ __device__ __noinline__ void merge_by_cta(const DecodeJob &j, const SharedPair *
     const SharedPair &sp = sps[x];
     float *mine = j.part + ((size_t)blockIdx.x * (2 + W) + ((int)blockIdx.x == sp.cta0 ? 1 : 0)) * C::kPart;
     for (int f = tid; f < C::kOut / 4; f += kThreads) {
+      // all parts asked for before the first is used
+      float4 v[W], y[W];
       float r[2] = {-a_inf(), -a_inf()}, l[2] = {0.f, 0.f};
-      for (int w = sp.wa; w <= sp.wb; ++w) {
-        const float2 y = *reinterpret_cast<const float2 *>(warp_part<D>(j, sp, sm, in_heads, w) + C::kOut + 4 * t);
-        r[0] = fmaxf(r[0], y.x);
-        r[1] = fmaxf(r[1], y.y);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        y[w] = make_float4(-a_inf(), -a_inf(), 0.f, 0.f);
+        v[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w >= sp.wa && w <= sp.wb) {
+          const float *p = warp_part<D>(j, sp, sm, in_heads, w);
+          y[w] = *reinterpret_cast<const float4 *>(p + C::kOut + 4 * t);
+          v[w] = *reinterpret_cast<const float4 *>(p + 4 * f);
+        }
+        r[0] = fmaxf(r[0], y[w].x);
+        r[1] = fmaxf(r[1], y[w].y);
       }
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = sp.wa; w <= sp.wb; ++w) {
-        const float *p = warp_part<D>(j, sp, sm, in_heads, w);
-        const float4 y = *reinterpret_cast<const float4 *>(p + C::kOut + 4 * t);
-        const float4 v = *reinterpret_cast<const float4 *>(p + 4 * f);
-        const float w0 = part_weight(y.x, r[0]), w1 = part_weight(y.y, r[1]);
-        l[0] += part_sum(y.z, w0);
-        l[1] += part_sum(y.w, w1);
-        a.x += v.x * w0;
-        a.y += v.y * w1;
-        a.z += v.z * w0;
-        a.w += v.w * w1;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float w0 = part_weight(y[w].x, r[0]), w1 = part_weight(y[w].y, r[1]);
+        l[0] += part_sum(y[w].z, w0);
+        l[1] += part_sum(y[w].w, w1);
+        a.x += v[w].x * w0;
+        a.y += v[w].y * w1;
+        a.z += v[w].z * w0;
+        a.w += v[w].w * w1;
       }
       if (sp.cta0 == sp.cta1) {
         result(sp, f, a, r, l);
