@@ -3,8 +3,8 @@
 //
 // o_i = sum_j 2^(t_ij - r_i) v_j / sum_j 2^(t_ij - r_i), t = scale log2(e) q_i . k_j,
 // over the keys that row i sees, in one pass over the keys.  A block's weights are formed
-// with the reference as it stands; only if their sum exceeds 2^8 (no weight of a smaller
-// sum is larger) is the block's largest score looked for and the reference moved to it,
+// with the reference as it stands; only if their sum exceeds 2^8 (fp16: 2^14; no weight of
+// a smaller sum is larger) is the block's largest score looked for and the reference moved to it,
 // and the sums so far scale.
 //
 // Bound: the tensor cores, 4 D flops per (query, key) pair and head; beside them an
@@ -45,6 +45,7 @@
 // Every wait is bounded; when one gives up all roles stop, rows become NaN and the
 // status word says so.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.cuh"
 
@@ -540,6 +541,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     const int hi = live ? max(0, w.n_k - w.n_q + tok + 1) : 0;
     const int lo = j.window > 0 ? max(0, hi - j.window) : 0;
     const float c = j.scale * kLog2e;
+    // fp16 has few numbers far below 1, so its weights go up to 2^6 before the reference has to move, and to 2^14 then
+    constexpr float kBelow = std::is_same<T, __half>::value ? 6.f : 0.f;
+    constexpr float kMostSum = std::is_same<T, __half>::value ? 16384.f : 256.f;
     float m = live ? -a_inf() : 0.f, l = 0.f;  // reference (log2 units) and sum
     bool ok = true;
     const uint32_t o_col = tmem + lanes + C::kOCol + t * D;
@@ -579,14 +583,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         f2_unpack(f2_add(sum[0], sum[1]), a, b);
         return a + b;
       };
-      // The old reference first, without looking for the largest score: a sum of at most 2^8 says that no weight of it
-      // was larger.
+      // The old reference first, without looking for the largest score: a sum of at most kMostSum says that no weight of
+      // it was larger.
       float sum = 0.f, ref = m == -a_inf() ? 0.f : m;
       bool again = n == 0;
       if (!again) {
 #pragma unroll
         for (int x = 0; x < BK; x += 32) sum += weights(x, ref);
-        again = __any_sync(0xffffffffu, live && (m == -a_inf() || !(sum <= 256.f)));
+        again = __any_sync(0xffffffffu, live && (m == -a_inf() || !(sum <= kMostSum)));
       }
       if (again) {
         float top[4];
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         for (int x = 0; x < BK; x += 8)
 #pragma unroll
           for (int z = 0; z < 4; ++z) top[z] = fmaxf(top[z], fmaxf(s[x + z], s[x + 4 + z]));
-        const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c);  // c > 0
+        const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c - kBelow);  // c > 0
         p_st_wait();  // of the weights that are written again
         const float a = m == -a_inf() ? 0.f : a_exp2(m - m_new);
         m = m_new;
