@@ -154,6 +154,23 @@ int moe_prompt_attention(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_he
                          const int32_t *cu_q, const int32_t *cu_k, int32_t n_seqs, float scale, int32_t window,
                          void *out, float *lse, int32_t dtype, int32_t *status, void *cuda_stream);
 
+/*
+ * The same with a workspace, for calls whose rows are few and whose keys are many
+ * (a chunk of a long prompt): what would leave part of the GPU idle then shares its
+ * keys out over more of it.  moe_prompt_attention_workspace gives the bytes for a
+ * call's sizes, on the current device, 0 where a workspace would not be used.
+ * workspace: device memory of at least as many bytes, 256-byte aligned, its first
+ * MOE_KV_COUNTER_BYTES zero before its first use; every call leaves it ready for
+ * the next one on the same stream.  NULL: as moe_prompt_attention.
+ */
+int64_t moe_prompt_attention_workspace(int32_t n_q_tokens, int32_t n_q_heads, int32_t n_k_tokens, int32_t n_kv_heads,
+                                       int32_t head_dim, int32_t n_seqs, int32_t window);
+int moe_prompt_attention_shared(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads, const moe_tensor *k,
+                                const moe_tensor *v, int32_t n_k_tokens, int32_t n_kv_heads, int32_t head_dim,
+                                const int32_t *cu_q, const int32_t *cu_k, int32_t n_seqs, float scale, int32_t window,
+                                void *out, float *lse, int32_t dtype, int32_t *status, void *workspace,
+                                int64_t workspace_bytes, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

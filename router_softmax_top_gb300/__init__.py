@@ -44,7 +44,8 @@ EXPORTS = ("moe_cache_init", "moe_layer_forward", "moe_cache_sync", "moe_cache_s
            "moe_cache_destroy", "moe_strerror", "moe_expert_ffn_static", "moe_cache_usage",
            "moe_cache_state_size", "moe_cache_save_state", "moe_cache_load_state",
            "moe_kv_page_bytes", "moe_kv_append", "moe_kv_read", "moe_kv_attention_workspace",
-           "moe_kv_attention", "moe_prompt_attention")
+           "moe_kv_attention", "moe_prompt_attention",
+           "moe_prompt_attention_workspace", "moe_prompt_attention_shared")
 
 MOE_STATE_MAGIC = 0x53454F4D
 MOE_STATE_VERSION = 1
@@ -360,9 +361,9 @@ class MoECache:
 
 
 # ------------------------------------------------------- attention operators
-_ATTENTION = ("kv_append", "kv_read", "kv_attention", "kv_attention_workspace", "prompt_attention", "kv_pages",
-              "kv_page_bytes", "rope_table", "status_message", "MOE_KV_BAD_PAGE", "MOE_KV_BAD_LENGTH", "MOE_KV_BAD_POSITION",
-              "MOE_KV_TIMED_OUT")
+_ATTENTION = ("kv_append", "kv_read", "kv_attention", "kv_attention_workspace", "prompt_attention",
+              "prompt_attention_workspace", "kv_pages", "kv_page_bytes", "rope_table", "status_message", "MOE_KV_BAD_PAGE",
+              "MOE_KV_BAD_LENGTH", "MOE_KV_BAD_POSITION", "MOE_KV_TIMED_OUT", "MOE_KV_COUNTER_BYTES")
 
 
 def __getattr__(name):

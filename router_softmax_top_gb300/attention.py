@@ -61,6 +61,10 @@ def _lib():
         L.moe_kv_attention_workspace.argtypes = [i32, i32, i32, i32]
         L.moe_kv_attention.argtypes = [vp, vp, vp, i32, i32, f32, i32, vp, vp, i32, vp, i64, vp]
         L.moe_prompt_attention.argtypes = [vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, i32, f32, i32, vp, vp, i32, vp, vp]
+        L.moe_prompt_attention_workspace.restype = i64
+        L.moe_prompt_attention_workspace.argtypes = [i32] * 7
+        L.moe_prompt_attention_shared.argtypes = [vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, i32, f32, i32, vp, vp, i32, vp,
+                                                  vp, i64, vp]
         _bound = L
     return _bound
 
@@ -224,6 +228,8 @@ def kv_read(pages, page_table, starts, cu_tokens, n_tokens, *, page_size, n_kv_h
 
 
 _workspaces = {}
+# prompts of at most so many keys or of more rows (tokens times heads) never use a workspace
+_FEW_KEYS, _FEW_ROWS = 256, 131072
 
 
 def kv_attention_workspace(n_q_heads, n_kv_heads, head_dim, q_tokens=1, device="cuda"):
@@ -231,19 +237,27 @@ def kv_attention_workspace(n_q_heads, n_kv_heads, head_dim, q_tokens=1, device="
     n = int(_lib().moe_kv_attention_workspace(n_q_heads, n_kv_heads, head_dim, q_tokens))
     if n <= 0:
         _refuse("kv_attention_workspace: unsupported sizes", MOE_ERR_UNSUPPORTED)
+    return _zero_counters(n, device)
+
+
+def _zero_counters(n, device):
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     ws[:MOE_KV_COUNTER_BYTES].zero_()
     return ws
 
 
-def _workspace(hq, hkv, d, q_tokens, handle, dev):
+def _kept(key, make):
     # one per stream, as calls on one stream follow each other; a capture gets its own, which its graph keeps
     if torch.cuda.is_current_stream_capturing():
-        return kv_attention_workspace(hq, hkv, d, q_tokens, _cuda(dev))
-    ws = _workspaces.get((dev, handle, d))
+        return make()
+    ws = _workspaces.get(key)
     if ws is None:
-        ws = _workspaces[dev, handle, d] = kv_attention_workspace(hq, hkv, d, q_tokens, _cuda(dev))
+        ws = _workspaces[key] = make()
     return ws
+
+
+def _workspace(hq, hkv, d, q_tokens, handle, dev):
+    return _kept((dev, handle, d), lambda: kv_attention_workspace(hq, hkv, d, q_tokens, _cuda(dev)))
 
 
 def kv_attention(q, pages, page_table, seq_lens, *, page_size, n_kv_heads, q_tokens=1, scale=None, window=0,
@@ -282,14 +296,23 @@ def kv_attention(q, pages, page_table, seq_lens, *, page_size, n_kv_heads, q_tok
     return _call(stream, dev, run)
 
 
-def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_lse=False, out=None, status=None,
-                     stream=None):
+def prompt_attention_workspace(n_q_tokens, n_q_heads, n_k_tokens, n_kv_heads, head_dim, n_seqs, window=0, device="cuda"):
+    """A workspace for prompt_attention, to be used by one stream (or one captured graph) at a time; None where a call
+    of these sizes would not use one."""
+    n = int(_lib().moe_prompt_attention_workspace(n_q_tokens, n_q_heads, n_k_tokens, n_kv_heads, head_dim, n_seqs, window))
+    return _zero_counters(n, device) if n > 0 else None
+
+
+def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_lse=False, out=None, workspace=None,
+                     status=None, stream=None):
     """Causal attention over packed prompts (moe_prompt_attention).
 
     q [n_q_tokens, n_q_heads, head_dim], k and v [n_k_tokens, n_kv_heads, head_dim], bfloat16 or float16;
     cu_q, cu_k int32 [n_seqs + 1] (cu_k None: cu_q).  With more keys than queries a sequence's queries are its
     last tokens.  window > 0: a token sees itself and the window - 1 tokens before it.  Returns q's shape, and
-    the log of the sums of exponentials (fp32 [n_q_tokens, n_q_heads]) with return_lse."""
+    the log of the sums of exponentials (fp32 [n_q_tokens, n_q_heads]) with return_lse.  Few queries of many keys
+    use a workspace: without `workspace` a module-level one per stream (inside a graph capture: one of the capture's
+    own); graphs that may run at the same time need their own."""
     dev, dtype = _device(q), q.dtype
     if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
         _refuse("q must be bfloat16 or float16 [tokens, heads, head_dim]", MOE_ERR_UNSUPPORTED)
@@ -304,13 +327,23 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_l
     pq = _index(cu_q, "cu_q", n_cu, dev)
     pk = pq if cu_k is None else _index(cu_k, "cu_k", n_cu, dev)
     word = _word(status, dev)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        _refuse("workspace must be a contiguous tensor on the GPU")
 
     def run(handle):
         o = _output(out, "out", shape, dtype, dev)
         lse = torch.empty((n, hq), dtype=torch.float32, device=_cuda(dev)) if return_lse else None
-        rc = _lib().moe_prompt_attention(tq, n, hq, tk, tv, nk, hkv, d, pq, pk, n_cu - 1,
-                                         d ** -0.5 if scale is None else scale, window, o.data_ptr(),
-                                         lse.data_ptr() if return_lse else None, _DTYPES[dtype], word, handle)
+        L, ws = _lib(), workspace
+        if ws is None and nk > _FEW_KEYS and n * hq <= _FEW_ROWS:
+            # (its size depends on the head size alone, once it is not 0)
+            if L.moe_prompt_attention_workspace(n, hq, nk, hkv, d, n_cu - 1, window) > 0:
+                ws = _kept((dev, handle, "prompt", d),
+                           lambda: prompt_attention_workspace(n, hq, nk, hkv, d, n_cu - 1, window, _cuda(dev)))
+        rc = L.moe_prompt_attention_shared(tq, n, hq, tk, tv, nk, hkv, d, pq, pk, n_cu - 1,
+                                           d ** -0.5 if scale is None else scale, window, o.data_ptr(),
+                                           lse.data_ptr() if return_lse else None, _DTYPES[dtype], word,
+                                           None if ws is None else ws.data_ptr(),
+                                           0 if ws is None else ws.numel() * ws.element_size(), handle)
         if rc:
             _check(rc, "moe_prompt_attention")
         return (o, lse) if return_lse else o

@@ -36,6 +36,7 @@
 // exponentials' chain and by the ends of short CTAs, hence two CTAs per SM (75 -> 68 us
 // for twelve packed prompts); heads of 256 by loads, as one row tile uses a block of keys
 // half as often (a block of 64 keys waits ~1100 cycles for its keys).
+// Few rows with many keys do not fill the GPU: their keys are shared out over several CTAs (below).
 // Two issuing warps (one per tile) were slower (422 us), as were handing the weights on
 // in two parts and testing barriers before suspending on them.
 // Blocks of keys that no row of a tile sees are skipped; only blocks that a row sees in
@@ -45,6 +46,7 @@
 // Every wait is bounded; when one gives up all roles stop, rows become NaN and the
 // status word says so.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -67,7 +69,26 @@ struct PromptJob {
   void *out;
   float *lse;
   int32_t *status;
+  // for sharing out keys (see kMinPart): CTAs that run at once, or 0 for no sharing; most parts of a group
+  int slots, most_parts;
+  float *part;      // [slots]: sums of a part
+  uint32_t *count;  // [slots]: parts of a group that are done
 };
+
+// Where a call's tile groups leave half the GPU idle or more, each group's keys are shared out over as many CTAs as there
+// is room for, and the last one done joins the parts.  It reads a part in about the time of a block, so there are no more
+// parts than a part has blocks.  Whole and shared, 32 heads of 128 on 8: 16 tokens after 1000 16.0 and 15.4 us, 37 after
+// 2000 29 and 21, 512 after 4096 58 and 43, 256 after 60,000 650 and 186, 5 after 100,000 980 and 77 us.
+// A part has at least kMinPart blocks (parts of 4 blocks of 64, 512 tokens: heads of 64 17.4 us, whole 13.8; heads of 256
+// 22.3, whole 14.2), and, where two parts are on the same SM (heads of 64), at least kMinPair (2 of 8, 1024 tokens: 24.0,
+// whole 20.6; 2 of 16, 1024 after 1024: 32.8, whole 33.1; 2 of 24, 16 sequences of 7 after 3000: 33.1, whole 41.6).
+// Groups of a last, partly filled wave are not shared: 300 tokens after 3000 of 4 sequences, window 1024, took 43.8 us so
+// and 41.2 whole, 777 and 1024 after 4096 of heads of 256 74.3 and 76.2.
+template <int D>
+constexpr int kMinPart = D == 128 ? 4 : 6;
+constexpr int kMinPair = 12;
+constexpr int kMostParts = 32;
+constexpr int kMaxSplitSeqs = 32;  // (those whose groups are counted by one warp at once)
 
 template <int D>
 struct PromptCfg {
@@ -77,6 +98,8 @@ struct PromptCfg {
   static constexpr int kStages = D == 64 ? 4 : 2;      // of keys, and of values
   static constexpr uint32_t kQBytes = kTileRows * D * 2, kKBytes = kBK * D * 2;
   static constexpr uint32_t kQOff = 0, kKOff = kNQ * kQBytes, kVOff = kKOff + kStages * kKBytes;
+  // a part of a shared group: its sums as [tile][D / 4][128 rows] of 4, then per row its reference and weight sum
+  static constexpr size_t kSums = (size_t)kNQ * kTileRows * D, kPart = kSums + 2 * kNQ * kTileRows;
   static constexpr size_t kSmem = kVOff + kStages * kKBytes + 1024;
   // tensor memory: score buffers, then outputs
   static constexpr uint32_t kOCol = kBuf * kBK;
@@ -198,6 +221,10 @@ struct PromptWork {
   int q0, n_q, k0, n_k;    // tokens of the sequence
   int bad_k;               // the key offsets make no sense
   int first_token;         // of tile 0, within the sequence
+  int kvh;
+  int unit, units;         // number of this group and key head, of how many (if keys are shared out)
+  int part, parts;         // this CTA's part of the keys, of how many
+  int begin, end;          // its blocks, if there are several
 };
 
 // Key blocks [jb, je) that a tile's rows see, and the range [whole_lo, whole_hi) that all its rows see.
@@ -220,6 +247,66 @@ __device__ __forceinline__ TileRange tile_range(const PromptJob &j, const Prompt
   r.jb = lo / BK;
   r.je = (hi + BK - 1) / BK;
   return r;
+}
+
+// The blocks of a shared group's part, of at most `parts`.
+template <int D>
+__device__ __noinline__ void share_keys(const PromptJob &j, PromptWork &w, int parts) {
+  using C = PromptCfg<D>;
+  int lo = 0x7fffffff, hi = 0;
+  for (int t = 0; t < C::kNQ; ++t) {
+    const TileRange r = tile_range<C::kBK>(j, w, t);
+    if (r.je <= r.jb) continue;
+    lo = min(lo, r.jb);
+    hi = max(hi, r.je);
+  }
+  const int n = max(0, hi - lo);
+  parts = max(1, min(min(parts, n / kMinPart<D>), (int)sqrtf((float)n)));
+  const int sms = j.slots / C::kCtas;
+  if (C::kCtas > 1 && n < kMinPair * parts) parts = min(parts, max(1, sms / w.units));
+  w.parts = parts;
+  if (w.part >= parts) {
+    w.seq = -1;
+  } else {
+    w.begin = lo + (int)((int64_t)n * w.part / parts);
+    w.end = lo + (int)((int64_t)n * (w.part + 1) / parts);
+  }
+}
+
+// A part's sums to the workspace; whether it was the last of the group.
+template <int D>
+__device__ __noinline__ bool write_part(const PromptJob &j, const PromptWork &w, uint32_t o_col, bool some, bool live,
+                                        float m, float l, int *last, uint32_t *redo) {
+  using C = PromptCfg<D>;
+  float *mine = j.part + (size_t)blockIdx.x * C::kPart;
+  const int tid = threadIdx.x, t = tid / kTileRows, r = tid % kTileRows;
+  if (live) reinterpret_cast<float2 *>(mine + C::kSums)[t * kTileRows + r] = make_float2(m, l);
+#pragma unroll 1
+  for (int x = 0; x < D; x += 32) {
+    float o[32];
+    if (some) {
+      p_ld32(o_col + x, o);
+      p_ld_wait();
+    } else {
+#pragma unroll
+      for (int z = 0; z < 32; ++z) o[z] = 0.f;
+    }
+    if (live)
+#pragma unroll
+      for (int z = 0; z < 32; z += 4)
+        reinterpret_cast<float4 *>(mine)[(size_t)(t * (D / 4) + (x + z) / 4) * kTileRows + r] =
+            make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
+  }
+  __threadfence();
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kSoftWarps) : "memory");
+  if (tid == 0) {
+    *last = atomicAdd(j.count + w.unit, 1u) == (uint32_t)w.parts - 1;
+    if (*last) j.count[w.unit] = 0;  // for the next call
+  }
+  if (tid < C::kSoftWarps) redo[tid] = 0;
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kSoftWarps) : "memory");
+  __threadfence();
+  return *last != 0;
 }
 
 // One row's output from the keys it sees, one by one: the warp's lanes hold D / 32 values each.
@@ -248,6 +335,92 @@ __device__ __noinline__ void row_by_keys(const PromptJob &j, int q_tok, int head
   for (int i = 0; i < N; ++i) out[lane * N + i] = T(acc[i] / sum);
 }
 
+// The results of a shared group from its parts, in the order of the keys.  A warp takes 32 rows, a lane each, and Q quads
+// of their columns, two parts at a time: enough loads in flight for what a trip to the L2 takes, however few rows there
+// are.  `redo` (0 before): per 32 rows, those whose result takes a second look.
+template <int D, typename T>
+__device__ __noinline__ void join_parts(const PromptJob &j, const PromptWork &w, uint32_t *redo) {
+  using C = PromptCfg<D>;
+  const float *first = j.part + (size_t)w.unit * C::kPart;
+  const size_t step = (size_t)w.units * C::kPart;  // from part to part
+  const int parts = w.parts;
+  constexpr int Q = D / 16, kItems = D / 4 / Q;  // (four items per 32 rows, as many as there are registers for)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows0 = min(j.tile_tokens, w.n_q - w.first_token) * j.group;
+  const int rows1 = C::kNQ == 1 ? 0 : max(0, min(j.tile_tokens, w.n_q - w.first_token - j.tile_tokens)) * j.group;
+  const int many0 = (rows0 + 31) / 32, many = many0 + (rows1 + 31) / 32;
+  for (int item = warp; item < many * kItems; item += C::kSoftWarps) {
+    const int rows32 = item / kItems, q0 = item % kItems * Q;
+    const int t = rows32 >= many0, r = 32 * (rows32 - (t ? many0 : 0)) + lane;
+    const bool live = r < (t ? rows1 : rows0);
+    const size_t at_ml = C::kSums + 2 * (t * kTileRows + r), at_q = 4 * ((size_t)(t * (D / 4) + q0) * kTileRows + r);
+    float m = -a_inf(), l = 0.f, acc[4 * Q];
+#pragma unroll
+    for (int x = 0; x < 4 * Q; ++x) acc[x] = 0.f;
+#pragma unroll 1
+    for (int y = 0; y < parts; y += 2) {
+      float2 ml[2];
+      float4 v[2][Q];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        ml[z] = make_float2(-a_inf(), 0.f);
+        if (live && y + z < parts) {
+          const float *p = first + (y + z) * step;
+          ml[z] = __ldcg(reinterpret_cast<const float2 *>(p + at_ml));
+#pragma unroll
+          for (int x = 0; x < Q; ++x) v[z][x] = __ldcg(reinterpret_cast<const float4 *>(p + at_q) + x * kTileRows);
+        }
+      }
+      const float top = fmaxf(m, fmaxf(ml[0].x, ml[1].x)), a = m == -a_inf() ? 0.f : a_exp2(m - top);
+      m = top;
+      l *= a;
+#pragma unroll
+      for (int x = 0; x < 4 * Q; ++x) acc[x] *= a;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        if (ml[z].y == 0.f) continue;  // the row sees none of the part's keys: its sums may be 0 x infinity
+        const float b = ml[z].x == -a_inf() ? 0.f : a_exp2(ml[z].x - top);
+        l += ml[z].y != ml[z].y ? ml[z].y : ml[z].y * b;
+#pragma unroll
+        for (int x = 0; x < Q; ++x) {
+          acc[4 * x] = fmaf(v[z][x].x, b, acc[4 * x]);
+          acc[4 * x + 1] = fmaf(v[z][x].y, b, acc[4 * x + 1]);
+          acc[4 * x + 2] = fmaf(v[z][x].z, b, acc[4 * x + 2]);
+          acc[4 * x + 3] = fmaf(v[z][x].w, b, acc[4 * x + 3]);
+        }
+      }
+    }
+    const int64_t at = (int64_t)(w.q0 + w.first_token + t * j.tile_tokens + r / j.group) * j.hq + w.kvh * j.group + r % j.group;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    bool finite = true;
+    uint32_t p[2 * Q];
+#pragma unroll
+    for (int x = 0; x < 2 * Q; ++x) {
+      finite = finite && fabsf(acc[2 * x]) < a_inf() && fabsf(acc[2 * x + 1]) < a_inf();
+      p[x] = l == 0.f ? 0u : pack16<T>(acc[2 * x] * inv, acc[2 * x + 1] * inv);
+    }
+    if (live) {
+      uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(j.out) + at * D + 4 * q0);
+#pragma unroll
+      for (int x = 0; x < Q / 2; ++x) o[x] = make_uint4(p[4 * x], p[4 * x + 1], p[4 * x + 2], p[4 * x + 3]);
+      if (q0 == 0 && j.lse) j.lse[at] = l == 0.f ? -a_inf() : (m + log2f(l)) * kLn2;
+    }
+    const uint32_t again = __ballot_sync(0xffffffffu, live && !finite && l > 0.f && l < a_inf());
+    if (again && lane == 0) atomicOr(&redo[rows32], again);
+  }
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kSoftWarps) : "memory");
+  for (int rows32 = warp; rows32 < many; rows32 += C::kSoftWarps)
+    for (uint32_t again = redo[rows32]; again; again &= again - 1) {
+      const int t = rows32 >= many0, r = 32 * (rows32 - (t ? many0 : 0)) + __ffs(again) - 1;
+      const int tok = w.first_token + t * j.tile_tokens + r / j.group, head = w.kvh * j.group + r % j.group;
+      float m = -a_inf();
+      for (int y = 0; y < parts; ++y) m = fmaxf(m, __ldcg(first + y * step + C::kSums + 2 * (t * kTileRows + r)));
+      const int hi = max(0, w.n_k - w.n_q + tok + 1);
+      row_by_keys<D, T>(j, w.q0 + tok, head, w.k0, j.window > 0 ? max(0, hi - j.window) : 0, hi, m,
+                        static_cast<T *>(j.out) + ((int64_t)(w.q0 + tok) * j.hq + head) * D);
+    }
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     prompt_attention_kernel(const __grid_constant__ PromptMaps maps, const PromptJob j) {
@@ -256,7 +429,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
   extern __shared__ __align__(1024) unsigned char sm_raw[];
   __shared__ uint64_t q_full, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], pv_done[NQ], k_first, done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_fail;
+  __shared__ int s_fail, s_last;
+  __shared__ uint32_t s_redo[C::kSoftWarps];  // (a warp has 32 rows)
   __shared__ PromptWork s_work;
   const uint32_t sm = (a_smem(sm_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -288,8 +462,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     // packed prompts of 3 to 1500 tokens: 68 us in the order of the sequences, 60 us so); of more, sequence by
     // sequence, as finding a group's place would take a CTA longer than it saves.
     const int per = NQ * j.tile_tokens;
-    const int mine = (int)(blockIdx.x / j.hkv);
-    const bool by_level = j.n_seqs <= 32;
+    int unit = blockIdx.x, of = 0, part = 0, parts = 1;  // unit: group and key head
+    const bool by_level = j.n_seqs <= kMaxSplitSeqs;
     int before = 0, seq = -1, group = 0, a = 0, b = 0, c = 0, d = 0, at = 0;
     for (int base = 0; base < j.n_seqs; base += 32) {
       const int s = base + lane;
@@ -307,8 +481,18 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
       }
       if (seq >= 0) continue;  // (the first CTA only: it looks at all offsets)
       bool hit = false;
+      auto beyond = [&](int level) { return (int)__reduce_add_sync(0xffffffffu, max(0, n - level)); };
+      if (j.slots > 0) {  // (then there are at most kMaxSplitSeqs sequences)
+        const int units = beyond(0) * j.hkv;
+        if (units > 0 && 2 * units <= j.slots) {
+          parts = min(j.slots / units, j.most_parts);
+          part = unit / units;  // (first parts first: not all groups may have more)
+          unit %= units;
+          of = units;
+        }
+      }
+      const int mine = unit / j.hkv;
       if (by_level) {
-        auto beyond = [&](int level) { return (int)__reduce_add_sync(0xffffffffu, max(0, n - level)); };
         int lo = 0, hi = __reduce_max_sync(0xffffffffu, n);
         if (j.n_seqs == 1) {
           lo = n - 1 - mine;
@@ -343,12 +527,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         if (lane == at) {
           const bool bad_k = c < 0 || d < c || d > j.n_k;
           if (bad_k && j.status) atomicOr(j.status, MOE_KV_BAD_LENGTH);
-          s_work = {seq, a, b - a, bad_k ? 0 : c, bad_k ? 0 : d - c, bad_k, group * per};
+          PromptWork w = {seq, a, b - a, bad_k ? 0 : c, bad_k ? 0 : d - c, bad_k, group * per, unit % j.hkv, unit, of, part, 1, 0, 0};
+          if (parts > 1) share_keys<D>(j, w, parts);
+          s_work = w;
         }
         if (blockIdx.x != 0) break;
       }
     }
-    if (seq < 0 && lane == 0) s_work = {-1, 0, 0, 0, 0, 0, 0};
+    if (seq < 0 && lane == 0) s_work = {-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 1, 0, 0};
   }
   if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(a_smem(&s_tmem)), "r"(C::kTmemCols));
@@ -359,13 +545,17 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
   p_fence_after();
   const uint32_t tmem = s_tmem;
   const PromptWork w = s_work;
-  const int kvh = (int)(blockIdx.x % j.hkv);
+  const int kvh = w.kvh;
 
   TileRange tr[NQ];
   int J0 = 0x7fffffff, J1 = 0;
 #pragma unroll
   for (int t = 0; t < NQ; ++t) {
     tr[t] = w.seq < 0 ? TileRange{0, 0, 0, 0} : tile_range<BK>(j, w, t);
+    if (w.parts > 1) {
+      tr[t].jb = max(tr[t].jb, w.begin);
+      tr[t].je = min(tr[t].je, w.end);
+    }
     if (tr[t].je > tr[t].jb) {
       J0 = min(J0, tr[t].jb);
       J1 = max(J1, tr[t].je);
@@ -644,11 +834,15 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
       ok = __all_sync(0xffffffffu, a_mbar_wait(&pv_done[t], NQ == 1 ? (uint32_t)(n_mine - 1) & 1u : 0u, &s_fail));
     if (!ok) s_fail = 1;
     p_fence_after();
-    if (w.seq >= 0) {
+    const bool some = n_mine > 0 && ok;
+    if (w.seq >= 0 && w.parts > 1) {
+      // a part of a shared group; the last one done joins all of them
+      if (write_part<D>(j, s_work, o_col, some, live, m, ok ? l : a_nan(), &s_last, s_redo))
+        join_parts<D, T>(j, s_work, s_redo);
+    } else if (w.seq >= 0) {
       const int64_t at = (int64_t)(w.q0 + tok) * j.hq + head;
       T *out = static_cast<T *>(j.out) + at * D;
       if (!ok || w.bad_k) l = a_nan();
-      const bool some = n_mine > 0 && ok;
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       bool finite = true;
 #pragma unroll 1
@@ -724,6 +918,30 @@ bool encode_map(CUtensorMap *m, const moe_tensor &t, int tokens, int heads, int 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kMaxSlots = 1024;  // parts' counters are MOE_KV_COUNTER_BYTES
+static_assert(kMaxSlots * 4 <= MOE_KV_COUNTER_BYTES, "a counter per group");
+
+// CTAs that run at once, for heads of D.
+int prompt_slots(int D) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return std::min(kMaxSlots, sms * (D == 64 ? PromptCfg<64>::kCtas : 1));
+}
+size_t prompt_part_bytes(int D) {
+  return 4 * (D == 64 ? PromptCfg<64>::kPart : D == 128 ? PromptCfg<128>::kPart : PromptCfg<256>::kPart);
+}
+// Most parts that a tile group of a call can have: at most this many blocks of keys are seen by its rows.
+int prompt_most_parts(int n_k, int n_seqs, int group, int D, int window) {
+  if (n_seqs > kMaxSplitSeqs) return 1;
+  const int bk = D == 128 ? PromptCfg<128>::kBK : 64, per = (D == 256 ? 1 : 2) * (kTileRows / group);
+  const int64_t keys = window > 0 ? std::min<int64_t>(n_k, (int64_t)window + per) : n_k, blocks = keys / bk + 2;
+  return (int)std::max(1.0, std::min({(double)kMostParts, (double)(blocks / (D == 64 ? kMinPart<64> : D == 128 ? kMinPart<128> : kMinPart<256>)), std::sqrt((double)blocks)}));
+}
+
 template <int D, typename T>
 int launch_prompt(PromptJob j, int dtype, cudaStream_t st) {
   using C = PromptCfg<D>;
@@ -741,7 +959,9 @@ int launch_prompt(PromptJob j, int dtype, cudaStream_t st) {
   // at most this many tile groups: a sequence's last one may be partly filled
   const int64_t groups = j.n_q / per + std::min<int64_t>(j.n_seqs, j.n_q);
   if (groups * j.hkv > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  prompt_attention_kernel<D, T><<<(unsigned)(groups * j.hkv), C::kThreads, C::kSmem, st>>>(maps, j);
+  int64_t grid = groups * j.hkv;
+  if (grid < j.slots) grid = std::min<int64_t>(j.slots, grid * j.most_parts);
+  prompt_attention_kernel<D, T><<<(unsigned)grid, C::kThreads, C::kSmem, st>>>(maps, j);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -750,10 +970,30 @@ int launch_prompt(PromptJob j, int dtype, cudaStream_t st) {
 
 using namespace moe;
 
+MOE_API int64_t moe_prompt_attention_workspace(int32_t n_q_tokens, int32_t n_q_heads, int32_t n_k_tokens,
+                                               int32_t n_kv_heads, int32_t head_dim, int32_t n_seqs, int32_t window) {
+  if (n_q_tokens <= 0 || n_k_tokens <= 0 || n_seqs <= 0 || n_kv_heads <= 0 || n_q_heads <= 0 ||
+      n_q_heads % n_kv_heads || n_q_heads / n_kv_heads > 64 || window < 0 || !kv_sizes_ok(n_kv_heads, head_dim, kKvTile))
+    return 0;
+  if (prompt_most_parts(n_k_tokens, n_seqs, n_q_heads / n_kv_heads, head_dim, window) < 2) return 0;
+  const int slots = prompt_slots(head_dim), per = (head_dim == 256 ? 1 : 2) * (kTileRows * n_kv_heads / n_q_heads);
+  const int64_t units = (int64_t)((n_q_tokens + per - 1) / per) * n_kv_heads;  // at least
+  return 2 * units <= slots ? MOE_KV_COUNTER_BYTES + (int64_t)slots * (int64_t)prompt_part_bytes(head_dim) : 0;
+}
+
 MOE_API int moe_prompt_attention(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads, const moe_tensor *k,
                                  const moe_tensor *v, int32_t n_k_tokens, int32_t n_kv_heads, int32_t head_dim,
                                  const int32_t *cu_q, const int32_t *cu_k, int32_t n_seqs, float scale, int32_t window,
                                  void *out, float *lse, int32_t dtype, int32_t *status, void *cuda_stream) {
+  return moe_prompt_attention_shared(q, n_q_tokens, n_q_heads, k, v, n_k_tokens, n_kv_heads, head_dim, cu_q, cu_k, n_seqs,
+                                     scale, window, out, lse, dtype, status, nullptr, 0, cuda_stream);
+}
+
+MOE_API int moe_prompt_attention_shared(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads, const moe_tensor *k,
+                                        const moe_tensor *v, int32_t n_k_tokens, int32_t n_kv_heads, int32_t head_dim,
+                                        const int32_t *cu_q, const int32_t *cu_k, int32_t n_seqs, float scale,
+                                        int32_t window, void *out, float *lse, int32_t dtype, int32_t *status,
+                                        void *workspace, int64_t workspace_bytes, void *cuda_stream) {
   if (n_q_tokens < 0 || n_k_tokens < 0 || n_seqs < 0 || n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads ||
       window < 0 || !(scale > 0.f && scale <= 3.4e38f))
     return MOE_ERR_INVALID_ARG;
@@ -788,6 +1028,16 @@ MOE_API int moe_prompt_attention(const moe_tensor *q, int32_t n_q_tokens, int32_
   j.out = out;
   j.lse = lse;
   j.status = status;
+  if (workspace) {
+    const int64_t need = moe_prompt_attention_workspace(n_q_tokens, n_q_heads, n_k_tokens, n_kv_heads, head_dim, n_seqs, window);
+    if ((uintptr_t)workspace % 256 || workspace_bytes < need) return MOE_ERR_INVALID_ARG;
+    if (need > 0) {
+      j.slots = prompt_slots(head_dim);
+      j.most_parts = prompt_most_parts(n_k_tokens, n_seqs, group, head_dim, window);
+      j.count = static_cast<uint32_t *>(workspace);
+      j.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + MOE_KV_COUNTER_BYTES);
+    }
+  }
   cudaStream_t st = (cudaStream_t)cuda_stream;
   if (dtype == MOE_BF16)
     return head_dim == 64    ? launch_prompt<64, __nv_bfloat16>(j, dtype, st)

@@ -140,6 +140,89 @@ def test_what_a_row_does_not_see_does_not_reach_it(d, value):
     assert bool(((got[49:].float() - w[49:].float()).abs() <= near * (1 + w[49:].float().abs())).all())
 
 
+# Few rows with many keys: the keys of a tile are shared out over several CTAs, whose sums the last one joins (each join
+# rounds in fp32, 2^-24 per part and so within the 2^-12 above).
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,hq,hkv,lens,extra,window", [
+    (128, 8, 2, [5], 9000, 0),
+    (64, 6, 2, [37], 3000, 0),
+    (256, 4, 1, [1], 5001, 0),
+    (256, 16, 4, [130], 2000, 0),
+    (128, 4, 4, [300, 0, 2, 65], 1800, 0),
+    (64, 3, 1, [1, 90, 700], 2500, 1024),
+    (128, 7, 1, [33, 40], 4100, 1500),
+    (128, 64, 1, [9, 3], 3333, 0)])
+def test_keys_shared_out(d, dtype, hq, hkv, lens, extra, window):
+    keys = [n + extra if n else 0 for n in lens]
+    q, k, v = inputs(sum(lens), sum(keys), hq, hkv, d, DT[dtype], d + len(lens))
+    ws = moe.prompt_attention_workspace(sum(lens), hq, sum(keys), hkv, d, len(lens), window)
+    assert ws is not None                     # these sizes do share
+    a, la = check(q, k, v, lens, keys, window)
+    for own in (None, ws, ws):                # a result does not depend on which part is done last
+        b, lb = moe.prompt_attention(q, k, v, i32(cu_of(lens)), i32(cu_of(keys)), window=window, return_lse=True,
+                                     workspace=own)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    assert not bool(ws[:moe.MOE_KV_COUNTER_BYTES].any())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_shared_keys_that_a_row_does_not_see(d, value):
+    n, m = 40, 3000
+    q, k, v = inputs(n, m, 4, 2, d, torch.bfloat16, 11)
+    cu_q, cu_k = i32([0, n]), i32([0, m])
+    assert moe.prompt_attention_workspace(n, 4, m, 2, d, 1, 2000) is not None
+    clean = moe.prompt_attention(q, k, v, cu_q, cu_k, window=2000)
+    near = R.EPS[torch.bfloat16] * 4
+    k2, v2 = k.clone(), v.clone()
+    k2[:970], v2[:970] = value, value         # before the window of all rows from 9 on, in its first block
+    k2[m - 5:], v2[m - 5:] = value, value     # after all rows but the last five
+    got = moe.prompt_attention(q, k2, v2, cu_q, cu_k, window=2000)
+    assert bool(((got[9:n - 5].float() - clean[9:n - 5].float()).abs() <= near * (1 + clean[9:n - 5].float().abs())).all())
+    assert bool((~torch.isfinite(got[n - 5:].float())).all())
+    if value == float("inf"):                 # a seen infinity is an infinity
+        v2 = v.clone()
+        v2[2000, 0, 5] = value
+        got = moe.prompt_attention(q, k, v2, cu_q, cu_k)
+        assert bool(torch.isinf(got[:, :2, 5]).all()) and bool(torch.isfinite(got[:, :2, 6].float()).all())
+
+
+def test_shared_keys_in_graphs_and_streams():
+    n, m = 20, 4000
+    q, k, v = inputs(n, m, 8, 2, 128, torch.bfloat16, 12)
+    cu_q, cu_k = i32([0, n]), i32([0, m])
+    want = moe.prompt_attention(q, k, v, cu_q, cu_k)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = moe.prompt_attention(q, k, v, cu_q, cu_k, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        one = moe.prompt_attention(q, k, v, cu_q, cu_k)
+        two = moe.prompt_attention(one, k, v, cu_q, cu_k)
+    for _ in range(2):
+        q.mul_(0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(one, moe.prompt_attention(q, k, v, cu_q, cu_k))
+        assert torch.equal(two, moe.prompt_attention(one, k, v, cu_q, cu_k))
+
+
+def test_workspaces_that_are_refused():
+    n, m = 20, 4000
+    q, k, v = inputs(n, m, 8, 2, 128, torch.bfloat16, 12)
+    cu_q, cu_k = i32([0, n]), i32([0, m])
+    ws = moe.prompt_attention_workspace(n, 8, m, 2, 128, 1)
+    for bad in (ws[:-256], ws[128:], ws.cpu(), ws[::2]):
+        with pytest.raises(moe.MoeError):
+            moe.prompt_attention(q, k, v, cu_q, cu_k, workspace=bad)
+    # sizes that do not share need none: few keys, many rows, many sequences
+    assert moe.prompt_attention_workspace(n, 8, 200, 2, 128, 1) is None
+    assert moe.prompt_attention_workspace(1 << 20, 8, 1 << 20, 2, 128, 1) is None
+    assert moe.prompt_attention_workspace(n, 8, m, 2, 128, 33) is None
+
+
 def test_bad_offsets_are_reported():
     q, k, v = inputs(100, 100, 4, 2, 64, torch.bfloat16, 8)
     clean = moe.prompt_attention(q, k, v, i32([0, 40, 100]))

@@ -224,6 +224,16 @@ def test_bad_prompt_calls_are_refused(lib, change, code):
     assert _prompt(lib, **change) == code
 
 
+def test_prompt_workspaces(lib):
+    t = ctypes.byref(A.MoeTensor(1 << 20, 2048, 128))
+    rc = lib.moe_prompt_attention_shared(t, 5, 16, t, t, 5000, 8, 128, 1 << 20, 1 << 20, 1, 0.1, 0, 1 << 20, None, 1, None,
+                                         (1 << 20) + 64, 1 << 30, None)
+    assert rc == moe.MOE_ERR_INVALID_ARG      # not 256-byte aligned
+    for bad in ((0, 8, 5000, 8, 128, 1, 0), (5, 8, 5000, 0, 128, 1, 0), (5, 12, 5000, 8, 128, 1, 0), (5, 8, 5000, 8, 96, 1, 0),
+                (5, 8, 5000, 8, 128, 0, 0), (5, 8, 5000, 8, 128, 1, -1), (5, 8, 0, 8, 128, 1, 0), (5, 65, 5000, 1, 128, 1, 0)):
+        assert lib.moe_prompt_attention_workspace(*bad) == 0
+
+
 def test_prompt_of_nothing_is_a_no_op(lib):
     assert _prompt(lib, nq=0) == moe.MOE_OK
     assert _prompt(lib, n=0) == moe.MOE_OK
