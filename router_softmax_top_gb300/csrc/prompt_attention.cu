@@ -34,8 +34,12 @@
 // in the loop a block takes ~2700 cycles, 2048 of them matrix instructions at their full
 // rate, and a CTA's ends about a tenth of its time.  Heads of 64 are bound by the
 // exponentials' chain and by the ends of short CTAs, hence two CTAs per SM (75 -> 68 us
-// for twelve packed prompts); heads of 256 by loads, as one row tile uses a block of keys
-// half as often (a block of 64 keys waits ~1100 cycles for its keys).
+// for twelve packed prompts).  Heads of 256 have one row tile: their queries are moved to
+// tensor memory, where they do not take a third of the shared memory's bandwidth, and
+// their place holds a third stage of keys and values (a block of 64 keys takes 0.78 us so,
+// 0.92 before; products alone would take 0.57); what is left is the chain of products and
+// exponentials of the one tile (weights through shared memory, so that scores run two blocks
+// ahead, made it 0.87).
 // Few rows with many keys do not fill the GPU: their keys are shared out over several CTAs (below).
 // Two issuing warps (one per tile) were slower (422 us), as were handing the weights on
 // in two parts and testing barriers before suspending on them.
@@ -83,7 +87,7 @@ struct PromptJob {
 // 22.3, whole 14.2), and, where two parts are on the same SM (heads of 64), at least kMinPair (2 of 8, 1024 tokens: 24.0,
 // whole 20.6; 2 of 16, 1024 after 1024: 32.8, whole 33.1; 2 of 24, 16 sequences of 7 after 3000: 33.1, whole 41.6).
 // Groups of a last, partly filled wave are not shared: 300 tokens after 3000 of 4 sequences, window 1024, took 43.8 us so
-// and 41.2 whole, 777 and 1024 after 4096 of heads of 256 74.3 and 76.2.
+// and 41.2 whole, 777 and 1024 after 4096 of heads of 256 74.3 and 76.2 (with queries in shared memory).
 template <int D>
 constexpr int kMinPart = D == 128 ? 4 : 6;
 constexpr int kMinPair = 12;
@@ -95,14 +99,16 @@ struct PromptCfg {
   static constexpr int kNQ = D == 256 ? 1 : 2;         // row tiles
   static constexpr int kBuf = 2;                       // score buffers (one per tile, or two of the one tile)
   static constexpr int kBK = D == 128 ? 128 : 64;      // keys of a block
-  static constexpr int kStages = D == 64 ? 4 : 2;      // of keys, and of values
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 2 : 3;  // of keys, and of values
+  static constexpr bool kQTmem = D == 256;             // queries in tensor memory (of two tiles it has no room for them)
   static constexpr uint32_t kQBytes = kTileRows * D * 2, kKBytes = kBK * D * 2;
-  static constexpr uint32_t kQOff = 0, kKOff = kNQ * kQBytes, kVOff = kKOff + kStages * kKBytes;
+  static constexpr uint32_t kKOff = kQTmem ? 0 : kNQ * kQBytes, kVOff = kKOff + kStages * kKBytes,
+                            kQOff = kQTmem ? kVOff : 0;  // (on their way to tensor memory: where values come later)
   // a part of a shared group: its sums as [tile][D / 4][128 rows] of 4, then per row its reference and weight sum
   static constexpr size_t kSums = (size_t)kNQ * kTileRows * D, kPart = kSums + 2 * kNQ * kTileRows;
   static constexpr size_t kSmem = kVOff + kStages * kKBytes + 1024;
-  // tensor memory: score buffers, then outputs
-  static constexpr uint32_t kOCol = kBuf * kBK;
+  // tensor memory: score buffers, then outputs, then queries
+  static constexpr uint32_t kOCol = kBuf * kBK, kQCol = kOCol + kNQ * D;
   static constexpr int kSoftWarps = 4 * kNQ, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1,
                        kReadyWarp = kSoftWarps + 2;  // (two tiles only)
   // a warpgroup for the two (a register split goes by warpgroups); its other warps have nothing to do
@@ -113,7 +119,7 @@ struct PromptCfg {
   static constexpr uint32_t kTmemCols = D == 64 ? 256 : 512;
   static constexpr bool kSplit = kNQ == 2;
   static_assert(!kSplit || 2 * kRegSoft + kRegRest <= 3 * kRegLaunch, "a split draws on what the launch has");
-  static_assert(kOCol + kNQ * D <= kTmemCols, "tensor memory");
+  static_assert(kQCol + (kQTmem ? D / 2 : 0) <= kTmemCols, "tensor memory");
   static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "shared memory");
 };
 
@@ -427,7 +433,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
   using C = PromptCfg<D>;
   constexpr int NQ = C::kNQ, BK = C::kBK, ST = C::kStages, DC = D / 64;
   extern __shared__ __align__(1024) unsigned char sm_raw[];
-  __shared__ uint64_t q_full, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], pv_done[NQ], k_first, done;
+  __shared__ uint64_t q_smem, q_full, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], pv_done[NQ], k_first, done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail, s_last;
   __shared__ uint32_t s_redo[C::kSoftWarps];  // (a warp has 32 rows)
@@ -439,7 +445,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v)));
   if (tid == 0) {
     s_fail = 0;
-    a_mbar_init(&q_full, 1);
+    a_mbar_init(&q_smem, 1);
+    a_mbar_init(&q_full, C::kQTmem ? kTileRows : 1);
     for (int i = 0; i < ST; ++i) {
       a_mbar_init(&k_full[i], 1);
       a_mbar_init(&k_empty[i], 1);
@@ -574,13 +581,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
 #pragma unroll
       for (int t = 0; t < NQ; ++t)
         if (tr[t].je > tr[t].jb) q_bytes += DC * q_rows_bytes;
-      a_expect_tx(&q_full, q_bytes);
+      uint64_t *q_bar = C::kQTmem ? &q_smem : &q_full;
+      a_expect_tx(q_bar, q_bytes);
 #pragma unroll
       for (int t = 0; t < NQ; ++t)
         if (tr[t].je > tr[t].jb)
           for (int c = 0; c < DC; ++c)
             p_tma_3d(sm + C::kQOff + t * C::kQBytes + c * kTileRows * 128, &maps.q, 64 * c, kvh * j.group,
-                     w.q0 + w.first_token + t * j.tile_tokens, &q_full);
+                     w.q0 + w.first_token + t * j.tile_tokens, q_bar);
       // block i's keys or values into their stage; keys go a block ahead of values, as they are used
       auto load = [&](const CUtensorMap *map, uint32_t off, uint64_t *full, int i, int &count) {
         const int st = i % ST;
@@ -607,11 +615,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         }
         if (x < n_blocks) load(&maps.k, C::kKOff, k_full, x, k_loaded);
         if (NQ == 1 && i >= ST && !(ok = free_from(v_empty, i - ST))) break;
+        if (C::kQTmem && i == 0 && !(ok = a_mbar_wait(&q_full, 0, &s_fail))) break;  // the queries are out of the way
         load(&maps.v, C::kVOff, v_full, i, v_loaded);
       }
       if (!ok) s_fail = 1;
       // no copy may be in flight when the CTA leaves
-      if (*(volatile int *)&s_fail) (void)a_mbar_wait(&q_full, 0);
+      if (*(volatile int *)&s_fail) (void)a_mbar_wait(q_bar, 0);
       for (int i = max(0, k_loaded - ST); i < k_loaded; ++i) (void)a_mbar_wait(&k_full[i % ST], (uint32_t)(i / ST) & 1u);
       for (int i = max(0, v_loaded - ST); i < v_loaded; ++i) (void)a_mbar_wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u);
     }
@@ -626,9 +635,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         const uint64_t b0 = p_desc_k(sm + C::kKOff + (i % ST) * C::kKBytes);
         if (one) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            p_mma_ss(tmem + buf * BK, a0 + (kk / 4) * (kTileRows * 128 / 16) + (kk % 4) * 2,
-                   b0 + (kk / 4) * (BK * 128 / 16) + (kk % 4) * 2, id_qk, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t b = b0 + (kk / 4) * (BK * 128 / 16) + (kk % 4) * 2;
+            if constexpr (C::kQTmem)
+              p_mma_ts(tmem + buf * BK, tmem + C::kQCol + kk * 8, b, id_qk, kk > 0);
+            else
+              p_mma_ss(tmem + buf * BK, a0 + (kk / 4) * (kTileRows * 128 / 16) + (kk % 4) * 2, b, id_qk, kk > 0);
+          }
           p_commit(&s_full[buf]);
         }
         __syncwarp();
@@ -737,7 +750,30 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     float m = live ? -a_inf() : 0.f, l = 0.f;  // reference (log2 units) and sum
     bool ok = true;
     const uint32_t o_col = tmem + lanes + C::kOCol + t * D;
-    for (int jj = range.jb; jj < range.je; ++jj) {
+    if constexpr (C::kQTmem) {
+      if (n_blocks > 0) {
+        ok = __all_sync(0xffffffffu, a_mbar_wait(&q_smem, 0, &s_fail));
+        const unsigned char *row = sm_raw + (sm - a_smem(sm_raw)) + C::kQOff + r * 128;
+#pragma unroll
+        for (int x = 0; x < DC; ++x) {
+          float q[32];
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            const float4 v = live && ok ? *reinterpret_cast<const float4 *>(row + x * kTileRows * 128 + ((z ^ (r & 7)) << 4))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+            q[4 * z] = v.x;
+            q[4 * z + 1] = v.y;
+            q[4 * z + 2] = v.z;
+            q[4 * z + 3] = v.w;
+          }
+          p_st32(tmem + lanes + C::kQCol + 32 * x, q);
+        }
+        p_st_wait();
+        p_fence_before();
+        a_mbar_arrive(&q_full);
+      }
+    }
+    for (int jj = range.jb; jj < range.je && ok; ++jj) {
       const int n = jj - range.jb, buf = NQ == 1 ? (n & 1) : t;
       const uint32_t ph = (uint32_t)(NQ == 1 ? n >> 1 : n) & 1u;
       ok = __all_sync(0xffffffffu, a_mbar_wait(&s_full[buf], ph, &s_fail));
