@@ -37,9 +37,10 @@
 // for twelve packed prompts).  Heads of 256 have one row tile: their queries are moved to
 // tensor memory, where they do not take a third of the shared memory's bandwidth, and
 // their place holds a third stage of keys and values (a block of 64 keys takes 0.78 us so,
-// 0.92 before; products alone would take 0.57); what is left is the chain of products and
-// exponentials of the one tile (weights through shared memory, so that scores run two blocks
-// ahead, made it 0.87).
+// 0.92 before; its products alone take 0.55: 32 cycles each of 64 keys with queries from
+// tensor memory, 48 from shared memory).  Neither the exponentials nor their chain bound
+// it: two threads per row took 0.79 us, weights through shared memory, so that scores run
+// two blocks ahead, 0.87.  What is left are the copies, 64 KB per block, 44 bytes per cycle.
 // Few rows with many keys do not fill the GPU: their keys are shared out over several CTAs (below).
 // Two issuing warps (one per tile) were slower (422 us), as were handing the weights on
 // in two parts and testing barriers before suspending on them.
