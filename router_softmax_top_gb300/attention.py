@@ -339,11 +339,13 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_l
             if L.moe_prompt_attention_workspace(n, hq, nk, hkv, d, n_cu - 1, window) > 0:
                 ws = _kept((dev, handle, "prompt", d),
                            lambda: prompt_attention_workspace(n, hq, nk, hkv, d, n_cu - 1, window, _cuda(dev)))
-        rc = L.moe_prompt_attention_shared(tq, n, hq, tk, tv, nk, hkv, d, pq, pk, n_cu - 1,
-                                           d ** -0.5 if scale is None else scale, window, o.data_ptr(),
-                                           lse.data_ptr() if return_lse else None, _DTYPES[dtype], word,
-                                           None if ws is None else ws.data_ptr(),
-                                           0 if ws is None else ws.numel() * ws.element_size(), handle)
+        factor, po, pl = d ** -0.5 if scale is None else scale, o.data_ptr(), lse.data_ptr() if return_lse else None
+        if ws is None:
+            rc = L.moe_prompt_attention(tq, n, hq, tk, tv, nk, hkv, d, pq, pk, n_cu - 1, factor, window, po, pl,
+                                        _DTYPES[dtype], word, handle)
+        else:
+            rc = L.moe_prompt_attention_shared(tq, n, hq, tk, tv, nk, hkv, d, pq, pk, n_cu - 1, factor, window, po, pl,
+                                               _DTYPES[dtype], word, ws.data_ptr(), ws.numel() * ws.element_size(), handle)
         if rc:
             _check(rc, "moe_prompt_attention")
         return (o, lse) if return_lse else o
