@@ -87,6 +87,9 @@ __device__ __forceinline__ bool a_mbar_wait(uint64_t *bar, uint32_t parity, cons
   }
   return false;
 }
+// The wait for work that still reads or writes memory about to be given back: bounded by time, but not cut short by
+// *fail, which is set just where such work may be in flight.
+__device__ __forceinline__ bool a_mbar_drain(uint64_t *bar, uint32_t parity) { return a_mbar_wait(bar, parity, nullptr); }
 // Bulk copy of contiguous bytes into shared memory (addresses and size multiples of 16).
 __device__ __forceinline__ void a_bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(

@@ -621,9 +621,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
       }
       if (!ok) s_fail = 1;
       // no copy may be in flight when the CTA leaves
-      if (*(volatile int *)&s_fail) (void)a_mbar_wait(q_bar, 0);
-      for (int i = max(0, k_loaded - ST); i < k_loaded; ++i) (void)a_mbar_wait(&k_full[i % ST], (uint32_t)(i / ST) & 1u);
-      for (int i = max(0, v_loaded - ST); i < v_loaded; ++i) (void)a_mbar_wait(&v_full[i % ST], (uint32_t)(i / ST) & 1u);
+      if (*(volatile int *)&s_fail) (void)a_mbar_drain(q_bar, 0);
+      for (int i = max(0, k_loaded - ST); i < k_loaded; ++i) (void)a_mbar_drain(&k_full[i % ST], (uint32_t)(i / ST) & 1u);
+      for (int i = max(0, v_loaded - ST); i < v_loaded; ++i) (void)a_mbar_drain(&v_full[i % ST], (uint32_t)(i / ST) & 1u);
     }
   } else if (warp == C::kMmaWarp) {
     // The whole warp walks through the blocks and one elected lane issues: descriptors then stay in uniform registers,
@@ -709,8 +709,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         }
       }
       if (!ok) s_fail = 1;
+      // no product may be running when the CTA gives its memory back, least of all after a wait that gave up
       commit(&done);
-      (void)wait(&done, 0);
+      (void)a_mbar_drain(&done, 0);
+      __syncwarp();
     }
   } else if (NQ == 2 && warp == C::kReadyWarp) {
     // block i's values and block i + 1's keys are there: one more arrival for the weights of block i
