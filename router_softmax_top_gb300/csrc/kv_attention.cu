@@ -124,6 +124,9 @@ __device__ __forceinline__ void store_pair(__half *p, float a, float b) {
   *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b);
 }
 
+// (out of line: a copy is nearly always there)
+__device__ __noinline__ bool wait_for_tile(uint64_t *bar, uint32_t parity) { return a_mbar_wait(bar, parity); }
+
 // What a pair costs beside its tiles, in tiles (its queries' set-up and its result).  Measured with 1, 2, 4, 8 and 16:
 // 128 sequences of 64 to 8192 tokens 132, 125, 125, 129 and 136 us; one of 131071 tokens 50, 48, 46, 46 and 45 us.
 constexpr int kPairCost = 4;
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     no_page[warp][0] = 0;
   }
   __syncwarp();
-  uint32_t used = 0;            // tiles consumed: tile x is in stage x % S
+  TileRing<S> tiles_on_way;
   int64_t src_off = -1;         // per lane: where one of the next tiles is in the cache, -1: the tile has no page
   int src_next = 0, src_n = 0;  // next lane's turn, and lanes in use
   uint32_t load_piece = 0;      // number of the copies' piece; ~0: no more
@@ -572,6 +575,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   };
   // Copies the share's tile x, if there is one, into its stage.
   auto issue = [&](uint32_t x) {
+    if (tiles_on_way.dead) return;
     if (src_next == src_n) {
       src_next = src_n = 0;
       refill();
@@ -598,7 +602,6 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
   asm volatile("mov.b32 %0, 0x80088008;\n mov.b32 %1, 0x80808080;\n mov.b32 %2, 0x80088008;\n mov.b32 %3, 0x80808080;"
                : "=r"(eight[0]), "=r"(eight[1]), "=r"(eight[2]), "=r"(eight[3]));
 
-  bool dead = false;  // a wait gave up: later ones do not wait
   for (uint32_t piece = 0; work; ++piece) {
     __syncwarp();
     const Walk &walk = walks[warp][0];
@@ -662,7 +665,6 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     float dtop = 0.f;                           // bound of the value scales seen
     __half2 dtop2 = __float2half2_rn(0.f);
     float shift = -7.f;                         // reference = m + shift
-    int poison = 0;                             // status bits: what the piece's result is worth
 
     // One tile.  Whole: every row sees all of it.
     auto compute = [&](const unsigned char *tp, const int tok0, auto is_whole) {
@@ -831,12 +833,11 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     auto tiles = [&](int from, int to, auto is_whole) {
 #pragma unroll 1
       for (int tile = from; tile < to; ++tile) {
-        const uint32_t x = used++;
-        if (!__all_sync(0xffffffffu, a_mbar_try(&bar[x % S], (x / S) & 1u))) {  // not there yet
-          if (!dead) dead = !__all_sync(0xffffffffu, a_mbar_wait(&bar[x % S], (x / S) & 1u));
-          // a tile that never came is computed on as it lies there: the result is NaN
-          if (dead) poison |= MOE_KV_TIMED_OUT;
-        }
+        const uint32_t x = tiles_on_way.used;
+        tiles_on_way.take(
+            [&](uint32_t y) { return __all_sync(0xffffffffu, a_mbar_try(&bar[y % S], TileRing<S>::parity(y))) != 0; },
+            [&](uint32_t y) { return __all_sync(0xffffffffu, wait_for_tile(&bar[y % S], TileRing<S>::parity(y))) != 0; });
+        // (a tile that never came is computed on as it lies there: the result is NaN)
         compute(ring + (x % S) * C::kTile, (walk.first + tile) * kKvTile, is_whole);
         __syncwarp();
         issue(x + S);
@@ -849,7 +850,9 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       if (pass == 0) tiles(w0, w1, std::true_type());
     }
     // ---- the piece: l over the lanes that share a row; accumulators without the nibbles' factors
+    int poison = 0;  // status bits: what the piece's result is worth
     if (no_page[warp][piece & 7]) poison |= MOE_KV_BAD_PAGE;
+    if (tiles_on_way.dead) poison |= MOE_KV_TIMED_OUT;
     if (poison) {
       l[0] = l[1] = a_nan();
       if (lane == 0 && j.c.status) atomicOr(j.c.status, poison);
@@ -889,7 +892,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
         if (g == 0 && j.lse) j.lse[at] = l[z] == 0.f ? -a_inf() : (r[z] + log2f(l[z])) * kLn2;
       }
     } else {
-      // a part: a last piece waits in the ring (every copy has been used by then), a first one that others follow
+      // a part: a last piece waits in the ring (no copy is on its way by then), a first one that others follow
       // in the workspace
       float *o = more ? heads_mem + (size_t)warp * C::kPart : reinterpret_cast<float *>(ring);
 #pragma unroll
@@ -932,9 +935,6 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     __syncwarp();
     if (lane == 0) walks[warp][0] = next;
   }
-  // copies that a wait gave up on must have landed before the CTA's memory is gone
-  if (dead)
-    for (uint32_t x = used > S ? used - S : 0; x < used; ++x) (void)a_mbar_wait(&bar[x % S], (x / S) & 1u);
   __syncthreads();
   if (has_pair[0] || has_pair[1] || has_pair[2])
     merge_by_cta<D, T>(j, cta_pairs, has_pair, sm, in_heads, sh_last);

@@ -71,4 +71,27 @@ KV_HD int64_t kv_tiles(int64_t len, int q_tokens, int window, int table_width, i
   return (len + kKvTile - 1) / kKvTile - *first;
 }
 
+// A warp's tiles on their way through its ring of S stages: tile x is in stage x % S and completes phase x / S of that
+// stage's barrier, which takes one arrival per phase.  Tiles 0..S - 1 are asked for at first, and tile x + S once tile x
+// has been taken, but only while every wait has been kept: a stage whose copy never came has a phase that is not over,
+// and must be neither armed nor written again.
+template <int S>
+struct TileRing {
+  uint32_t used = 0;  // tiles taken
+  bool dead = false;  // a wait gave up: nothing taken from then on counts, and nothing more may be asked for
+
+  static KV_HD uint32_t stage(uint32_t x) { return x % S; }
+  static KV_HD uint32_t parity(uint32_t x) { return (x / S) & 1u; }
+  // Takes the next tile.  there(x) looks, wait(x) waits, for a limited time, and says whether it came.  When it did not,
+  // whatever is on its way is waited for, with the same limit each, so that no copy goes into the ring any more; of a
+  // stage that nothing was asked into, the limit runs out.
+  template <typename There, typename Wait>
+  KV_HD void take(There there, Wait wait) {
+    const uint32_t x = used++;
+    if (there(x) || dead || wait(x)) return;
+    dead = true;
+    for (uint32_t y = x; y != x + S; ++y) (void)wait(y);
+  }
+};
+
 }  // namespace moe

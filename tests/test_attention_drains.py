@@ -77,3 +77,112 @@ def test_copies_are_drained_before_the_loader_leaves():
     lines = tail[:tail.index("kMmaWarp")].split("\n")
     waits = [x for x in lines if "_full[" in x or "q_bar" in x]
     assert len(waits) == 3 and all("a_mbar_drain(" in x and "a_mbar_wait(" not in x for x in waits)
+
+
+# ------------------------------------------------------------------- a warp's ring of tiles
+RING = r'''
+#include <stdint.h>
+#include <stdlib.h>
+#include <vector>
+#include "kv_layout.h"
+using namespace moe;
+
+// Barriers of one arrival per phase and copies that land when the clock says so, as the kernel's warp uses them.
+struct Bar { uint32_t phase = 0; int pending = 1; long landing = -1; };
+struct Model {
+  static constexpr int S = 2;
+  Bar bar[S];
+  long now = 0, limit;
+  int faults = 0;    // arrivals on a phase that has had its own, or copies into a stage that one is on its way to
+  explicit Model(long limit) : limit(limit) {}
+  void settle() {
+    for (Bar &b : bar)
+      if (b.pending == 0 && b.landing >= 0 && now >= b.landing) { b.landing = -1; b.pending = 1; ++b.phase; }
+  }
+  void ask(uint32_t x, long delay) {   // delay 0: the tile has no page, an arrival without a copy
+    settle();
+    Bar &b = bar[TileRing<S>::stage(x)];
+    if (b.pending == 0 || b.phase != x / S) ++faults;
+    b.pending = 0;
+    b.landing = now + delay;
+  }
+  bool there(uint32_t x) {
+    settle();
+    return (bar[TileRing<S>::stage(x)].phase & 1u) != TileRing<S>::parity(x);   // what a test of a phase's parity says
+  }
+  bool wait(uint32_t x) {
+    const long end = now + limit;
+    for (;; ++now) {
+      if (there(x)) return true;
+      if (now >= end) return false;
+    }
+  }
+  int on_way() { settle(); int n = 0; for (Bar &b : bar) n += b.pending == 0; return n; }
+};
+
+// A share of `tiles`; copies take delay[x].  Out: faults, copies on their way when the part is written, tiles that came,
+// and the clock.
+extern "C" void run(int tiles, const long *delay, long limit, long *out) {
+  Model m(limit);
+  TileRing<Model::S> ring;
+  auto issue = [&](uint32_t x) {
+    if (!ring.dead && (int)x < tiles) m.ask(x, delay[x]);
+  };
+  for (int i = 0; i < Model::S; ++i) issue(i);
+  long came = 0;
+  for (int t = 0; t < tiles; ++t) {
+    const uint32_t x = ring.used;
+    ring.take([&](uint32_t y) { return m.there(y); }, [&](uint32_t y) { return m.wait(y); });
+    came += !ring.dead;
+    m.now += 3;
+    issue(x + Model::S);
+  }
+  out[0] = m.faults; out[1] = m.on_way(); out[2] = came; out[3] = m.now;
+}
+'''
+
+
+@pytest.fixture(scope="module")
+def ring(tmp_path_factory):
+    d = tmp_path_factory.mktemp("ring")
+    (d / "r.cpp").write_text(RING)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-I", CSRC, "-o", str(d / "r.so"), str(d / "r.cpp")],
+                   check=True)
+    lib = ctypes.CDLL(str(d / "r.so"))
+
+    def run(delays, limit):
+        out = (ctypes.c_long * 4)()
+        lib.run(len(delays), (ctypes.c_long * len(delays))(*delays), ctypes.c_long(limit), out)
+        return list(out)
+    return run
+
+
+def test_a_ring_whose_copies_come(ring):
+    import random
+    rng = random.Random(1)
+    for _ in range(2000):
+        n = rng.randrange(0, 12)
+        delays = [rng.choice([0, 1, 5, 40]) for _ in range(n)]
+        assert ring(delays, 100)[:3] == [0, 0, n]
+
+
+def test_a_ring_whose_copy_is_late(ring):
+    # a copy that lands after the wait for it gave up, but within the wait after that
+    import random
+    rng = random.Random(2)
+    for _ in range(2000):
+        n = rng.randrange(1, 12)
+        delays = [rng.choice([0, 1, 5, 40]) for _ in range(n)]
+        late = rng.randrange(n)
+        delays[late] = rng.randrange(150, 190)
+        faults, on_way, came, _ = ring(delays, 100)
+        assert faults == 0 and on_way == 0 and came <= n and (came == late or came == n)
+
+
+def test_a_ring_whose_copies_never_come_ends(ring):
+    for n in (1, 2, 3, 9):
+        for lost in range(n):
+            delays = [1 << 40 if x >= lost else 5 for x in range(n)]
+            faults, on_way, came, clock = ring(delays, 100)
+            assert faults == 0 and came == lost and on_way <= 2
+            assert clock <= 4 * 100 + 20 * n     # one wait, and one more for each stage
