@@ -280,6 +280,26 @@ __device__ __noinline__ void share_keys(const PromptJob &j, PromptWork &w, int p
   }
 }
 
+// For offsets that do not all make sense: which of the sequences from `base` on (a lane's has the queries [a, b)) are worked
+// on; b = -1 for the others, which are reported.  One that begins before another that counts has ended is none of them:
+// it would be worked on twice, and the tile groups of all would be more than the launch has CTAs for.  end: where the
+// sequences before these end (-1: they made sense, so that they end where these begin); returns where these end.
+__device__ __noinline__ int queries_that_count(const PromptJob &j, int base, int a, int &b, int end) {
+  const int s = base + (threadIdx.x & 31);
+  if (end < 0) end = base > 0 ? __ldg(j.cu_q + base) : 0;
+  const bool bad = s >= j.n_seqs || a < 0 || b < a || b > j.n_q;
+  bool counts = false;
+  for (int k = 0; k < 32; ++k) {
+    const int ka = __shfl_sync(0xffffffffu, a, k), kb = __shfl_sync(0xffffffffu, b, k);
+    if (__shfl_sync(0xffffffffu, (int)bad, k) || ka < end) continue;
+    end = kb;
+    counts |= s == base + k;
+  }
+  if (!counts) b = -1;
+  if (!counts && s < j.n_seqs && blockIdx.x == 0 && j.status) atomicOr(j.status, MOE_KV_BAD_LENGTH);
+  return end;
+}
+
 // A part's sums to the workspace; whether it was the last of the group.
 template <int D>
 __device__ __noinline__ bool write_part(const PromptJob &j, const PromptWork &w, uint32_t o_col, bool some, bool live,
@@ -473,27 +493,31 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     int unit = blockIdx.x, of = 0, part = 0, parts = 1;  // unit: group and key head
     const bool by_level = j.n_seqs <= kMaxSplitSeqs;
     int before = 0, seq = -1, group = 0, a = 0, b = 0, c = 0, d = 0, at = 0;
+    int end = -1;  // where some offsets make no sense: where the sequences before these end
     for (int base = 0; base < j.n_seqs; base += 32) {
       const int s = base + lane;
       int n = 0;
+      bool bad = false;
       if (s < j.n_seqs) {
         a = __ldg(j.cu_q + s);
         b = __ldg(j.cu_q + s + 1);
         c = __ldg(j.cu_k + s);  // with the others: a trip to memory less
         d = __ldg(j.cu_k + s + 1);
-        if (a < 0 || b < a || b > j.n_q) {
-          if (blockIdx.x == 0 && j.status) atomicOr(j.status, MOE_KV_BAD_LENGTH);
-          a = b = 0;
-        }
+        bad = a < 0 || b < a || b > j.n_q;
         n = (b - a + per - 1) / per;
+      }
+      if (__any_sync(0xffffffffu, bad) || end >= 0) {
+        end = queries_that_count(j, base, a, b, end);
+        if (b < 0) a = b = n = 0;
       }
       if (seq >= 0) continue;  // (the first CTA only: it looks at all offsets)
       bool hit = false;
       auto beyond = [&](int level) { return (int)__reduce_add_sync(0xffffffffu, max(0, n - level)); };
       if (j.slots > 0) {  // (then there are at most kMaxSplitSeqs sequences)
-        const int units = beyond(0) * j.hkv;
-        if (units > 0 && 2 * units <= j.slots) {
-          parts = min(j.slots / units, j.most_parts);
+        // every part has to have its CTA: the last one done is told by their number
+        const int units = beyond(0) * j.hkv, room = min(j.slots, (int)gridDim.x);
+        if (units > 0 && 2 * units <= room) {
+          parts = min(room / units, j.most_parts);
           part = unit / units;  // (first parts first: not all groups may have more)
           unit %= units;
           of = units;
