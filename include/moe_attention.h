@@ -135,7 +135,7 @@ int moe_kv_attention(const moe_kv_cache *c, const int32_t *seq_lens, const moe_t
 /*
  * Causal attention over whole prompts, packed one after another.
  * Queries [cu_q[s], cu_q[s+1]) and keys [cu_k[s], cu_k[s+1]) are sequence s's
- * (device int32 [n_seqs + 1], increasing, from 0 to the tensors' tokens).  A
+ * (device int32 [n_seqs + 1], not decreasing, from 0 to the tensors' tokens).  A
  * sequence's queries stand at its last positions (keys before them: tokens that
  * an earlier call has seen): query i of n_q, with n_k keys, stands at p = n_k -
  * n_q + i and sees the keys [max(0, p - window + 1), p], or [0, p] when window
@@ -146,8 +146,10 @@ int moe_kv_attention(const moe_kv_cache *c, const int32_t *seq_lens, const moe_t
  * exponentials, or NULL.  dtype: MOE_BF16 or MOE_F16, of q, k, v and out; weights
  * are rounded to it before they meet the values, sums are fp32.  Strides are not 0.
  * A NaN or infinity that a row does not see does not reach it.
- * status: as above (bad offsets: a sequence whose cu_q makes no sense is skipped,
- * one whose cu_k makes none gives NaN), or NULL.
+ * status: as above, or NULL.  Rows that no sequence holds give NaN, and so do those of
+ * a sequence whose cu_k makes no sense; a sequence whose cu_q makes none (out of range,
+ * decreasing, or within an earlier sequence) holds no rows.  Nothing is written when
+ * n_q_tokens or n_seqs is 0.
  */
 int moe_prompt_attention(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads, const moe_tensor *k,
                          const moe_tensor *v, int32_t n_k_tokens, int32_t n_kv_heads, int32_t head_dim,

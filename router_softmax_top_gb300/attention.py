@@ -308,8 +308,8 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_l
     """Causal attention over packed prompts (moe_prompt_attention).
 
     q [n_q_tokens, n_q_heads, head_dim], k and v [n_k_tokens, n_kv_heads, head_dim], bfloat16 or float16;
-    cu_q, cu_k int32 [n_seqs + 1] (cu_k None: cu_q).  With more keys than queries a sequence's queries are its
-    last tokens.  window > 0: a token sees itself and the window - 1 tokens before it.  Returns q's shape, and
+    cu_q, cu_k int32 [n_seqs + 1] (cu_k None: cu_q); rows that no sequence holds give NaN, and a status.  With more keys
+    than queries a sequence's queries are its last tokens.  window > 0: a token sees itself and the window - 1 tokens before it.  Returns q's shape, and
     the log of the sums of exponentials (fp32 [n_q_tokens, n_q_heads]) with return_lse.  Few queries of many keys
     use a workspace: without `workspace` a module-level one per stream (inside a graph capture: one of the capture's
     own); graphs that may run at the same time need their own."""
@@ -321,8 +321,8 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_l
     tq, tk = _tokens(q, "q", n, hq, d, dtype, dev), _tokens(k, "k", None, None, d, dtype, dev)
     nk, hkv = k.shape[0], k.shape[1]
     tv = _tokens(v, "v", nk, hkv, d, dtype, dev)
-    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
-        _refuse("cu_q must hold n_seqs + 1 offsets")
+    if cu_q.dim() != 1 or cu_q.shape[0] < (2 if n else 1):
+        _refuse("cu_q must hold n_seqs + 1 offsets, of one sequence at least where there are tokens")
     n_cu = cu_q.shape[0]
     pq = _index(cu_q, "cu_q", n_cu, dev)
     pk = pq if cu_k is None else _index(cu_k, "cu_k", n_cu, dev)

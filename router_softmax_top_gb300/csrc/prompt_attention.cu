@@ -111,8 +111,9 @@ struct PromptCfg {
   // tensor memory: score buffers, then outputs, then queries
   static constexpr uint32_t kOCol = kBuf * kBK, kQCol = kOCol + kNQ * D;
   static constexpr int kSoftWarps = 4 * kNQ, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1,
-                       kReadyWarp = kSoftWarps + 2;  // (two tiles only)
-  // a warpgroup for the two (a register split goes by warpgroups); its other warps have nothing to do
+                       kReadyWarp = kSoftWarps + 2,  // (two tiles only)
+                       kCheckWarp = kSoftWarps + 3;  // (at the start of the first CTA only)
+  // a warpgroup for these (a register split goes by warpgroups)
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
   // registers per thread: what 384 threads can have at launch, then split; 256 threads need no split
   static constexpr int kCtas = D == 64 ? 2 : 1;  // on an SM: what one CTA waits for at its ends, the other hides
@@ -281,7 +282,7 @@ __device__ __noinline__ void share_keys(const PromptJob &j, PromptWork &w, int p
 }
 
 // For offsets that do not all make sense: which of the sequences from `base` on (a lane's has the queries [a, b)) are worked
-// on; b = -1 for the others, which are reported.  One that begins before another that counts has ended is none of them:
+// on; b = -1 for the others.  One that begins before another that counts has ended is none of them:
 // it would be worked on twice, and the tile groups of all would be more than the launch has CTAs for.  end: where the
 // sequences before these end (-1: they made sense, so that they end where these begin); returns where these end.
 __device__ __noinline__ int queries_that_count(const PromptJob &j, int base, int a, int &b, int end) {
@@ -296,8 +297,42 @@ __device__ __noinline__ int queries_that_count(const PromptJob &j, int base, int
     counts |= s == base + k;
   }
   if (!counts) b = -1;
-  if (!counts && s < j.n_seqs && blockIdx.x == 0 && j.status) atomicOr(j.status, MOE_KV_BAD_LENGTH);
   return end;
+}
+
+// Whether the queries' offsets leave tokens that no sequence holds, or make no sense; by a warp of the first CTA.
+__device__ __noinline__ bool rows_left_over(const PromptJob &j) {
+  const int lane = threadIdx.x & 31;
+  bool odd = __ldg(j.cu_q) != 0 || __ldg(j.cu_q + j.n_seqs) != j.n_q;
+  for (int s = lane; s < j.n_seqs; s += 32) {
+    const int a = __ldg(j.cu_q + s), b = __ldg(j.cu_q + s + 1);
+    odd |= a < 0 || b < a || b > j.n_q;
+  }
+  odd = __any_sync(0xffffffffu, odd);
+  if (odd && lane == 0 && j.status) atomicOr(j.status, MOE_KV_BAD_LENGTH);
+  return odd;
+}
+
+// NaN for the tokens [from, to), by all threads of the CTA.
+template <int D>
+__device__ __forceinline__ void fill_rows(const PromptJob &j, int from, int to) {
+  const uint4 none = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);  // NaN as bf16 and as fp16
+  uint4 *out = static_cast<uint4 *>(j.out);
+  for (int64_t i = (int64_t)from * j.hq * (D / 8) + threadIdx.x; i < (int64_t)to * j.hq * (D / 8); i += blockDim.x) out[i] = none;
+  if (j.lse)
+    for (int64_t i = (int64_t)from * j.hq + threadIdx.x; i < (int64_t)to * j.hq; i += blockDim.x) j.lse[i] = a_nan();
+}
+// The tokens that none of the sequences that are worked on (see queries_that_count) holds.
+template <int D>
+__device__ __noinline__ void fill_rows_left_over(const PromptJob &j) {
+  int end = 0;
+  for (int s = 0; s < j.n_seqs; ++s) {
+    const int a = __ldg(j.cu_q + s), b = __ldg(j.cu_q + s + 1);
+    if (a < end || b < a || b > j.n_q) continue;
+    fill_rows<D>(j, end, a);
+    end = b;
+  }
+  fill_rows<D>(j, end, j.n_q);
 }
 
 // A part's sums to the workspace; whether it was the last of the group.
@@ -456,7 +491,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
   extern __shared__ __align__(1024) unsigned char sm_raw[];
   __shared__ uint64_t q_smem, q_full, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], pv_done[NQ], k_first, done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_fail, s_last;
+  __shared__ int s_fail, s_last, s_left_over;
   __shared__ uint32_t s_redo[C::kSoftWarps];  // (a warp has 32 rows)
   __shared__ PromptWork s_work;
   const uint32_t sm = (a_smem(sm_raw) + 1023u) & ~1023u;
@@ -510,7 +545,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         end = queries_that_count(j, base, a, b, end);
         if (b < 0) a = b = n = 0;
       }
-      if (seq >= 0) continue;  // (the first CTA only: it looks at all offsets)
       bool hit = false;
       auto beyond = [&](int level) { return (int)__reduce_add_sync(0xffffffffu, max(0, n - level)); };
       if (j.slots > 0) {  // (then there are at most kMaxSplitSeqs sequences)
@@ -563,7 +597,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
           if (parts > 1) share_keys<D>(j, w, parts);
           s_work = w;
         }
-        if (blockIdx.x != 0) break;
+        break;
       }
     }
     if (seq < 0 && lane == 0) s_work = {-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 1, 0, 0};
@@ -572,9 +606,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(a_smem(&s_tmem)), "r"(C::kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  if (blockIdx.x == 0 && warp == C::kCheckWarp) {
+    const bool some = rows_left_over(j);
+    if (lane == 0) s_left_over = some;
+  }
   p_fence_before();
   __syncthreads();
   p_fence_after();
+  if (blockIdx.x == 0 && s_left_over) fill_rows_left_over<D>(j);
   const uint32_t tmem = s_tmem;
   const PromptWork w = s_work;
   const int kvh = w.kvh;
