@@ -2,8 +2,8 @@
 //
 // For a row (one query token of one head) with scores s_j = scale q . k_j over the
 // keys it sees, o = sum_j 2^(t_j - r) v_j / sum_j 2^(t_j - r), t = s log2(e), for any
-// reference r; a warp keeps one reference per row and moves it only when a score
-// exceeds it by more than 2^8 (the sums then scale by a power of two, rarely).
+// reference r; a warp keeps one reference per row and moves it rarely (the sums then
+// scale by a power of two).
 //
 // Bound: the cache's bytes (1.125 bytes per cached value of a head pair, each read
 // once, for all query heads that share the head).  What makes that hard is the
@@ -20,10 +20,14 @@
 //    block, which the key's scale multiplies in fp32.  The query is rounded to fp16
 //    after a power-of-two scaling per row (exact for bf16 and fp16 inputs down to
 //    2^-24 of the row's largest value).
-//  * Values: O^T = V^T P^T, P^T from the scores by an 8x8 transpose, multiplied by the
-//    value's scale per block (fp16: p and p d are each off by at most 2^-11 of
-//    themselves, for fp16 results p d alone; sums are fp32).  The reference r includes
-//    the largest scale seen, so p d stays inside fp16 whatever the scales are.
+//  * Values: O^T = V^T E^T, E = p d, a weight times its value's scale per block, formed
+//    in fp32, rounded to fp16 once and transposed 8x8 on the way.  A row's reference
+//    goes by its largest product p d, not by p and d apart: that product lies between
+//    2^10 (when the reference is set) and 2^14, so any other is off by at most 2^-11 of
+//    itself or by 2^-35 of the largest, however far apart scales and weights are, and
+//    what a row does not see has no part in it.  (With a reference from the largest score
+//    and the largest scale, a large scale on a key of no weight took the small weights'
+//    products to 0.)  Weights and their sums are fp32.
 //  * Rows in the matrix's N: 8 of them (heads sharing a key head x query tokens).
 // Measured: 128 sequences of 64 to 8192 tokens (8 key heads of 128, 611 MB of cache) in
 // 125 us, 4.9 TB/s or 0.72 of the measured copy rate; their tiles alone go by in 100 us,
@@ -52,7 +56,10 @@ namespace moe {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.f;  // log2 by which a score may exceed its row's reference
+// A row's reference is set so that its largest product of a weight with a scale is 2^kCentre, and moves when one exceeds
+// kMost; or, where values are small against their weights, so that no weight exceeds 2^kDeep, and moves at kDeepMost.
+constexpr float kCentre = 10.f, kMost = 16384.f, kDeep = 70.f, kDeepMost = 7.5557864e22f /* 2^76 */;
+constexpr float kNone = -3.3e38f;  // the reference of a row that has seen nothing: below any score
 constexpr int kDecodeWarps = 8;
 constexpr int kDecodeSms = 152, kDecodeCtasMost = 2 * kDecodeSms;  // CTAs of a launch at most
 constexpr int kRows = 8;      // rows (heads x query tokens) of one work unit
@@ -108,13 +115,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
-__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
-  return h2_bits(__hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b)));
-}
-__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
-  return h2_bits(__hfma2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b),
-                         *reinterpret_cast<__half2 *>(&c)));
-}
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float a, float b) {
@@ -389,9 +389,6 @@ template <int D, typename T>
 __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas) kv_attention_kernel(const DecodeJob j) {
   using C = DecodeCfg<D>;
   constexpr int W = C::kWarps, S = C::kStages, NB = D / 32;
-  // fp16 results show a weight's second rounding (3.5e-4 of the result against 2.9e-4): their weights are carried in two
-  // halves, so that p d is rounded once.  bf16 results do not.
-  constexpr bool kExactWeights = std::is_same<T, __half>::value;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ uint64_t bars[W][S];
   __shared__ SharedPair cta_pairs[3];  // pairs that the whole CTA merges
@@ -661,10 +658,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int z = 0; z < 4; ++z) acc[b][h][z] = 0.f;
-    float m[2] = {-a_inf(), -a_inf()}, l[2] = {0.f, 0.f};
-    float dtop = 0.f;                           // bound of the value scales seen
-    __half2 dtop2 = __float2half2_rn(0.f);
-    float shift = -7.f;                         // reference = m + shift
+    float ref[2] = {kNone, kNone}, l[2] = {0.f, 0.f};  // references (log2 units) and sums of the weights
 
     // One tile.  Whole: every row sees all of it.
     auto compute = [&](const unsigned char *tp, const int tok0, auto is_whole) {
@@ -710,7 +704,10 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
         }
       }
       // ---- what a row does not see scores -inf
+      uint32_t seen[4];  // of tokens 8 x + pg: all bits of the halves of the rows that see it
       if (!whole) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) seen[x] = 0;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const int rr = rt * kRows + 2 * t + z;
@@ -720,102 +717,114 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
           for (int x = 0; x < 4; ++x) {
             const int key = tok0 + 8 * x + pg;
             if (key < lo || key >= hi) s[x / 2][2 * (x % 2) + z] = -a_inf();
+            else seen[x] |= z ? 0xffff0000u : 0xffffu;
           }
         }
       }
-      float mx[2];  // log2 units; f > 0
+      // ---- the value scales of the lane's tokens, and the largest of them (NaN as none)
+      const unsigned char *vs = tp + 34 * D + pg * (D / 16);
+      __half2 vd[4][NB / 2];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) mx[z] = fmaxf(fmaxf(s[0][z], s[0][z + 2]), fmaxf(s[1][z], s[1][z + 2])) * f[z];
-      // ---- the largest value scale of the tile (those of tokens past the sequence count as 0, NaN as none)
-      const unsigned char *vs = tp + 34 * D;
-      __half2 dmax = __float2half2_rn(0.f);
+      for (int x = 0; x < 4; ++x) {
+        if constexpr (NB == 2) {
+          vd[x][0] = *reinterpret_cast<const __half2 *>(vs + 8 * x * (D / 16));
+        } else {
 #pragma unroll
-      for (int z = 0; z < D / 64; ++z) {
-        const int off = (z * 32 + lane) * 4;  // two scales of one token
-        __half2 w = *reinterpret_cast<const __half2 *>(vs + off);
-        if (!whole && tok0 + off / (D / 16) >= len) w = __float2half2_rn(0.f);
-        dmax = __hmax2(dmax, __habs2(w));
+          for (int z = 0; z < NB / 4; ++z)
+            *reinterpret_cast<uint2 *>(&vd[x][2 * z]) = *reinterpret_cast<const uint2 *>(vs + 8 * x * (D / 16) + 8 * z);
+        }
       }
-      const bool over = mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy || !__hble2(dmax, dtop2);
-      if (__any_sync(0xffffffffu, over)) {
-        float dn = fmaxf(__low2float(dmax), __high2float(dmax));
+      auto largest = [&](int x) {
+        __half2 m = __habs2(vd[x][0]);
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+        for (int z = 1; z < NB / 2; ++z) m = __hmax2(m, __habs2(vd[x][z]));
+        return m;
+      };
+      // ---- weights.  (The score is rounded before the reference is taken away, as it was when the reference was set: of
+      // scores so large that their rounding is more than a weight can bear, the largest has a weight of its own size.)
+      float p[4][2];
+      uint64_t sum;
+      auto weigh = [&]() {
+        const uint64_t f2 = f2_pack(f[0], f[1]), r2 = f2_pack(-ref[0], -ref[1]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float a, b;
+          f2_unpack(f2_add(f2_mul(f2_pack(s[x / 2][2 * (x % 2)], s[x / 2][2 * (x % 2) + 1]), f2), r2), a, b);
+          p[x][0] = a_exp2(a);
+          p[x][1] = a_exp2(b);
+          sum = x ? f2_add(sum, f2_pack(p[x][0], p[x][1])) : f2_pack(p[x][0], p[x][1]);
         }
+      };
+      weigh();
+      // The lane's weights times its largest scale bound its products.  Where that is too much, each row's own products
+      // say whether its reference moves, so that nothing that a row does not see takes part in that.
+      {
+        const __half2 d2 = __hmax2(__hmax2(largest(0), largest(1)), __hmax2(largest(2), largest(3)));
+        float sum0, sum1;
+        f2_unpack(sum, sum0, sum1);
+        const float most = fmaxf(sum0, sum1);
+        if (__any_sync(0xffffffffu, most * fmaxf(__low2float(d2), __high2float(d2)) > kMost || most > kDeepMost)) {
+          float pd[2] = {0.f, 0.f}, pm[2] = {0.f, 0.f}, td[2] = {-a_inf(), -a_inf()}, tm[2] = {-a_inf(), -a_inf()};
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) dn = fmaxf(dn, __shfl_xor_sync(0xffffffffu, dn, o));
-        float shift_n = shift;
-        if (dn > dtop) {
-          // the bound leaves room for scales up to twice the largest one; 2^(8 - shift) dtop < 2^16
-          dtop = fminf(dn * 2.f, 65504.f);
-          dtop2 = __float2half2_rn(dtop);
-          const int ex = (int)((__float_as_uint(dtop) >> 23) & 255) - 126;  // dtop < 2^ex
-          shift_n = fmaxf((float)ex - 6.f, -7.f);
-        }
+          for (int x = 0; x < 4; ++x) {
+            const __half2 m = largest(x);
+            const float d = fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f);
+            const float lg = __log2f(d);
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const float m_new = fmaxf(m[z], mx[z]);
-          const float a = m[z] == -a_inf() ? 0.f : a_exp2((m[z] - m_new) + (shift - shift_n));
-          m[z] = m_new;
-          l[z] *= a;
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              acc[b][h][z] *= a;
-              acc[b][h][z + 2] *= a;
+            for (int z = 0; z < 2; ++z) {
+              const float sc = __fmul_rn(s[x / 2][2 * (x % 2) + z], f[z]);
+              pd[z] = fmaxf(pd[z], p[x][z] * d);
+              pm[z] = fmaxf(pm[z], p[x][z]);
+              td[z] = fmaxf(td[z], __fadd_ru(sc, lg));
+              tm[z] = fmaxf(tm[z], sc);
             }
+          }
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              pd[z] = fmaxf(pd[z], __shfl_xor_sync(0xffffffffu, pd[z], o));
+              pm[z] = fmaxf(pm[z], __shfl_xor_sync(0xffffffffu, pm[z], o));
+              td[z] = fmaxf(td[z], __shfl_xor_sync(0xffffffffu, td[z], o));
+              tm[z] = fmaxf(tm[z], __shfl_xor_sync(0xffffffffu, tm[z], o));
+            }
+            if (pd[z] > kMost || pm[z] > kDeepMost) {
+              const float to = fmaxf(ref[z], fmaxf(__fadd_ru(td[z], -kCentre), __fadd_ru(tm[z], -kDeep)));
+              const float a = a_exp2(ref[z] - to);
+              ref[z] = to;
+              l[z] *= a;
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  acc[b][h][z] *= a;
+                  acc[b][h][z + 2] *= a;
+                }
+            }
+          }
+          weigh();
         }
-        shift = shift_n;
       }
-      const float r0 = m[0] == -a_inf() ? 0.f : -(m[0] + shift), r1 = m[1] == -a_inf() ? 0.f : -(m[1] + shift);
+      {
+        float sum0, sum1;
+        f2_unpack(sum, sum0, sum1);
+        l[0] += sum0;
+        l[1] += sum1;
+      }
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const float p0 = a_exp2(fmaf(s[mt][0], f[0], r0)), p1 = a_exp2(fmaf(s[mt][1], f[1], r1));
-        const float p2 = a_exp2(fmaf(s[mt][2], f[0], r0)), p3 = a_exp2(fmaf(s[mt][3], f[1], r1));
-        l[0] += p0 + p2;
-        l[1] += p1 + p3;
-        const __half2 ha = __floats2half2_rn(p0, p1), hb = __floats2half2_rn(p2, p3);
-        const uint32_t b0 = transpose8x8(h2_bits(ha));  // row g, tokens t and t + 4
-        const uint32_t b1 = transpose8x8(h2_bits(hb));  // row g, tokens t + 8 and t + 12
-        uint32_t b0_rest = 0, b1_rest = 0;
-        if (kExactWeights) {
-          b0_rest = transpose8x8(h2_bits(__floats2half2_rn(p0 - __low2float(ha), p1 - __high2float(ha))));
-          b1_rest = transpose8x8(h2_bits(__floats2half2_rn(p2 - __low2float(hb), p3 - __high2float(hb))));
-        }
         const int k0 = mt * 16 + t;
-        uint32_t d[4][NB / 2];  // scales of tokens t, t + 4, t + 8, t + 12
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const unsigned char *sp = vs + (k0 + 4 * z) * (D / 16);
-          if constexpr (NB == 2) {
-            d[z][0] = *reinterpret_cast<const uint32_t *>(sp);
-          } else {
-#pragma unroll
-            for (int y = 0; y < NB / 4; ++y) {
-              const uint2 v = *reinterpret_cast<const uint2 *>(sp + 8 * y);
-              d[z][2 * y] = v.x;
-              d[z][2 * y + 1] = v.y;
-            }
-          }
-        }
-        uint32_t unseen0 = 0, unseen1 = 0;
-        if (!whole) {
-          // a weight of 0 contributes 0 even where the scale is not finite: such a token may be unseen
-          unseen0 = __vcmpeq2(b0, 0u);
-          unseen1 = __vcmpeq2(b1, 0u);
-        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const uint32_t sel = (b & 1) ? 0x7632u : 0x5410u;
-          const uint32_t d0 = __byte_perm(d[0][b / 2], d[1][b / 2], sel), d1 = __byte_perm(d[2][b / 2], d[3][b / 2], sel);
-          uint32_t e0 = kExactWeights ? fma_h2(b0, d0, mul_h2(b0_rest, d0)) : mul_h2(b0, d0);
-          uint32_t e1 = kExactWeights ? fma_h2(b1, d1, mul_h2(b1_rest, d1)) : mul_h2(b1, d1);
-          if (!whole) {
-            e0 &= ~unseen0;
-            e1 &= ~unseen1;
+          // weights times scales, rounded once; row g's of tokens t, t + 4 and t + 8, t + 12 (an 8x8 transpose each)
+          uint32_t e[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int x = 2 * mt + y;
+            const float d = (b & 1) ? __high2float(vd[x][b / 2]) : __low2float(vd[x][b / 2]);
+            uint32_t h = h2_bits(__floats2half2_rn(p[x][0] * d, p[x][1] * d));
+            if (!whole) h &= seen[x];  // (a weight of 0 times a scale that is not finite is none)
+            e[y] = transpose8x8(h);
           }
           const unsigned char *cp = tp + 18 * D + (b * 32 + k0) * 16 + 2 * g;
           const uint32_t v0 = *reinterpret_cast<const uint16_t *>(cp), v1 = *reinterpret_cast<const uint16_t *>(cp + 64);
@@ -823,10 +832,10 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
                          v3 = *reinterpret_cast<const uint16_t *>(cp + 192);
           const uint32_t x = __byte_perm(v0, v1, 0x5410u), y = __byte_perm(v2, v3, 0x5410u);
           const uint32_t x8 = x >> 8, y8 = y >> 8;
-          mma16816(acc[b][0], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, e0, e1);
-          mma16816(acc[b][1], x8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x000F000Fu, y8 & 0x00F000F0u, e0, e1);
-          mma16816(acc[b][0], eight[0], eight[1], eight[2], eight[3], e0, e1);
-          mma16816(acc[b][1], eight[0], eight[1], eight[2], eight[3], e0, e1);
+          mma16816(acc[b][0], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, e[0], e[1]);
+          mma16816(acc[b][1], x8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x000F000Fu, y8 & 0x00F000F0u, e[0], e[1]);
+          mma16816(acc[b][0], eight[0], eight[1], eight[2], eight[3], e[0], e[1]);
+          mma16816(acc[b][1], eight[0], eight[1], eight[2], eight[3], e[0], e[1]);
         }
       }
     };
@@ -864,7 +873,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     }
     float r[2];
 #pragma unroll
-    for (int z = 0; z < 2; ++z) r[z] = m[z] == -a_inf() ? -a_inf() : m[z] + shift;
+    for (int z = 0; z < 2; ++z) r[z] = ref[z] == kNone ? -a_inf() : ref[z];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
