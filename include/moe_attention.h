@@ -118,7 +118,7 @@ int moe_kv_read(const moe_kv_cache *c, const int32_t *starts, const int32_t *cu_
  * of n_kv_heads; query head h reads key/value head h / (n_q_heads / n_kv_heads)).
  * Token j of a sequence of n tokens stands at position p = n - q_tokens + j and
  * sees the positions [max(0, p - window + 1), p], or [0, p] when window == 0; a
- * row that sees nothing gives 0 (and lse -inf).  scale: positive and finite.
+ * row that sees nothing gives 0 (and lse -inf).  scale: positive, at most 2.3e38.
  * out: [n_seqs * q_tokens][n_q_heads][head_dim] contiguous, in dtype (MOE_BF16
  * or MOE_F16, q's too).  lse: fp32 [n_seqs * q_tokens][n_q_heads], the natural
  * logarithm of the sum of exponentials, or NULL.
@@ -139,7 +139,7 @@ int moe_kv_attention(const moe_kv_cache *c, const int32_t *seq_lens, const moe_t
  * sequence's queries stand at its last positions (keys before them: tokens that
  * an earlier call has seen): query i of n_q, with n_k keys, stands at p = n_k -
  * n_q + i and sees the keys [max(0, p - window + 1), p], or [0, p] when window
- * == 0; a row that sees nothing gives 0 (and lse -inf).  scale: positive and finite.
+ * == 0; a row that sees nothing gives 0 (and lse -inf).  scale: positive, at most 2.3e38.
  * q [n_q_tokens][n_q_heads][head_dim]; k, v [n_k_tokens][n_kv_heads][head_dim];
  * n_q_heads a multiple of n_kv_heads, at most 64 times it.  out: contiguous, q's
  * shape; lse: fp32 [n_q_tokens][n_q_heads], the natural logarithm of the sum of

@@ -18,6 +18,8 @@ namespace moe {
 
 constexpr int kMaxAttnHeads = 1024;
 constexpr int kMaxPageSize = 65536;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kMostScale = 2.3e38f;  // of a score: times log2(e) it is still a number
 constexpr uint64_t kAttnWaitNs = 2000000000ull;  // limit of every device wait
 constexpr uint32_t kAttnSpin = 1u << 26;
 

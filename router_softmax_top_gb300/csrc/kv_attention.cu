@@ -55,10 +55,10 @@
 namespace moe {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A row's reference is set so that its largest product of a weight with a scale is 2^kCentre, and moves when one exceeds
 // kMost; or, where values are small against their weights, so that no weight exceeds 2^kDeep, and moves at kDeepMost.
 constexpr float kCentre = 10.f, kMost = 16384.f, kDeep = 70.f, kDeepMost = 7.5557864e22f /* 2^76 */;
+constexpr float kEarly = 1.3877787807814457e-17f;  // 2^-56: 2^24 less 2^80 (see the score's factor)
 constexpr float kNone = -3.3e38f;  // the reference of a row that has seen nothing: below any score
 constexpr int kDecodeWarps = 8;
 constexpr int kDecodeSms = 152, kDecodeCtasMost = 2 * kDecodeSms;  // CTAs of a launch at most
@@ -606,6 +606,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
     const int len = __ldg(j.lens + walk.seq);
     // ---- the rows' queries as matrix operands
     float f[2];
+    bool big;
     int w0, w1;  // tiles [w0, w1) of the piece are seen whole by every row
     {
       float top = 0.f;
@@ -641,7 +642,11 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
         if (g == 0) q_start[b * 4 + t] = make_float4(s0, s1, s0, s1);
       }
       __syncwarp();
-      const float mine_f = j.scale * kLog2e * down * 16777216.f;
+      // The score's factor, scale log2(e) 2^(24 - e).  Where it is past what fp32 holds (queries of 2^100 and more), 2^80
+      // of it go ahead into the scores, which are below 2^20.  (0 times the -inf of what is not seen would be NaN.)
+      const float to_log2 = j.scale * kLog2e;
+      big = __any_sync(0xffffffffu, to_log2 * down * 16777216.f > 1e30f);
+      const float mine_f = fminf(fmaxf(big ? to_log2 * (down * kEarly) : to_log2 * down * 16777216.f, 1.17549435e-38f), 3.4e38f);
 #pragma unroll
       for (int z = 0; z < 2; ++z) f[z] = __shfl_sync(0xffffffffu, mine_f, 8 * t + 4 * z);
       int64_t a, b, lo, hi;
@@ -703,6 +708,12 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
           s[mt][3] = b ? fmaf(c[mt][3], fb, s[mt][3]) : c[mt][3] * fb;
         }
       }
+      if (big)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[0][x] *= 16777216.f / kEarly;
+          s[1][x] *= 16777216.f / kEarly;
+        }
       // ---- what a row does not see scores -inf
       uint32_t seen[4];  // of tokens 8 x + pg: all bits of the halves of the rows that see it
       if (!whole) {
@@ -745,13 +756,14 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       float p[4][2];
       uint64_t sum;
       auto weigh = [&]() {
-        const uint64_t f2 = f2_pack(f[0], f[1]), r2 = f2_pack(-ref[0], -ref[1]);
+        const uint64_t f2 = f2_pack(f[0], f[1]);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
+          // (the sums one by one: of packed pairs a product and the sum after it come out fused)
           float a, b;
-          f2_unpack(f2_add(f2_mul(f2_pack(s[x / 2][2 * (x % 2)], s[x / 2][2 * (x % 2) + 1]), f2), r2), a, b);
-          p[x][0] = a_exp2(a);
-          p[x][1] = a_exp2(b);
+          f2_unpack(f2_mul(f2_pack(s[x / 2][2 * (x % 2)], s[x / 2][2 * (x % 2) + 1]), f2), a, b);
+          p[x][0] = a_exp2(__fadd_rn(a, -ref[0]));
+          p[x][1] = a_exp2(__fadd_rn(b, -ref[1]));
           sum = x ? f2_add(sum, f2_pack(p[x][0], p[x][1])) : f2_pack(p[x][0], p[x][1]);
         }
       };
@@ -982,7 +994,7 @@ MOE_API int moe_kv_attention(const moe_kv_cache *c, const int32_t *seq_lens, con
   if (c && c->n_seqs == 0) return MOE_OK;
   if (const int rc = check_cache(c)) return rc;
   if (!seq_lens || !out || n_q_heads <= 0 || n_q_heads % c->n_kv_heads || q_tokens <= 0 || window < 0 ||
-      !(scale > 0.f && scale <= 3.4e38f))
+      !(scale > 0.f && scale <= kMostScale))
     return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
   if (n_q_heads > kMaxAttnHeads || q_tokens > 1024) return MOE_ERR_UNSUPPORTED;

@@ -59,7 +59,6 @@
 namespace moe {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTileRows = 128;
 
 struct PromptMaps {
@@ -1097,7 +1096,7 @@ MOE_API int moe_prompt_attention_shared(const moe_tensor *q, int32_t n_q_tokens,
                                         int32_t window, void *out, float *lse, int32_t dtype, int32_t *status,
                                         void *workspace, int64_t workspace_bytes, void *cuda_stream) {
   if (n_q_tokens < 0 || n_k_tokens < 0 || n_seqs < 0 || n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads ||
-      window < 0 || !(scale > 0.f && scale <= 3.4e38f))
+      window < 0 || !(scale > 0.f && scale <= kMostScale))
     return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
   const int group = n_q_heads / n_kv_heads;
