@@ -60,6 +60,7 @@ namespace moe {
 namespace {
 
 constexpr int kTileRows = 128;
+constexpr float kFar = 1024.f;  // log2 units
 
 struct PromptMaps {
   CUtensorMap q, k, v;
@@ -389,7 +390,7 @@ __device__ __noinline__ void row_by_keys(const PromptJob &j, int q_tok, int head
     for (int i = 0; i < N; ++i) s = fmaf(q[i], p_float(kp[i]), s);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float p = a_exp2(s * (j.scale * kLog2e) - ref);
+    const float p = a_exp2(__fmul_rn(s, j.scale * kLog2e) - ref);
     sum += p;
     for (int i = 0; i < N; ++i) acc[i] = fmaf(p, p_float(vp[i]), acc[i]);
   }
@@ -808,11 +809,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     const bool live = w.seq >= 0 && r < j.group * j.tile_tokens && tok < w.n_q;
     const int hi = live ? max(0, w.n_k - w.n_q + tok + 1) : 0;
     const int lo = j.window > 0 ? max(0, hi - j.window) : 0;
-    const float c = j.scale * kLog2e;
     // fp16 has few numbers far below 1, so its weights go up to 2^6 before the reference has to move, and to 2^14 then
     constexpr float kBelow = std::is_same<T, __half>::value ? 6.f : 0.f;
     constexpr float kMostSum = std::is_same<T, __half>::value ? 16384.f : 256.f;
     float m = live ? -a_inf() : 0.f, l = 0.f;  // reference (log2 units) and sum
+    const float c = j.scale * kLog2e;
     bool ok = true;
     const uint32_t o_col = tmem + lanes + C::kOCol + t * D;
     if constexpr (C::kQTmem) {
@@ -841,6 +842,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
     for (int jj = range.jb; jj < range.je && ok; ++jj) {
       const int n = jj - range.jb, buf = NQ == 1 ? (n & 1) : t;
       const uint32_t ph = (uint32_t)(NQ == 1 ? n >> 1 : n) & 1u;
+      // (no reference yet, or one so far from 0 that the fast way would show it)
+      bool again = n == 0 || __any_sync(0xffffffffu, live && !(fabsf(m) < kFar));
       ok = __all_sync(0xffffffffu, a_mbar_wait(&s_full[buf], ph, &s_fail));
       if (!ok) break;
       p_fence_after();
@@ -855,15 +858,22 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         for (int x = 0; x < BK; ++x)
           if (key0 + x < lo || key0 + x >= hi) s[x] = -a_inf();
       }
-      // Weights of 32 columns from x on, over the scores' first half; their sum.
-      auto weights = [&](int x, float ref) {
+      // Weights of 32 columns from x on, over the scores' first half; their sum.  Scores so large that their rounding (2^-14
+      // at kFar) shows in a weight are rounded before the reference is taken away, as the largest was for the reference:
+      // its weight then is of its own size.
+      auto weights = [&](int x, float ref, auto rounded) {
         const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(-ref, -ref);
         uint64_t sum[2] = {0, 0};
         uint32_t p[16];
 #pragma unroll
         for (int z = 0; z < 16; ++z) {
           float a, b;
-          f2_unpack(f2_fma(f2_pack(s[x + 2 * z], s[x + 2 * z + 1]), c2, r2), a, b);
+          if (decltype(rounded)::value) {  // (one by one: of packed pairs a product and the sum after it come out fused)
+            a = __fadd_rn(__fmul_rn(s[x + 2 * z], c), -ref);
+            b = __fadd_rn(__fmul_rn(s[x + 2 * z + 1], c), -ref);
+          } else {
+            f2_unpack(f2_fma(f2_pack(s[x + 2 * z], s[x + 2 * z + 1]), c2, r2), a, b);
+          }
           a = a_exp2(a);
           b = a_exp2(b);
           sum[z & 1] = f2_add(sum[z & 1], f2_pack(a, b));
@@ -876,12 +886,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
       };
       // The old reference first, without looking for the largest score: a sum of at most kMostSum says that no weight of
       // it was larger.
-      float sum = 0.f, ref = m == -a_inf() ? 0.f : m;
-      bool again = n == 0;
+      float sum = 0.f;
       if (!again) {
 #pragma unroll
-        for (int x = 0; x < BK; x += 32) sum += weights(x, ref);
-        again = __any_sync(0xffffffffu, live && (m == -a_inf() || !(sum <= kMostSum)));
+        for (int x = 0; x < BK; x += 32) sum += weights(x, m, std::false_type());
+        again = __any_sync(0xffffffffu, live && !(sum <= kMostSum));
       }
       if (again) {
         float top[4];
@@ -891,7 +900,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
         for (int x = 0; x < BK; x += 8)
 #pragma unroll
           for (int z = 0; z < 4; ++z) top[z] = fmaxf(top[z], fmaxf(s[x + z], s[x + 4 + z]));
-        const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c - kBelow);  // c > 0
+        const float m_new =
+            fmaxf(m, __fadd_rn(__fmul_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), c), -kBelow));  // c > 0
         p_st_wait();  // of the weights that are written again
         const float a = m == -a_inf() ? 0.f : a_exp2(m - m_new);
         m = m_new;
@@ -912,10 +922,16 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, PromptCfg<D>::kCtas)
           }
           p_st_wait();
         }
-        ref = m == -a_inf() ? 0.f : m;
+        const float ref = m == -a_inf() ? 0.f : m;
         sum = 0.f;
+        // (with the slower form alone: twelve packed prompts 65 us, 63 so)
+        if (__any_sync(0xffffffffu, live && fabsf(m) >= kFar && m > -a_inf())) {
 #pragma unroll
-        for (int x = 0; x < BK; x += 32) sum += weights(x, ref);
+          for (int x = 0; x < BK; x += 32) sum += weights(x, ref, std::true_type());
+        } else {
+#pragma unroll
+          for (int x = 0; x < BK; x += 32) sum += weights(x, ref, std::false_type());
+        }
       }
       l += sum;
       p_st_wait();

@@ -43,3 +43,26 @@ def test_scales_whose_exponent_overflows_are_refused(scale):
         moe.kv_attention(q, pages, table, i32([40]), page_size=64, n_kv_heads=1, scale=scale)
     with pytest.raises(moe.MoeError):
         moe.prompt_attention(q, q[:, :1], q[:, :1], i32([0, 1]), scale=scale)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype,size", [(torch.bfloat16, 3e4), (torch.bfloat16, 1e10), (torch.bfloat16, 3e38), (torch.float16, 60000.0)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n,m", [(200, 200), (3, 200)])
+def test_prompts_of_any_finite_size(d, dtype, size, sign, n, m):
+    g = torch.Generator(device="cuda").manual_seed(d)
+    c = (torch.randperm(m, generator=g, device="cuda") + 1).float()          # whole numbers: exact in both types
+    k = (c * (2.0 ** -20 if size > 1e30 else 1.0))[:, None, None].expand(m, 1, d).to(dtype).contiguous()
+    v = torch.randn(m, 1, d, generator=g, device="cuda").to(dtype)
+    q = torch.full((n, 2, d), sign * size, device="cuda").to(dtype)
+    q[:, 1] = 0                                                              # a head beside it whose scores are 0
+    cu_q, cu_k = i32([0, n]), i32([0, m])
+    out, lse = moe.prompt_attention(q, k, v, cu_q, cu_k, return_lse=True)
+    for i in range(n):
+        hi = m - n + i + 1
+        best = int((sign * c[:hi]).argmax())
+        assert torch.equal(out[i, 0], v[best, 0]), i
+        mean, mag = v[:hi, 0].double().mean(0), v[:hi, 0].double().abs().mean(0)
+        u = torch.finfo(dtype).eps / 2
+        assert bool(((out[i, 1].double() - mean).abs() <= u * mean.abs() + (u + 2.0 ** -12) * mag).all()), i
+    assert bool(torch.isfinite(lse).all())
