@@ -249,8 +249,9 @@ __device__ __forceinline__ TileRange tile_range(const PromptJob &j, const Prompt
   r.whole_hi = max(0, off + a + 1);
   int lo = 0;
   if (j.window > 0) {
-    lo = max(0, off + a + 1 - j.window);
-    r.whole_lo = max(0, off + b + 1 - j.window);
+    // (a row before the first key: less the widest windows, its position would pass 32 bits)
+    lo = max(0, max(0, off + a + 1) - j.window);
+    r.whole_lo = max(0, hi - j.window);
   }
   r.jb = lo / BK;
   r.je = (hi + BK - 1) / BK;

@@ -87,3 +87,15 @@ def test_full_offsets_set_no_status():
         status = i32([0])
         out = moe.prompt_attention(q, k, v, i32(cu), status=status)
         assert int(status) == 0 and bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("nq,nk", [(50, 20), (300, 10), (7, 200)])
+def test_the_widest_window_is_no_window(d, nq, nk):
+    # with more queries than keys the first ones stand before position 0: that less the window passes 32 bits
+    q, _ = rows(nq, 4, 2, d=d)
+    k, v = rows(nk, 2, 2, d=d)
+    want, lse = moe.prompt_attention(q, k, v, i32([0, nq]), i32([0, nk]), return_lse=True)
+    for window in (2147483647, 2147483640):
+        got, l = moe.prompt_attention(q, k, v, i32([0, nq]), i32([0, nk]), window=window, return_lse=True)
+        assert torch.equal(got, want) and torch.equal(l, lse)
