@@ -31,8 +31,10 @@
  *
  * Bad contents of device arrays (page numbers, lengths, positions) cannot be
  * refused by the host.  The kernels check them before every access, touch
- * nothing out of range, give the rows concerned NaN (an append writes nothing
- * for such a token), and set bits in *status when status is not NULL:
+ * nothing out of range, give the rows concerned NaN (an append writes nothing into
+ * the cache for such a token; its rotated rows, which do not depend on the page,
+ * are NaN where its length or position is bad), and set bits in *status when status
+ * is not NULL:
  */
 #ifndef MOE_ATTENTION_H
 #define MOE_ATTENTION_H

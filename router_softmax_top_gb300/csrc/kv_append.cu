@@ -239,38 +239,42 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) kv_append_kern
                      (at.pos >= 0 && no_rot ? MOE_KV_BAD_POSITION : 0);
     if (bits) atomicOr(j.c.status, bits);
   }
+  T *const q_to = static_cast<T *>(j.q_out) + (int64_t)i * j.hq * D + dim;
+  T *const k_to = static_cast<T *>(j.k_out) + (int64_t)i * j.hkv * D + dim;
+  if (at.pos < 0 || no_rot) {  // the token has no place: its rows are NaN
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    const float none[8] = {a_nan(), a_nan(), a_nan(), a_nan(), a_nan(), a_nan(), a_nan(), a_nan()};
+    for (int h = h0 + sub; h < min(h1, first_v); h += HPW) {
+      if (h < first_k) store8(q_to + h * D, none);
+      else if (j.k_out) store8(k_to + (h - first_k) * D, none);
+    }
+    return;
+  }
   const bool turned = dim < j.rot;
   float c[8], s[8];  // of this thread's values; s carries the sign of the rotation's other term
   int partner = lane;
   if (turned) {
-    if (no_rot) {
+    const float *ct = j.cos + at.pos * (j.rot / 2), *st = j.sin + at.pos * (j.rot / 2);
+    if (j.interleaved) {
+      const float4 a = __ldg(reinterpret_cast<const float4 *>(ct + dim / 2));
+      const float4 b = __ldg(reinterpret_cast<const float4 *>(st + dim / 2));
+      const float cc[4] = {a.x, a.y, a.z, a.w}, ss[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int z = 0; z < 8; ++z) c[z] = s[z] = __int_as_float(0x7fffffff);
-    } else {
-      const float *ct = j.cos + at.pos * (j.rot / 2), *st = j.sin + at.pos * (j.rot / 2);
-      if (j.interleaved) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(ct + dim / 2));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(st + dim / 2));
-        const float cc[4] = {a.x, a.y, a.z, a.w}, ss[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int z = 0; z < 8; ++z) {
-          c[z] = cc[z / 2];
-          s[z] = (z & 1) ? ss[z / 2] : -ss[z / 2];
-        }
-      } else {
-        const int first = dim < j.rot / 2, o = first ? dim : dim - j.rot / 2;
-        float ss[8];
-        expand8(load_raw(ct + o), c);
-        expand8(load_raw(st + o), ss);
-#pragma unroll
-        for (int z = 0; z < 8; ++z) s[z] = first ? -ss[z] : ss[z];
-        partner = first ? lane + j.rot / 16 : lane - j.rot / 16;
+      for (int z = 0; z < 8; ++z) {
+        c[z] = cc[z / 2];
+        s[z] = (z & 1) ? ss[z / 2] : -ss[z / 2];
       }
+    } else {
+      const int first = dim < j.rot / 2, o = first ? dim : dim - j.rot / 2;
+      float ss[8];
+      expand8(load_raw(ct + o), c);
+      expand8(load_raw(st + o), ss);
+#pragma unroll
+      for (int z = 0; z < 8; ++z) s[z] = first ? -ss[z] : ss[z];
+      partner = first ? lane + j.rot / 16 : lane - j.rot / 16;
     }
   }
-  const bool writes = at.page >= 0 && !no_rot;
-  T *const q_to = static_cast<T *>(j.q_out) + (int64_t)i * j.hq * D + dim;
-  T *const k_to = static_cast<T *>(j.k_out) + (int64_t)i * j.hkv * D + dim;
+  const bool writes = at.page >= 0;
   uint8_t *const tiles = static_cast<uint8_t *>(j.c.pages) + (int64_t)(at.page < 0 ? 0 : at.page) * j.c.page_stride +
                          kv_tile_off(D, j.c.page_size, 0, at.in_page);
   const int64_t tile_stride = kv_tile_off(D, j.c.page_size, 1, 0);  // from head to head
