@@ -27,7 +27,8 @@
  * it shows it.
  *
  * Sequences.  page_table[s][i] is the page of tokens [i page_size, (i + 1)
- * page_size) of sequence s.  Entries past a sequence's tokens are not read.
+ * page_size) of sequence s.  Entries past a sequence's tokens are not read.  A call
+ * of no sequences and no tokens does nothing.
  *
  * Bad contents of device arrays (page numbers, lengths, positions) cannot be
  * refused by the host.  The kernels check them before every access, touch

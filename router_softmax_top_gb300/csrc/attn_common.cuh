@@ -35,8 +35,7 @@ inline int check_cache(const moe_kv_cache *c) {
   const int64_t need = (int64_t)c->n_kv_heads * (c->page_size / kKvTile) * kv_tile_bytes(c->head_dim);
   if (c->page_stride < need || c->page_stride % 16 || (uintptr_t)c->pages % 16 || (!c->pages && c->n_pages > 0))
     return MOE_ERR_INVALID_ARG;
-  if (c->n_seqs == 0 || (c->table_width > 0 && (!c->page_table || c->table_stride < c->table_width)))
-    return MOE_ERR_INVALID_ARG;
+  if (c->n_seqs > 0 && c->table_width > 0 && (!c->page_table || c->table_stride < c->table_width)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 

@@ -423,6 +423,7 @@ MOE_API int moe_kv_append(const moe_kv_cache *c, const int32_t *starts, const in
   if (const int rc = check_cache(c)) return rc;
   if (n_tokens < 0 || !k || !v || dtype < MOE_F32 || dtype > MOE_F16) return MOE_ERR_INVALID_ARG;
   if (n_tokens == 0) return MOE_OK;
+  if (c->n_seqs == 0) return MOE_ERR_INVALID_ARG;
   const int size = dtype == MOE_F32 ? 4 : 2;
   const bool has_q = q && q->data;
   if (!starts || !cu_tokens || rot_dim < 0 || rot_dim > c->head_dim || rot_dim % 16) return MOE_ERR_INVALID_ARG;
@@ -459,6 +460,7 @@ MOE_API int moe_kv_read(const moe_kv_cache *c, const int32_t *starts, const int3
   if (const int rc = check_cache(c)) return rc;
   if (n_tokens < 0 || dtype < MOE_F32 || dtype > MOE_F16) return MOE_ERR_INVALID_ARG;
   if (n_tokens == 0 || (!k_out && !v_out)) return MOE_OK;
+  if (c->n_seqs == 0) return MOE_ERR_INVALID_ARG;
   if (!starts || !cu_tokens || (uintptr_t)k_out % 16 || (uintptr_t)v_out % 16) return MOE_ERR_INVALID_ARG;
   AppendJob j = {};
   j.c = *c;

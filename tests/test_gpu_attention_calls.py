@@ -37,3 +37,20 @@ def test_rows_without_a_place_are_nan_whatever_is_rotated(rot, interleaved):
         gone[list(dead)] = True
         for y in (q, k):
             assert bool(torch.isnan(y[gone]).all()) and bool(torch.isfinite(y[~gone]).all())
+
+
+def test_a_step_of_no_sequences():
+    pages = moe.kv_pages(1, 2, 64, 32)
+    table, none, cu = i32([[0]])[:0], i32([]), i32([0])
+    q, k = [torch.zeros(0, h, 64, device="cuda", dtype=torch.bfloat16) for h in (4, 2)]
+    a, b = moe.kv_append(pages, table, none, cu, k, k, page_size=32, q=q)
+    assert a.shape == (0, 4, 64) and b.shape == (0, 2, 64)
+    for t in moe.kv_read(pages, table, none, cu, 0, page_size=32, n_kv_heads=2, head_dim=64):
+        assert t.shape == (0, 2, 64)
+    assert moe.kv_attention(q, pages, table, none, page_size=32, n_kv_heads=2).shape == (0, 4, 64)
+    assert moe.prompt_attention(q, k, k, cu).shape == (0, 4, 64)
+    one = torch.zeros(1, 2, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(moe.MoeError):       # tokens without a sequence
+        moe.kv_append(pages, table, none, cu, one, one, page_size=32)
+    with pytest.raises(moe.MoeError):
+        moe.kv_read(pages, table, none, cu, 1, page_size=32, n_kv_heads=2, head_dim=64)
