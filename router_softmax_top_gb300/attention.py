@@ -4,7 +4,11 @@ held in 4 bits, attention over it, and causal attention over packed prompts
 in the library's CUDA kernels).
 
 All calls are stream-ordered on ``stream`` (default: PyTorch's current stream),
-allocate only their outputs, and do not wait for the GPU.  Token tensors are
+allocate only their outputs, and do not wait for the GPU.  The caller orders that
+stream after the work that makes the inputs.  Of a ``torch.cuda.Stream`` the tensors
+given may be dropped once the call returns: they are recorded on it.  Of a raw handle
+or a ``torch.cuda.ExternalStream``, which may be gone before they are, the caller keeps
+them until the work is done.  Token tensors are
 ``[tokens, heads, head_dim]`` with a contiguous last dimension; other strides are
 free as long as base and strides are whole multiples of 16 bytes (slices of a
 fused projection's output are).  Index tensors are contiguous int32 on the GPU;
@@ -122,12 +126,16 @@ def _cuda(dev):
     return d
 
 
-def _call(stream, dev, run):
-    """run(handle of the stream), its outputs allocated for that stream."""
+def _call(stream, dev, run, *tensors):
+    """run(handle of the stream), its outputs allocated for that stream; tensors: what it reads and writes."""
     if stream is None:
         return run(torch._C._cuda_getCurrentRawStream(dev))
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
+    elif not isinstance(stream, torch.cuda.ExternalStream):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
     with torch.cuda.stream(stream):
         return run(stream.cuda_stream)
 
@@ -204,7 +212,7 @@ def kv_append(pages, page_table, starts, cu_tokens, k, v, *, page_size, q=None, 
         if rc:
             _check(rc, "moe_kv_append")
         return qo, ko
-    return _call(stream, dev, run)
+    return _call(stream, dev, run, pages, page_table, starts, cu_tokens, q, k, v, cos, sin, q_out, k_out, status)
 
 
 def kv_read(pages, page_table, starts, cu_tokens, n_tokens, *, page_size, n_kv_heads, head_dim,
@@ -224,7 +232,7 @@ def kv_read(pages, page_table, starts, cu_tokens, n_tokens, *, page_size, n_kv_h
         if rc:
             _check(rc, "moe_kv_read")
         return k, v
-    return _call(stream, dev, run)
+    return _call(stream, dev, run, pages, page_table, starts, cu_tokens, status)
 
 
 _workspaces = {}
@@ -293,7 +301,7 @@ def kv_attention(q, pages, page_table, seq_lens, *, page_size, n_kv_heads, q_tok
             if rc:
                 _check(rc, "moe_kv_attention")
         return (o, lse) if return_lse else o
-    return _call(stream, dev, run)
+    return _call(stream, dev, run, q, pages, page_table, seq_lens, out, workspace, status)
 
 
 def prompt_attention_workspace(n_q_tokens, n_q_heads, n_k_tokens, n_kv_heads, head_dim, n_seqs, window=0, device="cuda"):
@@ -349,7 +357,7 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_l
         if rc:
             _check(rc, "moe_prompt_attention")
         return (o, lse) if return_lse else o
-    return _call(stream, dev, run)
+    return _call(stream, dev, run, q, k, v, cu_q, cu_k, out, workspace, status)
 
 
 def status_message(status) -> str:

@@ -54,3 +54,36 @@ def test_a_step_of_no_sequences():
         moe.kv_append(pages, table, none, cu, one, one, page_size=32)
     with pytest.raises(moe.MoeError):
         moe.kv_read(pages, table, none, cu, 1, page_size=32, n_kv_heads=2, head_dim=64)
+
+
+def test_inputs_given_up_after_a_call_on_another_stream_keep_their_memory():
+    n = 300
+    pages, table = some_cache(n)
+    lens, cu, ks = i32([n]), i32([0, n]), i32([0])
+    q1 = torch.randn(1, 4, 64, device="cuda").bfloat16()
+    q, k, v = [torch.randn(n, h, 64, device="cuda").bfloat16() for h in (4, 2, 2)]
+    cos, sin = moe.rope_table(n, 64)
+    calls = {
+        "decode": (lambda q, s: moe.kv_attention(q, pages, table, lens, page_size=32, n_kv_heads=2, stream=s), [q1]),
+        "prompt": (lambda q, k, v, s: moe.prompt_attention(q, k, v, cu, stream=s), [q, k, v]),
+        "append": (lambda q, k, v, s: moe.kv_append(torch.zeros_like(pages) if s is None else scratch, table, ks, cu, k, v,
+                                                    page_size=32, q=q, cos=cos, sin=sin, stream=s), [q, k, v]),
+        "read": (lambda t, s: moe.kv_read(pages, t, ks, cu, n, page_size=32, n_kv_heads=2, head_dim=64, stream=s), [table])}
+    side = torch.cuda.Stream()
+    scratch = torch.zeros_like(pages)
+    for name, (call, inputs) in calls.items():
+        want = call(*inputs, None)
+        given = [t.clone() for t in inputs]
+        at = [t.data_ptr() for t in given]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)     # the call has to wait behind this
+        got = call(*given, side)
+        given = None
+        # memory of the same sizes, asked for on this stream, and written
+        new = [torch.zeros_like(t) for t in inputs]
+        reused = [t.data_ptr() in at for t in new]
+        torch.cuda.synchronize()
+        want, got = [x if isinstance(x, tuple) else (x,) for x in (want, got)]
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), name
+        assert not any(reused), name
