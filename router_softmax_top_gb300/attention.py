@@ -77,6 +77,14 @@ def _refuse(what: str, code: int = MOE_ERR_INVALID_ARG):
     raise MoeError(code, what)
 
 
+_WIDEST = 2147483647
+
+
+def _window(window):
+    # (ctypes keeps the low 32 bits of a number; no sequence is longer than the widest window)
+    return _WIDEST if window > _WIDEST else window if window >= 0 else -1
+
+
 def _index(t, name, n, dev):
     if t.dtype is not torch.int32 or t.get_device() != dev or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         _refuse(f"{name} must be a contiguous int32 tensor of {n} entries on the GPU")
@@ -290,6 +298,8 @@ def kv_attention(q, pages, page_table, seq_lens, *, page_size, n_kv_heads, q_tok
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         _refuse("workspace must be a contiguous tensor on the GPU")
 
+    window = _window(window)
+
     def run(handle):
         o = _output(out, "out", shape, dtype, dev)
         lse = torch.empty((n, hq), dtype=torch.float32, device=_cuda(dev)) if return_lse else None
@@ -307,7 +317,8 @@ def kv_attention(q, pages, page_table, seq_lens, *, page_size, n_kv_heads, q_tok
 def prompt_attention_workspace(n_q_tokens, n_q_heads, n_k_tokens, n_kv_heads, head_dim, n_seqs, window=0, device="cuda"):
     """A workspace for prompt_attention, to be used by one stream (or one captured graph) at a time; None where a call
     of these sizes would not use one."""
-    n = int(_lib().moe_prompt_attention_workspace(n_q_tokens, n_q_heads, n_k_tokens, n_kv_heads, head_dim, n_seqs, window))
+    n = int(_lib().moe_prompt_attention_workspace(n_q_tokens, n_q_heads, n_k_tokens, n_kv_heads, head_dim, n_seqs,
+                                                  _window(window)))
     return _zero_counters(n, device) if n > 0 else None
 
 
@@ -317,10 +328,10 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_l
 
     q [n_q_tokens, n_q_heads, head_dim], k and v [n_k_tokens, n_kv_heads, head_dim], bfloat16 or float16;
     cu_q, cu_k int32 [n_seqs + 1] (cu_k None: cu_q); rows that no sequence holds give NaN, and a status.  With more keys
-    than queries a sequence's queries are its last tokens.  window > 0: a token sees itself and the window - 1 tokens before it.  Returns q's shape, and
-    the log of the sums of exponentials (fp32 [n_q_tokens, n_q_heads]) with return_lse.  Few queries of many keys
-    use a workspace: without `workspace` a module-level one per stream (inside a graph capture: one of the capture's
-    own); graphs that may run at the same time need their own."""
+    than queries a sequence's queries are its last tokens.  window > 0: a token sees itself and the window - 1 tokens
+    before it.  Returns q's shape, and the log of the sums of exponentials (fp32 [n_q_tokens, n_q_heads]) with
+    return_lse.  Few queries of many keys use a workspace: without `workspace` a module-level one per stream (inside a
+    graph capture: one of the capture's own); graphs that may run at the same time need their own."""
     dev, dtype = _device(q), q.dtype
     if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
         _refuse("q must be bfloat16 or float16 [tokens, heads, head_dim]", MOE_ERR_UNSUPPORTED)
@@ -337,6 +348,8 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, window=0, return_l
     word = _word(status, dev)
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         _refuse("workspace must be a contiguous tensor on the GPU")
+
+    window = _window(window)
 
     def run(handle):
         o = _output(out, "out", shape, dtype, dev)

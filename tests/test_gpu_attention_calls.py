@@ -87,3 +87,24 @@ def test_inputs_given_up_after_a_call_on_another_stream_keep_their_memory():
         want, got = [x if isinstance(x, tuple) else (x,) for x in (want, got)]
         assert all(torch.equal(a, b) for a, b in zip(want, got)), name
         assert not any(reused), name
+
+
+@pytest.mark.parametrize("window", [1 << 31, (1 << 32) + 5, (1 << 63) - 1, 10 ** 30])
+def test_windows_past_32_bits_are_no_window(window):
+    n = 200
+    pages, table = some_cache(n)
+    q, k, v = [torch.randn(n, h, 64, device="cuda").bfloat16() for h in (4, 2, 2)]
+    assert torch.equal(moe.prompt_attention(q, k, v, i32([0, n]), window=window), moe.prompt_attention(q, k, v, i32([0, n])))
+    args = (q[:1], pages, table, i32([n]))
+    assert torch.equal(moe.kv_attention(*args, page_size=32, n_kv_heads=2, window=window),
+                       moe.kv_attention(*args, page_size=32, n_kv_heads=2))
+
+
+@pytest.mark.parametrize("window", [-1, -(1 << 31), 5 - (1 << 32)])
+def test_negative_windows_are_refused(window):
+    pages, table = some_cache(40)
+    q = torch.randn(1, 4, 64, device="cuda").bfloat16()
+    with pytest.raises(moe.MoeError):
+        moe.kv_attention(q, pages, table, i32([40]), page_size=32, n_kv_heads=2, window=window)
+    with pytest.raises(moe.MoeError):
+        moe.prompt_attention(q, q[:, :2], q[:, :2], i32([0, 1]), window=window)
