@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import threading
 
 import torch
 
@@ -244,6 +245,7 @@ def kv_read(pages, page_table, starts, cu_tokens, n_tokens, *, page_size, n_kv_h
 
 
 _workspaces = {}
+_PER_THREAD_STREAM = 2  # cudaStreamPerThread: one handle, another stream in every thread
 # prompts of at most so many keys or of more rows (tokens times heads) never use a workspace
 _FEW_KEYS, _FEW_ROWS = 256, 131072
 
@@ -266,6 +268,8 @@ def _kept(key, make):
     # one per stream, as calls on one stream follow each other; a capture gets its own, which its graph keeps
     if torch.cuda.is_current_stream_capturing():
         return make()
+    if key[1] == _PER_THREAD_STREAM:
+        key += (threading.get_ident(),)
     ws = _workspaces.get(key)
     if ws is None:
         ws = _workspaces[key] = make()

@@ -1,5 +1,6 @@
 """Calls of the attention operators that never reach a GPU."""
 import ctypes
+import threading
 
 import pytest
 
@@ -24,3 +25,38 @@ def test_a_step_of_no_sequences(lib, table):
         assert lib.moe_kv_read(c, 1 << 20, 1 << 20, n, 1 << 20, 1 << 20, 1, None) == code
     assert lib.moe_kv_attention(c, 1 << 20, t, 8, 1, 1.0, 0, 1 << 20, None, 1, 1 << 20, 1 << 30, None) == moe.MOE_OK
     assert lib.moe_prompt_attention(t, 0, 8, t, t, 0, 8, 128, 1 << 20, 1 << 20, 0, 0.1, 0, 1 << 20, None, 1, None, None) == moe.MOE_OK
+
+
+# ------------------------------------------------------------------- the workspaces that are kept
+@pytest.fixture
+def kept(monkeypatch):
+    monkeypatch.setattr(A.torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(A, "_workspaces", {})
+    made = []
+
+    def get(*key):
+        return A._kept(key, lambda: made.append(key) or object())
+    return get, made
+
+
+def test_a_stream_keeps_its_workspaces(kept):
+    get, made = kept
+    a, b, c = get(0, 5, 64), get(0, 5, "prompt", 64), get(0, 6, 64)
+    assert len({id(x) for x in (a, b, c)}) == 3
+    assert get(0, 5, 64) is a and get(0, 5, "prompt", 64) is b and len(made) == 3
+
+
+def test_threads_do_not_share_the_workspace_of_the_stream_each_has(kept):
+    # handle 2 is another stream in every thread, and two of them may run at once
+    get, _ = kept
+    mine, theirs = [get(0, 2, 64)], []
+    t = threading.Thread(target=lambda: theirs.append(get(0, 2, 64)))
+    t.start()
+    t.join()
+    assert theirs[0] is not mine[0] and get(0, 2, 64) is mine[0]
+    # of any other stream the threads share one
+    mine = get(0, 7, 64)
+    t = threading.Thread(target=lambda: theirs.append(get(0, 7, 64)))
+    t.start()
+    t.join()
+    assert theirs[1] is mine
