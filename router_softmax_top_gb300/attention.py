@@ -245,6 +245,10 @@ def kv_read(pages, page_table, starts, cu_tokens, n_tokens, *, page_size, n_kv_h
 
 
 _workspaces = {}
+_workspaces_lock = threading.Lock()
+# Workspaces kept at most, 6 to 20 MB each: a program that goes on making streams would keep one or two of each.  The
+# oldest goes first; work that still uses it is on the stream whose later allocations alone can have its memory.
+_MOST_KEPT = 32
 _PER_THREAD_STREAM = 2  # cudaStreamPerThread: one handle, another stream in every thread
 # prompts of at most so many keys or of more rows (tokens times heads) never use a workspace
 _FEW_KEYS, _FEW_ROWS = 256, 131072
@@ -272,7 +276,11 @@ def _kept(key, make):
         key += (threading.get_ident(),)
     ws = _workspaces.get(key)
     if ws is None:
-        ws = _workspaces[key] = make()
+        ws = make()
+        with _workspaces_lock:
+            while len(_workspaces) >= _MOST_KEPT:
+                del _workspaces[next(iter(_workspaces))]
+            _workspaces[key] = ws
     return ws
 
 

@@ -60,3 +60,12 @@ def test_threads_do_not_share_the_workspace_of_the_stream_each_has(kept):
     t.start()
     t.join()
     assert theirs[1] is mine
+
+
+def test_workspaces_of_streams_that_come_and_go_are_given_up(kept):
+    get, made = kept
+    for s in range(1000):
+        get(0, 16 * s + 16, 128)
+    assert len(made) == 1000 and len(A._workspaces) <= A._MOST_KEPT <= 64
+    get(0, 16 * 1000, 128)               # the last one is still there
+    assert len(made) == 1000
