@@ -11,15 +11,16 @@
 // two or three instruction lanes.  Hence:
 //  * Codes go to the matrix unit as they are.  A nibble masked out in place is, read
 //    as fp16, the subnormal q 2^-24 (bits 0-3) or q 2^-20 (bits 4-7), which the
-//    matrix instructions multiply exactly; so 8 codes take 4 masks and 1 shift, no
-//    conversion.  The -8 of (q - 8) is a constant of the query for the scores (it
-//    starts the accumulator) and a product with a constant matrix for the values.
-//    The two nibbles' factors meet in the query (q 2^-4 for high nibbles) and in the
-//    output's last scaling.
+//    matrix instructions multiply exactly; so 8 key codes take 4 masks and 1 shift, 8
+//    value codes 4 masks and 3 shifts, no conversion.  The -8 of (q - 8) is a constant
+//    of the query for the scores (it starts the accumulator) and a product with a
+//    constant matrix for the values.  The keys' nibbles' factors meet in the query
+//    (q 2^-4 for high nibbles).
 //  * Scores: S^T = K Q^T (m16n8k16): 16 keys x 8 rows, one accumulator per 32-value
 //    block, which the key's scale multiplies in fp32.  The query is rounded to fp16
 //    after a power-of-two scaling per row (exact for bf16 and fp16 inputs down to
-//    2^-24 of the row's largest value).
+//    2^-24 of the row's largest value).  Sums are fp32, cut off 2^-18 below the low
+//    nibbles' largest product of a block: 2^-17 scale sum |q k| covers a score.
 //  * Values: O^T = V^T E^T, E = p d, a weight times its value's scale per block, formed
 //    in fp32, rounded to fp16 once and transposed 8x8 on the way.  A row's reference
 //    goes by its largest product p d, not by p and d apart: that product lies between
@@ -593,10 +594,10 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
 #pragma unroll 1
     for (int x = 0; x < S; ++x) issue(x);
 
-  // -8 as fp16 pairs: -8 2^-24 for the low nibbles' rows, -8 2^-20 for the high ones'.  Four registers that the
-  // compiler cannot see through: it would build the operand anew, move by move, for every instruction.
+  // -8 2^-20 as fp16 pairs.  Four registers that the compiler cannot see through: it would build the operand anew, move
+  // by move, for every instruction.
   uint32_t eight[4];
-  asm volatile("mov.b32 %0, 0x80088008;\n mov.b32 %1, 0x80808080;\n mov.b32 %2, 0x80088008;\n mov.b32 %3, 0x80808080;"
+  asm volatile("mov.b32 %0, 0x80808080;\n mov.b32 %1, 0x80808080;\n mov.b32 %2, 0x80808080;\n mov.b32 %3, 0x80808080;"
                : "=r"(eight[0]), "=r"(eight[1]), "=r"(eight[2]), "=r"(eight[3]));
 
   for (uint32_t piece = 0; work; ++piece) {
@@ -843,9 +844,12 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
           const uint32_t v2 = *reinterpret_cast<const uint16_t *>(cp + 128),
                          v3 = *reinterpret_cast<const uint16_t *>(cp + 192);
           const uint32_t x = __byte_perm(v0, v1, 0x5410u), y = __byte_perm(v2, v3, 0x5410u);
-          const uint32_t x8 = x >> 8, y8 = y >> 8;
-          mma16816(acc[b][0], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, e[0], e[1]);
-          mma16816(acc[b][1], x8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x000F000Fu, y8 & 0x00F000F0u, e[0], e[1]);
+          // All codes go to bits 4 to 7: of an operand below the normal numbers the product is added by the exponent of
+          // the least normal one.  With the low nibbles left in bits 0 to 3 whatever is below 2^-18 of 8 w d was cut off
+          // the sums (so 2^-22; 128 sequences 131 and 134 us).
+          mma16816(acc[b][0], (x << 4) & 0x00F000F0u, x & 0x00F000F0u, (y << 4) & 0x00F000F0u, y & 0x00F000F0u, e[0], e[1]);
+          mma16816(acc[b][1], (x >> 4) & 0x00F000F0u, (x >> 8) & 0x00F000F0u, (y >> 4) & 0x00F000F0u,
+                   (y >> 8) & 0x00F000F0u, e[0], e[1]);
           mma16816(acc[b][0], eight[0], eight[1], eight[2], eight[3], e[0], e[1]);
           mma16816(acc[b][1], eight[0], eight[1], eight[2], eight[3], e[0], e[1]);
         }
@@ -870,7 +874,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
       tiles(pass ? w1 : walk.at, pass ? walk.end : w0, std::false_type());
       if (pass == 0) tiles(w0, w1, std::true_type());
     }
-    // ---- the piece: l over the lanes that share a row; accumulators without the nibbles' factors
+    // ---- the piece: l over the lanes that share a row; accumulators without the codes' factor
     int poison = 0;  // status bits: what the piece's result is worth
     if (no_page[warp][piece & 7]) poison |= MOE_KV_BAD_PAGE;
     if (tiles_on_way.dead) poison |= MOE_KV_TIMED_OUT;
@@ -891,7 +895,7 @@ __global__ void __launch_bounds__(32 * DecodeCfg<D>::kWarps, DecodeCfg<D>::kCtas
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int z = 0; z < 4; ++z) acc[b][h][z] *= z < 2 ? 16777216.f : 1048576.f;
+        for (int z = 0; z < 4; ++z) acc[b][h][z] *= 1048576.f;
     Walk next = walk;
     const bool more = walk_next(j, next);
     if (more) load_q(next);

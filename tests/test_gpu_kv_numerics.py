@@ -6,7 +6,9 @@ row's largest such product is at least 2^10.  A value is at most 8 scales, so n 
 most n 2^-35 T beside the relative part, T = max_j w_j max_d |v_jd|; where T is below 2^-70 of the
 weights the unit is tied to the largest weight instead, n 2^-92.  Scores are fp32 sums (2^-17 Z, Z = max_j
 scale sum |q k|), the result is rounded once.  Hence
-|error| <= sum_j w_j |v_j| (2^-11 + 2^-12 + 2^-17 Z) + n (2^-35 T + 2^-92) + half a step of the result."""
+|error| <= sum_j w_j |v_j| (2^-11 + 2^-12 + 2^-17 Z) + n (2^-35 T + 2^-92) + half a step of the result.
+(Beside that the accumulators' own rounding, where single keys of exact value 0 have most of the weight: see
+tests/test_gpu_kv_ragged.py.)"""
 import pytest
 import torch
 
