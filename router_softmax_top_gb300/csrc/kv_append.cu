@@ -7,11 +7,16 @@
 // with a border, and the same border has to be met by any other implementation.
 //
 // Bound: memory (every value is read once and written once); for a token or two, the
-// latency of the chain cu -> start -> table -> store.  18432 prompt tokens of 48 heads of
-// 128 (bf16) are appended in 86 us, 0.74 of the measured copy rate, with the SMs issuing
+// latency of the chain cu -> start -> table -> store.  18439 prompt tokens of 48 heads of
+// 128 are appended in 85 us as bf16, 0.77 of the measured copy rate, with the SMs issuing
 // in three cycles of four: the division of every key and value by its block's scale and
-// the packing of codes cost as much as the bytes do.  A single token takes 2.6 us, its
-// launch among them.  Layout of the work: a thread takes 8 consecutive
+// the packing of codes cost as much as the bytes do; as fp32, twice the bytes, in 137 us,
+// 0.93 of that rate.  A single token takes 3 us, its launch among them.  Reading 65536
+// cached tokens of 8 heads of 128 back takes 70 us, 0.73 of the copy rate, and the 18439
+// that were just appended 23.5 us (14.3 would be the copy rate): a warp reads a token, so
+// it uses half of every 32-byte sector of codes and 8 bytes of one of scales, and the
+// warps of the neighbouring tokens ask for the same sectors again.
+// Layout of the work: a thread takes 8 consecutive
 // values (one 16-byte load of a 16-bit type), so a head is D/8 lanes of one warp,
 // the rotation's other half sits in another lane of the same head (a shuffle), and
 // a quantisation block is 4 neighbouring lanes.  A warp stays on one token and
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_read_kernel(const Append
 }
 
 // Heads per warp, in whole turns of the warp: all of a token's where the tokens alone make 32 warps per SM, fewer where
-// they do not, one turn at least.  Measured with the read: 18432 tokens 107 us so and 308 us at one turn per warp (every
+// they do not, one turn at least.  Measured with the read: 18439 tokens 107 us so and 308 us at one turn per warp (every
 // warp finds its token's place anew); one token 5.1 us so and 11.0 us with all heads in one warp, 64 tokens 7.1 and 18.2.
 int heads_per_warp(int n_tokens, int total, int per_turn) {
   const int64_t warps = 152 * 32;

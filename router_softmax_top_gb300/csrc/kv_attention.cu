@@ -5,8 +5,10 @@
 // reference r; a warp keeps one reference per row and moves it rarely (the sums then
 // scale by a power of two).
 //
-// Bound: the cache's bytes (1.125 bytes per cached value of a head pair, each read
-// once, for all query heads that share the head).  What makes that hard is the
+// Bound: the cache's bytes (1.125 bytes per cached value of a head pair, each read once
+// for up to 8 rows, query heads that share the head times query tokens; every further 8
+// rows read and unpack them again: 64 sequences of 64 to 8192 tokens on 4 key heads of 128
+// take 49 us with 8 rows, 79 with 16 and 135 with 32).  What makes that hard is the
 // unpacking: at 6.8 TB/s an SM receives ~40 codes per cycle, so a code may cost it
 // two or three instruction lanes.  Hence:
 //  * Codes go to the matrix unit as they are.  A nibble masked out in place is, read
@@ -31,10 +33,10 @@
 //    products to 0.)  Weights and their sums are fp32.
 //  * Rows in the matrix's N: 8 of them (heads sharing a key head x query tokens).
 // Measured: 128 sequences of 64 to 8192 tokens (8 key heads of 128, 611 MB of cache) in
-// 125 us, 4.9 TB/s or 0.72 of the measured copy rate; their tiles alone go by in 100 us,
-// 6 us go to finding shares and the first bytes, 15 to 20 us to slower SMs and the last
-// merges.  One sequence of 131071 tokens takes 46 us, of which 23 us stream.  The unpacking
-// keeps the integer pipe half busy and the matrix pipe a third; scores and values
+// 133 us, 4.6 TB/s or 0.68 of the measured copy rate; 6 us of it go to finding shares and
+// the first bytes, 15 to 20 us to slower SMs and the last merges (stamps).  One sequence of
+// 131071 tokens takes 47 us, its bytes alone 22.  About 700 instructions per tile, all told,
+// keep the integer pipe half busy and the matrix pipe a third.  Scores and values
 // interleaved over two tiles, more or fewer warps, deeper rings and whole bytes instead of
 // masked high nibbles were all slower or less exact.
 //
@@ -129,13 +131,13 @@ __device__ __forceinline__ void store_pair(__half *p, float a, float b) {
 __device__ __noinline__ bool wait_for_tile(uint64_t *bar, uint32_t parity) { return a_mbar_wait(bar, parity); }
 
 // What a pair costs beside its tiles, in tiles (its queries' set-up and its result).  Measured with 1, 2, 4, 8 and 16:
-// 128 sequences of 64 to 8192 tokens 132, 125, 125, 129 and 136 us; one of 131071 tokens 50, 48, 46, 46 and 45 us.
+// 128 sequences of 64 to 8192 tokens 139, 133, 133, 136 and 144 us; one of 131071 tokens 53, 49, 47.5, 47 and 47 us.
 constexpr int kPairCost = 4;
 // Where there are CTAs for all pairs, a pair takes a CTA of its own and no more if its longest warp then has at most
 // this many tiles more than with even shares, which the merges across CTAs cost.  A CTA per pair against shares: 333
-// tokens 11.0 and 14.3 us, 1000 tokens 13.4 and 13.9 us, 32 sequences of 1024 tokens of 64 (256 pairs) 13.2 and 17.5 us,
-// 8 of 1000 (64 pairs) 13.9 and 15.4 us, 8 of 2000 18.3 and 18.2 us; but one of 2000 17.8 and 13.8 us, of 4000 26.3 and
-// 14.9 us.
+// tokens 10.3 and 14.6 us, 1000 tokens 13.2 and 15.0 us, 32 sequences of 1024 tokens of 64 (256 pairs) 13.2 and 17.9 us,
+// 8 of 1000 (64 pairs) 13.7 and 15.8 us, 8 of 2000 18.5 and 18.9 us; but one of 2000 17.9 and 14.8 us, of 4000 27.1 and
+// 14.6 us.
 constexpr int kAloneMore = 4;
 
 // A walk over the pieces (tiles of one pair) of a warp's share.  Pairs are ordered by sequence, then key head

@@ -28,15 +28,19 @@
 //    issuing warp waits for is time that the tensor cores lose, as their queue is short:
 //    it waits once per product, on the weights' barrier, which a helper holds back
 //    until the keys and values are there too.
-// Measured: 8192 tokens, 32 heads of 128 on 8: 360 us, 1.53 PFLOP/s or 0.80 of the
-// measured bf16 rate (454 us with descriptors outside uniform registers, 393 us with
-// four waits and six commits per block).  The tensor pipe is active 65% of all cycles;
-// in the loop a block takes ~2700 cycles, 2048 of them matrix instructions at their full
-// rate, and a CTA's ends about a tenth of its time.  Heads of 64 are bound by the
-// exponentials' chain and by the ends of short CTAs, hence two CTAs per SM (75 -> 68 us
-// for twelve packed prompts).  Heads of 256 have one row tile: their queries are moved to
-// tensor memory, where they do not take a third of the shared memory's bandwidth, and
-// their place holds a third stage of keys and values (a block of 64 keys takes 0.78 us so,
+// Measured: 8192 tokens, 32 heads of 128 on 8: 357 us in short runs and 382 in long ones,
+// 1.54 and 1.44 PFLOP/s or 0.80 and 0.75 of the measured bf16 rate (454 us with
+// descriptors outside uniform registers, 393 us with four waits and six commits per
+// block).  The tensor pipe is active 65% of all cycles; in the loop a block takes ~2700
+// cycles, 2048 of them matrix instructions at their full rate, and a CTA's ends about a
+// tenth of its time.  Heads of 64 (twelve packed prompts 61 us, their products alone 15)
+// fill no pipe: tensor cores and exponentials a quarter each, issue slots 42%.  Their warps
+// wait, for scores to arrive from tensor memory and for each other; a block has 64 keys,
+// so half the work between two waits, and CTAs are short.  Two CTAs per SM fill some of
+// that (75 -> 68 us, in the order of the sequences).  Heads of 256 have one row tile: their
+// queries are moved to tensor memory, where they do not take a third of the shared
+// memory's bandwidth, and their place holds a third stage of keys and values (a block of
+// 64 keys takes 0.78 us so,
 // 0.92 before; its products alone take 0.55: 32 cycles each of 64 keys with queries from
 // tensor memory, 48 from shared memory).  Neither the exponentials nor their chain bound
 // it: two threads per row took 0.79 us, weights through shared memory, so that scores run
@@ -82,8 +86,8 @@ struct PromptJob {
 
 // Where a call's tile groups leave half the GPU idle or more, each group's keys are shared out over as many CTAs as there
 // is room for, and the last one done joins the parts.  It reads a part in about the time of a block, so there are no more
-// parts than a part has blocks.  Whole and shared, 32 heads of 128 on 8: 16 tokens after 1000 16.0 and 15.4 us, 37 after
-// 2000 29 and 21, 512 after 4096 58 and 43, 256 after 60,000 650 and 186, 5 after 100,000 980 and 77 us.
+// parts than a part has blocks.  Whole and shared, 32 heads of 128 on 8: 16 tokens after 1000 15.9 and 15.4 us, 37 after
+// 2000 29 and 22, 512 after 4096 57 and 45, 256 after 60,000 645 and 185, 5 after 100,000 968 and 77 us.
 // A part has at least kMinPart blocks (parts of 4 blocks of 64, 512 tokens: heads of 64 17.4 us, whole 13.8; heads of 256
 // 22.3, whole 14.2), and, where two parts are on the same SM (heads of 64), at least kMinPair (2 of 8, 1024 tokens: 24.0,
 // whole 20.6; 2 of 16, 1024 after 1024: 32.8, whole 33.1; 2 of 24, 16 sequences of 7 after 3000: 33.1, whole 41.6).
