@@ -143,7 +143,7 @@ def _call(stream, dev, run, *tensors):
         stream = torch.cuda.ExternalStream(stream)
     elif not isinstance(stream, torch.cuda.ExternalStream):
         for t in tensors:
-            if t is not None:
+            if t is not None and t.is_cuda:  # (an output that is not is refused below)
                 t.record_stream(stream)
     with torch.cuda.stream(stream):
         return run(stream.cuda_stream)

@@ -108,3 +108,16 @@ def test_negative_windows_are_refused(window):
         moe.kv_attention(q, pages, table, i32([40]), page_size=32, n_kv_heads=2, window=window)
     with pytest.raises(moe.MoeError):
         moe.prompt_attention(q, q[:, :2], q[:, :2], i32([0, 1]), window=window)
+
+
+def test_outputs_that_are_refused_are_refused_on_any_stream():
+    pages, table = some_cache(40)
+    q, k = [torch.randn(1, h, 64, device="cuda").bfloat16() for h in (4, 2)]
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        with pytest.raises(moe.MoeError):
+            moe.kv_attention(q, pages, table, i32([40]), page_size=32, n_kv_heads=2, out=q.cpu(), stream=stream)
+        with pytest.raises(moe.MoeError):
+            moe.prompt_attention(q, k, k, i32([0, 1]), out=q.cpu(), stream=stream)
+        with pytest.raises(moe.MoeError):
+            moe.kv_append(pages, table, i32([0]), i32([0, 1]), k, k, page_size=32, k_out=k.cpu(), stream=stream)
