@@ -36,7 +36,7 @@ MOE_POLICY_LRU = 0
 MOE_POLICY_SCORE = 1
 MOE_POLICY_ADOPT = 2
 
-# every symbol include/moe_cache.h declares
+# every symbol the headers in include/ declare
 EXPORTS = ("moe_cache_init", "moe_layer_forward", "moe_cache_sync", "moe_cache_stats",
            "moe_layer_last_plan", "moe_cache_preload", "moe_cache_inject", "moe_cache_set_timing",
            "moe_cache_timing",
@@ -45,7 +45,8 @@ EXPORTS = ("moe_cache_init", "moe_layer_forward", "moe_cache_sync", "moe_cache_s
            "moe_cache_state_size", "moe_cache_save_state", "moe_cache_load_state",
            "moe_kv_page_bytes", "moe_kv_append", "moe_kv_read", "moe_kv_attention_workspace",
            "moe_kv_attention", "moe_prompt_attention",
-           "moe_prompt_attention_workspace", "moe_prompt_attention_shared")
+           "moe_prompt_attention_workspace", "moe_prompt_attention_shared",
+           "moe_route", "moe_layer_forward_routed")
 
 MOE_STATE_MAGIC = 0x53454F4D
 MOE_STATE_VERSION = 1
@@ -111,6 +112,8 @@ def lib() -> ctypes.CDLL:
                                      vp, ctypes.POINTER(vp)]
         L.moe_layer_forward.restype = ctypes.c_int
         L.moe_layer_forward.argtypes = [vp, i32, vp, vp, i32, vp, vp]
+        L.moe_layer_forward_routed.restype = ctypes.c_int
+        L.moe_layer_forward_routed.argtypes = [vp, i32, vp, vp, vp, i32, vp, vp]
         L.moe_cache_sync.restype = ctypes.c_int
         L.moe_cache_sync.argtypes = [vp, vp]
         L.moe_cache_stats.restype = ctypes.c_int
@@ -264,6 +267,23 @@ class MoECache:
         _check(rc, "moe_layer_forward")
         return out
 
+    def forward_routed(self, layer: int, ids, weights, x, out=None, stream=None):
+        """The layer with a choice of experts made before (``route``): ids cuda int32 [T, k], weights cuda fp32 [T, k];
+        x and the result as for ``forward``.  Ids outside the experts, twice in a token, or weights that are not finite
+        are an error of the handle, like a non-finite logit."""
+        import torch
+        T = x.shape[0]
+        assert ids.is_cuda and ids.dtype == torch.int32 and ids.is_contiguous() and ids.shape == (T, self.k)
+        assert weights.is_cuda and weights.dtype == torch.float32 and weights.is_contiguous() and weights.shape == (T, self.k)
+        assert x.is_cuda and x.is_contiguous()
+        if out is None:
+            out = torch.empty((T, self.H), dtype=torch.float32, device=x.device)
+        _check(int(lib().moe_layer_forward_routed(self.handle, layer, ctypes.c_void_p(ids.data_ptr()),
+                                                  ctypes.c_void_p(weights.data_ptr()), ctypes.c_void_p(x.data_ptr()), T,
+                                                  ctypes.c_void_p(out.data_ptr()), _stream_handle(stream))),
+               "moe_layer_forward_routed")
+        return out
+
     def forward_rc(self, layer: int, logits, x, out, stream=None) -> int:
         """Same as forward but returns the status code instead of raising."""
         return moe_layer_forward(self.handle, layer, logits.data_ptr(), x.data_ptr(),
@@ -366,8 +386,16 @@ _ATTENTION = ("kv_append", "kv_read", "kv_attention", "kv_attention_workspace", 
               "MOE_KV_BAD_LENGTH", "MOE_KV_BAD_POSITION", "MOE_KV_TIMED_OUT", "MOE_KV_COUNTER_BYTES")
 
 
+_ROUTING = ("route", "MOE_ROUTE_BAD_LOGIT")
+
+
 def __getattr__(name):
     # loaded on first use: the rest of this module does without PyTorch
+    if name in _ROUTING:
+        from . import routing
+        for n in _ROUTING:
+            globals()[n] = getattr(routing, n)
+        return globals()[name]
     if name in _ATTENTION:
         from . import attention
         for n in _ATTENTION:

@@ -28,6 +28,7 @@ MOE_KV_BAD_PAGE = 1
 MOE_KV_BAD_LENGTH = 2
 MOE_KV_BAD_POSITION = 4
 MOE_KV_TIMED_OUT = 8
+MOE_ROUTE_BAD_LOGIT = 16
 MOE_KV_COUNTER_BYTES = 4096
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -391,5 +392,6 @@ def status_message(status) -> str:
     names = ((MOE_KV_BAD_PAGE, "a page number outside the cache"),
              (MOE_KV_BAD_LENGTH, "a length or offset outside the page table or the tensor"),
              (MOE_KV_BAD_POSITION, "a position past the rotation table"),
-             (MOE_KV_TIMED_OUT, "a device wait gave up"))
+             (MOE_KV_TIMED_OUT, "a device wait gave up"),
+             (MOE_ROUTE_BAD_LOGIT, "a logit that is NaN or +infinity, or a bias that is not finite"))
     return "; ".join(text for bit, text in names if bits & bit)

@@ -146,7 +146,9 @@ inline cudaError_t ensure_dyn_smem(Kern kernel, size_t bytes, DynSmemLimit &limi
 
 // ------------------------------------------------------------ launchers
 struct PlanArgs {
-  const float *logits;  // [T, E]
+  const float *logits;  // [T, E], or null: the caller chose
+  const int32_t *given_ids;  // the caller's choice [T, k], and its weights, or null
+  const float *given_w;
   int T, E, k, S, weight_mode;
   // per-layer state
   int32_t *slot_expert;  // [S]
@@ -173,7 +175,7 @@ struct PlanArgs {
   int32_t *sync;      // per-call counters, the first sync_n zeroed here
   int sync_n;
   int32_t *route_bad; // device word for the grid router's non-finite flag (zero between calls)
-  int routed;         // set by launch_plan when route_kernel produced ids and w
+  int routed;         // set by launch_plan when an earlier kernel produced ids and w
   Mailbox *mailbox;   // device alias of the mapped host mailbox, or null
   int mailbox_stage_cap;  // capacity of the mailbox's unit_begin array
   uint32_t seq;

@@ -25,6 +25,7 @@
 
 #include "common.cuh"
 #include "moe_cache.h"
+#include "moe_route.h"
 #include "plan_check.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -539,8 +540,9 @@ MOE_API int moe_cache_init(const moe_cache_config *cfg, const moe_host_store *st
   return MOE_OK;
 }
 
-MOE_API int moe_layer_forward(moe_cache *c, int32_t layer, const float *d_logits, const void *d_x,
-                              int32_t n_tokens, float *d_out, void *cuda_stream) {
+// d_logits, or d_ids and d_weights
+static int layer_forward(moe_cache *c, int32_t layer, const float *d_logits, const int32_t *d_ids, const float *d_weights,
+                         const void *d_x, int32_t n_tokens, float *d_out, void *cuda_stream) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (c->poisoned) return MOE_ERR_POISONED;
   if (const int de = device_error_code(c)) return poison(c, de);
@@ -548,7 +550,7 @@ MOE_API int moe_layer_forward(moe_cache *c, int32_t layer, const float *d_logits
   if (layer < 0 || layer >= g.n_layers || n_tokens < 0 || n_tokens > g.max_tokens)
     return MOE_ERR_INVALID_ARG;
   if (n_tokens == 0) return MOE_OK;
-  if (!d_logits || !d_x || !d_out) return MOE_ERR_INVALID_ARG;
+  if ((!d_logits && (!d_ids || !d_weights)) || !d_x || !d_out) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)cuda_stream;
   const int E = g.n_experts, k = g.top_k, S = g.slots_per_layer, T = n_tokens;
   const int P = T * k;
@@ -562,6 +564,8 @@ MOE_API int moe_layer_forward(moe_cache *c, int32_t layer, const float *d_logits
   if (c->seq == 0) c->seq = 1;
   PlanArgs pa;
   pa.logits = d_logits;
+  pa.given_ids = d_logits ? nullptr : d_ids;
+  pa.given_w = d_weights;
   pa.T = T;
   pa.E = E;
   pa.k = k;
@@ -958,6 +962,16 @@ MOE_API int moe_layer_forward(moe_cache *c, int32_t layer, const float *d_logits
     }
   }
   return MOE_OK;
+}
+
+MOE_API int moe_layer_forward(moe_cache *c, int32_t layer, const float *d_logits, const void *d_x, int32_t n_tokens,
+                              float *d_out, void *cuda_stream) {
+  return layer_forward(c, layer, d_logits, nullptr, nullptr, d_x, n_tokens, d_out, cuda_stream);
+}
+
+MOE_API int moe_layer_forward_routed(moe_cache *c, int32_t layer, const int32_t *d_ids, const float *d_weights,
+                                     const void *d_x, int32_t n_tokens, float *d_out, void *cuda_stream) {
+  return layer_forward(c, layer, nullptr, d_ids, d_weights, d_x, n_tokens, d_out, cuda_stream);
 }
 
 MOE_API int moe_cache_sync(moe_cache *c, void *cuda_stream) {

@@ -161,6 +161,35 @@ __global__ void __launch_bounds__(256) route_kernel(const float *logits, int T, 
   route_token<VPL>(logits + (size_t)t * E, E, k, weight_mode, ids + (size_t)t * k, w + (size_t)t * k, bad);
 }
 
+// One token's choice as the caller made it: distinct experts of [0, E) and finite weights, or *bad is set and nothing of
+// the token written.
+__device__ void take_choice(const int32_t *given_ids, const float *given_w, int E, int k, int32_t *ids, float *w,
+                            int *bad_flag, int32_t *s_ids = nullptr) {
+  const int lane = threadIdx.x & 31;
+  const int id = lane < k ? given_ids[lane] : -1 - lane;
+  const float wt = lane < k ? given_w[lane] : 0.f;
+  const uint32_t same = __match_any_sync(0xffffffffu, id);  // (by all lanes, whatever else is wrong with theirs)
+  const bool bad = (lane < k && (id < 0 || id >= E)) || !isfinite(wt) || (same & (same - 1)) != 0;
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0) atomicExch(bad_flag, 1);
+    return;
+  }
+  if (lane < k) {
+    ids[lane] = id;
+    if (s_ids) s_ids[lane] = id;
+    w[lane] = wt;
+  }
+}
+
+// The same of a large call as its own grid.
+__global__ void __launch_bounds__(256) choice_kernel(const int32_t *given_ids, const float *given_w, int T, int E, int k,
+                                                     int32_t *ids, float *w, int *bad) {
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= T) return;
+  const size_t at = (size_t)t * k;
+  take_choice(given_ids + at, given_w + at, E, k, ids + at, w + at, bad);
+}
+
 template <int VPL>
 __device__ void route_all(const PlanArgs &a, int *bad_flag) {
   const int warp = threadIdx.x >> 5;
@@ -247,11 +276,15 @@ __global__ void __launch_bounds__(NT, 1) plan_kernel(PlanArgs a) {
   const uint32_t epoch = *a.epoch + 1u;
   __syncthreads();
   if (a.routed) {
-    // ids and weights come from route_kernel (earlier on the stream)
+    // ids and weights come from route_kernel or choice_kernel (earlier on the stream)
     if (tid == 0) {
       scal[0] = *a.route_bad;
       *a.route_bad = 0;
     }
+  } else if (a.given_ids) {
+    for (int t = tid >> 5; t < T; t += NW)
+      take_choice(a.given_ids + (size_t)t * k, a.given_w + (size_t)t * k, E, k, a.ids + (size_t)t * k, a.w + (size_t)t * k,
+                  &scal[0]);
   } else {
     int *bad = &scal[0];
     if (E <= 128) route_all<4>(a, bad);
@@ -596,7 +629,8 @@ __global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   float lg4[4], lg8[8];
-  if (E <= 128) load_logits<4>(a.logits, E, lg4);
+  if (a.given_ids) {
+  } else if (E <= 128) load_logits<4>(a.logits, E, lg4);
   else if (E <= 256) load_logits<8>(a.logits, E, lg8);
   if (lane == 0) s_bad = 0;
   if (lane < kSmallMaxSlots / 32) s_pinned[lane] = 0;
@@ -604,7 +638,9 @@ __global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanArgs a) {
   __syncwarp();
   for (int t = 0; t < T; ++t) {
     const float *row = a.logits + (size_t)t * E;
-    if (E <= 128) {
+    if (a.given_ids) {
+      take_choice(a.given_ids + t * k, a.given_w + t * k, E, k, a.ids + t * k, a.w + t * k, &s_bad, s_ids + t * k);
+    } else if (E <= 128) {
       if (t > 0) load_logits<4>(row, E, lg4);
       route_values<4>(lg4, E, k, a.weight_mode, a.ids + t * k, a.w + t * k, &s_bad, s_ids + t * k);
     } else if (E <= 256) {
@@ -956,7 +992,9 @@ cudaError_t launch_plan(const PlanArgs &a_in, cudaStream_t st) {
   if (a.T > kRouteGridMin && a.route_bad) {
     // many tokens: route them grid-wide first (one warp per token)
     const dim3 grid((a.T + 7) / 8);
-    if (a.E <= 128)
+    if (a.given_ids)
+      choice_kernel<<<grid, 256, 0, st>>>(a.given_ids, a.given_w, a.T, a.E, a.k, a.ids, a.w, a.route_bad);
+    else if (a.E <= 128)
       route_kernel<4><<<grid, 256, 0, st>>>(a.logits, a.T, a.E, a.k, a.weight_mode, a.ids, a.w, a.route_bad);
     else if (a.E <= 256)
       route_kernel<8><<<grid, 256, 0, st>>>(a.logits, a.T, a.E, a.k, a.weight_mode, a.ids, a.w, a.route_bad);
