@@ -176,6 +176,23 @@ int moe_prompt_attention_shared(const moe_tensor *q, int32_t n_q_tokens, int32_t
                                 void *out, float *lse, int32_t dtype, int32_t *status, void *workspace,
                                 int64_t workspace_bytes, void *cuda_stream);
 
+/*
+ * Totals: the attention weight that cached tokens have received, summed over queries
+ * and over the query heads that share a key head; what moe_kv_evict goes by.  fp32
+ * [n_pages][n_kv_heads][page_size] contiguous, of the same pages as the tokens.  A token
+ * that a call queries is new: its total begins at 0 with that call; those of the other
+ * tokens that a row sees are added to, and the rest is left as it is.  With restart all
+ * tokens of the sequences begin at 0 (a pool whose totals were never set).
+ * A page belongs to one sequence, once (as for an append).
+ *
+ * moe_kv_weigh adds the weights exp(scale q . k - lse) of the last q_tokens tokens of
+ * every sequence over the cache; the arguments are those of moe_kv_attention, lse being
+ * what it wrote.  A row of lse -inf that sees nothing adds nothing.
+ */
+int moe_kv_weigh(const moe_kv_cache *c, const int32_t *seq_lens, const moe_tensor *q, int32_t n_q_heads,
+                 int32_t q_tokens, float scale, int32_t window, const float *lse, float *totals, int32_t restart,
+                 int32_t dtype, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -46,7 +46,7 @@ EXPORTS = ("moe_cache_init", "moe_layer_forward", "moe_cache_sync", "moe_cache_s
            "moe_kv_page_bytes", "moe_kv_append", "moe_kv_read", "moe_kv_attention_workspace",
            "moe_kv_attention", "moe_prompt_attention",
            "moe_prompt_attention_workspace", "moe_prompt_attention_shared",
-           "moe_route", "moe_layer_forward_routed")
+           "moe_route", "moe_layer_forward_routed", "moe_kv_weigh")
 
 MOE_STATE_MAGIC = 0x53454F4D
 MOE_STATE_VERSION = 1
@@ -387,6 +387,7 @@ _ATTENTION = ("kv_append", "kv_read", "kv_attention", "kv_attention_workspace", 
 
 
 _ROUTING = ("route", "MOE_ROUTE_BAD_LOGIT")
+_EVICTION = ("kv_totals", "kv_weigh")
 
 
 def __getattr__(name):
@@ -395,6 +396,11 @@ def __getattr__(name):
         from . import routing
         for n in _ROUTING:
             globals()[n] = getattr(routing, n)
+        return globals()[name]
+    if name in _EVICTION:
+        from . import eviction
+        for n in _EVICTION:
+            globals()[n] = getattr(eviction, n)
         return globals()[name]
     if name in _ATTENTION:
         from . import attention

@@ -1,0 +1,75 @@
+"""A cache of bounded size, for PyTorch tensors: the attention weight that cached tokens
+receive, and keeping those with most of it (``include/moe_attention.h``; argument checks
+and marshalling only).
+
+Totals are float32 ``[n_pages, n_kv_heads, page_size]``, of the same pages as the cache's
+tokens.  Streams, outputs and errors are as for the attention operators; a page belongs
+to one sequence, once.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import MOE_ERR_UNSUPPORTED, _check, lib
+from .attention import _DTYPES, _cache, _call, _device, _index, _refuse, _tokens, _window, _word, kv_page_bytes  # noqa: F401
+
+_bound = None
+
+
+def _lib():
+    global _bound
+    if _bound is None:
+        L = lib()
+        vp, i32, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
+        L.moe_kv_weigh.argtypes = [vp, vp, vp, i32, i32, f32, i32, vp, vp, i32, i32, vp]
+        _bound = L
+    return _bound
+
+
+def kv_totals(n_pages: int, n_kv_heads: int, page_size: int, device="cuda"):
+    """Totals of an empty cache: zeros, float32 [n_pages, n_kv_heads, page_size]."""
+    return torch.zeros(n_pages, n_kv_heads, page_size, dtype=torch.float32, device=device)
+
+
+def _totals(t, n_pages, hkv, page_size, dev):
+    if t.dtype is not torch.float32 or tuple(t.shape) != (n_pages, hkv, page_size) or t.get_device() != dev \
+            or not t.is_contiguous():
+        _refuse(f"totals must be a contiguous float32 tensor [{n_pages}, {hkv}, {page_size}] on the GPU")
+    return t.data_ptr()
+
+
+def _lse(t, n, hq, dev):
+    if t.dtype is not torch.float32 or tuple(t.shape) != (n, hq) or t.get_device() != dev or not t.is_contiguous():
+        _refuse(f"lse must be a contiguous float32 tensor [{n}, {hq}] on the GPU")
+    return t.data_ptr()
+
+
+def kv_weigh(q, pages, page_table, seq_lens, lse, *, totals, page_size, n_kv_heads, q_tokens=1, scale=None, window=0,
+             restart=False, status=None, stream=None):
+    """Adds the attention weights of every sequence's last q_tokens tokens to the totals of the tokens that they see
+    (moe_kv_weigh).
+
+    The arguments are those of ``kv_attention``, lse what it returns with return_lse.  The queried tokens are new: their
+    totals begin at 0; with restart all tokens' of the sequences do.  Returns totals, written in place."""
+    dev, dtype = _device(q), q.dtype
+    if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
+        _refuse("q must be bfloat16 or float16 [tokens, heads, head_dim]", MOE_ERR_UNSUPPORTED)
+    n, hq, d = q.shape
+    c, n_seqs = _cache(pages, page_table, page_size, n_kv_heads, d, status, dev)
+    if n != n_seqs * q_tokens or n_kv_heads <= 0 or hq % n_kv_heads:
+        _refuse("q must hold q_tokens tokens of every sequence, its heads a multiple of n_kv_heads")
+    tq = _tokens(q, "q", n, hq, d, dtype, dev)
+    pl = _index(seq_lens, "seq_lens", n_seqs, dev)
+    pe, pt = _lse(lse, n, hq, dev), _totals(totals, pages.shape[0], n_kv_heads, page_size, dev)
+    window = _window(window)
+
+    def run(handle):
+        if n:
+            rc = _lib().moe_kv_weigh(c, pl, tq, hq, q_tokens, d ** -0.5 if scale is None else scale, window, pe, pt,
+                                     bool(restart), _DTYPES[dtype], handle)
+            if rc:
+                _check(rc, "moe_kv_weigh")
+        return totals
+    return _call(stream, dev, run, q, pages, page_table, seq_lens, lse, totals, status)
