@@ -193,6 +193,26 @@ int moe_kv_weigh(const moe_kv_cache *c, const int32_t *seq_lens, const moe_tenso
                  int32_t q_tokens, float scale, int32_t window, const float *lse, float *totals, int32_t restart,
                  int32_t dtype, void *cuda_stream);
 
+/*
+ * Keeps budget tokens of every sequence that has more, per key/value head: its first
+ * `first` and its last `recent` tokens (first + recent <= budget), and of those between
+ * the ones with the largest totals (ties: the earlier token; NaN counts as largest).
+ * They move together, in place and in their order: keys, values and totals of the token
+ * of rank r go to slot r.  What the slots from budget on hold is left as it is, but for
+ * their totals, which become 0.  Positions are not kept: a key stays as it was rotated.
+ * new_lens: device int32 [n_seqs], min(seq_lens, budget); not seq_lens itself.
+ * kept: device int32 [n_seqs][n_kv_heads][budget], the slots that the kept tokens had;
+ * of a sequence of n <= budget tokens 0..n-1, then -1.
+ * A sequence whose length makes no sense, or one of whose pages is none, is left as it
+ * is, with its length, and -1 for all of kept.
+ * workspace: moe_kv_evict_workspace bytes, 256-byte aligned, of any contents; used by one
+ * call at a time.
+ */
+int64_t moe_kv_evict_workspace(const moe_kv_cache *c);
+int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *totals, int32_t budget, int32_t first,
+                 int32_t recent, int32_t *new_lens, int32_t *kept, void *workspace, int64_t workspace_bytes,
+                 void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

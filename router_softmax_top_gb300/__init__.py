@@ -46,7 +46,8 @@ EXPORTS = ("moe_cache_init", "moe_layer_forward", "moe_cache_sync", "moe_cache_s
            "moe_kv_page_bytes", "moe_kv_append", "moe_kv_read", "moe_kv_attention_workspace",
            "moe_kv_attention", "moe_prompt_attention",
            "moe_prompt_attention_workspace", "moe_prompt_attention_shared",
-           "moe_route", "moe_layer_forward_routed", "moe_kv_weigh")
+           "moe_route", "moe_layer_forward_routed", "moe_kv_weigh",
+           "moe_kv_evict_workspace", "moe_kv_evict")
 
 MOE_STATE_MAGIC = 0x53454F4D
 MOE_STATE_VERSION = 1
@@ -387,7 +388,7 @@ _ATTENTION = ("kv_append", "kv_read", "kv_attention", "kv_attention_workspace", 
 
 
 _ROUTING = ("route", "MOE_ROUTE_BAD_LOGIT")
-_EVICTION = ("kv_totals", "kv_weigh")
+_EVICTION = ("kv_totals", "kv_weigh", "kv_evict")
 
 
 def __getattr__(name):

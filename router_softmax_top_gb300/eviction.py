@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import MOE_ERR_UNSUPPORTED, _check, lib
-from .attention import _DTYPES, _cache, _call, _device, _index, _refuse, _tokens, _window, _word, kv_page_bytes  # noqa: F401
+from .attention import _DTYPES, _cache, _call, _cuda, _device, _index, _refuse, _tokens, _window
 
 _bound = None
 
@@ -24,6 +24,9 @@ def _lib():
         L = lib()
         vp, i32, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
         L.moe_kv_weigh.argtypes = [vp, vp, vp, i32, i32, f32, i32, vp, vp, i32, i32, vp]
+        L.moe_kv_evict_workspace.restype = ctypes.c_int64
+        L.moe_kv_evict_workspace.argtypes = [vp]
+        L.moe_kv_evict.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, ctypes.c_int64, vp]
         _bound = L
     return _bound
 
@@ -73,3 +76,37 @@ def kv_weigh(q, pages, page_table, seq_lens, lse, *, totals, page_size, n_kv_hea
                 _check(rc, "moe_kv_weigh")
         return totals
     return _call(stream, dev, run, q, pages, page_table, seq_lens, lse, totals, status)
+
+
+def kv_evict(pages, page_table, seq_lens, budget, *, totals, page_size, n_kv_heads, head_dim, first=0, recent=0, status=None,
+             stream=None):
+    """Keeps budget tokens of every sequence that has more (moe_kv_evict): per head its first `first` and last `recent`
+    tokens and the heaviest by totals of those between, moved together in place, in their order.
+
+    Returns the new lengths int32 [n_seqs] and the slots that the kept tokens had, int32 [n_seqs, n_kv_heads, budget]
+    (ascending; -1 past a shorter sequence's tokens).  pages and totals are written in place; the totals of the slots given
+    free become 0.  A kept key stays as it was rotated: tokens appended from then on need ``positions`` of their own
+    (``kv_append``)."""
+    dev = _device(pages)
+    c, n_seqs = _cache(pages, page_table, page_size, n_kv_heads, head_dim, status, dev)
+    pl = _index(seq_lens, "seq_lens", n_seqs, dev)
+    pt = _totals(totals, pages.shape[0], n_kv_heads, page_size, dev)
+    if not 0 <= budget < 2 ** 31 or first < 0 or recent < 0 or first + recent > budget:
+        _refuse("budget must be at least first + recent, none of them negative")
+
+    def run(handle):
+        d = _cuda(dev)
+        new_lens = torch.empty(n_seqs, dtype=torch.int32, device=d)
+        kept = torch.empty((n_seqs, n_kv_heads, budget), dtype=torch.int32, device=d)
+        if n_seqs:
+            L = _lib()
+            size = L.moe_kv_evict_workspace(c)
+            if size <= 0:
+                _refuse("kv_evict: unsupported sizes", MOE_ERR_UNSUPPORTED)
+            ws = torch.empty(size, dtype=torch.uint8, device=d)
+            rc = L.moe_kv_evict(c, pl, pt, budget, first, recent, new_lens.data_ptr(), kept.data_ptr(), ws.data_ptr(), size,
+                                handle)
+            if rc:
+                _check(rc, "moe_kv_evict")
+        return new_lens, kept
+    return _call(stream, dev, run, pages, page_table, seq_lens, totals, status)
