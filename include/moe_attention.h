@@ -194,6 +194,22 @@ int moe_kv_weigh(const moe_kv_cache *c, const int32_t *seq_lens, const moe_tenso
                  int32_t dtype, void *cuda_stream);
 
 /*
+ * The same of whole prompts, packed one after another: adds the weights of the queries
+ * [cu_q[s], cu_q[s+1]) on the keys [cu_k[s], cu_k[s+1]), as moe_prompt_attention forms them
+ * (arguments as there, lse what it wrote), to the totals of the sequence's cached tokens:
+ * key i of a sequence is its cached token i.  page_table [n_seqs][table_stride], n_pages and
+ * page_size are the cache's.  The queries stand at the sequence's last positions: they are
+ * the new tokens, whose totals begin at 0.
+ * A sequence whose offsets make no sense, whose keys begin before an earlier sequence's
+ * have ended or are more than its row of the page table holds, gets nothing, and a status.
+ */
+int moe_prompt_weigh(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads, const moe_tensor *k, int32_t n_k_tokens,
+                     int32_t n_kv_heads, int32_t head_dim, const int32_t *cu_q, const int32_t *cu_k, int32_t n_seqs,
+                     float scale, int32_t window, const float *lse, const int32_t *page_table, int64_t table_stride,
+                     int32_t table_width, int32_t n_pages, int32_t page_size, float *totals, int32_t restart,
+                     int32_t dtype, int32_t *status, void *cuda_stream);
+
+/*
  * Keeps budget tokens of every sequence that has more, per key/value head: its first
  * `first` and its last `recent` tokens (first + recent <= budget), and of those between
  * the ones with the largest totals (ties: the earlier token; NaN counts as largest).

@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import MOE_ERR_UNSUPPORTED, _check, lib
-from .attention import _DTYPES, _cache, _call, _cuda, _device, _index, _refuse, _tokens, _window
+from .attention import _DTYPES, _cache, _call, _cuda, _device, _index, _refuse, _tokens, _window, _word
 
 _bound = None
 
@@ -27,6 +27,8 @@ def _lib():
         L.moe_kv_evict_workspace.restype = ctypes.c_int64
         L.moe_kv_evict_workspace.argtypes = [vp]
         L.moe_kv_evict.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, ctypes.c_int64, vp]
+        L.moe_prompt_weigh.argtypes = [vp, i32, i32, vp, i32, i32, i32, vp, vp, i32, f32, i32, vp, vp, ctypes.c_int64, i32, i32,
+                                       i32, vp, i32, i32, vp, vp]
         _bound = L
     return _bound
 
@@ -76,6 +78,46 @@ def kv_weigh(q, pages, page_table, seq_lens, lse, *, totals, page_size, n_kv_hea
                 _check(rc, "moe_kv_weigh")
         return totals
     return _call(stream, dev, run, q, pages, page_table, seq_lens, lse, totals, status)
+
+
+def prompt_weigh(q, k, lse, cu_q, cu_k=None, *, totals, page_table, scale=None, window=0, restart=False, status=None,
+                 stream=None):
+    """Adds the attention weights of whole prompts' queries, packed one after another, to the totals of the tokens that they
+    see (moe_prompt_weigh).
+
+    The arguments are those of ``prompt_attention``, lse what it returns with return_lse; key i of a sequence is its cached
+    token i, whose total is found by page_table int32 [n_seqs, width].  The queried tokens, a sequence's last ones, are
+    new: their totals begin at 0; with restart all tokens' of the sequences do.  Returns totals, written in place."""
+    dev, dtype = _device(q), q.dtype
+    if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
+        _refuse("q must be bfloat16 or float16 [tokens, heads, head_dim]", MOE_ERR_UNSUPPORTED)
+    n, hq, d = q.shape
+    tq, tk = _tokens(q, "q", n, hq, d, dtype, dev), _tokens(k, "k", None, None, d, dtype, dev)
+    nk, hkv = k.shape[0], k.shape[1]
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        _refuse("cu_q must hold n_seqs + 1 offsets")
+    n_cu = cu_q.shape[0]
+    pq = _index(cu_q, "cu_q", n_cu, dev)
+    pk = pq if cu_k is None else _index(cu_k, "cu_k", n_cu, dev)
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n_cu - 1 \
+            or page_table.get_device() != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        _refuse("page_table must be int32 [n_seqs, width] on the GPU, rows contiguous")
+    if totals.dim() != 3:
+        _refuse("totals must be float32 [n_pages, n_kv_heads, page_size]")
+    n_pages, _, page_size = totals.shape
+    pe, pt = _lse(lse, n, hq, dev), _totals(totals, n_pages, hkv, page_size, dev)
+    width = page_table.shape[1]
+    row = page_table.stride(0) if n_cu > 2 else width
+    word, window = _word(status, dev), _window(window)
+
+    def run(handle):
+        rc = _lib().moe_prompt_weigh(tq, n, hq, tk, nk, hkv, d, pq, pk, n_cu - 1, d ** -0.5 if scale is None else scale, window, pe,
+                                     page_table.data_ptr(), row, width, n_pages, page_size, pt, bool(restart), _DTYPES[dtype],
+                                     word, handle)
+        if rc:
+            _check(rc, "moe_prompt_weigh")
+        return totals
+    return _call(stream, dev, run, q, k, lse, cu_q, cu_k, totals, page_table, status)
 
 
 def kv_evict(pages, page_table, seq_lens, budget, *, totals, page_size, n_kv_heads, head_dim, first=0, recent=0, status=None,
