@@ -107,6 +107,17 @@ int moe_kv_append(const moe_kv_cache *c, const int32_t *starts, const int32_t *c
                   void *q_out, void *k_out, int32_t dtype, void *cuda_stream);
 
 /*
+ * The same with positions of their own: the tokens of sequence s are rotated by positions[s],
+ * positions[s] + 1, ... (device int32 [n_seqs]; NULL: by their places in the cache), and
+ * take the places starts[s], starts[s] + 1, ...  Of a cache that tokens were evicted from a
+ * place is no longer a position.
+ */
+int moe_kv_append_at(const moe_kv_cache *c, const int32_t *starts, const int32_t *positions, const int32_t *cu_tokens,
+                     int32_t n_tokens, const moe_tensor *q, int32_t n_q_heads, const moe_tensor *k, const moe_tensor *v,
+                     const float *cos, const float *sin, int32_t rot_dim, int32_t n_positions, int32_t interleaved,
+                     void *q_out, void *k_out, int32_t dtype, void *cuda_stream);
+
+/*
  * The values that cached tokens stand for: k_out, v_out [n_tokens][n_kv_heads]
  * [head_dim] contiguous in dtype, for tokens starts[s] + (i - cu_tokens[s]).
  * Either output may be NULL.

@@ -47,7 +47,7 @@ EXPORTS = ("moe_cache_init", "moe_layer_forward", "moe_cache_sync", "moe_cache_s
            "moe_kv_attention", "moe_prompt_attention",
            "moe_prompt_attention_workspace", "moe_prompt_attention_shared",
            "moe_route", "moe_layer_forward_routed", "moe_kv_weigh",
-           "moe_kv_evict_workspace", "moe_kv_evict", "moe_prompt_weigh")
+           "moe_kv_evict_workspace", "moe_kv_evict", "moe_prompt_weigh", "moe_kv_append_at")
 
 MOE_STATE_MAGIC = 0x53454F4D
 MOE_STATE_VERSION = 1

@@ -62,6 +62,7 @@ def _lib():
         L.moe_kv_page_bytes.restype = i64
         L.moe_kv_page_bytes.argtypes = [i32, i32, i32]
         L.moe_kv_append.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp]
+        L.moe_kv_append_at.argtypes = [vp, vp, vp, vp, i32, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp]
         L.moe_kv_read.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp]
         L.moe_kv_attention_workspace.restype = i64
         L.moe_kv_attention_workspace.argtypes = [i32, i32, i32, i32]
@@ -188,10 +189,11 @@ def _cache(pages, page_table, page_size, n_kv_heads, head_dim, status, dev):
 
 
 def kv_append(pages, page_table, starts, cu_tokens, k, v, *, page_size, q=None, cos=None, sin=None,
-              interleaved=False, q_out=None, k_out=None, status=None, stream=None):
+              interleaved=False, q_out=None, k_out=None, positions=None, status=None, stream=None):
     """Append new tokens to the cache, rotating their keys and queries (moe_kv_append).
 
-    Tokens [cu_tokens[s], cu_tokens[s+1]) go to positions starts[s], starts[s] + 1, ... of sequence s.
+    Tokens [cu_tokens[s], cu_tokens[s+1]) go to positions starts[s], starts[s] + 1, ... of sequence s; with `positions` (int32
+    [n_seqs], moe_kv_append_at) they are rotated by positions[s], positions[s] + 1, ... instead.
     cos, sin [n_positions, rot_dim / 2] (``rope_table``); None: no rotation.  Returns the rotated queries
     (None without q) and the rotated keys, both contiguous in the inputs' type; the cache holds the keys
     quantised from their fp32 values."""
@@ -202,6 +204,7 @@ def kv_append(pages, page_table, starts, cu_tokens, k, v, *, page_size, q=None, 
     c, n_seqs = _cache(pages, page_table, page_size, hkv, d, status, dev)
     tk, tv = _tokens(k, "k", T, hkv, d, dtype, dev), _tokens(v, "v", T, hkv, d, dtype, dev)
     ps, pc = _index(starts, "starts", n_seqs, dev), _index(cu_tokens, "cu_tokens", n_seqs + 1, dev)
+    pp = None if positions is None else _index(positions, "positions", n_seqs, dev)
     tq, hq, rot, n_pos, cp, sp = None, 0, 0, 0, None, None
     if q is not None:
         hq = q.shape[1] if q.dim() == 3 else 0
@@ -217,12 +220,16 @@ def kv_append(pages, page_table, starts, cu_tokens, k, v, *, page_size, q=None, 
     def run(handle):
         qo = None if tq is None else _output(q_out, "q_out", (T, hq, d), dtype, dev)
         ko = _output(k_out, "k_out", (T, hkv, d), dtype, dev)
-        rc = _lib().moe_kv_append(c, ps, pc, T, tq, hq, tk, tv, cp, sp, rot, n_pos, int(interleaved),
-                                  None if qo is None else qo.data_ptr(), ko.data_ptr(), _DTYPES[dtype], handle)
+        if pp is None:
+            rc = _lib().moe_kv_append(c, ps, pc, T, tq, hq, tk, tv, cp, sp, rot, n_pos, int(interleaved),
+                                      None if qo is None else qo.data_ptr(), ko.data_ptr(), _DTYPES[dtype], handle)
+        else:
+            rc = _lib().moe_kv_append_at(c, ps, pp, pc, T, tq, hq, tk, tv, cp, sp, rot, n_pos, int(interleaved),
+                                         None if qo is None else qo.data_ptr(), ko.data_ptr(), _DTYPES[dtype], handle)
         if rc:
             _check(rc, "moe_kv_append")
         return qo, ko
-    return _call(stream, dev, run, pages, page_table, starts, cu_tokens, q, k, v, cos, sin, q_out, k_out, status)
+    return _call(stream, dev, run, pages, page_table, starts, cu_tokens, q, k, v, cos, sin, q_out, k_out, positions, status)
 
 
 def kv_read(pages, page_table, starts, cu_tokens, n_tokens, *, page_size, n_kv_heads, head_dim,

@@ -31,7 +31,7 @@ namespace {
 
 struct AppendJob {
   moe_kv_cache c;
-  const int32_t *starts, *cu;
+  const int32_t *starts, *cu, *positions;  // positions: of a sequence's first token, or null: its place in the cache
   int n_tokens;
   moe_tensor q, k, v;
   int hq, hkv;
@@ -238,7 +238,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) kv_append_kern
 #pragma unroll 1
   for (int u = 0; u < kAhead; ++u) fetch(h0 + u * HPW, u);
   const TokenPlace at = place_token(j.c, j.starts, j.cu, i);
-  const bool no_rot = j.rot > 0 && (at.pos < 0 || at.pos >= j.n_pos);
+  int64_t turn = at.pos;  // the position that the rotation goes by
+  if (j.positions) turn = kv_position(i, __ldg(j.cu + at.seq), __ldg(j.cu + at.seq + 1), __ldg(j.positions + at.seq));
+  const bool no_rot = j.rot > 0 && (turn < 0 || turn >= j.n_pos);
   if (lane == 0 && j.c.status) {
     const int bits = (at.pos < 0 ? MOE_KV_BAD_LENGTH : (at.page < 0 ? MOE_KV_BAD_PAGE : 0)) |
                      (at.pos >= 0 && no_rot ? MOE_KV_BAD_POSITION : 0);
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) kv_append_kern
   float c[8], s[8];  // of this thread's values; s carries the sign of the rotation's other term
   int partner = lane;
   if (turned) {
-    const float *ct = j.cos + at.pos * (j.rot / 2), *st = j.sin + at.pos * (j.rot / 2);
+    const float *ct = j.cos + turn * (j.rot / 2), *st = j.sin + turn * (j.rot / 2);
     if (j.interleaved) {
       const float4 a = __ldg(reinterpret_cast<const float4 *>(ct + dim / 2));
       const float4 b = __ldg(reinterpret_cast<const float4 *>(st + dim / 2));
@@ -425,6 +427,14 @@ MOE_API int moe_kv_append(const moe_kv_cache *c, const int32_t *starts, const in
                           const moe_tensor *q, int32_t n_q_heads, const moe_tensor *k, const moe_tensor *v,
                           const float *cos, const float *sin, int32_t rot_dim, int32_t n_positions,
                           int32_t interleaved, void *q_out, void *k_out, int32_t dtype, void *cuda_stream) {
+  return moe_kv_append_at(c, starts, nullptr, cu_tokens, n_tokens, q, n_q_heads, k, v, cos, sin, rot_dim, n_positions,
+                          interleaved, q_out, k_out, dtype, cuda_stream);
+}
+
+MOE_API int moe_kv_append_at(const moe_kv_cache *c, const int32_t *starts, const int32_t *positions, const int32_t *cu_tokens,
+                             int32_t n_tokens, const moe_tensor *q, int32_t n_q_heads, const moe_tensor *k,
+                             const moe_tensor *v, const float *cos, const float *sin, int32_t rot_dim, int32_t n_positions,
+                             int32_t interleaved, void *q_out, void *k_out, int32_t dtype, void *cuda_stream) {
   if (const int rc = check_cache(c)) return rc;
   if (n_tokens < 0 || !k || !v || dtype < MOE_F32 || dtype > MOE_F16) return MOE_ERR_INVALID_ARG;
   if (n_tokens == 0) return MOE_OK;
@@ -443,6 +453,7 @@ MOE_API int moe_kv_append(const moe_kv_cache *c, const int32_t *starts, const in
   AppendJob j = {};
   j.c = *c;
   j.starts = starts;
+  j.positions = positions;
   j.cu = cu_tokens;
   j.n_tokens = n_tokens;
   if (has_q) j.q = *q;
