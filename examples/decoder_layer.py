@@ -9,6 +9,10 @@ over that and itself.  Tokens after it come one per sequence (`decode`), attendi
 the 4-bit cache; that step has fixed shapes and no host work, so it is captured into a
 CUDA graph once and replayed.  Projections are plain matrix products; the norms are a
 line of torch each.
+
+`BoundedDecoderLayer` is the same with a cache of bounded size and grouped routing: what
+attention each cached token has received is summed as prompts and tokens go by, `bound`
+keeps the tokens with most of it, and the experts come from sigmoid scores with a bias.
 """
 import os
 import sys
@@ -58,8 +62,11 @@ class DecoderLayer:
         y = torch.empty_like(h)
         for i in range(0, x.shape[0], most):
             part = h[i:i + most].contiguous()
-            self.experts.forward(self.layer, part @ self.w_router, part, out=y[i:i + most])
+            self._experts(part, y[i:i + most])
         return x + y
+
+    def _experts(self, part, out):
+        self.experts.forward(self.layer, part @ self.w_router, part, out=out)
 
     def prompt(self, x, cu):
         """x [tokens, hidden] fp32, sequence s's tokens [cu[s], cu[s+1]); nothing is cached before."""
@@ -88,14 +95,66 @@ class DecoderLayer:
                                               n_kv_heads=self.hkv, status=self.status))
 
 
-def build(seqs=3, longest=512):
+class BoundedDecoderLayer(DecoderLayer):
+    """budget: tokens that `bound` keeps per sequence, the first four and the last `recent` among them; routing: keyword
+    arguments of `moe.route`, None: the expert cache's own router."""
+
+    def __init__(self, *args, budget, recent=16, routing=None, **kw):
+        super().__init__(*args, **kw)
+        self.budget, self.recent, self.routing = budget, recent, routing
+        self.totals = moe.kv_totals(self.pages.shape[0], self.hkv, self.page_size)
+        self.positions = torch.zeros_like(self.lens)  # tokens seen; lens are those still cached
+
+    def _append(self, x, cu):
+        qkv = (rms(x).bfloat16() @ self.w_qkv).view(x.shape[0], self.hq + 2 * self.hkv, self.d)
+        q, k, v = qkv.split([self.hq, self.hkv, self.hkv], 1)
+        q, k = moe.kv_append(self.pages, self.table, self.lens, cu, k, v, page_size=self.page_size, q=q, cos=self.cos,
+                             sin=self.sin, positions=self.positions, status=self.status)
+        return q, k, v
+
+    def _experts(self, part, out):
+        if self.routing is None:
+            return super()._experts(part, out)
+        ids, w = moe.route(part @ self.w_router, self.experts.k, status=self.status, **self.routing)
+        self.experts.forward_routed(self.layer, ids, w, part, out=out)
+
+    def prompt(self, x, cu):
+        q, k, v = self._append(x, cu)
+        o, lse = moe.prompt_attention(q, k, v, cu, return_lse=True, status=self.status)
+        moe.prompt_weigh(q, k, lse, cu, totals=self.totals, page_table=self.table, status=self.status)
+        new = cu.diff()
+        self.lens += new
+        self.positions += new
+        return self._rest(x, o)
+
+    def chunk(self, x, cu, n_cached):
+        raise NotImplementedError("prompts enter in one piece")
+
+    def decode(self, x):
+        q, _, _ = self._append(x, self.one_each)
+        self.lens += 1
+        self.positions += 1
+        args = dict(page_size=self.page_size, n_kv_heads=self.hkv, status=self.status)
+        o, lse = moe.kv_attention(q, self.pages, self.table, self.lens, return_lse=True, **args)
+        moe.kv_weigh(q, self.pages, self.table, self.lens, lse, totals=self.totals, **args)
+        return self._rest(x, o)
+
+    def bound(self):
+        """Keeps the budget of every sequence that is over it; the slots that the kept tokens had."""
+        lens, kept = moe.kv_evict(self.pages, self.table, self.lens, self.budget, totals=self.totals, page_size=self.page_size,
+                                  n_kv_heads=self.hkv, head_dim=self.d, first=4, recent=self.recent, status=self.status)
+        self.lens.copy_(lens)
+        return kept
+
+
+def build(seqs=3, longest=512, kind=DecoderLayer, **kw):
     import synth
     sh = synth.TINY
     store = torch.empty(sh.L * sh.E * synth.expert_bytes(sh.H, sh.F), dtype=torch.uint8, pin_memory=True)
     synth.fill_store(store.data_ptr(), sh.L, sh.E, sh.H, sh.F, 0)
     experts = moe.MoECache(n_layers=sh.L, n_experts=sh.E, top_k=sh.k, hidden=sh.H, ffn=sh.F, slots_per_layer=sh.E,
                            max_tokens=4, store=store, fill_mode=moe.MOE_FILL_PULL)
-    return DecoderLayer(experts, 0, sh.H, 4, 2, 64, sh.E, seqs=seqs, longest=longest), sh.H
+    return kind(experts, 0, sh.H, 4, 2, 64, sh.E, seqs=seqs, longest=longest, **kw), sh.H
 
 
 def main():
@@ -117,6 +176,18 @@ def main():
     torch.cuda.synchronize()
     assert layer.experts.sync() == moe.MOE_OK
     print("decode", tuple(out.shape), "lengths", layer.lens.tolist(), moe.status_message(layer.status) or "status ok")
+
+    layer, hidden = build(kind=BoundedDecoderLayer, budget=96, routing=dict(
+        score="sigmoid", bias=torch.linspace(-0.1, 0.1, 8, device="cuda"), n_groups=4, top_groups=2, renormalise=True))
+    layer.prompt(x, cu)
+    for _ in range(3):
+        layer.bound()
+        for _ in range(8):
+            out = layer.decode(step)
+    torch.cuda.synchronize()
+    assert layer.experts.sync() == moe.MOE_OK
+    print("bounded", tuple(out.shape), "cached", layer.lens.tolist(), "of", layer.positions.tolist(),
+          moe.status_message(layer.status) or "status ok")
 
 
 if __name__ == "__main__":
