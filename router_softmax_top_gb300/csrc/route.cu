@@ -39,257 +39,399 @@ __device__ __forceinline__ float r_float(float x) { return x; }
 __device__ __forceinline__ float r_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float r_float(__half x) { return __half2float(x); }
 
-// Keys that order like the values (-0 as +0); 0 is below all of them.
-__device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float of_key(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-}
+// A key that orders like the value (-0 as +0); 0 is below all of them.
 __device__ __forceinline__ uint64_t key_of(double v) {
   const uint64_t b = (uint64_t)__double_as_longlong(v == 0. ? 0. : v);
   return (b >> 63) ? ~b : (b | (1ull << 63));
 }
-__device__ __forceinline__ double of_key(uint64_t k) {
-  return __longlong_as_double((long long)((k >> 63) ? (k & ~(1ull << 63)) : ~k));
-}
-__device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(0xffffffffu, k); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
   const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
   return ((uint64_t)hi << 32) | lo;
 }
-__device__ __forceinline__ float x_exp(float x) { return expf(x); }
-__device__ __forceinline__ double x_exp(double x) { return exp(x); }
-template <typename F>
-__device__ __forceinline__ F inf_of() { return (F)a_inf(); }
-
-// Bound on the error of a value c = p + b formed in 32 bits: `arg` is the exponential's argument, whose rounding (softmax
-// takes the largest logit away) is relative to p.  expf is good to 2 steps, the sum over E to 2^-19 for E <= 1024 in
-// strides and a tree (32 + 5 additions), quotient and sum to a step each.
-__device__ __forceinline__ float error_of(float p, float arg, float c) {
-  return p * fmaf(fabsf(arg), 1.2e-7f, 4e-6f) + fabsf(c) * 1.2e-7f + 1e-37f;
+// The largest of a warp's values; NaN where there is one.
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
 }
 
-// The choice, with values of type F (float or double): ids on lanes 0..k (the k + 1st too, where there is one; -1: none).
-// Float: returns whether the choice is certain.  v: the lane's logits; x of experts past E is never looked at.
-template <typename F, int VPL>
-__device__ __forceinline__ bool choose(const RouteJob &j, const float (&x)[VPL], float top, float *group_mem, int *id_out) {
-  using K = decltype(key_of(F(0)));
-  const int lane = threadIdx.x & 31, e0 = lane * VPL;
-  constexpr bool rough = sizeof(F) == 4;
-  K key[VPL];
-  const bool by_logit = !j.bias;
-  F z = 0;
-  if (!j.sigmoid && (j.bias || (j.groups > 1 && j.top2))) {
+// VPL neighbouring values, in as wide loads as their address allows.
+template <int VPL, typename T>
+__device__ __forceinline__ void load_values(const T *p, float (&x)[VPL]) {
+  constexpr int kBytes = VPL * (int)sizeof(T), kVec = kBytes >= 16 ? 16 : kBytes;
+  if (VPL > 1 && ((uintptr_t)p & (kVec - 1)) == 0) {
+    if constexpr (kVec == 16) {
 #pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        constexpr int n = 16 / (int)sizeof(T);
+#pragma unroll
+        for (int z = 0; z < n; ++z) x[i * n + z] = r_float(reinterpret_cast<const T *>(&w)[z]);
+      }
+    } else if constexpr (kVec == 8) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+#pragma unroll
+      for (int z = 0; z < VPL; ++z) x[z] = r_float(reinterpret_cast<const T *>(&w)[z]);
+    } else if constexpr (kVec == 4) {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(p));
+#pragma unroll
+      for (int z = 0; z < VPL; ++z) x[z] = r_float(reinterpret_cast<const T *>(&w)[z]);
+    }
+  } else {
+#pragma unroll
+    for (int z = 0; z < VPL; ++z) x[z] = r_float(p[z]);
+  }
+}
+
+// A score in 32 bits, and what its error is at most relative to it: the exponential's argument counts 2^-24 of itself twice,
+// ex2 and the quotient 2^-22 each, the sum over E <= 1024 of softmax (32 + 5 additions) 2^-18.
+__device__ __forceinline__ float quick_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float quick_sigmoid(float x) { return quick_inverse(1.f + a_exp2(x * -kLog2e)); }
+__device__ __forceinline__ float quick_exp(float x) { return a_exp2(x * kLog2e); }
+__device__ __forceinline__ float score_error(bool sigmoid, float arg) { return fmaf(fabsf(arg), 2e-7f, sigmoid ? 8e-7f : 5e-6f); }
+constexpr float kSumStep = 1.2e-7f;   // of a sum's two roundings
+constexpr float kFloor = 1e-37f;      // below it, scores are not held with their bits
+
+// What the groups' members are worth, by lanes that have some of them each: a the largest, b the next.
+template <typename F>
+__device__ __forceinline__ void top_two(F c, F &a, F &b) {
+  b = c > a ? a : (c > b ? c : b);
+  a = c > a ? c : a;
+}
+template <typename F>
+__device__ __forceinline__ void join_two(F &a, F &b, int o) {
+  const F oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+  b = oa > a ? (a > ob ? a : ob) : (oa > b ? oa : b);
+  a = oa > a ? oa : a;
+}
+
+// The kept groups: lane `first` of a group, h * lanes, has its worth.  Returns a bit per group, at h * lanes; rank: the
+// calling lane's group's.
+template <typename F>
+__device__ __forceinline__ uint32_t keep_groups(F worth, int groups, int kept, int lanes, int g, int *rank) {
+  int r = 0;
+  for (int h = 0; h < groups; ++h) {
+    const F w = __shfl_sync(0xffffffffu, worth, h * lanes);
+    r += w > worth || (w == worth && h < g);
+  }
+  *rank = r;
+  return __ballot_sync(0xffffffffu, g < groups && (threadIdx.x & 31) % lanes == 0 && r < kept);
+}
+
+struct Pick {
+  float c[33];
+  int id[33];
+  float cand_c[32];  // values that may be among them, in any order
+  int cand_id[32];
+};
+
+// The choice in 32 bits, into `pick`; whether it is certain.  x: the lane's logits (-inf past E), b: their bias.
+template <int VPL, typename T>
+__device__ __forceinline__ bool choose_quick(const RouteJob &j, const T *row, const float (&x)[VPL], const float (&b)[VPL],
+                                             float top, float z, float *group_mem, Pick &pick) {
+  const int lane = threadIdx.x & 31, e0 = lane * VPL;
+  const bool by_logit = !j.bias, sums = j.top2 && j.size > 1;
+  float c[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) c[i] = x[i];
+  float most_p = 0.f;
+  if (!by_logit) {
+    const float inv = quick_inverse(z);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float p = j.sigmoid ? quick_sigmoid(x[i]) : quick_exp(x[i] - top) * inv;
+      most_p = fmaxf(most_p, p);
+      c[i] = x[i] > -a_inf() ? p + b[i] : -a_inf();
+    }
+  }
+  bool sure = true;
+  if (j.groups > 1) {
+    float d[VPL];
+    if (by_logit && sums) {
+      const float inv = quick_inverse(z);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const float p = j.sigmoid ? quick_sigmoid(x[i]) : quick_exp(x[i] - top) * inv;
+        most_p = fmaxf(most_p, p);
+        d[i] = x[i] > -a_inf() ? p : -a_inf();
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) d[i] = c[i];
+    }
+    // (a power of two of lanes per group, each lane's experts of one group: no shared memory needed)
+    int lanes = j.size / VPL;
+    const bool direct = j.size % VPL == 0 && (lanes & (lanes - 1)) == 0;
+    float w1 = -a_inf(), w2 = -a_inf();
+    if (direct) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) top_two(d[i], w1, w2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (e0 + i < j.E) group_mem[e0 + i] = d[i];
+      __syncwarp();
+      lanes = 1;
+      while (2 * lanes * j.groups <= 32) lanes *= 2;
+      if (lane / lanes < j.groups)
+        for (int m = lane % lanes; m < j.size; m += lanes) top_two(group_mem[lane / lanes * j.size + m], w1, w2);
+    }
+    for (int o = 1; o < lanes; o <<= 1) join_two(w1, w2, o);
+    const int g = lane / lanes;
+    const float worth = sums && w2 > -a_inf() ? w1 + w2 : w1;
+    int rank;
+    const uint32_t keep = keep_groups(worth, j.groups, j.kept, lanes, g, &rank);
+    if (j.kept < j.groups && !(by_logit && !sums)) {
+      const uint32_t first = __ballot_sync(0xffffffffu, g < j.groups && lane % lanes == 0);
+      const int in = __ffs(__ballot_sync(0xffffffffu, rank == j.kept - 1) & first) - 1;
+      const int out = __ffs(__ballot_sync(0xffffffffu, rank == j.kept) & first) - 1;
+      const float wi = __shfl_sync(0xffffffffu, worth, in), wo = __shfl_sync(0xffffffffu, worth, out);
+      // any group's error: p |argument| is at most 0.37 for what is below 1, and (1 - p) x for sigmoid's large ones
+      const float size = w1 > -a_inf() && g < j.groups ? fmaxf(fabsf(w1), w2 > -a_inf() ? fabsf(w2) : 0.f) : 0.f;
+      const float err = 2.f * (warp_max(most_p) * (j.sigmoid ? 8e-7f : 5e-6f) + 1e-7f + 2.f * kSumStep * warp_max(size));
+      sure = wi - wo > 2.f * err || (wo == -a_inf() && wi > wo);
+    }
+    if (direct) {
+      if (!((keep >> (g * lanes)) & 1u)) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = -a_inf();
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (e0 + i < j.E && !((keep >> ((e0 + i) / j.size * lanes)) & 1u)) c[i] = -a_inf();
+    }
+  }
+  float best = c[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) best = fmaxf(best, c[i]);
+  const int rounds = j.k + (by_logit ? 0 : 1);
+  // Values from `least` on to the candidates; how many there are (the first 32 are kept).
+  auto collect = [&](float least) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool in = c[i] >= least && c[i] > -a_inf();
+      const uint32_t who = __ballot_sync(0xffffffffu, in);
+      const int at = n + __popc(who & ((1u << lane) - 1u));
+      if (in && at < 32) {
+        pick.cand_c[at] = c[i];
+        pick.cand_id[at] = e0 + i;
+      }
+      n += __popc(who);
+    }
+    __syncwarp();
+    return n;
+  };
+  // The lanes' largest: with `rounds` of them taken, what is below the last of these is not among the chosen.  What is
+  // left is as a rule few enough for a lane each, and a candidate's place is the number of those before it.
+  float least = best, mine = best;
+  for (int q = 0; q < rounds; ++q) {
+    least = warp_max(mine);
+    if (least == -a_inf()) break;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, mine == least)) - 1) mine = -a_inf();
+  }
+  const int n = collect(least);
+  if (n < j.k) return false;  // closed experts follow, of the kept groups first: not told apart here
+  if (n <= 32) {
+    const float own = lane < n ? pick.cand_c[lane] : 0.f;
+    const int id = lane < n ? pick.cand_id[lane] : 0;
+    int place = 0;
+    for (int s = 0; s < n; ++s) {
+      const float o = pick.cand_c[s];
+      place += o > own || (o == own && pick.cand_id[s] < id);
+    }
+    if (lane < n && place < rounds) {
+      pick.c[place] = own;
+      pick.id[place] = id;
+    }
+    if (lane == 0 && n < rounds) pick.id[n] = -1;
+    __syncwarp();
+  } else {
+    // round by round: the largest left, of equal ones the lowest; the lane that has it looks for its next
+    float left[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) left[i] = c[i];
+    for (int q = 0; q < rounds; ++q) {
+      const float m = warp_max(best);  // (there are more than 32)
+      if (lane == __ffs(__ballot_sync(0xffffffffu, best == m)) - 1) {
+        bool taken = false;
+        int at = 0;
+        best = -a_inf();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          if (!taken && left[i] == m) {
+            taken = true;
+            at = i;
+            left[i] = -a_inf();
+          }
+          best = fmaxf(best, left[i]);
+        }
+        pick.c[q] = m;
+        pick.id[q] = e0 + at;
+      }
+      __syncwarp();
+    }
+  }
+  if (!sure || by_logit) return sure;
+  // Neighbours in the order, the one after the last among them, are further apart than their errors, or equal by having the
+  // same logit and bias.
+  bool near = false;
+  if (lane < j.k) {
+    const int a = pick.id[lane], e = pick.id[lane + 1];
+    if (e >= 0) {
+      const float ca = pick.c[lane], ce = pick.c[lane + 1], va = r_float(row[a]), ve = r_float(row[e]);
+      const float ba = __ldg(j.bias + a), be = __ldg(j.bias + e);
+      const float inv = quick_inverse(z);
+      const float pa = j.sigmoid ? quick_sigmoid(va) : quick_exp(va - top) * inv;
+      const float pe = j.sigmoid ? quick_sigmoid(ve) : quick_exp(ve - top) * inv;
+      const float err = pa * score_error(j.sigmoid, j.sigmoid ? va : va - top) + pe * score_error(j.sigmoid, j.sigmoid ? ve : ve - top) +
+                        kSumStep * (fabsf(ca) + fabsf(ce)) + kFloor;
+      near = !(ca - ce > err) && !(va == ve && ba == be);
+    }
+  }
+  if (!__any_sync(0xffffffffu, near)) return true;
+  // Some are not: 64 bits for the few that may be chosen.
+  const float last = pick.c[j.k - 1];
+  const float off = warp_max(most_p) * (j.sigmoid ? 8e-7f : 5e-6f) + 1e-7f + kSumStep * fabsf(last);
+  const int few = collect(last - 2.1f * off);
+  if (few > 32) return false;
+  uint64_t own = 0;
+  int id = 0;
+  double z64 = 0.;
+  if (!j.sigmoid) {
+#pragma unroll 4
+    for (int i = 0; i < VPL; ++i) z64 += x[i] > -a_inf() ? exp((double)x[i] - (double)top) : 0.;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z64 += __shfl_xor_sync(0xffffffffu, z64, o);
+  }
+  if (lane < few) {
+    id = pick.cand_id[lane];
+    const double v = (double)r_float(row[id]);
+    own = key_of((j.sigmoid ? 1. / (1. + exp(-v)) : exp(v - (double)top) / z64) + (double)__ldg(j.bias + id));
+  }
+  int place = 0;
+  for (int s = 0; s < few; ++s) {
+    const uint64_t o = __shfl_sync(0xffffffffu, own, s);
+    const int oid = __shfl_sync(0xffffffffu, id, s);
+    place += o > own || (o == own && oid < id);
+  }
+  __syncwarp();
+  if (lane < few && place < j.k) pick.id[place] = id;
+  __syncwarp();
+  return true;
+}
+
+// The choice in 64 bits: ids into `pick`.
+template <int VPL>
+__device__ __noinline__ void choose_exact(const RouteJob &j, const float (&x)[VPL], float top, double *group_mem, Pick &pick) {
+  const int lane = threadIdx.x & 31, e0 = lane * VPL;
+  const bool by_logit = !j.bias, sums = j.top2 && j.size > 1;
+  double z = 0.;
+  if (!j.sigmoid) {
+#pragma unroll 1
     for (int i = 0; i < VPL; ++i)
-      if (e0 + i < j.E) z += x_exp((F)x[i] - (F)top);
+      if (e0 + i < j.E) z += exp((double)x[i] - (double)top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   }
-  auto score = [&](float v) -> F {
-    return j.sigmoid ? F(1) / (F(1) + x_exp(-(F)v)) : x_exp((F)v - (F)top) / z;
-  };
-  auto argument = [&](float v) { return j.sigmoid ? v : v - top; };
-  bool sure = true;
+  uint64_t key[VPL];
+  const bool grouped = j.groups > 1;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     key[i] = 0;
     if (e0 + i < j.E) {
-      F c = (F)x[i];
-      if (!by_logit && x[i] > -a_inf()) c = score(x[i]) + (F)__ldg(j.bias + e0 + i);
+      double c = (double)x[i], d = c;
+      if (x[i] > -a_inf() && (!by_logit || (grouped && sums))) {
+        const double p = j.sigmoid ? 1. / (1. + exp(-(double)x[i])) : exp((double)x[i] - (double)top) / z;
+        if (by_logit) d = p;
+        else c = d = p + (double)__ldg(j.bias + e0 + i);
+      }
       key[i] = key_of(c);
+      if (grouped) group_mem[e0 + i] = d;
     }
   }
-  if (j.groups > 1) {
-    // a group's worth: its members by `lanes` lanes each, then theirs joined
-    F *mem = reinterpret_cast<F *>(group_mem);
-    float *err_mem = group_mem + (rough ? 1 : 2) * 32 * VPL;
-    const bool sums = j.top2 && j.size > 1;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (e0 + i < j.E) {
-        F c = of_key(key[i]);
-        float err = 0.f;
-        if (sums && x[i] > -a_inf()) {
-          const F p = score(x[i]);
-          if (by_logit) c = p;
-          if (rough) err = error_of((float)p, argument(x[i]), (float)c);
-        } else if (rough && !by_logit && x[i] > -a_inf()) {
-          err = error_of((float)score(x[i]), argument(x[i]), (float)c);
-        }
-        mem[e0 + i] = c;
-        if (rough) err_mem[e0 + i] = err;
-      }
-    __syncwarp();
+  __syncwarp();
+  if (grouped) {
+    const double none = -(double)a_inf();
     int lanes = 1;
     while (2 * lanes * j.groups <= 32) lanes *= 2;
     const int g = lane / lanes;
-    F a = -inf_of<F>(), b = -inf_of<F>();
-    float err = 0.f;  // the largest of the group's (of two members: twice that)
+    double w1 = none, w2 = none;
     if (g < j.groups)
-      for (int m = lane % lanes; m < j.size; m += lanes) {
-        const F c = mem[g * j.size + m];
-        if (rough) err = fmaxf(err, err_mem[g * j.size + m]);
-        b = c > a ? a : (c > b ? c : b);
-        a = c > a ? c : a;
-      }
-    for (int o = 1; o < lanes; o <<= 1) {
-      const F oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
-      if (rough) err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, o));
-      b = oa > a ? (a > ob ? a : ob) : (oa > b ? oa : b);
-      a = oa > a ? oa : a;
-    }
-    F worth = a;
-    if (sums && b > -inf_of<F>()) {
-      worth = a + b;
-      err = 2.f * err + fabsf((float)worth) * 1.2e-7f;
-    }
-    // kept: fewer than `kept` groups are worth more (or as much, and come before)
-    int rank = 0;
-    for (int h = 0; h < j.groups; ++h) {
-      const F w = __shfl_sync(0xffffffffu, worth, h * lanes);
-      rank += w > worth || (w == worth && h < g);
-    }
-    const bool mine = g < j.groups && lane % lanes == 0;
-    const uint32_t keep = __ballot_sync(0xffffffffu, mine && rank < j.kept);  // bit g * lanes
-    if (rough && j.kept < j.groups && !(by_logit && !sums)) {
-      const int in = __ffs(__ballot_sync(0xffffffffu, mine && rank == j.kept - 1)) - 1;
-      const int out = __ffs(__ballot_sync(0xffffffffu, mine && rank == j.kept)) - 1;
-      const F wi = __shfl_sync(0xffffffffu, worth, in), wo = __shfl_sync(0xffffffffu, worth, out);
-      // (of the groups beyond these two some may have a larger bound)
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, o));
-      sure = (float)wi - (float)wo > 2.f * err || (wo == -inf_of<F>() && wi > wo);
-    }
+      for (int m = lane % lanes; m < j.size; m += lanes) top_two(group_mem[g * j.size + m], w1, w2);
+    for (int o = 1; o < lanes; o <<= 1) join_two(w1, w2, o);
+    int rank;
+    const uint32_t keep = keep_groups(sums && w2 > none ? w1 + w2 : w1, j.groups, j.kept, lanes, g, &rank);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (e0 + i < j.E && !((keep >> ((e0 + i) / j.size * lanes)) & 1u)) key[i] = 0;
-    __syncwarp();
   }
-  // rounds: the largest key left; the lane's own largest, and where it is (its first among equals)
-  K best = 0;
-  int at = 0;
-  auto search = [&]() {
-    best = key[0];
-    at = 0;
+  for (int q = 0; q < j.k; ++q) {
+    uint64_t best = 0;
+    int at = 0;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
+    for (int i = 0; i < VPL; ++i)
       if (key[i] > best) {
         best = key[i];
         at = i;
       }
-  };
-  search();
-  K my_key = 0;
-  int my_id = -1;
-  const int rounds = min(j.k + (rough && !by_logit ? 1 : 0), 32 + 1);
-  K extra = 0;
-  int extra_id = -1;
-  for (int q = 0; q < rounds; ++q) {
-    const K m = warp_max(best);
-    if (m == 0) break;  // none left
-    const int who = __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
-    const int id = __shfl_sync(0xffffffffu, e0 + at, who);
-    if (q < 32) {
-      if (lane == q) {
-        my_key = m;
-        my_id = id;
-      }
-    } else {
-      extra = m;
-      extra_id = id;
-    }
-    if (lane == who) {
+    const uint64_t m = warp_max(best);
+    if (lane == __ffs(__ballot_sync(0xffffffffu, best == m)) - 1) {
+      pick.id[q] = e0 + at;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
         if (i == at) key[i] = 0;
-      search();
     }
   }
-  *id_out = my_id;
-  if constexpr (rough) {
-    if (by_logit) return sure;
-    // neighbours in the order: lane q against lane q + 1
-    K next = __shfl_down_sync(0xffffffffu, my_key, 1);
-    int next_id = __shfl_down_sync(0xffffffffu, my_id, 1);
-    if (lane == 31) {
-      next = extra;
-      next_id = extra_id;
-    }
-    // their logits, from the lanes that hold them
-    float mine_x = 0.f, next_x = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const float a = __shfl_sync(0xffffffffu, x[i], max(my_id, 0) / VPL), b = __shfl_sync(0xffffffffu, x[i], max(next_id, 0) / VPL);
-      if (max(my_id, 0) % VPL == i) mine_x = a;
-      if (max(next_id, 0) % VPL == i) next_x = b;
-    }
-    bool near = false;
-    if (lane < j.k && my_id >= 0 && next_id >= 0) {
-      const float c = of_key((uint32_t)my_key), d = of_key((uint32_t)next);
-      const bool open = mine_x > -a_inf(), next_open = next_x > -a_inf();
-      if (open && next_open) {
-        const float err = error_of((float)score(mine_x), argument(mine_x), c) +
-                          error_of((float)score(next_x), argument(next_x), d);
-        near = !(c - d > err) && !(mine_x == next_x && __ldg(j.bias + my_id) == __ldg(j.bias + next_id));
-      }
-    }
-    return sure && !__any_sync(0xffffffffu, near);
-  }
-  return true;
+  __syncwarp();
 }
 
 template <typename T, int VPL>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteJob j) {
-  // per warp: values and bounds of the experts, for the groups' worth
-  __shared__ __align__(16) float group_mem[kRouteWarps][VPL * 32 * 2];
+  __shared__ __align__(16) double group_mem[kRouteWarps][VPL * 32];  // values of the experts, for the groups' worth
+  __shared__ Pick picks[kRouteWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * VPL;
   const int t = blockIdx.x * kRouteWarps + warp;
   if (t >= j.n) return;
   const T *row = static_cast<const T *>(j.logits) + (int64_t)t * j.stride;
-  float x[VPL];
-  constexpr int kVec = VPL * (int)sizeof(T) >= 16 ? 16 : VPL * (int)sizeof(T);  // bytes of a load
-  if (VPL > 1 && j.E % VPL == 0 && ((uintptr_t)row & (kVec - 1)) == 0) {
-    if (e0 < j.E) {
-      if constexpr (kVec == 16) {
-        uint4 w[VPL * sizeof(T) / 16];
+  Pick &pick = picks[warp];
+  float x[VPL], b[VPL];
+  float finite = 0.f;  // stays 0 unless a bias is not finite
+  if (e0 + VPL <= j.E) {
+    load_values<VPL>(row + e0, x);
+    if (j.bias) {
+      load_values<VPL>(j.bias + e0, b);
 #pragma unroll
-        for (int i = 0; i < (int)(VPL * sizeof(T) / 16); ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(row + e0) + i);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) x[i] = r_float(reinterpret_cast<const T *>(w)[i]);
-      } else if constexpr (kVec == 8) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(row + e0));
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) x[i] = r_float(reinterpret_cast<const T *>(&w)[i]);
-      } else if constexpr (kVec == 4) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(row + e0));
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) x[i] = r_float(reinterpret_cast<const T *>(&w)[i]);
-      }
+      for (int i = 0; i < VPL; ++i) finite = fmaf(b[i], 0.f, finite);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (e0 + i < j.E) x[i] = r_float(row[e0 + i]);
-  }
-  float top = -a_inf();
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    if (e0 + i >= j.E) {
-      x[i] = -a_inf();
-    } else {
-      bad |= !(x[i] < a_inf());
-      if (j.bias) bad |= !(fabsf(__ldg(j.bias + e0 + i)) < a_inf());
+    for (int i = 0; i < VPL; ++i) {
+      x[i] = e0 + i < j.E ? r_float(row[e0 + i]) : -a_inf();
+      if (j.bias) {
+        b[i] = e0 + i < j.E ? __ldg(j.bias + e0 + i) : 0.f;
+        finite = fmaf(b[i], 0.f, finite);
+      }
     }
-    top = fmaxf(top, x[i]);
   }
+  float top = x[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) top = max_nan(top, x[i]);
+  top = warp_max(top);
   int32_t *ids = j.ids + (int64_t)t * j.k;
   float *weights = j.weights + (int64_t)t * j.k;
-  if (__any_sync(0xffffffffu, bad)) {
+  if (!(top < a_inf()) || __any_sync(0xffffffffu, !(finite == 0.f))) {
     if (lane == 0 && j.status) atomicOr(j.status, MOE_ROUTE_BAD_LOGIT);
     if (lane < j.k) {
       ids[lane] = lane;
@@ -297,30 +439,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteJob 
     }
     return;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (top == -a_inf()) top = 0.f;  // all closed
-  int id;
-  if (!choose<float, VPL>(j, x, top, group_mem[warp], &id)) choose<double, VPL>(j, x, top, group_mem[warp], &id);
-  // ---- weights: lane q has the choice q
-  const bool live = lane < j.k;
-  float v = -a_inf();
+  float z = 1.f;
+  if (!j.sigmoid && !(j.renorm && !j.bias && j.groups == 1)) {
+    z = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const float a = __shfl_sync(0xffffffffu, x[i], max(id, 0) / VPL);
-    if (max(id, 0) % VPL == i) v = a;
+    for (int i = 0; i < VPL; ++i) z += quick_exp(x[i] - top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   }
-  if (!live) v = -a_inf();
+  const bool sure = choose_quick<VPL>(j, row, x, b, top, z, reinterpret_cast<float *>(group_mem[warp]), pick);
+  __syncwarp();
+  if (!sure) choose_exact<VPL>(j, x, top, group_mem[warp], pick);
+  const bool live = lane < j.k;
+  const int id = live ? pick.id[lane] : 0;
+  const float v = live ? r_float(row[id]) : -a_inf();
+  // ---- weights: lane q has the choice q
   float w;
   if (j.renorm) {
     // p over the sum of p, with a common factor taken out that keeps both numbers
-    float m = j.sigmoid ? fminf(v, 0.f) : v;
-    float most = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float m = j.sigmoid ? fminf(v, 0.f) : v, most = warp_max(m);
     w = v > -a_inf() ? expf(m - most) : 0.f;
-    if (j.sigmoid) w /= 1.f + expf(-fabsf(v));
-    if (!(v > -a_inf())) w = 0.f;
+    if (j.sigmoid) w = v > -a_inf() ? w / (1.f + expf(-fabsf(v))) : 0.f;
     float sum = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -328,11 +468,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteJob 
   } else if (j.sigmoid) {
     w = 1.f / (1.f + expf(-v));
   } else {
-    float z = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) z += expf(x[i] - top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     w = z > 0.f ? expf(v - top) / z : 0.f;
   }
   if (live) {
