@@ -16,13 +16,15 @@
 // having the same logit and bias, the token is done again in 64 bits.
 #include <math.h>
 
+#include <algorithm>
+
 #include "attn_common.cuh"
 #include "moe_route.h"
 
 namespace moe {
 namespace {
 
-constexpr int kRouteWarps = 4;
+constexpr int kRouteWarps = 4, kRouteSms = 152;
 
 struct RouteJob {
   const void *logits;
@@ -103,36 +105,42 @@ constexpr float kSumStep = 1.2e-7f;   // of a sum's two roundings
 constexpr float kFloor = 1e-37f;      // below it, scores are not held with their bits
 
 // What the groups' members are worth, by lanes that have some of them each: a the largest, b the next.
+__device__ __forceinline__ float least_of(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ float most_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double least_of(double a, double b) { return fmin(a, b); }
+__device__ __forceinline__ double most_of(double a, double b) { return fmax(a, b); }
 template <typename F>
 __device__ __forceinline__ void top_two(F c, F &a, F &b) {
-  b = c > a ? a : (c > b ? c : b);
-  a = c > a ? c : a;
+  b = most_of(b, least_of(a, c));
+  a = most_of(a, c);
 }
 template <typename F>
 __device__ __forceinline__ void join_two(F &a, F &b, int o) {
   const F oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
-  b = oa > a ? (a > ob ? a : ob) : (oa > b ? oa : b);
-  a = oa > a ? oa : a;
+  b = most_of(least_of(a, oa), most_of(b, ob));
+  a = most_of(a, oa);
 }
 
-// The kept groups: lane `first` of a group, h * lanes, has its worth.  Returns a bit per group, at h * lanes; rank: the
-// calling lane's group's.
+// The kept groups: the 2^lg lanes of group h, from h 2^lg on, have its worth.  Returns a bit per group, at h 2^lg; rank:
+// the calling lane's group's.
 template <typename F>
-__device__ __forceinline__ uint32_t keep_groups(F worth, int groups, int kept, int lanes, int g, int *rank) {
+__device__ __forceinline__ uint32_t keep_groups(F worth, int groups, int kept, int lg, int *rank) {
+  const int lane = threadIdx.x & 31, g = lane >> lg;
   int r = 0;
+#pragma unroll 4
   for (int h = 0; h < groups; ++h) {
-    const F w = __shfl_sync(0xffffffffu, worth, h * lanes);
+    const F w = __shfl_sync(0xffffffffu, worth, h << lg);
     r += w > worth || (w == worth && h < g);
   }
   *rank = r;
-  return __ballot_sync(0xffffffffu, g < groups && (threadIdx.x & 31) % lanes == 0 && r < kept);
+  return __ballot_sync(0xffffffffu, g < groups && (g << lg) == lane && r < kept);
 }
 
-struct Pick {
+struct __align__(16) Pick {
+  float cand_c[32];  // values that may be among the chosen, in the order of their experts
+  int cand_id[32];
   float c[33];
   int id[33];
-  float cand_c[32];  // values that may be among them, in any order
-  int cand_id[32];
 };
 
 // The choice in 32 bits, into `pick`; whether it is certain.  x: the lane's logits (-inf past E), b: their bias.
@@ -170,8 +178,9 @@ __device__ __forceinline__ bool choose_quick(const RouteJob &j, const T *row, co
       for (int i = 0; i < VPL; ++i) d[i] = c[i];
     }
     // (a power of two of lanes per group, each lane's experts of one group: no shared memory needed)
-    int lanes = j.size / VPL;
-    const bool direct = j.size % VPL == 0 && (lanes & (lanes - 1)) == 0;
+    const int many = j.size / VPL;
+    const bool direct = j.size % VPL == 0 && (many & (many - 1)) == 0;
+    int lg = 31 - __clz(many);
     float w1 = -a_inf(), w2 = -a_inf();
     if (direct) {
 #pragma unroll
@@ -181,18 +190,18 @@ __device__ __forceinline__ bool choose_quick(const RouteJob &j, const T *row, co
       for (int i = 0; i < VPL; ++i)
         if (e0 + i < j.E) group_mem[e0 + i] = d[i];
       __syncwarp();
-      lanes = 1;
-      while (2 * lanes * j.groups <= 32) lanes *= 2;
-      if (lane / lanes < j.groups)
-        for (int m = lane % lanes; m < j.size; m += lanes) top_two(group_mem[lane / lanes * j.size + m], w1, w2);
+      lg = 0;
+      while ((2 << lg) * j.groups <= 32) ++lg;
+      if ((lane >> lg) < j.groups)
+        for (int m = lane & ((1 << lg) - 1); m < j.size; m += 1 << lg) top_two(group_mem[(lane >> lg) * j.size + m], w1, w2);
     }
-    for (int o = 1; o < lanes; o <<= 1) join_two(w1, w2, o);
-    const int g = lane / lanes;
+    const int g = lane >> lg;
+    for (int o = 0; o < lg; ++o) join_two(w1, w2, 1 << o);
     const float worth = sums && w2 > -a_inf() ? w1 + w2 : w1;
     int rank;
-    const uint32_t keep = keep_groups(worth, j.groups, j.kept, lanes, g, &rank);
+    const uint32_t keep = keep_groups(worth, j.groups, j.kept, lg, &rank);
     if (j.kept < j.groups && !(by_logit && !sums)) {
-      const uint32_t first = __ballot_sync(0xffffffffu, g < j.groups && lane % lanes == 0);
+      const uint32_t first = __ballot_sync(0xffffffffu, g < j.groups && (g << lg) == lane);
       const int in = __ffs(__ballot_sync(0xffffffffu, rank == j.kept - 1) & first) - 1;
       const int out = __ffs(__ballot_sync(0xffffffffu, rank == j.kept) & first) - 1;
       const float wi = __shfl_sync(0xffffffffu, worth, in), wo = __shfl_sync(0xffffffffu, worth, out);
@@ -202,33 +211,44 @@ __device__ __forceinline__ bool choose_quick(const RouteJob &j, const T *row, co
       sure = wi - wo > 2.f * err || (wo == -a_inf() && wi > wo);
     }
     if (direct) {
-      if (!((keep >> (g * lanes)) & 1u)) {
+      if (!((keep >> (g << lg)) & 1u)) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) c[i] = -a_inf();
       }
     } else {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (e0 + i < j.E && !((keep >> ((e0 + i) / j.size * lanes)) & 1u)) c[i] = -a_inf();
+        if (e0 + i < j.E && !((keep >> ((e0 + i) / j.size << lg)) & 1u)) c[i] = -a_inf();
     }
   }
   float best = c[0];
 #pragma unroll
   for (int i = 1; i < VPL; ++i) best = fmaxf(best, c[i]);
   const int rounds = j.k + (by_logit ? 0 : 1);
-  // Values from `least` on to the candidates; how many there are (the first 32 are kept).
-  auto collect = [&](float least) {
+  // Values from `least` on to the candidates, and nothing to the places after them; how many there are (of more than 32
+  // not all are kept).
+  auto collect = [&](float from) {
+    const float least = fmaxf(from, -3.4028235e38f);  // what is closed is none
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const bool in = c[i] >= least && c[i] > -a_inf();
-      const uint32_t who = __ballot_sync(0xffffffffu, in);
-      const int at = n + __popc(who & ((1u << lane) - 1u));
-      if (in && at < 32) {
-        pick.cand_c[at] = c[i];
-        pick.cand_id[at] = e0 + i;
-      }
-      n += __popc(who);
+    for (int i = 0; i < VPL; ++i) n += c[i] >= least;
+    int end = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += v;
+    }
+    int at = end - n;
+    n = __shfl_sync(0xffffffffu, end, 31);
+    pick.cand_c[lane] = -a_inf();
+    __syncwarp();
+    if (n <= 32) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (c[i] >= least) {
+          pick.cand_c[at] = c[i];
+          pick.cand_id[at++] = e0 + i;
+        }
     }
     __syncwarp();
     return n;
@@ -238,22 +258,23 @@ __device__ __forceinline__ bool choose_quick(const RouteJob &j, const T *row, co
   float least = best, mine = best;
   for (int q = 0; q < rounds; ++q) {
     least = warp_max(mine);
-    if (least == -a_inf()) break;
-    if (lane == __ffs(__ballot_sync(0xffffffffu, mine == least)) - 1) mine = -a_inf();
+    if (mine == least) mine = -a_inf();
   }
   const int n = collect(least);
   if (n < j.k) return false;  // closed experts follow, of the kept groups first: not told apart here
   if (n <= 32) {
-    const float own = lane < n ? pick.cand_c[lane] : 0.f;
-    const int id = lane < n ? pick.cand_id[lane] : 0;
+    const float own = pick.cand_c[lane];
     int place = 0;
-    for (int s = 0; s < n; ++s) {
-      const float o = pick.cand_c[s];
-      place += o > own || (o == own && pick.cand_id[s] < id);
+    uint32_t equal = 0;
+    for (int s = 0; s < n; s += 4) {
+      const float4 o = *reinterpret_cast<const float4 *>(&pick.cand_c[s]);
+      place += (o.x > own) + (o.y > own) + (o.z > own) + (o.w > own);
+      equal |= (uint32_t)((o.x == own ? 1 : 0) | (o.y == own ? 2 : 0) | (o.z == own ? 4 : 0) | (o.w == own ? 8 : 0)) << s;
     }
+    place += __popc(equal & ((1u << lane) - 1u));  // (the candidates are in the order of their experts)
     if (lane < n && place < rounds) {
       pick.c[place] = own;
-      pick.id[place] = id;
+      pick.id[place] = pick.cand_id[lane];
     }
     if (lane == 0 && n < rounds) pick.id[n] = -1;
     __syncwarp();
@@ -286,20 +307,28 @@ __device__ __forceinline__ bool choose_quick(const RouteJob &j, const T *row, co
   if (!sure || by_logit) return sure;
   // Neighbours in the order, the one after the last among them, are further apart than their errors, or equal by having the
   // same logit and bias.
-  bool near = false;
-  if (lane < j.k) {
-    const int a = pick.id[lane], e = pick.id[lane + 1];
-    if (e >= 0) {
-      const float ca = pick.c[lane], ce = pick.c[lane + 1], va = r_float(row[a]), ve = r_float(row[e]);
-      const float ba = __ldg(j.bias + a), be = __ldg(j.bias + e);
-      const float inv = quick_inverse(z);
-      const float pa = j.sigmoid ? quick_sigmoid(va) : quick_exp(va - top) * inv;
-      const float pe = j.sigmoid ? quick_sigmoid(ve) : quick_exp(ve - top) * inv;
-      const float err = pa * score_error(j.sigmoid, j.sigmoid ? va : va - top) + pe * score_error(j.sigmoid, j.sigmoid ? ve : ve - top) +
-                        kSumStep * (fabsf(ca) + fabsf(ce)) + kFloor;
-      near = !(ca - ce > err) && !(va == ve && ba == be);
+  const float inv = quick_inverse(z);
+  auto error_of = [&](float v, float c) {
+    const float arg = j.sigmoid ? v : v - top;
+    return (j.sigmoid ? quick_sigmoid(v) : quick_exp(arg) * inv) * score_error(j.sigmoid, arg) + kSumStep * fabsf(c) + kFloor;
+  };
+  const int a = lane <= j.k ? pick.id[lane] : -1;  // (at -1 the logit and the bias are not looked at)
+  const float ca = pick.c[lane], va = r_float(row[max(a, 0)]), ba = __ldg(j.bias + max(a, 0)), ea = error_of(va, ca);
+  int e = __shfl_down_sync(0xffffffffu, a, 1);
+  float ce = __shfl_down_sync(0xffffffffu, ca, 1), ve = __shfl_down_sync(0xffffffffu, va, 1);
+  float be = __shfl_down_sync(0xffffffffu, ba, 1), ee = __shfl_down_sync(0xffffffffu, ea, 1);
+  if (j.k == 32) {  // lane 31's neighbour is no lane's
+    const int id = pick.id[32];
+    const float v = r_float(row[max(id, 0)]), c32 = pick.c[32], e32 = error_of(v, c32);
+    if (lane == 31) {
+      e = id;
+      ce = c32;
+      ve = v;
+      be = __ldg(j.bias + max(id, 0));
+      ee = e32;
     }
   }
+  const bool near = lane < j.k && e >= 0 && !(ca - ce > ea + ee) && !(va == ve && ba == be);
   if (!__any_sync(0xffffffffu, near)) return true;
   // Some are not: 64 bits for the few that may be chosen.
   const float last = pick.c[j.k - 1];
@@ -364,18 +393,17 @@ __device__ __noinline__ void choose_exact(const RouteJob &j, const float (&x)[VP
   __syncwarp();
   if (grouped) {
     const double none = -(double)a_inf();
-    int lanes = 1;
-    while (2 * lanes * j.groups <= 32) lanes *= 2;
-    const int g = lane / lanes;
+    int lg = 0;
+    while ((2 << lg) * j.groups <= 32) ++lg;
     double w1 = none, w2 = none;
-    if (g < j.groups)
-      for (int m = lane % lanes; m < j.size; m += lanes) top_two(group_mem[g * j.size + m], w1, w2);
-    for (int o = 1; o < lanes; o <<= 1) join_two(w1, w2, o);
+    if ((lane >> lg) < j.groups)
+      for (int m = lane & ((1 << lg) - 1); m < j.size; m += 1 << lg) top_two(group_mem[(lane >> lg) * j.size + m], w1, w2);
+    for (int o = 0; o < lg; ++o) join_two(w1, w2, 1 << o);
     int rank;
-    const uint32_t keep = keep_groups(sums && w2 > none ? w1 + w2 : w1, j.groups, j.kept, lanes, g, &rank);
+    const uint32_t keep = keep_groups(sums && w2 > none ? w1 + w2 : w1, j.groups, j.kept, lg, &rank);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (e0 + i < j.E && !((keep >> ((e0 + i) / j.size * lanes)) & 1u)) key[i] = 0;
+      if (e0 + i < j.E && !((keep >> ((e0 + i) / j.size << lg)) & 1u)) key[i] = 0;
   }
   for (int q = 0; q < j.k; ++q) {
     uint64_t best = 0;
@@ -402,83 +430,87 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteJob 
   __shared__ __align__(16) double group_mem[kRouteWarps][VPL * 32];  // values of the experts, for the groups' worth
   __shared__ Pick picks[kRouteWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * VPL;
-  const int t = blockIdx.x * kRouteWarps + warp;
-  if (t >= j.n) return;
-  const T *row = static_cast<const T *>(j.logits) + (int64_t)t * j.stride;
   Pick &pick = picks[warp];
-  float x[VPL], b[VPL];
+  float b[VPL];
   float finite = 0.f;  // stays 0 unless a bias is not finite
-  if (e0 + VPL <= j.E) {
-    load_values<VPL>(row + e0, x);
-    if (j.bias) {
+  if (j.bias) {
+    if (e0 + VPL <= j.E) {
       load_values<VPL>(j.bias + e0, b);
+    } else {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) finite = fmaf(b[i], 0.f, finite);
+      for (int i = 0; i < VPL; ++i) b[i] = e0 + i < j.E ? __ldg(j.bias + e0 + i) : 0.f;
     }
-  } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      x[i] = e0 + i < j.E ? r_float(row[e0 + i]) : -a_inf();
-      if (j.bias) {
-        b[i] = e0 + i < j.E ? __ldg(j.bias + e0 + i) : 0.f;
-        finite = fmaf(b[i], 0.f, finite);
-      }
-    }
+    for (int i = 0; i < VPL; ++i) finite = fmaf(b[i], 0.f, finite);
   }
-  float top = x[0];
-#pragma unroll
-  for (int i = 1; i < VPL; ++i) top = max_nan(top, x[i]);
-  top = warp_max(top);
-  int32_t *ids = j.ids + (int64_t)t * j.k;
-  float *weights = j.weights + (int64_t)t * j.k;
-  if (!(top < a_inf()) || __any_sync(0xffffffffu, !(finite == 0.f))) {
-    if (lane == 0 && j.status) atomicOr(j.status, MOE_ROUTE_BAD_LOGIT);
-    if (lane < j.k) {
-      ids[lane] = lane;
-      weights[lane] = a_nan();
-    }
-    return;
-  }
-  if (top == -a_inf()) top = 0.f;  // all closed
-  float z = 1.f;
-  if (!j.sigmoid && !(j.renorm && !j.bias && j.groups == 1)) {
-    z = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) z += quick_exp(x[i] - top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  }
-  const bool sure = choose_quick<VPL>(j, row, x, b, top, z, reinterpret_cast<float *>(group_mem[warp]), pick);
-  __syncwarp();
-  if (!sure) choose_exact<VPL>(j, x, top, group_mem[warp], pick);
+  const bool bad_bias = __any_sync(0xffffffffu, !(finite == 0.f));
   const bool live = lane < j.k;
-  const int id = live ? pick.id[lane] : 0;
-  const float v = live ? r_float(row[id]) : -a_inf();
-  // ---- weights: lane q has the choice q
-  float w;
-  if (j.renorm) {
-    // p over the sum of p, with a common factor taken out that keeps both numbers
-    const float m = j.sigmoid ? fminf(v, 0.f) : v, most = warp_max(m);
-    w = v > -a_inf() ? expf(m - most) : 0.f;
-    if (j.sigmoid) w = v > -a_inf() ? w / (1.f + expf(-fabsf(v))) : 0.f;
-    float sum = w;
+#pragma unroll 1
+  for (int t = blockIdx.x * kRouteWarps + warp; t < j.n; t += gridDim.x * kRouteWarps) {
+    const T *row = static_cast<const T *>(j.logits) + (int64_t)t * j.stride;
+    float x[VPL];
+    if (e0 + VPL <= j.E) {
+      load_values<VPL>(row + e0, x);
+    } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    w = sum > 0.f ? w / sum : 0.f;
-  } else if (j.sigmoid) {
-    w = 1.f / (1.f + expf(-v));
-  } else {
-    w = z > 0.f ? expf(v - top) / z : 0.f;
-  }
-  if (live) {
-    ids[lane] = id;
-    weights[lane] = w * j.scale;
+      for (int i = 0; i < VPL; ++i) x[i] = e0 + i < j.E ? r_float(row[e0 + i]) : -a_inf();
+    }
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) top = max_nan(top, x[i]);
+    top = warp_max(top);
+    int32_t *ids = j.ids + (int64_t)t * j.k + lane;
+    float *weights = j.weights + (int64_t)t * j.k + lane;
+    if (!(top < a_inf()) || bad_bias) {
+      if (lane == 0 && j.status) atomicOr(j.status, MOE_ROUTE_BAD_LOGIT);
+      if (live) {
+        *ids = lane;
+        *weights = a_nan();
+      }
+      continue;
+    }
+    if (top == -a_inf()) top = 0.f;  // all closed
+    float z = 1.f;
+    if (!j.sigmoid && !(j.renorm && !j.bias && j.groups == 1)) {
+      z = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) z += quick_exp(x[i] - top);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    }
+    const bool sure = choose_quick<VPL>(j, row, x, b, top, z, reinterpret_cast<float *>(group_mem[warp]), pick);
+    __syncwarp();
+    if (!sure) choose_exact<VPL>(j, x, top, group_mem[warp], pick);
+    // ---- weights: lane q has the choice q
+    const int id = live ? pick.id[lane] : 0;
+    const float v = live ? r_float(row[id]) : -a_inf();
+    __syncwarp();
+    float w;
+    if (j.renorm) {
+      // p over the sum of p, with a common factor taken out that keeps both numbers
+      const float m = j.sigmoid ? fminf(v, 0.f) : v, most = warp_max(m);
+      w = v > -a_inf() ? expf(m - most) : 0.f;
+      if (j.sigmoid) w = v > -a_inf() ? __fdividef(w, 1.f + expf(-fabsf(v))) : 0.f;
+      float sum = w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      w = sum > 0.f ? __fdividef(w, sum) : 0.f;
+    } else if (j.sigmoid) {
+      w = 1.f / (1.f + expf(-v));
+    } else {
+      w = z > 0.f ? expf(v - top) / z : 0.f;
+    }
+    if (live) {
+      *ids = id;
+      *weights = w * j.scale;
+    }
   }
 }
 
 template <typename T>
 int launch_route(const RouteJob &j, cudaStream_t st) {
-  const unsigned grid = (unsigned)((j.n + kRouteWarps - 1) / kRouteWarps);
+  // (CTAs that run at once: of more tokens a warp takes several, and loads the bias once)
+  const unsigned grid = (unsigned)std::min((j.n + kRouteWarps - 1) / kRouteWarps, kRouteSms * 8);
   const int v = (j.E + 31) / 32;
   if (v <= 1) route_kernel<T, 1><<<grid, 32 * kRouteWarps, 0, st>>>(j);
   else if (v <= 2) route_kernel<T, 2><<<grid, 32 * kRouteWarps, 0, st>>>(j);
