@@ -425,8 +425,12 @@ __device__ __noinline__ void choose_exact(const RouteJob &j, const float (&x)[VP
   __syncwarp();
 }
 
+// CTAs of an SM that registers are left for.
+template <int VPL>
+constexpr int kRouteCtas = VPL <= 8 ? 6 : VPL <= 16 ? 4 : 2;
+
 template <typename T, int VPL>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteJob j) {
+__global__ void __launch_bounds__(32 * kRouteWarps, kRouteCtas<VPL>) route_kernel(const RouteJob j) {
   __shared__ __align__(16) double group_mem[kRouteWarps][VPL * 32];  // values of the experts, for the groups' worth
   __shared__ Pick picks[kRouteWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * VPL;
@@ -507,17 +511,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteJob 
   }
 }
 
+template <typename T, int VPL>
+void run_route(const RouteJob &j, cudaStream_t st) {
+  // (CTAs that run at once: of more tokens a warp takes several, and loads the bias once)
+  const int grid = std::min((j.n + kRouteWarps - 1) / kRouteWarps, kRouteSms * kRouteCtas<VPL>);
+  route_kernel<T, VPL><<<grid, 32 * kRouteWarps, 0, st>>>(j);
+}
 template <typename T>
 int launch_route(const RouteJob &j, cudaStream_t st) {
-  // (CTAs that run at once: of more tokens a warp takes several, and loads the bias once)
-  const unsigned grid = (unsigned)std::min((j.n + kRouteWarps - 1) / kRouteWarps, kRouteSms * 8);
   const int v = (j.E + 31) / 32;
-  if (v <= 1) route_kernel<T, 1><<<grid, 32 * kRouteWarps, 0, st>>>(j);
-  else if (v <= 2) route_kernel<T, 2><<<grid, 32 * kRouteWarps, 0, st>>>(j);
-  else if (v <= 4) route_kernel<T, 4><<<grid, 32 * kRouteWarps, 0, st>>>(j);
-  else if (v <= 8) route_kernel<T, 8><<<grid, 32 * kRouteWarps, 0, st>>>(j);
-  else if (v <= 16) route_kernel<T, 16><<<grid, 32 * kRouteWarps, 0, st>>>(j);
-  else route_kernel<T, 32><<<grid, 32 * kRouteWarps, 0, st>>>(j);
+  if (v <= 1) run_route<T, 1>(j, st);
+  else if (v <= 2) run_route<T, 2>(j, st);
+  else if (v <= 4) run_route<T, 4>(j, st);
+  else if (v <= 8) run_route<T, 8>(j, st);
+  else if (v <= 16) run_route<T, 16>(j, st);
+  else run_route<T, 32>(j, st);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
