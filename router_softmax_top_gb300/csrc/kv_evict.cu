@@ -5,13 +5,14 @@
 // (ties: the earlier token), all in their order, in the slots [0, budget).
 //
 // Choosing: a radix search for the smallest total that stays, 11, 11 and 10 bits of a key
-// that orders like the value, by a cluster of CTAs per (sequence, head): each holds its part
-// of the keys in shared memory, counts are added over the cluster's shared memory.  Then the
-// kept tokens' numbers are written in order, from counts per warp.
+// that orders like the value, until few keys are left, which are compared each with each; by
+// a CTA, or a cluster of them, per (sequence, head): each holds its part of the keys in shared
+// memory, counts are added over the cluster's shared memory.  Then the kept tokens' numbers
+// are written in order, from counts per warp.
 //
 // Moving, in place: the token of rank r goes to slot r, which is never after its own.  A CTA
-// takes the 256 slots of a group: it loads what is to go there into registers, says so, waits
-// for the groups that load from its own 256 slots to have said so (at most two, and none
+// takes the 128 slots of a group: it loads what is to go there into shared memory, says so,
+// waits for the groups that load from its own slots to have said so (at most two, and none
 // later than itself), and writes.  Groups are handed out in order, so whatever one waits for
 // has been begun by a CTA that is running, and loading waits for nothing.
 //
@@ -28,11 +29,11 @@ namespace cg = cooperative_groups;
 namespace moe {
 namespace {
 
-constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kFew = 128;         // keys that are compared each with each
 constexpr int kMostHeld = 49152;  // keys that a CTA's shared memory holds (more are read again for every pass)
-constexpr int kMoveThreads = 256;
-constexpr int kSlots = 256;       // slots of a group
+constexpr int kSmallTokens = 4096;  // caches of so many tokens a sequence at most take a CTA of 256 threads
+constexpr int kSlots = 128;       // slots of a group, a thread each
 constexpr int kEvictSms = 152;
 
 struct EvictJob {
@@ -60,12 +61,26 @@ __device__ __forceinline__ bool length_ok(const EvictJob &j, int n) {
   return n >= 0 && n <= (int64_t)j.c.table_width * j.c.page_size;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictJob j) {
+// CL: a cluster per pair, else one CTA.  NT: its threads.
+template <int NT, bool CL>
+__global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
+  constexpr int NW = NT / 32, PER = kBins / NT;
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[kBins];
-  __shared__ int s_bad, s_bin, s_above, s_warp[2][kSelectWarps], s_count[2], s_scan[kSelectWarps];
+  __shared__ uint32_t hist[3][kBins], s_keys[kFew];
+  __shared__ int s_bad, s_bin, s_above, s_in, s_warp[2][32], s_count[2], s_scan[32], s_few;
+  __shared__ uint32_t s_least;
+  __shared__ int s_need;
+  asm volatile("griddepcontrol.launch_dependents;");
   const cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int ranks = CL ? (int)cluster.num_blocks() : 1, rank = CL ? (int)cluster.block_rank() : 0;
+  auto sync = [&]() {
+    if constexpr (CL) cluster.sync();
+    else __syncthreads();
+  };
+  auto of_rank = [&](auto *p, int r) {
+    if constexpr (CL) return cluster.map_shared_rank(p, r);
+    else return p;
+  };
   const int pair = blockIdx.x / ranks, seq = pair / j.heads, head = pair % j.heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = __ldg(j.lens + seq);
@@ -73,7 +88,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   if (blockIdx.x == 0 && tid == 0) *j.ticket = 0;
   const bool ok = length_ok(j, n);
   if (!ok || n <= j.budget) {  // (all CTAs of the cluster alike)
-    for (int i = rank * kSelectThreads + tid; i < j.budget; i += ranks * kSelectThreads) kept[i] = ok && i < n ? i : -1;
+    for (int i = rank * NT + tid; i < j.budget; i += ranks * NT) kept[i] = ok && i < n ? i : -1;
     if (rank == 0 && tid == 0) {
       j.skip[pair] = 1;
       if (head == 0) j.new_lens[seq] = n;
@@ -84,8 +99,16 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   const int32_t *row = j.c.page_table + (int64_t)seq * j.c.table_stride;
   const int per = ((n + ranks - 1) / ranks + 31) / 32 * 32, a = min(n, rank * per), b = min(n, a + per);
   const bool hold = per <= j.held;
+  const float inverse = 1.f / (float)j.c.page_size;
   auto load = [&](int i) {  // the key of token i; a token without a page has none
-    const int slot = i / j.c.page_size;
+    int slot;
+    if (n <= 1 << 22) {
+      slot = (int)((float)i * inverse);  // its page, or one beside: the product is off by 2^-22 of itself, below 2^17
+      slot -= slot * j.c.page_size > i;
+      slot += (slot + 1) * j.c.page_size <= i;
+    } else {
+      slot = i / j.c.page_size;
+    }
     const int p = __ldg(row + slot);
     if (p < 0 || p >= j.c.n_pages) {
       s_bad = 1;
@@ -94,54 +117,51 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     return total_key(j.totals[((int64_t)p * j.heads + head) * j.c.page_size + (i - slot * j.c.page_size)]);
   };
   auto key = [&](int i) { return hold ? keys[i - a] : load(i); };
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_few = 0;
+  for (int i = tid; i < 3 * kBins; i += NT) hist[0][i] = 0;
   __syncthreads();
+  // ---- the smallest key that stays, and how many of that key
+  const int c0 = j.first, c1 = n - j.recent;  // tokens that may go
+  int need = j.budget - j.first - j.recent;
+  const bool some = need > 0;
 #pragma unroll 4
-  for (int i = a + tid; i < b; i += kSelectThreads) {
+  for (int i = a + tid; i < b; i += NT) {
     const uint32_t k = load(i);
     if (hold) keys[i - a] = k;
+    if (i >= c0 && i < c1) atomicAdd(&hist[0][k >> 21], 1u);
   }
-  for (int g = rank * kSelectThreads + tid; g < (n + kSlots - 1) / kSlots; g += ranks * kSelectThreads)
-    j.loaded[(int64_t)pair * j.groups + g] = 0;
-  cluster.sync();
+  for (int g = rank * NT + tid; g < (n + kSlots - 1) / kSlots; g += ranks * NT) j.loaded[(int64_t)pair * j.groups + g] = 0;
+  sync();
   bool bad = false;
-  for (int r = 0; r < ranks; ++r) bad |= *cluster.map_shared_rank(&s_bad, r) != 0;
+  for (int r = 0; r < ranks; ++r) bad |= *of_rank(&s_bad, r) != 0;
   if (bad) {
-    for (int i = rank * kSelectThreads + tid; i < j.budget; i += ranks * kSelectThreads) kept[i] = -1;
+    for (int i = rank * NT + tid; i < j.budget; i += ranks * NT) kept[i] = -1;
     if (rank == 0 && tid == 0) {
       j.skip[pair] = 1;
       if (head == 0) j.new_lens[seq] = n;
       if (j.c.status) atomicOr(j.c.status, MOE_KV_BAD_PAGE);
     }
-    cluster.sync();  // (the others look at this one's word)
+    sync();  // (the others look at this one's word)
     return;
   }
-  // ---- the smallest key that stays, and how many of that key
-  const int c0 = j.first, c1 = n - j.recent;  // tokens that may go
-  int need = j.budget - j.first - j.recent;
   uint32_t least = 0;
-  const bool some = need > 0;
   if (some) {
-    int done = 0;  // bits found
+    int shift = 21;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int bits = pass < 2 ? 11 : 10, shift = 32 - done - bits;
-      for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = max(a, c0) + tid; i < min(b, c1); i += kSelectThreads) {
-        const uint32_t k = key(i);
-        if (done == 0 || (k >> (shift + bits)) == least) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
-      }
-      cluster.sync();
-      // counts over the cluster, largest key first: this thread's two bins
-      const int hi = kBins - 1 - 2 * tid;
-      int n0 = 0, n1 = 0;
+      // counts over the cluster, largest key first: this thread's bins
+      const int hi = kBins - 1 - PER * tid;
+      int n_bin[PER], inc = 0;
+#pragma unroll
+      for (int z = 0; z < PER; ++z) n_bin[z] = 0;
       for (int r = 0; r < ranks; ++r) {
-        const uint32_t *h = cluster.map_shared_rank(hist, r);
-        n0 += (int)h[hi];
-        n1 += (int)h[hi - 1];
+        const uint32_t *h = of_rank(&hist[pass][0], r);
+#pragma unroll
+        for (int z = 0; z < PER; ++z) n_bin[z] += (int)h[hi - z];
       }
-      int inc = n0 + n1;
+#pragma unroll
+      for (int z = 0; z < PER; ++z) inc += n_bin[z];
+      const int mine = inc;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -149,40 +169,76 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
       }
       if (lane == 31) s_scan[warp] = inc;
       __syncthreads();
-      if (warp == 0) {
-        int v = s_scan[lane];
+      int before = inc - mine;
+      for (int w = 0; w < NW; ++w) before += w < warp ? s_scan[w] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += u;
+      for (int z = 0; z < PER; ++z) {
+        if (before < need && before + n_bin[z] >= need) {
+          s_bin = hi - z;
+          s_above = before;
+          s_in = n_bin[z];
         }
-        s_scan[lane] = v;
+        before += n_bin[z];
       }
       __syncthreads();
-      const int before = inc - n0 - n1 + (warp ? s_scan[warp - 1] : 0);
-      if (before < need && before + n0 >= need) {
-        s_bin = hi;
-        s_above = before;
-      } else if (before + n0 < need && before + n0 + n1 >= need) {
-        s_bin = hi - 1;
-        s_above = before + n0;
-      }
-      cluster.sync();  // (no CTA's counts are needed any more)
-      least = (least << bits) | (uint32_t)s_bin;
+      least = pass == 0 ? (uint32_t)s_bin : (least << (pass == 1 ? 11 : 10)) | (uint32_t)s_bin;
       need -= s_above;
-      done += bits;
-      __syncthreads();
+      const int in = s_in;
+      if (pass == 2) break;
+      if (in <= kFew) {
+        // few enough to be compared each with each: the first CTA's list has them all
+        int *count = of_rank(&s_few, 0);
+        uint32_t *list = of_rank(s_keys, 0);
+        for (int i = max(a, c0) + tid; i < min(b, c1); i += NT) {
+          const uint32_t k = key(i);
+          if ((k >> shift) == least) list[atomicAdd(count, 1)] = k;
+        }
+        sync();
+        uint32_t own = 0;
+        if (tid < in) own = list[tid];
+        if constexpr (CL) {
+          if (rank > 0 && tid < in) s_keys[tid] = own;  // (the first CTA's stays as it is)
+          __syncthreads();
+        }
+        if (tid < in) {
+          int more = 0, equal = 0;
+          for (int s = 0; s < in; ++s) {
+            more += s_keys[s] > own;
+            equal += s_keys[s] == own;
+          }
+          if (more < need && more + equal >= need) {  // (threads of the same key write the same)
+            s_least = own;
+            s_need = need - more;
+          }
+        }
+        __syncthreads();
+        least = s_least;
+        need = s_need;
+        break;
+      }
+      // the next digit of those keys
+      const int bits = pass == 0 ? 11 : 10, down = shift - bits;
+      for (int i = max(a, c0) + tid; i < min(b, c1); i += NT) {
+        const uint32_t k = key(i);
+        if ((k >> shift) == least) atomicAdd(&hist[pass + 1][(k >> down) & ((1u << bits) - 1u)], 1u);
+      }
+      shift = down;
+      sync();
     }
   }
   // ---- the kept tokens in order: a warp takes neighbouring steps of 32; first their counts
-  const int steps = (b - a + 31) / 32, w0 = (int)((int64_t)steps * warp / kSelectWarps), w1 = (int)((int64_t)steps * (warp + 1) / kSelectWarps);
-  auto more = [&](int i) { return some && i >= c0 && i < c1 && i < b && key(i) > least; };
-  auto equal = [&](int i) { return some && i >= c0 && i < c1 && i < b && key(i) == least; };
+  const int steps = (b - a + 31) / 32, w0 = (int)((int64_t)steps * warp / NW), w1 = (int)((int64_t)steps * (warp + 1) / NW);
+  // 2: above the least that stays, 1: that one, 0: goes or is not asked
+  auto kind = [&](int i) {
+    if (!some || i < c0 || i >= c1) return 0;
+    const uint32_t k = key(i);
+    return k > least ? 2 : k == least ? 1 : 0;
+  };
   int gt = 0, eq = 0;
   for (int s = w0; s < w1; ++s) {
-    const int i = a + 32 * s + lane;
-    gt += more(i);
-    eq += equal(i);
+    const int i = a + 32 * s + lane, x = i < b ? kind(i) : 0;
+    gt += x == 2;
+    eq += x == 1;
   }
   gt = (int)__reduce_add_sync(0xffffffffu, gt);
   eq = (int)__reduce_add_sync(0xffffffffu, eq);
@@ -192,7 +248,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   }
   __syncthreads();
   if (warp < 2) {
-    int v = s_warp[warp][lane];
+    int v = lane < NW ? s_warp[warp][lane] : 0;
     const int own = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -202,11 +258,11 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     s_warp[warp][lane] = v - own;
     if (lane == 31) s_count[warp] = v;
   }
-  cluster.sync();
+  sync();
   gt = s_warp[0][warp];
   eq = s_warp[1][warp];
   for (int r = 0; r < rank; ++r) {
-    const int *c = cluster.map_shared_rank(s_count, r);
+    const int *c = of_rank(&s_count[0], r);
     gt += c[0];
     eq += c[1];
   }
@@ -215,10 +271,9 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     const int start = a + 32 * w0;
     int at = min(start, c0) + max(0, start - c1) + gt + min(eq, need);  // kept tokens before the step
     for (int s = w0; s < w1; ++s) {
-      const int i = a + 32 * s + lane;
-      const uint32_t eqs = __ballot_sync(0xffffffffu, equal(i));
-      const bool stay = i < b && (i < c0 || i >= c1 || more(i) ||
-                                  (equal(i) && eq + __popc(eqs & ((1u << lane) - 1u)) < need));
+      const int i = a + 32 * s + lane, x = i < b ? kind(i) : 0;
+      const uint32_t eqs = __ballot_sync(0xffffffffu, x == 1);
+      const bool stay = i < b && (i < c0 || i >= c1 || x == 2 || (x == 1 && eq + __popc(eqs & ((1u << lane) - 1u)) < need));
       const uint32_t stays = __ballot_sync(0xffffffffu, stay);
       if (lane == 0 && (a + 32 * s) % kSlots == 0) group_before[(a + 32 * s) / kSlots] = at;
       if (stay) kept[at + __popc(stays & ((1u << lane) - 1u))] = i;
@@ -231,13 +286,16 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     j.skip[pair] = 0;
     if (head == 0) j.new_lens[seq] = j.budget;
   }
-  cluster.sync();  // (a CTA's counts are read by those after it)
+  if constexpr (CL) cluster.sync();  // (a CTA's counts are read by those after it)
 }
 
-__device__ __forceinline__ uint4 e_load16(const unsigned char *p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-  return v;
+// N bytes (4, 8 or 16) into shared memory, asynchronously.
+template <int N>
+__device__ __forceinline__ void e_copy(void *dst, const void *src) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a_smem(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(a_smem(dst)), "l"(src), "n"(N) : "memory");
 }
 __device__ __forceinline__ bool wait_loaded(const uint32_t *flag) {
   uint64_t t0 = 0;
@@ -254,19 +312,27 @@ __device__ __forceinline__ bool wait_loaded(const uint32_t *flag) {
   return false;
 }
 
-// A token's bytes: codes of keys and values, block by block, their scales, and its total.
 template <int D>
-struct TokenBytes {
-  uint4 codes[2][D / 32];
-  uint32_t scales[2][D / 64];
-  float total;
+struct MoveCfg {
+  static constexpr int kPieces = 2 * (D / 32);  // 16-byte pieces of codes of a token
+  // per thread: its token's codes, the scales of keys and of values (D / 16 bytes each), its total
+  static constexpr int kScale = D / 16;
+  static constexpr size_t kSmem = (size_t)kSlots * (16 * kPieces + 2 * kScale + 4);
+  static constexpr int kCtas = D == 256 ? 6 : 10;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictJob j) {
+__global__ void __launch_bounds__(kSlots) evict_move_kernel(const EvictJob j) {
+  using C = MoveCfg<D>;
+  extern __shared__ __align__(16) unsigned char sm[];
   __shared__ int s_seq, s_head, s_group, s_ok;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (j.c.n_seqs + 31) / 32;
+  // this thread's token on its way: each piece in a row over the threads
+  auto codes = [&](int piece) { return sm + ((size_t)piece * kSlots + tid) * 16; };
+  auto scales = [&](int v) { return sm + (size_t)kSlots * 16 * C::kPieces + ((size_t)v * kSlots + tid) * C::kScale; };
+  float *const my_total = reinterpret_cast<float *>(sm + (size_t)kSlots * (16 * C::kPieces + 2 * C::kScale)) + tid;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (;;) {
     if (warp == 0) {
       // the next group: sequences in order, in one the heads' groups side by side
@@ -287,7 +353,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictJob
       }
       before -= mine;
       u = __shfl_sync(0xffffffffu, u, 0);
-      if (lane == 0) s_seq = -1;
+      if (lane == 0) {
+        s_seq = -1;
+        s_ok = 1;
+      }
       __syncwarp();
       if ((int64_t)u >= before && (int64_t)u < before + mine) {
         int64_t left = (int64_t)u - before;
@@ -308,14 +377,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictJob
     const int seq = s_seq, head = s_head, g = s_group;
     if (seq < 0) return;
     const int pair = seq * j.heads + head;
-    if (j.skip[pair]) {
-      __syncthreads();
-      continue;
-    }
     const int n = __ldg(j.lens + seq), slot = g * kSlots + tid;
     const int32_t *row = j.c.page_table + (int64_t)seq * j.c.table_stride;
-    const int src = slot < j.budget ? j.kept[(int64_t)pair * j.budget + slot] : -1;
-    const bool moves = src > slot, clears = slot >= j.budget && slot < n;
+    const bool skip = j.skip[pair] != 0;
+    const int src = !skip && slot < j.budget ? j.kept[(int64_t)pair * j.budget + slot] : -1;
+    const bool moves = src > slot, clears = !skip && slot >= j.budget && slot < n;
     uint32_t *loaded = j.loaded + (int64_t)pair * j.groups;
     unsigned char *const pages = static_cast<unsigned char *>(j.c.pages);
     // where a token's tile is, and the token in it; the page was seen to be there
@@ -326,7 +392,6 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictJob
       *total = (p * j.heads + head) * j.c.page_size + in;
       return in % kKvTile;
     };
-    TokenBytes<D> x;
     if (moves) {
       int64_t tile, total;
       const int tok = place(src, &tile, &total);
@@ -334,24 +399,26 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictJob
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) x.codes[v][b] = e_load16(tp + kv_code_off(D, v, b, tok));
-#pragma unroll
-        for (int b = 0; b < D / 64; ++b)
-          x.scales[v][b] = *reinterpret_cast<const volatile uint32_t *>(tp + kv_scale_off(D, v, 2 * b, tok));
+        for (int b = 0; b < D / 32; ++b) e_copy<16>(codes(v * (D / 32) + b), tp + kv_code_off(D, v, b, tok));
+        e_copy<C::kScale>(scales(v), tp + kv_scale_off(D, v, 0, tok));
       }
-      x.total = *const_cast<const volatile float *>(j.totals + total);
+      e_copy<4>(my_total, j.totals + total);
     }
-    __threadfence();
+    // who loads from these slots: the groups of the ranks that their tokens have (kSlots at most)
+    int r0 = 0, r1 = 0;
+    if (warp == 0 && !skip) {
+      r0 = j.before[(int64_t)pair * j.groups + g];
+      r1 = j.before[(int64_t)pair * j.groups + g + 1];
+    }
+    int64_t tile = 0, total = 0;
+    int tok = 0;
+    if (moves || clears) tok = place(slot, &tile, &total);
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (what has arrived has been read)
     const bool work = __syncthreads_or(moves || clears);
-    if (tid == 0) {
-      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(loaded + g), "r"(1u) : "memory");
-      s_ok = 1;
-    }
+    // (a release: what the CTA's threads have read before the barrier, they have read before this)
+    if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(loaded + g), "r"(1u) : "memory");
     if (!work) continue;
-    __syncthreads();
     if (warp == 0) {
-      // who loads from these slots: the groups of the ranks that their tokens have (256 at most)
-      const int r0 = j.before[(int64_t)pair * j.groups + g], r1 = j.before[(int64_t)pair * j.groups + g + 1];
       const int h = r0 / kSlots + lane;
       if (r1 > r0 && h <= (r1 - 1) / kSlots && h < g && !wait_loaded(loaded + h)) s_ok = 0;
     }
@@ -361,31 +428,61 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictJob
       __syncthreads();
       continue;
     }
-    __threadfence();
-    if (moves || clears) {
-      int64_t tile, total;
-      const int tok = place(slot, &tile, &total);
-      if (moves) {
-        unsigned char *tp = pages + tile;
+    if (moves) {
+      unsigned char *tp = pages + tile;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
+      for (int v = 0; v < 2; ++v) {
 #pragma unroll
-          for (int b = 0; b < D / 32; ++b) *reinterpret_cast<uint4 *>(tp + kv_code_off(D, v, b, tok)) = x.codes[v][b];
-#pragma unroll
-          for (int b = 0; b < D / 64; ++b) *reinterpret_cast<uint32_t *>(tp + kv_scale_off(D, v, 2 * b, tok)) = x.scales[v][b];
-        }
+        for (int b = 0; b < D / 32; ++b)
+          *reinterpret_cast<uint4 *>(tp + kv_code_off(D, v, b, tok)) = *reinterpret_cast<const uint4 *>(codes(v * (D / 32) + b));
+        unsigned char *sp = tp + kv_scale_off(D, v, 0, tok);
+        if constexpr (C::kScale == 4) *reinterpret_cast<uint32_t *>(sp) = *reinterpret_cast<const uint32_t *>(scales(v));
+        else if constexpr (C::kScale == 8) *reinterpret_cast<uint2 *>(sp) = *reinterpret_cast<const uint2 *>(scales(v));
+        else *reinterpret_cast<uint4 *>(sp) = *reinterpret_cast<const uint4 *>(scales(v));
       }
-      j.totals[total] = moves ? x.total : 0.f;
     }
+    if (moves || clears) j.totals[total] = moves ? *my_total : 0.f;
     __syncthreads();
   }
 }
 
+template <typename... A>
+cudaError_t launch_with(void (*kernel)(A...), int64_t grid, int threads, size_t smem, cudaLaunchAttribute attr, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int NT, bool CL>
+cudaError_t launch_select(const EvictJob &j, int64_t pairs, int ranks, cudaStream_t st) {
+  static DynSmemLimit limit;
+  const size_t smem = (size_t)j.held * 4;
+  // (raised from 16 KB on: the kernel's own arrays, 25 KB, count towards what needs no raising)
+  const cudaError_t e = ensure_dyn_smem(evict_select_kernel<NT, CL>, smem > 16 * 1024 ? std::max<size_t>(smem, 64 * 1024) : smem, limit);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)ranks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  return launch_with(evict_select_kernel<NT, CL>, pairs * ranks, NT, smem, attr, st, j);
+}
+
 template <int D>
-int launch_move(const EvictJob &j, int64_t groups, cudaStream_t st) {
-  const int grid = (int)std::min<int64_t>(groups, kEvictSms * (D == 256 ? 2 : 4));
-  evict_move_kernel<D><<<grid, kMoveThreads, 0, st>>>(j);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+cudaError_t launch_move(const EvictJob &j, int64_t groups, cudaStream_t st) {
+  using C = MoveCfg<D>;
+  static DynSmemLimit limit;
+  const cudaError_t e = ensure_dyn_smem(evict_move_kernel<D>, C::kSmem, limit);
+  if (e != cudaSuccess) return e;
+  // a programmatic dependent of the kernel before it: its CTAs are there when that ends
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return launch_with(evict_move_kernel<D>, std::min<int64_t>(groups, (int64_t)kEvictSms * C::kCtas), kSlots, C::kSmem, attr, st, j);
 }
 
 int64_t evict_groups(const moe_kv_cache *c) { return ((int64_t)c->table_width * c->page_size + kSlots - 1) / kSlots + 1; }
@@ -429,32 +526,19 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
   j.loaded = reinterpret_cast<uint32_t *>(j.before + pairs * j.groups);
   // a cluster per pair, of as many CTAs as there is room for and keys to count
   int ranks = 1;
-  while (ranks < 8 && pairs * ranks < 2 * kEvictSms && tokens > 2048 * (int64_t)ranks) ranks *= 2;
+  while (ranks < 8 && pairs * ranks * 2 <= 2 * kEvictSms && tokens > kSmallTokens * (int64_t)ranks) ranks *= 2;
   j.held = (int)std::min<int64_t>(kMostHeld, ((tokens + ranks - 1) / ranks + 31) / 32 * 32);
   cudaStream_t st = (cudaStream_t)cuda_stream;
-  static DynSmemLimit limit;
-  const size_t smem = (size_t)j.held * 4;
-  // (raised from 32 KB on: the kernel's own arrays count towards what needs no raising)
-  if (ensure_dyn_smem(evict_select_kernel, smem > 32 * 1024 ? std::max<size_t>(smem, 64 * 1024) : smem, limit) != cudaSuccess) {
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
+  cudaError_t e = ranks > 1               ? launch_select<1024, true>(j, pairs, ranks, st)
+                  : tokens > kSmallTokens ? launch_select<1024, false>(j, pairs, 1, st)
+                                          : launch_select<256, false>(j, pairs, 1, st);
+  if (e == cudaSuccess && tokens > budget) {  // (else no sequence is over it)
+    const int64_t groups = pairs * (j.groups - 1);
+    e = c->head_dim == 64    ? launch_move<64>(j, groups, st)
+        : c->head_dim == 128 ? launch_move<128>(j, groups, st)
+                             : launch_move<256>(j, groups, st);
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ranks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(pairs * ranks));
-  cfg.blockDim = dim3(kSelectThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, j) != cudaSuccess) {
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  if (tokens <= budget) return MOE_OK;  // no sequence is over it
-  const int64_t groups = pairs * (j.groups - 1);
-  return c->head_dim == 64 ? launch_move<64>(j, groups, st) : c->head_dim == 128 ? launch_move<128>(j, groups, st) : launch_move<256>(j, groups, st);
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
 }
