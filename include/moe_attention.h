@@ -232,8 +232,8 @@ int moe_prompt_weigh(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads,
  * of a sequence of n <= budget tokens 0..n-1, then -1.
  * A sequence whose length makes no sense, or one of whose pages is none, is left as it
  * is, with its length, and -1 for all of kept.
- * workspace: moe_kv_evict_workspace bytes, 256-byte aligned, of any contents; used by one
- * call at a time.
+ * totals: 16-byte aligned.  workspace: moe_kv_evict_workspace bytes, 256-byte aligned, of
+ * any contents; used by one call at a time.
  */
 int64_t moe_kv_evict_workspace(const moe_kv_cache *c);
 int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *totals, int32_t budget, int32_t first,

@@ -65,7 +65,7 @@ __device__ __forceinline__ bool length_ok(const EvictJob &j, int n) {
 template <int NT, bool CL>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
   constexpr int NW = NT / 32, PER = kBins / NT;
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[3][kBins], s_keys[kFew];
   __shared__ int s_bad, s_bin, s_above, s_in, s_warp[2][32], s_count[2], s_scan[32], s_few;
   __shared__ uint32_t s_least;
@@ -97,10 +97,11 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
     return;
   }
   const int32_t *row = j.c.page_table + (int64_t)seq * j.c.table_stride;
-  const int per = ((n + ranks - 1) / ranks + 31) / 32 * 32, a = min(n, rank * per), b = min(n, a + per);
+  const int per = ((n + ranks - 1) / ranks + kSlots - 1) / kSlots * kSlots, a = min(n, rank * per), b = min(n, a + per);
   const bool hold = per <= j.held;
   const float inverse = 1.f / (float)j.c.page_size;
-  auto load = [&](int i) {  // the key of token i; a token without a page has none
+  // the keys of tokens i to i + 3, i a multiple of 4 below n; tokens without a page have none
+  auto load = [&](int i) {
     int slot;
     if (n <= 1 << 22) {
       slot = (int)((float)i * inverse);  // its page, or one beside: the product is off by 2^-22 of itself, below 2^17
@@ -112,23 +113,38 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
     const int p = __ldg(row + slot);
     if (p < 0 || p >= j.c.n_pages) {
       s_bad = 1;
-      return 0u;
+      return make_uint4(0u, 0u, 0u, 0u);
     }
-    return total_key(j.totals[((int64_t)p * j.heads + head) * j.c.page_size + (i - slot * j.c.page_size)]);
+    const float4 v = *reinterpret_cast<const float4 *>(j.totals + ((int64_t)p * j.heads + head) * j.c.page_size + (i - slot * j.c.page_size));
+    return make_uint4(total_key(v.x), total_key(v.y), total_key(v.z), total_key(v.w));
   };
-  auto key = [&](int i) { return hold ? keys[i - a] : load(i); };
+  auto four = [&](int i) { return hold ? *reinterpret_cast<const uint4 *>(keys + (i - a)) : load(i); };
+  // f(token, key) for those of tokens i to i + 3 that may go
+  const int c0 = j.first, c1 = n - j.recent;
+  auto each = [&](int i, const uint4 &k, auto f) {
+    if (i >= c0 && i + 4 <= min(b, c1)) {
+      f(i, k.x);
+      f(i + 1, k.y);
+      f(i + 2, k.z);
+      f(i + 3, k.w);
+    } else {
+      const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        if (i + z >= c0 && i + z < min(b, c1)) f(i + z, w[z]);
+    }
+  };
   if (tid == 0) s_bad = s_few = 0;
   for (int i = tid; i < 3 * kBins; i += NT) hist[0][i] = 0;
   __syncthreads();
   // ---- the smallest key that stays, and how many of that key
-  const int c0 = j.first, c1 = n - j.recent;  // tokens that may go
   int need = j.budget - j.first - j.recent;
   const bool some = need > 0;
 #pragma unroll 4
-  for (int i = a + tid; i < b; i += NT) {
-    const uint32_t k = load(i);
-    if (hold) keys[i - a] = k;
-    if (i >= c0 && i < c1) atomicAdd(&hist[0][k >> 21], 1u);
+  for (int i = a + 4 * tid; i < b; i += 4 * NT) {
+    const uint4 k = load(i);
+    if (hold) *reinterpret_cast<uint4 *>(keys + (i - a)) = k;
+    each(i, k, [&](int, uint32_t x) { atomicAdd(&hist[0][x >> 21], 1u); });
   }
   for (int g = rank * NT + tid; g < (n + kSlots - 1) / kSlots; g += ranks * NT) j.loaded[(int64_t)pair * j.groups + g] = 0;
   sync();
@@ -189,10 +205,10 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
         // few enough to be compared each with each: the first CTA's list has them all
         int *count = of_rank(&s_few, 0);
         uint32_t *list = of_rank(s_keys, 0);
-        for (int i = max(a, c0) + tid; i < min(b, c1); i += NT) {
-          const uint32_t k = key(i);
-          if ((k >> shift) == least) list[atomicAdd(count, 1)] = k;
-        }
+        for (int i = a + 4 * tid; i < b; i += 4 * NT)
+          each(i, four(i), [&](int, uint32_t x) {
+            if ((x >> shift) == least) list[atomicAdd(count, 1)] = x;
+          });
         sync();
         uint32_t own = 0;
         if (tid < in) own = list[tid];
@@ -218,32 +234,34 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
       }
       // the next digit of those keys
       const int bits = pass == 0 ? 11 : 10, down = shift - bits;
-      for (int i = max(a, c0) + tid; i < min(b, c1); i += NT) {
-        const uint32_t k = key(i);
-        if ((k >> shift) == least) atomicAdd(&hist[pass + 1][(k >> down) & ((1u << bits) - 1u)], 1u);
-      }
+      for (int i = a + 4 * tid; i < b; i += 4 * NT)
+        each(i, four(i), [&](int, uint32_t x) {
+          if ((x >> shift) == least) atomicAdd(&hist[pass + 1][(x >> down) & ((1u << bits) - 1u)], 1u);
+        });
       shift = down;
       sync();
     }
   }
-  // ---- the kept tokens in order: a warp takes neighbouring steps of 32; first their counts
-  const int steps = (b - a + 31) / 32, w0 = (int)((int64_t)steps * warp / NW), w1 = (int)((int64_t)steps * (warp + 1) / NW);
-  // 2: above the least that stays, 1: that one, 0: goes or is not asked
-  auto kind = [&](int i) {
-    if (!some || i < c0 || i >= c1) return 0;
-    const uint32_t k = key(i);
-    return k > least ? 2 : k == least ? 1 : 0;
+  // ---- the kept tokens in order.  Before a token come S that stay in any case and E whose key is the least that stays:
+  // its rank is S + min(E, need).  A warp takes neighbouring steps of 128 tokens; first their counts.
+  const int steps = (b - a + kSlots - 1) / kSlots, w0 = (int)((int64_t)steps * warp / NW), w1 = (int)((int64_t)steps * (warp + 1) / NW);
+  // of tokens i to i + 3: bit z for one that stays, bit 4 + z for one of the least key
+  auto kinds = [&](int i) {
+    uint32_t bits = 0;
+    if (i >= b) return bits;
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      if (i + z < b && (i + z < c0 || i + z >= c1)) bits |= 1u << z;
+    if (some)
+      each(i, four(i), [&](int x, uint32_t k) { bits |= k > least ? 1u << (x - i) : k == least ? 16u << (x - i) : 0u; });
+    return bits;
   };
-  int gt = 0, eq = 0;
-  for (int s = w0; s < w1; ++s) {
-    const int i = a + 32 * s + lane, x = i < b ? kind(i) : 0;
-    gt += x == 2;
-    eq += x == 1;
-  }
-  gt = (int)__reduce_add_sync(0xffffffffu, gt);
-  eq = (int)__reduce_add_sync(0xffffffffu, eq);
+  auto counts = [](uint32_t bits) { return (uint64_t)__popc(bits & 15u) | (uint64_t)__popc(bits >> 4) << 32; };
+  uint64_t mine = 0;
+  for (int s = w0; s < w1; ++s) mine += counts(kinds(a + kSlots * s + 4 * lane));
+  int sure = (int)__reduce_add_sync(0xffffffffu, (uint32_t)mine), eq = (int)__reduce_add_sync(0xffffffffu, (uint32_t)(mine >> 32));
   if (lane == 0) {
-    s_warp[0][warp] = gt;
+    s_warp[0][warp] = sure;
     s_warp[1][warp] = eq;
   }
   __syncthreads();
@@ -259,27 +277,36 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
     if (lane == 31) s_count[warp] = v;
   }
   sync();
-  gt = s_warp[0][warp];
+  sure = s_warp[0][warp];
   eq = s_warp[1][warp];
   for (int r = 0; r < rank; ++r) {
     const int *c = of_rank(&s_count[0], r);
-    gt += c[0];
+    sure += c[0];
     eq += c[1];
   }
   int32_t *group_before = j.before + (int64_t)pair * j.groups;
-  {
-    const int start = a + 32 * w0;
-    int at = min(start, c0) + max(0, start - c1) + gt + min(eq, need);  // kept tokens before the step
-    for (int s = w0; s < w1; ++s) {
-      const int i = a + 32 * s + lane, x = i < b ? kind(i) : 0;
-      const uint32_t eqs = __ballot_sync(0xffffffffu, x == 1);
-      const bool stay = i < b && (i < c0 || i >= c1 || x == 2 || (x == 1 && eq + __popc(eqs & ((1u << lane) - 1u)) < need));
-      const uint32_t stays = __ballot_sync(0xffffffffu, stay);
-      if (lane == 0 && (a + 32 * s) % kSlots == 0) group_before[(a + 32 * s) / kSlots] = at;
-      if (stay) kept[at + __popc(stays & ((1u << lane) - 1u))] = i;
-      at += __popc(stays);
-      eq += __popc(eqs);
+  for (int s = w0; s < w1; ++s) {
+    const int i = a + kSlots * s + 4 * lane;
+    const uint32_t bits = kinds(i);
+    // counts of the lanes before, of a step at most 128 each
+    uint32_t own = (uint32_t)__popc(bits & 15u) | (uint32_t)__popc(bits >> 4) << 16, inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
     }
+    int S = sure + (int)((inc - own) & 0xffffu), E = eq + (int)((inc - own) >> 16);
+    if (lane == 0) group_before[(a + kSlots * s) / kSlots] = S + min(E, need);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      const bool same = (bits >> (4 + z)) & 1u;
+      if (((bits >> z) & 1u) || (same && E < need)) kept[S + min(E, need)] = i + z;
+      S += (bits >> z) & 1u;
+      E += same;
+    }
+    inc = __shfl_sync(0xffffffffu, inc, 31);
+    sure += (int)(inc & 0xffffu);
+    eq += (int)(inc >> 16);
   }
   if (rank == 0 && tid == 0) {
     group_before[(n + kSlots - 1) / kSlots] = j.budget;
@@ -503,7 +530,7 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
   if (c && c->n_seqs == 0) return MOE_OK;
   if (const int rc = check_cache(c)) return rc;
   if (!seq_lens || !totals || !new_lens || budget < 0 || first < 0 || recent < 0 || (int64_t)first + recent > budget ||
-      (!kept && budget > 0) || (uintptr_t)totals % 4 || (uintptr_t)kept % 4 || (uintptr_t)new_lens % 4)
+      (!kept && budget > 0) || (uintptr_t)totals % 16 || (uintptr_t)kept % 4 || (uintptr_t)new_lens % 4)
     return MOE_ERR_INVALID_ARG;
   if ((int64_t)c->table_width * c->page_size > 0x7fffffff || (int64_t)c->n_seqs * c->n_kv_heads > 0x7fffffff / 8)
     return MOE_ERR_UNSUPPORTED;
@@ -527,7 +554,7 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
   // a cluster per pair, of as many CTAs as there is room for and keys to count
   int ranks = 1;
   while (ranks < 8 && pairs * ranks * 2 <= 2 * kEvictSms && tokens > kSmallTokens * (int64_t)ranks) ranks *= 2;
-  j.held = (int)std::min<int64_t>(kMostHeld, ((tokens + ranks - 1) / ranks + 31) / 32 * 32);
+  j.held = (int)std::min<int64_t>(kMostHeld, ((tokens + ranks - 1) / ranks + kSlots - 1) / kSlots * kSlots);
   cudaStream_t st = (cudaStream_t)cuda_stream;
   cudaError_t e = ranks > 1               ? launch_select<1024, true>(j, pairs, ranks, st)
                   : tokens > kSmallTokens ? launch_select<1024, false>(j, pairs, 1, st)
