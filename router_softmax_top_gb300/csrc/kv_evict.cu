@@ -32,6 +32,7 @@ namespace {
 constexpr int kBins = 2048;
 constexpr int kFew = 128;         // keys that are compared each with each
 constexpr int kMostHeld = 49152;  // keys that a CTA's shared memory holds (more are read again for every pass)
+constexpr int kMostHeldByTwo = 16384;  // of two CTAs on an SM
 constexpr int kSmallTokens = 4096;  // caches of so many tokens a sequence at most take a CTA of 256 threads
 constexpr int kSlots = 128;       // slots of a group, a thread each
 constexpr int kEvictSms = 152;
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
   constexpr int NW = NT / 32, PER = kBins / NT;
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[3][kBins], s_keys[kFew];
-  __shared__ int s_bad, s_bin, s_above, s_in, s_warp[2][32], s_count[2], s_scan[32], s_few;
+  __shared__ int s_bad, s_share[3], s_found[3][3], s_warp[2][32], s_count[2], s_scan[32], s_few;
   __shared__ uint32_t s_least;
   __shared__ int s_need;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -165,16 +166,18 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
     int shift = 21;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      // counts over the cluster, largest key first: this thread's bins
-      const int hi = kBins - 1 - PER * tid;
+      // Counts over the cluster, largest key first: a CTA adds up its share of the bins, `pt` of them a thread.
+      const int share = kBins / ranks, pt = max(1, share / NT), hi = kBins - 1 - rank * share - pt * tid;
       int n_bin[PER], inc = 0;
 #pragma unroll
       for (int z = 0; z < PER; ++z) n_bin[z] = 0;
-      for (int r = 0; r < ranks; ++r) {
-        const uint32_t *h = of_rank(&hist[pass][0], r);
+      if (pt * tid < share)
+        for (int r = 0; r < ranks; ++r) {
+          const uint32_t *h = of_rank(&hist[pass][0], r);
 #pragma unroll
-        for (int z = 0; z < PER; ++z) n_bin[z] += (int)h[hi - z];
-      }
+          for (int z = 0; z < PER; ++z)
+            if (z < pt) n_bin[z] += (int)h[hi - z];
+        }
 #pragma unroll
       for (int z = 0; z < PER; ++z) inc += n_bin[z];
       const int mine = inc;
@@ -185,21 +188,39 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
       }
       if (lane == 31) s_scan[warp] = inc;
       __syncthreads();
-      int before = inc - mine;
-      for (int w = 0; w < NW; ++w) before += w < warp ? s_scan[w] : 0;
+      int before = inc - mine, all = 0;
+      for (int w = 0; w < NW; ++w) {
+        const int v = s_scan[w];
+        before += w < warp ? v : 0;
+        all += v;
+      }
+      int owner = 0;  // the CTA whose share the count is reached in
+      if constexpr (CL) {
+        if (tid == 0) s_share[pass] = all;
+        sync();
+        int sum = 0;
+        owner = -1;
+        for (int r = 0; r < ranks; ++r) {
+          const int v = *of_rank(&s_share[pass], r);
+          before += r < rank ? v : 0;
+          sum += v;
+          if (owner < 0 && sum >= need) owner = r;
+        }
+      }
 #pragma unroll
       for (int z = 0; z < PER; ++z) {
         if (before < need && before + n_bin[z] >= need) {
-          s_bin = hi - z;
-          s_above = before;
-          s_in = n_bin[z];
+          s_found[pass][0] = hi - z;
+          s_found[pass][1] = before;
+          s_found[pass][2] = n_bin[z];
         }
         before += n_bin[z];
       }
-      __syncthreads();
-      least = pass == 0 ? (uint32_t)s_bin : (least << (pass == 1 ? 11 : 10)) | (uint32_t)s_bin;
-      need -= s_above;
-      const int in = s_in;
+      sync();
+      const int *found = of_rank(&s_found[pass][0], owner);
+      least = pass == 0 ? (uint32_t)found[0] : (least << (pass == 1 ? 11 : 10)) | (uint32_t)found[0];
+      need -= found[1];
+      const int in = found[2];
       if (pass == 2) break;
       if (in <= kFew) {
         // few enough to be compared each with each: the first CTA's list has them all
@@ -496,7 +517,39 @@ cudaError_t launch_select(const EvictJob &j, int64_t pairs, int ranks, cudaStrea
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = (unsigned)ranks;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  if (ranks > 8) {
+    const cudaError_t f = cudaFuncSetAttribute(evict_select_kernel<NT, CL>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (f != cudaSuccess) return f;
+  }
   return launch_with(evict_select_kernel<NT, CL>, pairs * ranks, NT, smem, attr, st, j);
+}
+
+// Clusters of 16 CTAs that run at once on the current device.
+int wide_clusters() {
+  static std::atomic<int> known[DynSmemLimit::kDevices] = {};
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= DynSmemLimit::kDevices) return 0;
+  if (const int k = known[dev].load(std::memory_order_relaxed)) return k - 1;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 16;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(1024);
+  cfg.dynamicSmemBytes = kMostHeld * 4;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const auto kernel = evict_select_kernel<1024, true>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
 }
 
 template <int D>
@@ -551,13 +604,16 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
   j.skip = static_cast<int32_t *>(workspace) + 64;
   j.before = j.skip + pairs;
   j.loaded = reinterpret_cast<uint32_t *>(j.before + pairs * j.groups);
-  // a cluster per pair, of as many CTAs as there is room for and keys to count
+  // A cluster per pair, of as many CTAs as there is room for and keys to count; one of 1024 threads is alone on its SM, of
+  // 512 two are.  Sixteen CTAs are more than every GPU has room for.
   int ranks = 1;
   while (ranks < 8 && pairs * ranks * 2 <= 2 * kEvictSms && tokens > kSmallTokens * (int64_t)ranks) ranks *= 2;
+  if (ranks == 8 && pairs * 16 <= kEvictSms && tokens > kSmallTokens * 8 && wide_clusters() >= pairs) ranks = 16;
   j.held = (int)std::min<int64_t>(kMostHeld, ((tokens + ranks - 1) / ranks + kSlots - 1) / kSlots * kSlots);
   cudaStream_t st = (cudaStream_t)cuda_stream;
-  cudaError_t e = ranks > 1               ? launch_select<1024, true>(j, pairs, ranks, st)
-                  : tokens > kSmallTokens ? launch_select<1024, false>(j, pairs, 1, st)
+  const bool two = pairs * ranks > kEvictSms && j.held <= kMostHeldByTwo;
+  cudaError_t e = ranks > 1 ? (two ? launch_select<512, true>(j, pairs, ranks, st) : launch_select<1024, true>(j, pairs, ranks, st))
+                  : tokens > kSmallTokens ? (two ? launch_select<512, false>(j, pairs, 1, st) : launch_select<1024, false>(j, pairs, 1, st))
                                           : launch_select<256, false>(j, pairs, 1, st);
   if (e == cudaSuccess && tokens > budget) {  // (else no sequence is over it)
     const int64_t groups = pairs * (j.groups - 1);
