@@ -117,6 +117,9 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
       return make_uint4(0u, 0u, 0u, 0u);
     }
     const float4 v = *reinterpret_cast<const float4 *>(j.totals + ((int64_t)p * j.heads + head) * j.c.page_size + (i - slot * j.c.page_size));
+    const uint4 u = make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w));
+    if (max(max(u.x, u.y), max(u.z, u.w)) <= 0x7f800000u)  // the usual: none negative, none NaN
+      return make_uint4(u.x | 0x80000000u, u.y | 0x80000000u, u.z | 0x80000000u, u.w | 0x80000000u);
     return make_uint4(total_key(v.x), total_key(v.y), total_key(v.z), total_key(v.w));
   };
   auto four = [&](int i) { return hold ? *reinterpret_cast<const uint4 *>(keys + (i - a)) : load(i); };
@@ -270,17 +273,28 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
   auto kinds = [&](int i) {
     uint32_t bits = 0;
     if (i >= b) return bits;
+    if (some) {
+      const uint4 k = four(i);
+      bits = (k.x > least ? 1u : 0u) | (k.y > least ? 2u : 0u) | (k.z > least ? 4u : 0u) | (k.w > least ? 8u : 0u);
+      bits |= (k.x == least ? 16u : 0u) | (k.y == least ? 32u : 0u) | (k.z == least ? 64u : 0u) | (k.w == least ? 128u : 0u);
+    }
+    if (i < c0 || i + 4 > c1) {
 #pragma unroll
-    for (int z = 0; z < 4; ++z)
-      if (i + z < b && (i + z < c0 || i + z >= c1)) bits |= 1u << z;
-    if (some)
-      each(i, four(i), [&](int x, uint32_t k) { bits |= k > least ? 1u << (x - i) : k == least ? 16u << (x - i) : 0u; });
+      for (int z = 0; z < 4; ++z)
+        if (i + z < c0 || i + z >= c1) bits = (bits & ~(17u << z)) | (i + z < b ? 1u << z : 0u);
+    }
     return bits;
   };
-  auto counts = [](uint32_t bits) { return (uint64_t)__popc(bits & 15u) | (uint64_t)__popc(bits >> 4) << 32; };
-  uint64_t mine = 0;
-  for (int s = w0; s < w1; ++s) mine += counts(kinds(a + kSlots * s + 4 * lane));
-  int sure = (int)__reduce_add_sync(0xffffffffu, (uint32_t)mine), eq = (int)__reduce_add_sync(0xffffffffu, (uint32_t)(mine >> 32));
+  uint32_t saved = 0;  // of the warp's first four steps
+  int sure = 0, eq = 0;
+  for (int s = w0; s < w1; ++s) {
+    const uint32_t bits = kinds(a + kSlots * s + 4 * lane);
+    if (s < w0 + 4) saved |= bits << (8 * (s - w0));
+    sure += __popc(bits & 15u);
+    eq += __popc(bits >> 4);
+  }
+  sure = (int)__reduce_add_sync(0xffffffffu, (uint32_t)sure);
+  eq = (int)__reduce_add_sync(0xffffffffu, (uint32_t)eq);
   if (lane == 0) {
     s_warp[0][warp] = sure;
     s_warp[1][warp] = eq;
@@ -308,7 +322,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
   int32_t *group_before = j.before + (int64_t)pair * j.groups;
   for (int s = w0; s < w1; ++s) {
     const int i = a + kSlots * s + 4 * lane;
-    const uint32_t bits = kinds(i);
+    const uint32_t bits = s < w0 + 4 ? (saved >> (8 * (s - w0))) & 255u : kinds(i);
     // counts of the lanes before, of a step at most 128 each
     uint32_t own = (uint32_t)__popc(bits & 15u) | (uint32_t)__popc(bits >> 4) << 16, inc = own;
 #pragma unroll
@@ -318,12 +332,11 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
     }
     int S = sure + (int)((inc - own) & 0xffffu), E = eq + (int)((inc - own) >> 16);
     if (lane == 0) group_before[(a + kSlots * s) / kSlots] = S + min(E, need);
+    int32_t *to = kept + S + min(E, need);
 #pragma unroll
     for (int z = 0; z < 4; ++z) {
-      const bool same = (bits >> (4 + z)) & 1u;
-      if (((bits >> z) & 1u) || (same && E < need)) kept[S + min(E, need)] = i + z;
-      S += (bits >> z) & 1u;
-      E += same;
+      const bool stays = ((bits >> z) & 1u) || (((bits >> (4 + z)) & 1u) && E++ < need);
+      if (stays) *to++ = i + z;
     }
     inc = __shfl_sync(0xffffffffu, inc, 31);
     sure += (int)(inc & 0xffffu);
@@ -604,17 +617,18 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
   j.skip = static_cast<int32_t *>(workspace) + 64;
   j.before = j.skip + pairs;
   j.loaded = reinterpret_cast<uint32_t *>(j.before + pairs * j.groups);
-  // A cluster per pair, of as many CTAs as there is room for and keys to count; one of 1024 threads is alone on its SM, of
-  // 512 two are.  Sixteen CTAs are more than every GPU has room for.
+  // A cluster per pair where pairs alone leave SMs idle and have many keys (32 sequences of 12000 tokens on 4 heads: 21 us
+  // as clusters of two, 15 us so; one of 131071 on 8 heads 8 CTAs each).  A CTA of 1024 threads is alone on its SM, of 512
+  // two are.  Sixteen CTAs are more than every GPU has room for.
   int ranks = 1;
-  while (ranks < 8 && pairs * ranks * 2 <= 2 * kEvictSms && tokens > kSmallTokens * (int64_t)ranks) ranks *= 2;
+  while (ranks < 8 && pairs * ranks * 2 <= kEvictSms && tokens > 2 * kSmallTokens * (int64_t)ranks) ranks *= 2;
   if (ranks == 8 && pairs * 16 <= kEvictSms && tokens > kSmallTokens * 8 && wide_clusters() >= pairs) ranks = 16;
   j.held = (int)std::min<int64_t>(kMostHeld, ((tokens + ranks - 1) / ranks + kSlots - 1) / kSlots * kSlots);
   cudaStream_t st = (cudaStream_t)cuda_stream;
-  const bool two = pairs * ranks > kEvictSms && j.held <= kMostHeldByTwo;
-  cudaError_t e = ranks > 1 ? (two ? launch_select<512, true>(j, pairs, ranks, st) : launch_select<1024, true>(j, pairs, ranks, st))
-                  : tokens > kSmallTokens ? (two ? launch_select<512, false>(j, pairs, 1, st) : launch_select<1024, false>(j, pairs, 1, st))
-                                          : launch_select<256, false>(j, pairs, 1, st);
+  cudaError_t e = ranks > 1                                            ? launch_select<1024, true>(j, pairs, ranks, st)
+                  : tokens <= kSmallTokens                             ? launch_select<256, false>(j, pairs, 1, st)
+                  : pairs <= kEvictSms || j.held > kMostHeldByTwo ? launch_select<1024, false>(j, pairs, 1, st)
+                                                                       : launch_select<512, false>(j, pairs, 1, st);
   if (e == cudaSuccess && tokens > budget) {  // (else no sequence is over it)
     const int64_t groups = pairs * (j.groups - 1);
     e = c->head_dim == 64    ? launch_move<64>(j, groups, st)
