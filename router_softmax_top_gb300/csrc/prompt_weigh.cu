@@ -16,14 +16,16 @@
 //  * Tiles of keys are handed out in their order: earlier ones are seen by more rows, so the
 //    longest come first.  Where there are fewer tiles than room for CTAs, a cluster shares a
 //    tile's rows, and sums are joined in a fixed order: results do not depend on timing.
-//  * The score less lse is formed before the factor log2(e), which keeps large weights, whose
-//    difference is small, to the score's own rounding.  Sums are fp32, of a tile's rows first.
+//  * The factor log2(e) is in the score's, c, and lse is multiplied by c / scale in two parts:
+//    of large weights, whose difference is small, only the score's own rounding is left.  Sums
+//    are fp32, of a tile's rows first.
 //  * Only tiles of rows that do not all see all keys are masked.  A row that a key does not
 //    see cannot reach it, whatever it holds.
 // Every wait is bounded; when one gives up all roles stop, the tile's totals become NaN and the
 // status word says so.
 #include <algorithm>
 #include <cooperative_groups.h>
+#include <type_traits>
 
 #include "tc_common.cuh"
 
@@ -43,7 +45,7 @@ struct SumJob {
   int64_t table_stride;
   int table_width, n_pages, page_size;
   int n_q, n_k, n_seqs, hq, hkv, group, tile_tokens, window, restart;
-  float scale;
+  float c, k_high, k_low;  // the scale times log2(e), rounded, and c / scale, in two parts
   int32_t *status;
 };
 
@@ -250,22 +252,42 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
     const int r_tok = tid / j.group, r_head = w.head * j.group + tid % j.group;
     bool ok = true;
     float total = 0.f;
-    // row `tid` of a tile: its lse (with a row that is none: infinity) and position
+    // row `tid` of a tile: less its lse, in log2 units (with a row that is none: less infinity), and its position
     auto row_of = [&](int i, float *l, int *pos) {
       const int tok = first_token(i) + r_tok;
       const bool live = tid < live_rows && tok < w.row1;
-      *l = live ? __ldg(j.lse + (int64_t)(w.q0 + tok) * j.hq + r_head) : a_inf();
+      const float x = live ? __ldg(j.lse + (int64_t)(w.q0 + tok) * j.hq + r_head) : a_inf();
+      *l = fabsf(x) < a_inf() ? -fmaf(x, j.k_low, x * j.k_high) : -x;
       *pos = live ? off + tok : -1;
     };
     if (n_tiles > 0) {
       float l;
       int pos;
       row_of(0, &l, &pos);
-      s_lse[0][tid] = -l;
+      s_lse[0][tid] = l;
       s_pos[0][tid] = pos;
       asm volatile("bar.sync 1, 128;" ::: "memory");
     }
-    const uint64_t scale2 = f2_pack(j.scale, j.scale), log2e2 = f2_pack(kLog2e, kLog2e);
+    const uint64_t c2 = f2_pack(j.c, j.c);
+    // 32 columns' weights, added to sum.  (Masked or not as a whole: a branch per column would leave nothing to overlap.)
+    auto weigh = [&](const float *v, const float *ls, const int *ps, uint64_t (&sum)[2], auto is_masked) {
+#pragma unroll
+      for (int z = 0; z < 32; z += 4) {
+        const float4 l4 = *reinterpret_cast<const float4 *>(ls + z);
+        float a, b, c, d;
+        f2_unpack(f2_fma(f2_pack(v[z], v[z + 1]), c2, f2_pack(l4.x, l4.y)), a, b);
+        f2_unpack(f2_fma(f2_pack(v[z + 2], v[z + 3]), c2, f2_pack(l4.z, l4.w)), c, d);
+        if constexpr (decltype(is_masked)::value) {
+          const int4 p4 = *reinterpret_cast<const int4 *>(ps + z);
+          a = key <= p4.x && key > p4.x - back ? a : -a_inf();
+          b = key <= p4.y && key > p4.y - back ? b : -a_inf();
+          c = key <= p4.z && key > p4.z - back ? c : -a_inf();
+          d = key <= p4.w && key > p4.w - back ? d : -a_inf();
+        }
+        sum[0] = f2_add(sum[0], f2_pack(a_exp2(a), a_exp2(b)));
+        sum[1] = f2_add(sum[1], f2_pack(a_exp2(c), a_exp2(d)));
+      }
+    };
     for (int i = 0; i < n_tiles; ++i) {
       const int buf = i % NB;
       float l = 0.f;
@@ -295,29 +317,14 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
             __syncwarp();
             if (lane == 0) a_mbar_arrive(&s_empty[buf]);
           }
-          const bool masked = !whole || 32 * (x + 1) > live_rows;
-#pragma unroll
-          for (int z = 0; z < 32; z += 4) {
-            const float4 l4 = *reinterpret_cast<const float4 *>(ls + 32 * x + z);
-            float a, b, c, d;
-            f2_unpack(f2_mul(f2_fma(f2_pack(v[z], v[z + 1]), scale2, f2_pack(l4.x, l4.y)), log2e2), a, b);
-            f2_unpack(f2_mul(f2_fma(f2_pack(v[z + 2], v[z + 3]), scale2, f2_pack(l4.z, l4.w)), log2e2), c, d);
-            if (masked) {
-              const int4 p4 = *reinterpret_cast<const int4 *>(ps + 32 * x + z);
-              a = key <= p4.x && key > p4.x - back ? a : -a_inf();
-              b = key <= p4.y && key > p4.y - back ? b : -a_inf();
-              c = key <= p4.z && key > p4.z - back ? c : -a_inf();
-              d = key <= p4.w && key > p4.w - back ? d : -a_inf();
-            }
-            sum[0] = f2_add(sum[0], f2_pack(a_exp2(a), a_exp2(b)));
-            sum[1] = f2_add(sum[1], f2_pack(a_exp2(c), a_exp2(d)));
-          }
+          if (!whole || 32 * (x + 1) > live_rows) weigh(v, ls + 32 * x, ps + 32 * x, sum, std::true_type());
+          else weigh(v, ls + 32 * x, ps + 32 * x, sum, std::false_type());
         }
         float a, b;
         f2_unpack(f2_add(sum[0], sum[1]), a, b);
         total += a + b;
       }
-      s_lse[(i + 1) & 1][tid] = -l;
+      s_lse[(i + 1) & 1][tid] = l;
       s_pos[(i + 1) & 1][tid] = pos;
       asm volatile("bar.sync 1, 128;" ::: "memory");
     }
@@ -429,7 +436,12 @@ MOE_API int moe_prompt_weigh(const moe_tensor *q, int32_t n_q_tokens, int32_t n_
   j.tile_tokens = kTileRows / group;
   j.window = window;
   j.restart = restart != 0;
-  j.scale = scale;
+  // t = c s - k lse with k = c / scale: the same rounding of c in both, so that of large weights, whose difference is small,
+  // only the score's own rounding is left.  (Of a scale near the least numbers c is too coarse for that.)
+  j.c = scale * kLog2e;
+  const double ratio = j.c > 1e-36f ? (double)j.c / (double)scale : 1.4426950408889634;
+  j.k_high = (float)ratio;
+  j.k_low = (float)(ratio - (double)j.k_high);
   j.status = status;
   // without queries none are loaded, but the map wants an address and a size
   if (n_q_tokens == 0 && !j.restart) return MOE_OK;
