@@ -54,8 +54,9 @@ struct SumCfg {
   static constexpr int kStages = 2;
   static constexpr int kBufs = 2;
   static constexpr int kCtas = D == 256 ? 1 : 2;
-  static constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5;
-  static constexpr int kThreads = 32 * 6;
+  // two warpgroups for the weights, a score buffer each
+  static constexpr int kSoftWarps = 4 * kBufs, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+  static constexpr int kThreads = 32 * (kSoftWarps + 2);
   static constexpr uint32_t kTile = kTileRows * D * 2;  // bytes of 128 rows or keys
   static constexpr uint32_t kQOff = kTile;
   static constexpr size_t kSmem = (1 + kStages) * (size_t)kTile + 1024;
@@ -92,9 +93,9 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   __shared__ SumWork s_work;
-  __shared__ __align__(16) float s_lse[2][kTileRows];
-  __shared__ __align__(16) int s_pos[2][kTileRows];
-  __shared__ float s_sum[kTileRows];
+  __shared__ __align__(16) float s_lse[NB][2][kTileRows];
+  __shared__ __align__(16) int s_pos[NB][2][kTileRows];
+  __shared__ float s_sum[NB][kTileRows];
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   unsigned char *const sm_al = sm_raw + ((1024u - (a_smem(sm_raw) & 1023u)) & 1023u);
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
     }
     for (int i = 0; i < NB; ++i) {
       a_mbar_init(&s_full[i], 1);
-      a_mbar_init(&s_empty[i], C::kSoftWarps);
+      a_mbar_init(&s_empty[i], 4);
     }
     a_mbar_init(&done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -244,29 +245,32 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
       __syncwarp();
     }
   } else {
-    // ---- weights: thread = key
-    const int key = w.key0 + tid, off = w.n_k - w.n_q;
-    const int last_key = min(w.n_k, w.key0 + kTileRows) - 1;
+    // ---- weights: thread = key; warpgroup `buf` has the tiles of that buffer
+    const int buf = warp / 4, r = tid & 127;
+    const int key = w.key0 + r, off = w.n_k - w.n_q, last_key = min(w.n_k, w.key0 + kTileRows) - 1;
     const int back = j.window > 0 ? j.window : 0x7fffffff;
-    const uint32_t lanes = (uint32_t)warp << 21;  // 32 warp in the lane field
-    const int r_tok = tid / j.group, r_head = w.head * j.group + tid % j.group;
+    const uint32_t s_col = tmem + ((uint32_t)(warp & 3) << 21) + buf * kTileRows;  // 32 (warp % 4) in the lane field
+    const int r_tok = r / j.group, r_head = w.head * j.group + r % j.group;
     bool ok = true;
     float total = 0.f;
-    // row `tid` of a tile: less its lse, in log2 units (with a row that is none: less infinity), and its position
+    // row r of a tile: its lse (infinity for a row that is none) and position
     auto row_of = [&](int i, float *l, int *pos) {
       const int tok = first_token(i) + r_tok;
-      const bool live = tid < live_rows && tok < w.row1;
-      const float x = live ? __ldg(j.lse + (int64_t)(w.q0 + tok) * j.hq + r_head) : a_inf();
-      *l = fabsf(x) < a_inf() ? -fmaf(x, j.k_low, x * j.k_high) : -x;
+      const bool live = r < live_rows && tok < w.row1;
+      *l = live ? __ldg(j.lse + (int64_t)(w.q0 + tok) * j.hq + r_head) : a_inf();
       *pos = live ? off + tok : -1;
     };
-    if (n_tiles > 0) {
+    // for the warpgroup: less the lse, in log2 units (of a row that is none: less infinity)
+    auto put_row = [&](int at, float l, int pos) {
+      s_lse[buf][at][r] = fabsf(l) < a_inf() ? -fmaf(l, j.k_low, l * j.k_high) : -l;
+      s_pos[buf][at][r] = pos;
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + buf) : "memory");
+    };
+    if (buf < n_tiles) {
       float l;
       int pos;
-      row_of(0, &l, &pos);
-      s_lse[0][tid] = l;
-      s_pos[0][tid] = pos;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      row_of(buf, &l, &pos);
+      put_row(0, l, pos);
     }
     const uint64_t c2 = f2_pack(j.c, j.c);
     // 32 columns' weights, added to sum.  (Masked or not as a whole: a branch per column would leave nothing to overlap.)
@@ -288,29 +292,25 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
         sum[1] = f2_add(sum[1], f2_pack(a_exp2(c), a_exp2(d)));
       }
     };
-    for (int i = 0; i < n_tiles; ++i) {
-      const int buf = i % NB;
+    for (int i = buf, n = 0; i < n_tiles; i += NB, ++n) {
       float l = 0.f;
       int pos = -1;
-      if (i + 1 < n_tiles) row_of(i + 1, &l, &pos);
+      if (i + NB < n_tiles) row_of(i + NB, &l, &pos);
       // (after a failure the warp goes on to the barrier, which counts all four)
-      ok = ok && __all_sync(0xffffffffu, a_mbar_wait(&s_full[buf], (uint32_t)(i / NB) & 1u, &s_fail)) != 0;
+      ok = ok && __all_sync(0xffffffffu, a_mbar_wait(&s_full[buf], (uint32_t)n & 1u, &s_fail)) != 0;
       if (!ok) s_fail = 1;
       if (ok) {
         p_fence_after();
         const int t0 = first_token(i), t1 = min(w.row1, t0 + j.tile_tokens) - 1;  // the tile's tokens
         const bool whole = off + t0 >= last_key && (int64_t)off + t1 - back < w.key0 && t1 - t0 + 1 == j.tile_tokens;
-        const uint32_t s_col = tmem + lanes + buf * kTileRows;
-        const float *ls = s_lse[i & 1];
-        const int *ps = s_pos[i & 1];
-        float s[2][32];
+        const float *ls = s_lse[buf][n & 1];
+        const int *ps = s_pos[buf][n & 1];
         uint64_t sum[2] = {0, 0};
-        p_ld32(s_col, s[0]);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          float *v = s[x & 1];
+          float v[32];
+          p_ld32(s_col + 32 * x, v);
           ld_wait32(v);
-          if (x < 3) p_ld32(s_col + 32 * (x + 1), s[(x + 1) & 1]);
           if (x == 3) {
             // (all scores are in registers)
             p_fence_before();
@@ -324,11 +324,9 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
         f2_unpack(f2_add(sum[0], sum[1]), a, b);
         total += a + b;
       }
-      s_lse[(i + 1) & 1][tid] = l;
-      s_pos[(i + 1) & 1][tid] = pos;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      put_row((n + 1) & 1, l, pos);
     }
-    s_sum[tid] = ok ? total : a_nan();
+    s_sum[buf][r] = ok ? total : a_nan();
   }
   p_fence_before();
   __syncthreads();
@@ -338,8 +336,12 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
   if (ranks > 1) cluster.sync();
   if (rank == 0 && w.seq >= 0 && tid < kTileRows && (all_tiles > 0 || j.restart)) {
     const int key = w.key0 + tid;
-    float total = s_sum[tid];
-    for (int r = 1; r < ranks; ++r) total += *cluster.map_shared_rank(&s_sum[tid], r);
+    float total = 0.f;
+    for (int r = 0; r < ranks; ++r) {
+      const float *sum = ranks > 1 ? cluster.map_shared_rank(&s_sum[0][tid], r) : &s_sum[0][tid];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) total += sum[b * kTileRows];
+    }
     if (key < w.n_k) {
       int in_page = 0;
       const int p = kv_page(j.page_table + (int64_t)w.seq * j.table_stride, j.table_width, j.n_pages, j.page_size, key / kKvTile,
