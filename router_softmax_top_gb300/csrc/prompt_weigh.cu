@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
       put_row(0, l, pos);
     }
     const uint64_t c2 = f2_pack(j.c, j.c);
-    // 32 columns' weights, added to sum.  (Masked or not as a whole: a branch per column would leave nothing to overlap.)
+    // 32 columns' weights, added to sum.  (No branch within a tile: it would leave less to overlap.)
     auto weigh = [&](const float *v, const float *ls, const int *ps, uint64_t (&sum)[2], auto is_masked) {
 #pragma unroll
       for (int z = 0; z < 32; z += 4) {
@@ -292,6 +292,23 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
         sum[1] = f2_add(sum[1], f2_pack(a_exp2(c), a_exp2(d)));
       }
     };
+    // A tile's 128 columns, the first `plain` 32s of them not masked.
+    auto tile = [&](const float *ls, const int *ps, uint64_t (&sum)[2], auto plain) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float v[32];
+        p_ld32(s_col + 32 * x, v);
+        ld_wait32(v);
+        if (x == 3) {
+          // (all scores are in registers)
+          p_fence_before();
+          __syncwarp();
+          if (lane == 0) a_mbar_arrive(&s_empty[buf]);
+        }
+        if (x < decltype(plain)::value) weigh(v, ls + 32 * x, ps + 32 * x, sum, std::false_type());
+        else weigh(v, ls + 32 * x, ps + 32 * x, sum, std::true_type());
+      }
+    };
     for (int i = buf, n = 0; i < n_tiles; i += NB, ++n) {
       float l = 0.f;
       int pos = -1;
@@ -306,20 +323,9 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
         const float *ls = s_lse[buf][n & 1];
         const int *ps = s_pos[buf][n & 1];
         uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          float v[32];
-          p_ld32(s_col + 32 * x, v);
-          ld_wait32(v);
-          if (x == 3) {
-            // (all scores are in registers)
-            p_fence_before();
-            __syncwarp();
-            if (lane == 0) a_mbar_arrive(&s_empty[buf]);
-          }
-          if (!whole || 32 * (x + 1) > live_rows) weigh(v, ls + 32 * x, ps + 32 * x, sum, std::true_type());
-          else weigh(v, ls + 32 * x, ps + 32 * x, sum, std::false_type());
-        }
+        if (whole && live_rows == kTileRows) tile(ls, ps, sum, std::integral_constant<int, 4>());
+        else if (whole && live_rows >= 96) tile(ls, ps, sum, std::integral_constant<int, 3>());
+        else tile(ls, ps, sum, std::integral_constant<int, 0>());
         float a, b;
         f2_unpack(f2_add(sum[0], sum[1]), a, b);
         total += a + b;
