@@ -49,6 +49,11 @@ struct SumJob {
   int32_t *status;
 };
 
+constexpr int kSumSms = 152;
+// CTAs that a call is to have at least, in those that run at once: with 1, 2, 4 and 8 of them 8192 tokens of 32 heads of
+// 128 on 8 take 249, 228, 243 and 286 us, twelve packed prompts with 24 heads of 64 on 8 44, 44, 58 and 84 us.
+constexpr int kSumShare = 2;
+
 template <int D>
 struct SumCfg {
   static constexpr int kStages = 2;
@@ -119,7 +124,8 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
-    // the sequence and tile of this CTA: sequences in order, in one the key heads of a tile side by side
+    // The sequence and tile of this CTA, the key heads of a tile side by side.  Tiles far from their sequence's end are seen
+    // by most rows: of up to 32 sequences they are taken by that, of more sequence by sequence.
     const int unit = blockIdx.x / ranks, mine = unit / j.hkv;
     const bool look_at_all = blockIdx.x == 0 && j.status;  // (the first CTA tells what is wrong with any offset)
     int before = 0, end = 0;  // tiles of the sequences before; where the latest of their keys end
@@ -149,15 +155,36 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
         if (bad && look_at_all) atomicOr(j.status, MOE_KV_BAD_LENGTH);
         n = bad ? 0 : (d - c + kTileRows - 1) / kTileRows;
       }
-      int inc = n;
+      bool hit = false;
+      int tile = 0;
+      if (j.n_seqs <= 32) {
+        // all sequences' tiles, furthest from their sequence's end first: tiles that are `level` before the last
+        auto beyond = [&](int level) { return (int)__reduce_add_sync(0xffffffffu, max(0, n - level)); };
+        int lo = 0, hi = __reduce_max_sync(0xffffffffu, n);
+        if (mine < beyond(0)) {
+          while (hi - lo > 1) {  // beyond(lo) > mine >= beyond(hi)
+            const int mid = (lo + hi) / 2;
+            if (beyond(mid) > mine) lo = mid;
+            else hi = mid;
+          }
+          const int rank_in = mine - beyond(lo + 1);  // among the sequences that reach this level
+          const uint32_t reach = __ballot_sync(0xffffffffu, n > lo);
+          hit = n > lo && __popc(reach & ((1u << lane) - 1u)) == rank_in;
+        }
+        tile = n - 1 - lo;
+      } else {
+        int inc = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        hit = mine >= before + inc - n && mine < before + inc;
+        tile = mine - (before + inc - n);
+        before += __shfl_sync(0xffffffffu, inc, 31);
       }
-      const bool hit = mine >= before + inc - n && mine < before + inc;
       if (hit) {
-        const int tile = mine - (before + inc - n), off = (d - c) - (b - a), key0 = tile * kTileRows;
+        const int off = (d - c) - (b - a), key0 = tile * kTileRows;
         const int last_key = min(d - c, key0 + kTileRows) - 1;
         // rows stand at off + i; those from key0 on see some of the keys, unless they are a window past the last
         const int row0 = min(b - a, max(0, key0 - off));
@@ -165,7 +192,6 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
         if (j.window > 0) row1 = (int)min((int64_t)row1, max((int64_t)row0, (int64_t)last_key + j.window - off));
         s_work = {s, a, b - a, c, d - c, key0, unit % j.hkv, row0, row1};
       }
-      before += __shfl_sync(0xffffffffu, inc, 31);
       found |= __any_sync(0xffffffffu, hit) != 0;
     }
     if (!found && lane == 0) s_work = {-1, 0, 0, 0, 0, 0, 0, 0, 0};
@@ -378,9 +404,11 @@ int launch_sum(const SumJob &j, const moe_tensor &q, const moe_tensor &k, int dt
   // at most this many tiles of keys: a sequence's last one may be partly filled
   const int64_t units = ((int64_t)j.n_k / kTileRows + std::min<int64_t>(j.n_seqs, j.n_k)) * j.hkv;
   if (units * 8 > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  // a tile's rows shared by a cluster where that fills the GPU; never more CTAs than tiles of rows
+  // A tile's rows are shared by a cluster, so that the longest tile is no more than a part of what an SM gets of all:
+  // a causal sequence's first tile has twice the mean.  Never more CTAs than tiles of rows for their warpgroups.
   int ranks = 1;
-  while (ranks < 8 && units * ranks * 2 <= 152 * C::kCtas && (int64_t)ranks * 2 * j.tile_tokens <= j.n_q) ranks *= 2;
+  while (ranks < 8 && units * ranks < (int64_t)kSumShare * kSumSms * C::kCtas && (int64_t)ranks * 2 * C::kBufs * j.tile_tokens <= j.n_q)
+    ranks *= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
