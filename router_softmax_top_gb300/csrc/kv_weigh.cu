@@ -63,6 +63,12 @@ __device__ __forceinline__ void w_mma(float c[4], uint32_t a0, uint32_t a1, uint
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void w_mma_first(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // Low nibbles of bytes 0 and 2, less 8, as fp16; and the high ones.
 __device__ __forceinline__ uint32_t low_codes(uint32_t w) {
   const uint32_t x = (w & 0x000F000Fu) | 0x64006400u;  // 1024 + q
@@ -177,8 +183,8 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
       int64_t first_seen, unused;
       kv_visible(len, j.q_tokens, 0, j.window, &first_seen, &unused);
       // tokens whose totals begin at 0, and those that are written at all
-      const int64_t new_from = j.restart ? 0 : max(0, len - j.q_tokens);
-      const int64_t write_from = j.restart ? 0 : first_seen;
+      const int new_from = j.restart ? 0 : max(0, len - j.q_tokens);
+      const int write_from = j.restart ? 0 : (int)first_seen;
       const int32_t *row = j.c.page_table + (int64_t)seq * j.c.table_stride;
 #pragma unroll 1
       for (int r0 = 0; r0 < n_rows; r0 += 8 * RT) {
@@ -240,9 +246,14 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
         big = __any_sync(0xffffffffu, big);
         __syncwarp();
         // tiles that all rows of this pass see whole
-        int64_t lo, hi, whole_lo, whole_hi;
-        kv_visible(len, j.q_tokens, (min(n_rows, r0 + 8 * RT) - 1) / j.group, j.window, &whole_lo, &hi);
-        kv_visible(len, j.q_tokens, r0 / j.group, j.window, &lo, &whole_hi);
+        int whole_lo, whole_hi;
+        {
+          int64_t lo, hi, a, b;
+          kv_visible(len, j.q_tokens, (min(n_rows, r0 + 8 * RT) - 1) / j.group, j.window, &a, &hi);
+          kv_visible(len, j.q_tokens, r0 / j.group, j.window, &lo, &b);
+          whole_lo = (int)a;
+          whole_hi = (int)b;
+        }
 
         // ---- loads, a tile ahead; a lane looks up the page of one of the next 32 tiles
         int64_t my_src = -1, my_total = -1;
@@ -289,13 +300,7 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
             float c[RT][2][4];
             uint4 qf[RT];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              qf[rt] = q_mem[(rt * NB + b) * 32 + lane];
-#pragma unroll
-              for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) c[rt][mt][z] = 0.f;
-            }
+            for (int rt = 0; rt < RT; ++rt) qf[rt] = q_mem[(rt * NB + b) * 32 + lane];
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
               const uint32_t wa = k.w[b][2 * mt], wb = k.w[b][2 * mt + 1], wa8 = wa >> 8, wb8 = wb >> 8;
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
               const uint32_t h0 = high_codes(wa), h1 = high_codes(wb), h2 = high_codes(wa8), h3 = high_codes(wb8);
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt) {
-                w_mma(c[rt][mt], a0, a1, a2, a3, qf[rt].x, qf[rt].y);
+                w_mma_first(c[rt][mt], a0, a1, a2, a3, qf[rt].x, qf[rt].y);
                 w_mma(c[rt][mt], h0, h1, h2, h3, qf[rt].z, qf[rt].w);
               }
             }
@@ -326,25 +331,30 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
               for (int x = 0; x < 8; ++x) s[rt][x / 4][x % 4] *= ahead[rt][x & 1];
-          const bool whole = tok0 >= whole_lo && tok0 + kKvTile <= whole_hi;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};  // of tokens 8 x + g
+          auto weights = [&](auto is_whole) {
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
+            for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              int64_t rlo = 0, rhi = 0x7fffffff;
-              if (!whole) {
-                const int rr = r0 + 8 * rt + 2 * t + z;
-                rhi = 0;
-                if (rr < n_rows) kv_visible(len, j.q_tokens, rr / j.group, j.window, &rlo, &rhi);
+              for (int z = 0; z < 2; ++z) {
+                int rlo = 0, rhi = 0;
+                if (!decltype(is_whole)::value) {
+                  const int rr = r0 + 8 * rt + 2 * t + z;
+                  int64_t lo64 = 0, hi64 = 0;
+                  if (rr < n_rows) kv_visible(len, j.q_tokens, rr / j.group, j.window, &lo64, &hi64);
+                  rlo = (int)lo64;
+                  rhi = (int)hi64;
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const float p = a_exp2(fmaf(s[rt][x / 2][2 * (x % 2) + z], f[rt][z], -lse[rt][z]) * kLog2e);
+                  const int tok = tok0 + 8 * x + g;
+                  sum[x] += decltype(is_whole)::value || (tok >= rlo && tok < rhi) ? p : 0.f;
+                }
               }
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float p = a_exp2(fmaf(s[rt][x / 2][2 * (x % 2) + z], f[rt][z], -lse[rt][z]) * kLog2e);
-                const int tok = tok0 + 8 * x + g;
-                sum[x] += whole || (tok >= rlo && tok < rhi) ? p : 0.f;
-              }
-            }
+          };
+          if (tok0 >= whole_lo && tok0 + kKvTile <= whole_hi) weights(std::true_type());
+          else weights(std::false_type());
           // over the four lanes of a token; lane t is left with tokens 8 t + g
           const float a0 = t & 2 ? sum[2] : sum[0], a1 = t & 2 ? sum[3] : sum[1];
           const float b0 = t & 2 ? sum[0] : sum[2], b1 = t & 2 ? sum[1] : sum[3];
