@@ -7,12 +7,13 @@
 // Bound: the key half of the cache (18 D bytes per tile of 32 tokens and head), and the
 // totals, read and written.  The 32-token tiles of all (sequence, key head) pairs in a row,
 // plus a few tiles' worth per pair for its set-up, are split evenly over all warps; a warp
-// loads the next tile into registers while it works on one, each load being 128 neighbouring
-// bytes (8 tokens' 16-byte pieces of a block), so nothing passes through shared memory.
-//  * Scores: K Q^T (m16n8k16), codes as the whole numbers q - 8 in fp16: a nibble under the
-//    exponent of 1024 (or its 16-fold) is one mask and one packed addition away from it.  The
-//    query is rounded to fp16 after a power-of-two scaling per row (exact for bf16 and fp16
-//    inputs down to 2^-37 of the row's largest value); products are exact, sums fp32.
+// copies its own tiles (the key half of a tile is contiguous: one bulk copy) into a ring of its
+// own, two to four ahead, and no barrier stands in the loop.
+//  * Scores: K Q^T (m16n8k16), codes as the whole numbers q - 8 in fp16 (high nibbles times 16,
+//    which the query's share takes back): a nibble under the exponent of 1024 is one operation
+//    and one packed addition away from it.  The query is rounded to fp16 after a power-of-two
+//    scaling per row (exact for bf16 and fp16 inputs down to 2^-23 of the row's largest value,
+//    what is smaller to 2^-34 of that); products are exact, sums fp32.
 //  * The score less lse is formed before the factor log2(e): of large weights, whose
 //    difference is small, only the score's own rounding is left.
 //  * Sums over rows stay in registers, then among the four lanes that share a token; the
@@ -43,19 +44,19 @@ struct WeighJob {
 template <int D, int RT>
 struct WeighCfg {
   static constexpr int NB = D / 32;
-  static constexpr int kCtas = D == 256 ? 1 : 2;               // per SM
-  static constexpr int kQuery = RT * NB * 32 * 16;             // bytes of a warp's query operand
-  static constexpr size_t kSmem = (size_t)kWeighWarps * kQuery;
+  static constexpr int kStages = D == 64 ? 4 : 2;                        // of a warp's ring
+  static constexpr int kTile = 18 * D;                                   // bytes of a tile's keys and their scales
+  static constexpr int kQuery = RT * NB * 32 * 16;                       // bytes of a warp's query operand
+  static constexpr int kWarp = kStages * kTile + kQuery;
+  static constexpr size_t kSmem = (size_t)kWeighWarps * kWarp;
+  // per SM, by registers (24, 16 or 8 warps) and shared memory
+  static constexpr int kCtas = RT == 1 ? (D == 256 ? 2 : 3) : RT == 2 ? (D == 256 ? 1 : 2) : 1;
+  static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ float w_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float w_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ uint32_t w_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
-__device__ __forceinline__ uint32_t w_load(const unsigned char *p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
 // (not volatile: the compiler may hoist it over the arithmetic before it)
 __device__ __forceinline__ void w_mma(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
@@ -69,15 +70,18 @@ __device__ __forceinline__ void w_mma_first(float c[4], uint32_t a0, uint32_t a1
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// Low nibbles of bytes 0 and 2, less 8, as fp16; and the high ones.
-__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
-  const uint32_t x = (w & 0x000F000Fu) | 0x64006400u;  // 1024 + q
+// Codes of bytes 0 and 2 under the exponent of 1024 (magic: 0x64006400, in a register that the compiler cannot see
+// through: it would split the operation for two constants), less 1032: q - 8 of low nibbles, exactly; 16 (q - 8) of high
+// ones, less 1152.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t magic) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(x) : "r"(w), "r"(magic));
   return w_bits(__hadd2(*reinterpret_cast<const __half2 *>(&x), __floats2half2_rn(-1032.f, -1032.f)));
 }
-__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
-  const uint32_t x = (w & 0x00F000F0u) | 0x64006400u;  // 1024 + 16 q
-  return w_bits(__hfma2(*reinterpret_cast<const __half2 *>(&x), __floats2half2_rn(0.0625f, 0.0625f),
-                        __floats2half2_rn(-72.f, -72.f)));
+__device__ __forceinline__ uint32_t high_codes(uint32_t w, uint32_t magic) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(x) : "r"(w), "r"(magic));
+  return w_bits(__hadd2(*reinterpret_cast<const __half2 *>(&x), __floats2half2_rn(-1152.f, -1152.f)));
 }
 
 // Tiles of sequence s that the call has to do with; the first of them.  0 for a length that makes no sense.
@@ -94,23 +98,26 @@ __device__ __forceinline__ int weigh_tiles(const WeighJob &j, int s, int *first,
   return n < 0 ? 0 : (int)n;
 }
 
-// One tile's keys on their way: codes [block][half tile][token g and g + 8], scales of the lane's four tokens, and the
-// total of the token that the lane writes.
-template <int D>
-struct KeyTile {
-  uint32_t w[D / 32][4];
-  uint32_t d[4][D / 64];
-  float before;
-  int64_t total;  // index of the tile's totals, -1: no page
-};
+// (out of line: a copy is nearly always there)
+__device__ __noinline__ bool w_wait(uint64_t *bar, uint32_t parity) { return a_mbar_wait(bar, parity); }
 
 template <int D, int RT, typename T>
 __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_weigh_kernel(const WeighJob j) {
   using C = WeighCfg<D, RT>;
-  constexpr int NB = C::NB, W = kWeighWarps;
-  extern __shared__ __align__(16) unsigned char sm[];
+  constexpr int NB = C::NB, W = kWeighWarps, S = C::kStages;
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ uint64_t bars[W][S];
+  __shared__ int64_t totals_at[W][S];  // index of a stage's tile's totals, -1: it has no page
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  uint4 *q_mem = reinterpret_cast<uint4 *>(sm + (size_t)warp * C::kQuery);  // [RT][NB][32]
+  unsigned char *ring = sm + (size_t)warp * C::kWarp;
+  uint4 *q_mem = reinterpret_cast<uint4 *>(ring + S * C::kTile);  // [RT][NB][32]
+  uint64_t *bar = bars[warp];
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) a_mbar_init(&bar[s], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
   const int heads = j.c.n_kv_heads, n_rows = j.group * j.q_tokens;
 
   // ---- this warp's share of the places
@@ -173,7 +180,10 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
   pair0 += (int64_t)head * (n + kWeighPairCost);
   int64_t left = min(share, total - u0), off = u0 - pair0;
 
+  uint32_t magic;
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
   // ---- pieces: tiles [at, end) of a pair
+  TileRing<S> on_way;
   while (left > 0) {
     const int64_t take = min(left, (int64_t)(n + kWeighPairCost) - off);
     const int at = (int)max((int64_t)0, off - kWeighPairCost), end = (int)max((int64_t)at, off + take - kWeighPairCost);
@@ -224,7 +234,7 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
           for (int b = 0; b < NB; ++b) {
             __half h[8];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) h[z] = __float2half_rn(w_float(reinterpret_cast<const T *>(&raw[b][z / 4])[z % 4]) * up);
+            for (int z = 0; z < 8; ++z) h[z] = __float2half_rn(w_float(reinterpret_cast<const T *>(&raw[b][z / 4])[z % 4]) * up * (z < 4 ? 1.f : 0.0625f));
             q_mem[(rt * NB + b) * 32 + lane] =
                 make_uint4(w_bits(__halves2half2(h[0], h[2])), w_bits(__halves2half2(h[1], h[3])),
                            w_bits(__halves2half2(h[4], h[6])), w_bits(__halves2half2(h[5], h[7])));
@@ -255,11 +265,11 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
           whole_hi = (int)b;
         }
 
-        // ---- loads, a tile ahead; a lane looks up the page of one of the next 32 tiles
+        // ---- copies, S tiles ahead; a lane looks up the page of one of the next 32 tiles
         int64_t my_src = -1, my_total = -1;
         int looked = at;  // tiles before it are looked up
-        auto load = [&](KeyTile<D> &k, int tile) {
-          if (tile >= end) return;
+        auto issue = [&](int tile, uint32_t x) {
+          if (tile >= end || on_way.dead) return;
           if (tile == looked) {
             my_src = my_total = -1;
             if (tile + lane < end) {
@@ -274,26 +284,32 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
             }
             looked += 32;
           }
-          const int from = tile - (looked - 32);
-          const int64_t src = __shfl_sync(0xffffffffu, my_src, from);
-          k.total = __shfl_sync(0xffffffffu, my_total, from);
-          if (src < 0) return;
-          const unsigned char *tp = static_cast<const unsigned char *>(j.c.pages) + src;
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) k.w[b][x] = w_load(tp + (b * 32 + 8 * x + g) * 16 + 4 * t);
+          if (lane == tile - (looked - 32)) {
+            const uint32_t st = TileRing<S>::stage(x);
+            totals_at[warp][st] = my_total;
+            if (my_src < 0) {
+              a_mbar_arrive(&bar[st]);
+            } else {
+              a_expect_tx(&bar[st], C::kTile);
+              a_bulk_load(ring + st * C::kTile, static_cast<const unsigned char *>(j.c.pages) + my_src, C::kTile, &bar[st]);
+            }
+          }
+        };
+        auto compute = [&](const unsigned char *tp, int64_t at_total, int tile) {
+          const float before = j.totals[at_total + 8 * t + g];
+          const int tok0 = (first + tile) * kKvTile;
+          uint32_t kd[4][D / 64];  // key scales of tokens 8 x + g
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const unsigned char *sa = tp + 16 * D + (8 * x + g) * (D / 16);
+            if constexpr (D == 64) {
+              kd[x][0] = *reinterpret_cast<const uint32_t *>(sa);
+            } else {
 #pragma unroll
-            for (int z = 0; z < D / 64; ++z) k.d[x][z] = w_load(sa + 4 * z);
+              for (int z = 0; z < D / 128; ++z)
+                *reinterpret_cast<uint2 *>(&kd[x][2 * z]) = *reinterpret_cast<const uint2 *>(sa + 8 * z);
+            }
           }
-          k.before = j.totals[k.total + 8 * t + g];
-        };
-        auto compute = [&](const KeyTile<D> &k, int tile) {
-          if (tile >= end || k.total < 0) return;
-          const int tok0 = (first + tile) * kKvTile;
           float s[RT][2][4];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
@@ -303,9 +319,11 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
             for (int rt = 0; rt < RT; ++rt) qf[rt] = q_mem[(rt * NB + b) * 32 + lane];
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-              const uint32_t wa = k.w[b][2 * mt], wb = k.w[b][2 * mt + 1], wa8 = wa >> 8, wb8 = wb >> 8;
-              const uint32_t a0 = low_codes(wa), a1 = low_codes(wb), a2 = low_codes(wa8), a3 = low_codes(wb8);
-              const uint32_t h0 = high_codes(wa), h1 = high_codes(wb), h2 = high_codes(wa8), h3 = high_codes(wb8);
+              const unsigned char *kp = tp + (b * 32 + mt * 16 + g) * 16 + 4 * t;
+              const uint32_t wa = *reinterpret_cast<const uint32_t *>(kp), wb = *reinterpret_cast<const uint32_t *>(kp + 128);
+              const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
+              const uint32_t a0 = low_codes(wa, magic), a1 = low_codes(wb, magic), a2 = low_codes(wa8, magic), a3 = low_codes(wb8, magic);
+              const uint32_t h0 = high_codes(wa, magic), h1 = high_codes(wb, magic), h2 = high_codes(wa8, magic), h3 = high_codes(wb8, magic);
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt) {
                 w_mma_first(c[rt][mt], a0, a1, a2, a3, qf[rt].x, qf[rt].y);
@@ -314,8 +332,8 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
             }
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-              const __half2 da = *reinterpret_cast<const __half2 *>(&k.d[2 * mt][b / 2]);
-              const __half2 db = *reinterpret_cast<const __half2 *>(&k.d[2 * mt + 1][b / 2]);
+              const __half2 da = *reinterpret_cast<const __half2 *>(&kd[2 * mt][b / 2]);
+              const __half2 db = *reinterpret_cast<const __half2 *>(&kd[2 * mt + 1][b / 2]);
               const float fa = (b & 1) ? __high2float(da) : __low2float(da), fb = (b & 1) ? __high2float(db) : __low2float(db);
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt) {
@@ -362,17 +380,32 @@ __global__ void __launch_bounds__(32 * kWeighWarps, WeighCfg<D, RT>::kCtas) kv_w
           const float own = (t & 1 ? c1 : c0) + __shfl_xor_sync(0xffffffffu, t & 1 ? c0 : c1, 1);
           const int tok = tok0 + 8 * t + g;
           if (tok >= write_from && tok < len)
-            j.totals[k.total + 8 * t + g] = (r0 == 0 && tok >= new_from ? 0.f : k.before) + own;
+            j.totals[at_total + 8 * t + g] = (r0 == 0 && tok >= new_from ? 0.f : before) + own;
         };
-        KeyTile<D> a, b;
-        a.total = b.total = -1;
-        load(a, at);
+        const uint32_t x0 = on_way.used;
 #pragma unroll 1
-        for (int tile = at; tile < end; tile += 2) {
-          load(b, tile + 1);
-          compute(a, tile);
-          load(a, tile + 2);
-          compute(b, tile + 1);
+        for (int s = 0; s < S; ++s) issue(at + s, x0 + s);
+        __syncwarp();
+#pragma unroll 1
+        for (int tile = at; tile < end; ++tile) {
+          const uint32_t x = on_way.used;
+          on_way.take(
+              [&](uint32_t y) { return __all_sync(0xffffffffu, a_mbar_try(&bar[y % S], TileRing<S>::parity(y))) != 0; },
+              [&](uint32_t y) { return __all_sync(0xffffffffu, w_wait(&bar[y % S], TileRing<S>::parity(y))) != 0; });
+          if (on_way.dead) {
+            // a copy that never came, and what nothing is asked for any more after it: NaN
+            int in_page = 0;
+            const int p = kv_page(row, j.c.table_width, j.c.n_pages, j.c.page_size, first + tile, &in_page);
+            const int tok = (first + tile) * kKvTile + lane;
+            if (p >= 0 && tok >= write_from && tok < len)
+              j.totals[((int64_t)p * heads + head) * j.c.page_size + in_page * kKvTile + lane] = a_nan();
+            if (lane == 0 && j.c.status) atomicOr(j.c.status, MOE_KV_TIMED_OUT);
+            continue;
+          }
+          const int64_t at_total = totals_at[warp][x % S];
+          if (at_total >= 0) compute(ring + (x % S) * C::kTile, at_total, tile);
+          __syncwarp();
+          issue(tile + S, x + S);
         }
       }
     }
