@@ -16,9 +16,10 @@
 //  * Tiles of keys are handed out in their order: earlier ones are seen by more rows, so the
 //    longest come first.  Where there are fewer tiles than room for CTAs, a cluster shares a
 //    tile's rows, and sums are joined in a fixed order: results do not depend on timing.
-//  * The factor log2(e) is in the score's, c, and lse is multiplied by c / scale in two parts:
-//    of large weights, whose difference is small, only the score's own rounding is left.  Sums
-//    are fp32, of a tile's rows first.
+//  * The score less lse is formed before the factor log2(e): of large weights, whose difference
+//    is small, only the score's own rounding is left.  (With that factor in the scale and in lse
+//    2% less time, and twice the error, from lse's rounding.)  Sums are fp32, of a tile's rows
+//    first.
 //  * Only tiles of rows that do not all see all keys are masked.  A row that a key does not
 //    see cannot reach it, whatever it holds.
 // Every wait is bounded; when one gives up all roles stop, the tile's totals become NaN and the
@@ -45,7 +46,7 @@ struct SumJob {
   int64_t table_stride;
   int table_width, n_pages, page_size;
   int n_q, n_k, n_seqs, hq, hkv, group, tile_tokens, window, restart;
-  float c, k_high, k_low;  // the scale times log2(e), rounded, and c / scale, in two parts
+  float scale;
   int32_t *status;
 };
 
@@ -286,9 +287,9 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
       *l = live ? __ldg(j.lse + (int64_t)(w.q0 + tok) * j.hq + r_head) : a_inf();
       *pos = live ? off + tok : -1;
     };
-    // for the warpgroup: less the lse, in log2 units (of a row that is none: less infinity)
+    // for the warpgroup: less the lse (of a row that is none: less infinity)
     auto put_row = [&](int at, float l, int pos) {
-      s_lse[buf][at][r] = fabsf(l) < a_inf() ? -fmaf(l, j.k_low, l * j.k_high) : -l;
+      s_lse[buf][at][r] = -l;
       s_pos[buf][at][r] = pos;
       asm volatile("bar.sync %0, 128;" ::"r"(1 + buf) : "memory");
     };
@@ -298,15 +299,15 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
       row_of(buf, &l, &pos);
       put_row(0, l, pos);
     }
-    const uint64_t c2 = f2_pack(j.c, j.c);
+    const uint64_t scale2 = f2_pack(j.scale, j.scale), log2e2 = f2_pack(kLog2e, kLog2e);
     // 32 columns' weights, added to sum.  (No branch within a tile: it would leave less to overlap.)
     auto weigh = [&](const float *v, const float *ls, const int *ps, uint64_t (&sum)[2], auto is_masked) {
 #pragma unroll
       for (int z = 0; z < 32; z += 4) {
         const float4 l4 = *reinterpret_cast<const float4 *>(ls + z);
         float a, b, c, d;
-        f2_unpack(f2_fma(f2_pack(v[z], v[z + 1]), c2, f2_pack(l4.x, l4.y)), a, b);
-        f2_unpack(f2_fma(f2_pack(v[z + 2], v[z + 3]), c2, f2_pack(l4.z, l4.w)), c, d);
+        f2_unpack(f2_mul(f2_fma(f2_pack(v[z], v[z + 1]), scale2, f2_pack(l4.x, l4.y)), log2e2), a, b);
+        f2_unpack(f2_mul(f2_fma(f2_pack(v[z + 2], v[z + 3]), scale2, f2_pack(l4.z, l4.w)), log2e2), c, d);
         if constexpr (decltype(is_masked)::value) {
           const int4 p4 = *reinterpret_cast<const int4 *>(ps + z);
           a = key <= p4.x && key > p4.x - back ? a : -a_inf();
@@ -472,12 +473,7 @@ MOE_API int moe_prompt_weigh(const moe_tensor *q, int32_t n_q_tokens, int32_t n_
   j.tile_tokens = kTileRows / group;
   j.window = window;
   j.restart = restart != 0;
-  // t = c s - k lse with k = c / scale: the same rounding of c in both, so that of large weights, whose difference is small,
-  // only the score's own rounding is left.  (Of a scale near the least numbers c is too coarse for that.)
-  j.c = scale * kLog2e;
-  const double ratio = j.c > 1e-36f ? (double)j.c / (double)scale : 1.4426950408889634;
-  j.k_high = (float)ratio;
-  j.k_low = (float)(ratio - (double)j.k_high);
+  j.scale = scale;
   j.status = status;
   // without queries none are loaded, but the map wants an address and a size
   if (n_q_tokens == 0 && !j.restart) return MOE_OK;
