@@ -219,6 +219,21 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
   const int all_tiles = w.seq < 0 ? 0 : (w.row1 - w.row0 + j.tile_tokens - 1) / j.tile_tokens;
   const int n_tiles = all_tiles > rank ? (all_tiles - rank + ranks - 1) / ranks : 0;
   auto first_token = [&](int i) { return w.row0 + (rank + i * ranks) * j.tile_tokens; };
+  // A thread's key's total and what it was: looked up ahead, as it is a chain of loads.
+  float *to = nullptr;
+  float before = 0.f;
+  if (rank == 0 && w.seq >= 0 && tid < kTileRows && w.key0 + tid < w.n_k && (all_tiles > 0 || j.restart)) {
+    const int key = w.key0 + tid;
+    int in_page = 0;
+    const int p = kv_page(j.page_table + (int64_t)w.seq * j.table_stride, j.table_width, j.n_pages, j.page_size, key / kKvTile,
+                          &in_page);
+    if (p >= 0) {
+      to = j.totals + ((int64_t)p * j.hkv + w.head) * j.page_size + in_page * kKvTile + key % kKvTile;
+      if (!j.restart && key < w.n_k - w.n_q) before = *to;
+    } else if (j.status) {
+      atomicOr(j.status, MOE_KV_BAD_PAGE);
+    }
+  }
 
   if (warp == C::kLoadWarp) {
     if (lane == 0 && n_tiles > 0) {
@@ -367,25 +382,14 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
   if (warp == C::kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
   if (ranks > 1) cluster.sync();
-  if (rank == 0 && w.seq >= 0 && tid < kTileRows && (all_tiles > 0 || j.restart)) {
-    const int key = w.key0 + tid;
+  if (to) {
     float total = 0.f;
     for (int r = 0; r < ranks; ++r) {
       const float *sum = ranks > 1 ? cluster.map_shared_rank(&s_sum[0][tid], r) : &s_sum[0][tid];
 #pragma unroll
       for (int b = 0; b < NB; ++b) total += sum[b * kTileRows];
     }
-    if (key < w.n_k) {
-      int in_page = 0;
-      const int p = kv_page(j.page_table + (int64_t)w.seq * j.table_stride, j.table_width, j.n_pages, j.page_size, key / kKvTile,
-                            &in_page);
-      if (p < 0) {
-        if (j.status) atomicOr(j.status, MOE_KV_BAD_PAGE);
-      } else {
-        float *at = j.totals + ((int64_t)p * j.hkv + w.head) * j.page_size + in_page * kKvTile + key % kKvTile;
-        *at = j.restart || key >= w.n_k - w.n_q ? total : *at + total;
-      }
-    }
+    *to = before + total;
   }
   if (ranks > 1) cluster.sync();  // (the sums are read until here)
 }
