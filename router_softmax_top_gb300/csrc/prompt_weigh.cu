@@ -55,18 +55,21 @@ constexpr int kSumSms = 152;
 // 128 on 8 take 249, 228, 243 and 286 us, twelve packed prompts with 24 heads of 64 on 8 44, 44, 58 and 84 us.
 constexpr int kSumShare = 2;
 
-template <int D>
+// SHORT: of a call whose rows fit one tile, so that a CTA is a chain of waits: more of them, with one stage and buffer.  16
+// tokens of 32 heads on 60016 keys of 8 heads of 128 take 76 us with two of each and two CTAs per SM, and 57 us so.
+template <int D, bool SHORT>
 struct SumCfg {
-  static constexpr int kStages = 2;
-  static constexpr int kBufs = 2;
-  static constexpr int kCtas = D == 256 ? 1 : 2;
-  // two warpgroups for the weights, a score buffer each
+  static constexpr int kStages = SHORT ? 1 : 2;
+  static constexpr int kBufs = SHORT ? 1 : 2;
+  static constexpr int kCtas = D == 256 ? 1 : SHORT ? (D == 64 ? 4 : 3) : 2;
+  // a warpgroup for the weights of each score buffer
   static constexpr int kSoftWarps = 4 * kBufs, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
   static constexpr int kThreads = 32 * (kSoftWarps + 2);
   static constexpr uint32_t kTile = kTileRows * D * 2;  // bytes of 128 rows or keys
   static constexpr uint32_t kQOff = kTile;
   static constexpr size_t kSmem = (1 + kStages) * (size_t)kTile + 1024;
   static constexpr uint32_t kTmemCols = kBufs * kTileRows;
+  static_assert(kCtas * kTmemCols <= 512, "tensor memory");
 };
 
 // The wait for a load from tensor memory, tied to what it loads.
@@ -89,10 +92,10 @@ struct SumWork {
   int row0, row1;        // query tokens that see any of its keys
 };
 
-template <int D, typename T>
-__global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
+template <int D, typename T, bool SHORT>
+__global__ void __launch_bounds__(SumCfg<D, SHORT>::kThreads, SumCfg<D, SHORT>::kCtas)
     prompt_weigh_kernel(const __grid_constant__ SumMaps maps, const SumJob j) {
-  using C = SumCfg<D>;
+  using C = SumCfg<D, SHORT>;
   constexpr int ST = C::kStages, NB = C::kBufs, DC = D / 64;
   extern __shared__ __align__(1024) unsigned char sm_raw[];
   __shared__ uint64_t k_full, q_full[ST], q_empty[ST], s_full[NB], s_empty[NB], done;
@@ -394,11 +397,11 @@ __global__ void __launch_bounds__(SumCfg<D>::kThreads, SumCfg<D>::kCtas)
   if (ranks > 1) cluster.sync();  // (the sums are read until here)
 }
 
-template <int D, typename T>
-int launch_sum(const SumJob &j, const moe_tensor &q, const moe_tensor &k, int dtype, cudaStream_t st) {
-  using C = SumCfg<D>;
+template <int D, typename T, bool SHORT>
+int run_sum(const SumJob &j, const moe_tensor &q, const moe_tensor &k, int dtype, cudaStream_t st) {
+  using C = SumCfg<D, SHORT>;
   static DynSmemLimit limit;
-  if (ensure_dyn_smem(prompt_weigh_kernel<D, T>, C::kSmem, limit) != cudaSuccess) {
+  if (ensure_dyn_smem(prompt_weigh_kernel<D, T, SHORT>, C::kSmem, limit) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
@@ -425,11 +428,16 @@ int launch_sum(const SumJob &j, const moe_tensor &q, const moe_tensor &k, int dt
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, prompt_weigh_kernel<D, T>, maps, j) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, prompt_weigh_kernel<D, T, SHORT>, maps, j) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
+}
+
+template <int D, typename T>
+int launch_sum(const SumJob &j, const moe_tensor &q, const moe_tensor &k, int dtype, cudaStream_t st) {
+  return j.n_q <= j.tile_tokens ? run_sum<D, T, true>(j, q, k, dtype, st) : run_sum<D, T, false>(j, q, k, dtype, st);
 }
 
 }  // namespace
