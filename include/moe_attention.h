@@ -194,7 +194,8 @@ int moe_prompt_attention_shared(const moe_tensor *q, int32_t n_q_tokens, int32_t
  * that a call queries is new: its total begins at 0 with that call; those of the other
  * tokens that a row sees are added to, and the rest is left as it is.  With restart all
  * tokens of the sequences begin at 0 (a pool whose totals were never set).
- * A page belongs to one sequence, once (as for an append).
+ * A page belongs to one sequence, once (as for an append).  For these calls a row of the
+ * page table holds 2^30 tokens at most.
  *
  * moe_kv_weigh adds the weights exp(scale q . k - lse) of the last q_tokens tokens of
  * every sequence over the cache; the arguments are those of moe_kv_attention, lse being

@@ -36,6 +36,7 @@ constexpr int kMostHeldByTwo = 16384;  // of two CTAs on an SM
 constexpr int kSmallTokens = 4096;  // caches of so many tokens a sequence at most take a CTA of 256 threads
 constexpr int kSlots = 128;       // slots of a group, a thread each
 constexpr int kEvictSms = 152;
+constexpr int64_t kMostTokens = 1 << 30;  // that a row of the page table may hold (counts and steps stay within 32 bits)
 
 struct EvictJob {
   moe_kv_cache c;
@@ -586,7 +587,7 @@ int64_t evict_groups(const moe_kv_cache *c) { return ((int64_t)c->table_width * 
 using namespace moe;
 
 MOE_API int64_t moe_kv_evict_workspace(const moe_kv_cache *c) {
-  if (check_cache(c) != MOE_OK || (int64_t)c->table_width * c->page_size > 0x7fffffff) return 0;
+  if (check_cache(c) != MOE_OK || (int64_t)c->table_width * c->page_size > kMostTokens) return 0;
   return 256 + (int64_t)c->n_seqs * c->n_kv_heads * (4 + 8 * evict_groups(c));
 }
 
@@ -598,7 +599,7 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
   if (!seq_lens || !totals || !new_lens || budget < 0 || first < 0 || recent < 0 || (int64_t)first + recent > budget ||
       (!kept && budget > 0) || (uintptr_t)totals % 16 || (uintptr_t)kept % 4 || (uintptr_t)new_lens % 4)
     return MOE_ERR_INVALID_ARG;
-  if ((int64_t)c->table_width * c->page_size > 0x7fffffff || (int64_t)c->n_seqs * c->n_kv_heads > 0x7fffffff / 8)
+  if ((int64_t)c->table_width * c->page_size > kMostTokens || (int64_t)c->n_seqs * c->n_kv_heads > 0x7fffffff / 8)
     return MOE_ERR_UNSUPPORTED;
   if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < moe_kv_evict_workspace(c)) return MOE_ERR_INVALID_ARG;
   const int64_t pairs = (int64_t)c->n_seqs * c->n_kv_heads, tokens = (int64_t)c->table_width * c->page_size;

@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kWeighWarps = 8;
 constexpr int kWeighSms = 152;
+constexpr int64_t kMostTokens = 1 << 30;  // that a row of the page table may hold
 // What a pair costs beside its tiles, in tiles.
 constexpr int kWeighPairCost = 2;
 
@@ -459,7 +460,7 @@ MOE_API int moe_kv_weigh(const moe_kv_cache *c, const int32_t *seq_lens, const m
     return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
   if (n_q_heads > kMaxAttnHeads || q_tokens > 1024) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)c->table_width * c->page_size > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)c->table_width * c->page_size > kMostTokens) return MOE_ERR_UNSUPPORTED;
   if (const int rc = check_tensor(q, 2)) return rc;
   WeighJob j = {};
   j.c = *c;

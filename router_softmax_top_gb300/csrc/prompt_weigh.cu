@@ -457,7 +457,7 @@ MOE_API int moe_prompt_weigh(const moe_tensor *q, int32_t n_q_tokens, int32_t n_
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
   const int group = n_q_heads / n_kv_heads;
   if (!kv_sizes_ok(n_kv_heads, head_dim, page_size) || n_q_heads > kMaxAttnHeads || group > 64 ||
-      n_q_tokens > (1 << 29) || n_k_tokens > (1 << 29) || (int64_t)table_width * page_size > 0x7fffffff)
+      n_q_tokens > (1 << 29) || n_k_tokens > (1 << 29) || (int64_t)table_width * page_size > (1 << 30))
     return MOE_ERR_UNSUPPORTED;
   if (n_seqs == 0 || n_k_tokens == 0) return MOE_OK;
   if (!cu_q || !cu_k || !totals || (uintptr_t)totals % 4 || (uintptr_t)lse % 4 || (uintptr_t)status % 4 ||

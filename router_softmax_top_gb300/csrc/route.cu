@@ -450,8 +450,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, kRouteCtas<VPL>) route_kerne
   const bool bad_bias = __any_sync(0xffffffffu, !(finite == 0.f));
   const bool live = lane < j.k;
 #pragma unroll 1
-  for (int t = blockIdx.x * kRouteWarps + warp; t < j.n; t += gridDim.x * kRouteWarps) {
-    const T *row = static_cast<const T *>(j.logits) + (int64_t)t * j.stride;
+  for (int64_t t = blockIdx.x * kRouteWarps + warp; t < j.n; t += gridDim.x * kRouteWarps) {
+    const T *row = static_cast<const T *>(j.logits) + t * j.stride;
     float x[VPL];
     if (e0 + VPL <= j.E) {
       load_values<VPL>(row + e0, x);
@@ -463,8 +463,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, kRouteCtas<VPL>) route_kerne
 #pragma unroll
     for (int i = 1; i < VPL; ++i) top = max_nan(top, x[i]);
     top = warp_max(top);
-    int32_t *ids = j.ids + (int64_t)t * j.k + lane;
-    float *weights = j.weights + (int64_t)t * j.k + lane;
+    int32_t *ids = j.ids + t * j.k + lane;
+    float *weights = j.weights + t * j.k + lane;
     if (!(top < a_inf()) || bad_bias) {
       if (lane == 0 && j.status) atomicOr(j.status, MOE_ROUTE_BAD_LOGIT);
       if (live) {
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, kRouteCtas<VPL>) route_kerne
 template <typename T, int VPL>
 void run_route(const RouteJob &j, cudaStream_t st) {
   // (CTAs that run at once: of more tokens a warp takes several, and loads the bias once)
-  const int grid = std::min((j.n + kRouteWarps - 1) / kRouteWarps, kRouteSms * kRouteCtas<VPL>);
+  const int grid = std::min((j.n - 1) / kRouteWarps + 1, kRouteSms * kRouteCtas<VPL>);
   route_kernel<T, VPL><<<grid, 32 * kRouteWarps, 0, st>>>(j);
 }
 template <typename T>

@@ -86,6 +86,15 @@ def test_large_and_small_logits(score):
     check(x.cuda(), 8, score, torch.full((64,), 3e38).cuda(), 8, 2, "top2")
 
 
+def test_logits_below_the_normal_numbers():
+    g = torch.Generator().manual_seed(4)
+    for E, k in ((100, 6), (1024, 32), (40, 32)):
+        x = (torch.rand(5, E, generator=g) * 2 - 1) * 1e-40
+        for y in (x, x.abs(), -x.abs()):
+            check(y.cuda(), k)
+            check(y.cuda(), min(k, 8), "sigmoid", None, 4, 2, "max")
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups,kept", [(1, 1), (8, 2)])
 def test_closed_experts(score, groups, kept):
