@@ -104,6 +104,22 @@ def test_large_and_small_queries():
         check(case([90], 2, 1, 64, "bf16", scale=scale, q_size=size, seed=4))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq", [2, 3])
+def test_lse_of_any_size_over_whole_tiles(dtype, hq):
+    # rows that all see all keys of a tile, with scores and scales from small to near the types' limits
+    for size, scale in ((1.0, None), (0.01, 3.0), (300.0, 1e-4), (3000.0, 1e-10), (1e-3, 1e4)):
+        check(case([450], hq, 1, 64, dtype, prefix=40, scale=scale, q_size=size, seed=14))
+    if dtype == "bf16":
+        for size, scale in ((2.0 ** 100, 2.0 ** -104), (2.0 ** -100, 2.0 ** 97), (2.0 ** 110, 2.0 ** -126)):
+            check(case([450], hq, 1, 64, dtype, scale=scale, q_size=size, seed=15))
+    c = case([450], hq, 1, 64, dtype, seed=16)
+    c["lse"][400:405] += 40.0          # rows that count for little, for nothing and for much
+    c["lse"][410] = float("inf")
+    c["lse"][420] -= 30.0
+    check(c)
+
+
 def test_attentions_own_lse_gives_weights_that_sum_to_one():
     c = case([700, 33, 1], 16, 4, 128, "bf16", seed=5)
     _, lse = moe.prompt_attention(c["q"], c["k"], c["k"], i32(c["cu"]), return_lse=True)

@@ -24,7 +24,9 @@ def received(q, k, lse, at, n_keys, scale, window):
         z = torch.einsum("hd,nhd->nh", q[i].abs(), kk.abs()) * scale
         w = a.exp()
         out[lo:hi] += w.unflatten(1, (hkv, g)).sum(2)
-        tol[lo:hi] += (w * (2.0 ** -19 * z + 2.0 ** -21 * (1 + a.abs()))).unflatten(1, (hkv, g)).sum(2)
+        # (what is below the normal numbers is 0: at most 2^-126 each)
+        off = torch.where(w > 0, w * (2.0 ** -19 * z + 2.0 ** -21 * (1 + a.abs())), 0.0) + 2.0 ** -126
+        tol[lo:hi] += off.unflatten(1, (hkv, g)).sum(2)
     return out, tol + 2.0 ** -21 * out
 
 
