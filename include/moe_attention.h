@@ -223,8 +223,8 @@ int moe_prompt_weigh(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads,
 
 /*
  * Keeps budget tokens of every sequence that has more, per key/value head: its first
- * `first` and its last `recent` tokens (first + recent <= budget), and of those between
- * the ones with the largest totals (ties: the earlier token; NaN counts as largest).
+ * `first` and its last `recent` tokens (first + recent <= budget <= 2^30), and of those
+ * between the ones with the largest totals (ties: the earlier token; NaN counts as largest).
  * They move together, in place and in their order: keys, values and totals of the token
  * of rank r go to slot r.  What the slots from budget on hold is left as it is, but for
  * their totals, which become 0.  Positions are not kept: a key stays as it was rotated.

@@ -599,9 +599,11 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
   if (!seq_lens || !totals || !new_lens || budget < 0 || first < 0 || recent < 0 || (int64_t)first + recent > budget ||
       (!kept && budget > 0) || (uintptr_t)totals % 16 || (uintptr_t)kept % 4 || (uintptr_t)new_lens % 4)
     return MOE_ERR_INVALID_ARG;
-  if ((int64_t)c->table_width * c->page_size > kMostTokens || (int64_t)c->n_seqs * c->n_kv_heads > 0x7fffffff / 8)
+  if (budget > kMostTokens || (int64_t)c->table_width * c->page_size > kMostTokens ||
+      (int64_t)c->n_seqs * c->n_kv_heads > 0x7fffffff / 8)
     return MOE_ERR_UNSUPPORTED;
-  if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < moe_kv_evict_workspace(c)) return MOE_ERR_INVALID_ARG;
+  if (new_lens == seq_lens || !workspace || (uintptr_t)workspace % 256 || workspace_bytes < moe_kv_evict_workspace(c))
+    return MOE_ERR_INVALID_ARG;
   const int64_t pairs = (int64_t)c->n_seqs * c->n_kv_heads, tokens = (int64_t)c->table_width * c->page_size;
   EvictJob j = {};
   j.c = *c;

@@ -133,8 +133,8 @@ def kv_evict(pages, page_table, seq_lens, budget, *, totals, page_size, n_kv_hea
     c, n_seqs = _cache(pages, page_table, page_size, n_kv_heads, head_dim, status, dev)
     pl = _index(seq_lens, "seq_lens", n_seqs, dev)
     pt = _totals(totals, pages.shape[0], n_kv_heads, page_size, dev)
-    if not 0 <= budget < 2 ** 31 or first < 0 or recent < 0 or first + recent > budget:
-        _refuse("budget must be at least first + recent, none of them negative")
+    if not 0 <= budget <= 2 ** 30 or first < 0 or recent < 0 or first + recent > budget:
+        _refuse("budget must be at least first + recent and at most 2^30, none of them negative")
 
     def run(handle):
         d = _cuda(dev)

@@ -84,6 +84,15 @@ def test_kv_evict(lib, kw, code):
     assert evict(lib, **kw) == code
 
 
+def test_kv_evict_of_budgets_that_counts_do_not_hold(lib):
+    assert evict(lib, budget=(1 << 30) + 1) == evict(lib, budget=2147483647) == UNSUPPORTED
+    assert evict(lib, budget=1 << 30, size=100) == INVALID
+
+
+def test_kv_evict_of_lengths_written_over_themselves(lib):
+    assert evict(lib, lens=AT + 64, new=AT + 64) == INVALID
+
+
 def test_tables_wider_than_is_supported(lib):
     c = _cache(table_width=1 << 25, table_stride=1 << 25)
     assert weigh(lib, c) == evict(lib, c) == UNSUPPORTED
