@@ -63,13 +63,18 @@ __device__ __forceinline__ bool length_ok(const EvictJob &j, int n) {
   return n >= 0 && n <= (int64_t)j.c.table_width * j.c.page_size;
 }
 
+struct __align__(8) BinPair {
+  int low, high;
+};
+
 // CL: a cluster per pair, else one CTA.  NT: its threads.
 template <int NT, bool CL>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
   constexpr int NW = NT / 32, PER = kBins / NT;
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ uint32_t hist[3][kBins], s_keys[kFew];
-  __shared__ int s_bad, s_share[3], s_found[3][3], s_warp[2][32], s_count[2], s_scan[32], s_few;
+  __shared__ __align__(16) uint32_t hist[3][kBins];
+  __shared__ uint32_t s_keys[kFew];
+  __shared__ int s_bad, s_found[3][3], s_warp[2][32], s_count[2], s_scan[32], s_few;
   __shared__ uint32_t s_least;
   __shared__ int s_need;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -153,8 +158,8 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
   }
   for (int g = rank * NT + tid; g < (n + kSlots - 1) / kSlots; g += ranks * NT) j.loaded[(int64_t)pair * j.groups + g] = 0;
   sync();
-  bool bad = false;
-  for (int r = 0; r < ranks; ++r) bad |= *of_rank(&s_bad, r) != 0;
+  // (a lane looks at a CTA of the cluster, here and below: one after another they would be a chain of waits)
+  const bool bad = __any_sync(0xffffffffu, lane < ranks && *of_rank(&s_bad, lane) != 0);
   if (bad) {
     for (int i = rank * NT + tid; i < j.budget; i += ranks * NT) kept[i] = -1;
     if (rank == 0 && tid == 0) {
@@ -170,18 +175,30 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
     int shift = 21;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      // Counts over the cluster, largest key first: a CTA adds up its share of the bins, `pt` of them a thread.
-      const int share = kBins / ranks, pt = max(1, share / NT), hi = kBins - 1 - rank * share - pt * tid;
+      // Counts over the cluster, largest key first, PER bins a thread.  Every CTA adds up all bins: a share of them each
+      // would cost two more barriers over the cluster.
+      const int hi = kBins - 1 - PER * tid;
       int n_bin[PER], inc = 0;
 #pragma unroll
       for (int z = 0; z < PER; ++z) n_bin[z] = 0;
-      if (pt * tid < share)
-        for (int r = 0; r < ranks; ++r) {
-          const uint32_t *h = of_rank(&hist[pass][0], r);
+      constexpr int AT_ONCE = CL ? 8 : 1;  // loads on their way together
+      for (int r0 = 0; r0 < ranks; r0 += AT_ONCE) {
+        BinPair v[AT_ONCE][PER / 2];
 #pragma unroll
-          for (int z = 0; z < PER; ++z)
-            if (z < pt) n_bin[z] += (int)h[hi - z];
-        }
+        for (int r = 0; r < AT_ONCE; ++r)
+#pragma unroll
+          for (int z = 0; z < PER / 2; ++z) {
+            v[r][z] = {0, 0};
+            if (r0 + r < ranks) v[r][z] = *reinterpret_cast<const BinPair *>(of_rank(&hist[pass][0], r0 + r) + hi - 2 * z - 1);
+          }
+#pragma unroll
+        for (int r = 0; r < AT_ONCE; ++r)
+#pragma unroll
+          for (int z = 0; z < PER / 2; ++z) {
+            n_bin[2 * z] += v[r][z].high;
+            n_bin[2 * z + 1] += v[r][z].low;
+          }
+      }
 #pragma unroll
       for (int z = 0; z < PER; ++z) inc += n_bin[z];
       const int mine = inc;
@@ -192,25 +209,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
       }
       if (lane == 31) s_scan[warp] = inc;
       __syncthreads();
-      int before = inc - mine, all = 0;
-      for (int w = 0; w < NW; ++w) {
-        const int v = s_scan[w];
-        before += w < warp ? v : 0;
-        all += v;
-      }
-      int owner = 0;  // the CTA whose share the count is reached in
-      if constexpr (CL) {
-        if (tid == 0) s_share[pass] = all;
-        sync();
-        int sum = 0;
-        owner = -1;
-        for (int r = 0; r < ranks; ++r) {
-          const int v = *of_rank(&s_share[pass], r);
-          before += r < rank ? v : 0;
-          sum += v;
-          if (owner < 0 && sum >= need) owner = r;
-        }
-      }
+      int before = inc - mine + (int)__reduce_add_sync(0xffffffffu, (uint32_t)(lane < warp ? s_scan[lane] : 0));
 #pragma unroll
       for (int z = 0; z < PER; ++z) {
         if (before < need && before + n_bin[z] >= need) {
@@ -220,8 +219,8 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
         }
         before += n_bin[z];
       }
-      sync();
-      const int *found = of_rank(&s_found[pass][0], owner);
+      __syncthreads();
+      const int *found = s_found[pass];
       least = pass == 0 ? (uint32_t)found[0] : (least << (pass == 1 ? 11 : 10)) | (uint32_t)found[0];
       need -= found[1];
       const int in = found[2];
@@ -315,10 +314,9 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictJob j) {
   sync();
   sure = s_warp[0][warp];
   eq = s_warp[1][warp];
-  for (int r = 0; r < rank; ++r) {
-    const int *c = of_rank(&s_count[0], r);
-    sure += c[0];
-    eq += c[1];
+  if constexpr (CL) {
+    sure += __reduce_add_sync(0xffffffffu, lane < rank ? of_rank(&s_count[0], lane)[0] : 0);
+    eq += __reduce_add_sync(0xffffffffu, lane < rank ? of_rank(&s_count[0], lane)[1] : 0);
   }
   int32_t *group_before = j.before + (int64_t)pair * j.groups;
   for (int s = w0; s < w1; ++s) {
@@ -622,10 +620,11 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
   j.loaded = reinterpret_cast<uint32_t *>(j.before + pairs * j.groups);
   // A cluster per pair where pairs alone leave SMs idle and have many keys (32 sequences of 12000 tokens on 4 heads: 21 us
   // as clusters of two, 15 us so; one of 131071 on 8 heads 8 CTAs each).  A CTA of 1024 threads is alone on its SM, of 512
-  // two are.  Sixteen CTAs are more than every GPU has room for.
+  // two are.  Sixteen CTAs, if the GPU has room for such clusters, of more keys than fill half of what eight hold (one head
+  // by eight and by sixteen, both kernels: 131071 tokens 40 and 43 us, 180000 45 and 46, 290000 55 and 53, 600000 115 and 72).
   int ranks = 1;
   while (ranks < 8 && pairs * ranks * 2 <= kEvictSms && tokens > 2 * kSmallTokens * (int64_t)ranks) ranks *= 2;
-  if (ranks == 8 && pairs * 16 <= kEvictSms && tokens > kSmallTokens * 8 && wide_clusters() >= pairs) ranks = 16;
+  if (ranks == 8 && pairs * 16 <= kEvictSms && tokens > (int64_t)kMostHeld * 4 && wide_clusters() >= pairs) ranks = 16;
   j.held = (int)std::min<int64_t>(kMostHeld, ((tokens + ranks - 1) / ranks + kSlots - 1) / kSlots * kSlots);
   cudaStream_t st = (cudaStream_t)cuda_stream;
   cudaError_t e = ranks > 1                                            ? launch_select<1024, true>(j, pairs, ranks, st)

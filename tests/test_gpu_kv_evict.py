@@ -140,6 +140,22 @@ def test_more_keys_than_shared_memory_holds():
     assert torch.equal(t[k], v[want]) and not bool(t[150000:].any())
 
 
+def test_more_keys_than_sixteen_ctas_hold():
+    n, budget = 16 * 49152 + 4321, 300000
+    pages, table, totals = pool([n], 1024, 1, 64, 8)
+    p, t = pages.cuda(), totals.cuda()
+    new, kept = moe.kv_evict(p, table.cuda(), i32([n]), budget, totals=t, page_size=1024, n_kv_heads=1, head_dim=64, first=5, recent=1000)
+    tok = torch.arange(n)
+    v = totals[table[0][tok // 1024].long(), 0, tok % 1024]
+    mid = v[5:n - 1000].sort(descending=True, stable=True).indices[:budget - 1005] + 5
+    want = torch.cat([torch.arange(5), mid.sort().values, torch.arange(n - 1000, n)])
+    assert torch.equal(kept[0, 0].cpu().long(), want) and new.tolist() == [budget]
+    k = torch.arange(budget)
+    assert torch.equal(rows(p.cpu(), table[0], budget, 1024, 1, 64), rows(pages, table[0], n, 1024, 1, 64)[want])
+    t = t.cpu()[table[0][tok // 1024].long(), 0, tok % 1024]
+    assert torch.equal(t[k], v[want]) and not bool(t[budget:].any())
+
+
 def test_more_sequences_than_lanes():
     lens = [(37 * i) % 400 for i in range(130)]
     check(lens, 32, 2, 64, 120, 2, 10, seed=8)
