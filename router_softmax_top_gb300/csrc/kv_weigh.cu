@@ -5,7 +5,8 @@
 // result: no maximum, no sum over keys, so tiles of keys have nothing to do with each other.
 //
 // Bound: the key half of the cache (18 D bytes per tile of 32 tokens and head), and the
-// totals, read and written.  The 32-token tiles of all (sequence, key head) pairs in a row,
+// totals, read and written; in fact the instructions that unpack it (about 470 per tile of
+// 128 wide heads, an SM issuing 70% of the time).  The 32-token tiles of all (sequence, key head) pairs in a row,
 // plus a few tiles' worth per pair for its set-up, are split evenly over all warps; a warp
 // copies its own tiles (the key half of a tile is contiguous: one bulk copy) into a ring of its
 // own, two to four ahead, and no barrier stands in the loop.
@@ -18,6 +19,9 @@
 //    difference is small, only the score's own rounding is left.
 //  * Sums over rows stay in registers, then among the four lanes that share a token; the
 //    lane that writes a token's total is the one that reads it, whatever the pass.
+// Measured, 32 heads of 128 on 8: 128 sequences of 64 to 8192 tokens 78 us (4.4 TB/s of what
+// it has to read and write; loads into registers instead of the rings 91), one of 131071
+// 25 us (31), one of 333 5.6 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -29,7 +33,7 @@ namespace {
 constexpr int kWeighWarps = 8;
 constexpr int kWeighSms = 152;
 constexpr int64_t kMostTokens = 1 << 30;  // that a row of the page table may hold
-// What a pair costs beside its tiles, in tiles.
+// What a pair costs beside its tiles, in tiles (its queries, lse and page numbers are about as many instructions).
 constexpr int kWeighPairCost = 2;
 
 struct WeighJob {
@@ -45,7 +49,8 @@ struct WeighJob {
 template <int D, int RT>
 struct WeighCfg {
   static constexpr int NB = D / 32;
-  static constexpr int kStages = D == 64 ? 4 : 2;                        // of a warp's ring
+  // Of a warp's ring: what is on its way per SM is then 48 to 110 KB, 44 KB at the full rate and a microsecond's latency.
+  static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kTile = 18 * D;                                   // bytes of a tile's keys and their scales
   static constexpr int kQuery = RT * NB * 32 * 16;                       // bytes of a warp's query operand
   static constexpr int kWarp = kStages * kTile + kQuery;

