@@ -11,19 +11,19 @@
 // are written in order, from counts per warp.
 //
 // Moving, in place: the token of rank r goes to slot r, which is never after its own.  A CTA
-// takes the 128 slots of a group: it loads what is to go there into shared memory, says so,
-// waits for the groups that load from its own slots to have said so (at most two, and none
-// later than itself), and writes.  Groups are handed out in order, so whatever one waits for
-// has been begun by a CTA that is running, and loading waits for nothing.
+// takes the 128 tokens of a group: it loads those that stay into shared memory, says so, waits
+// for the groups whose tokens are in the slots that these go to to have said so (at most two,
+// and none later than itself), and writes.  Groups are handed out in order, so whatever one
+// waits for has been begun by a CTA that is running, and loading waits for nothing.
 //
 // Bound: memory (the kept tokens' bytes read and written; DRAM gives 64 bytes at least, which
 // four neighbouring tokens' pieces of 16 bytes share, so that where half the tokens stay
 // nearly all of the cache is read), the totals, and for one sequence the search's passes over a
 // few CTAs and the barriers between them.
-// Measured: one sequence of 131071 tokens on 8 heads of 128, half of them kept, 72 us: search
-// 23, moving 46 (at the copy rate all bytes that DRAM has to move would take 35).  32 sequences
-// of 3000 to 12000 tokens on 4 heads of 256, 4096 kept, 105 us (search 14, moving 88; 64).  One
-// of 1100 tokens, 1024 kept, 13 us.
+// Measured: one sequence of 131071 tokens on 8 heads of 128, half of them kept, 67 us: search
+// 23 (at the copy rate all bytes that DRAM has to move would take 35).  32 sequences of 3000 to
+// 12000 tokens on 4 heads of 256, 4096 kept, 95 us (search 14; DRAM 57).  One of 1100 tokens,
+// 1024 kept, 13 us.
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -39,7 +39,11 @@ constexpr int kFew = 128;         // keys that are compared each with each
 constexpr int kMostHeld = 49152;  // keys that a CTA's shared memory holds (more are read again for every pass)
 constexpr int kMostHeldByTwo = 16384;  // of two CTAs on an SM
 constexpr int kSmallTokens = 4096;  // caches of so many tokens a sequence at most take a CTA of 256 threads
-constexpr int kSlots = 128;       // slots of a group, a thread each
+constexpr int kSlots = 128;       // tokens of a group, a thread each
+// Kept tokens of a group from which on its tiles are loaded whole, by a bulk copy each, rather than the tokens' pieces: 32
+// sequences of 12000 tokens on 4 heads of 256 take 127 us whole and 122 in pieces with 26 of 128 kept, 133 and 137 with 38,
+// 173 and 186 with 96; heads of 64 alike.
+constexpr int kWhole = 36;
 constexpr int kEvictSms = 152;
 constexpr int64_t kMostTokens = 1 << 30;  // that a row of the page table may hold (counts and steps stay within 32 bits)
 
@@ -362,12 +366,15 @@ __device__ __forceinline__ void e_copy(void *dst, const void *src) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(a_smem(dst)), "l"(src), "n"(N) : "memory");
 }
+__device__ __forceinline__ bool is_loaded(const uint32_t *flag) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+  return v != 0;
+}
 __device__ __forceinline__ bool wait_loaded(const uint32_t *flag) {
   uint64_t t0 = 0;
   for (uint32_t i = 0; i < kAttnSpin; ++i) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
-    if (v) return true;
+    if (is_loaded(flag)) return true;
     if ((i & 255u) == 255u) {
       const uint64_t now = a_now_ns();
       if (t0 == 0) t0 = now;
@@ -380,23 +387,28 @@ __device__ __forceinline__ bool wait_loaded(const uint32_t *flag) {
 template <int D>
 struct MoveCfg {
   static constexpr int kPieces = 2 * (D / 32);  // 16-byte pieces of codes of a token
-  // per thread: its token's codes, the scales of keys and of values (D / 16 bytes each), its total
-  static constexpr int kScale = D / 16;
-  static constexpr size_t kSmem = (size_t)kSlots * (16 * kPieces + 2 * kScale + 4);
-  static constexpr int kCtas = D == 256 ? 6 : 10;
+  static constexpr int kScale = D / 16;         // bytes of a token's scales of keys, and of values
+  static constexpr int kTile = 36 * D;
+  // a group's tiles, or its kept tokens: of each a row of pieces over the threads, then of scales
+  static constexpr size_t kSmem = (size_t)kSlots / kKvTile * kTile;
+  static_assert(kSmem == (size_t)kSlots * (16 * kPieces + 2 * kScale), "the two ways of holding a group");
+  static constexpr int kCtas = D == 256 ? 6 : D == 128 ? 11 : 16;  // per SM, by shared memory and threads
 };
 
 template <int D>
-__global__ void __launch_bounds__(kSlots) evict_move_kernel(const EvictJob j) {
+__global__ void __launch_bounds__(kSlots, MoveCfg<D>::kCtas) evict_move_kernel(const EvictJob j) {
   using C = MoveCfg<D>;
-  extern __shared__ __align__(16) unsigned char sm[];
-  __shared__ int s_seq, s_head, s_group, s_ok;
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ uint64_t bar;
+  __shared__ int s_seq, s_head, s_group, s_ok, s_wait;
+  __shared__ float s_total[kSlots];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (j.c.n_seqs + 31) / 32;
-  // this thread's token on its way: each piece in a row over the threads
-  auto codes = [&](int piece) { return sm + ((size_t)piece * kSlots + tid) * 16; };
-  auto scales = [&](int v) { return sm + (size_t)kSlots * 16 * C::kPieces + ((size_t)v * kSlots + tid) * C::kScale; };
-  float *const my_total = reinterpret_cast<float *>(sm + (size_t)kSlots * (16 * C::kPieces + 2 * C::kScale)) + tid;
+  uint32_t phase = 0;
+  if (tid == 0) {
+    a_mbar_init(&bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (;;) {
     if (warp == 0) {
@@ -442,12 +454,18 @@ __global__ void __launch_bounds__(kSlots) evict_move_kernel(const EvictJob j) {
     const int seq = s_seq, head = s_head, g = s_group;
     if (seq < 0) return;
     const int pair = seq * j.heads + head;
-    const int n = __ldg(j.lens + seq), slot = g * kSlots + tid;
+    const int n = __ldg(j.lens + seq), t0 = g * kSlots, n_own = min(kSlots, n - t0);  // the group's tokens
     const int32_t *row = j.c.page_table + (int64_t)seq * j.c.table_stride;
     const bool skip = j.skip[pair] != 0;
-    const int src = !skip && slot < j.budget ? j.kept[(int64_t)pair * j.budget + slot] : -1;
-    const bool moves = src > slot, clears = !skip && slot >= j.budget && slot < n;
+    // the ranks of those that stay: [r0, r1).  (Where the sequence is left as it is, neither is of use.)
+    const int r0 = j.before[(int64_t)pair * j.groups + g], r1 = j.before[(int64_t)pair * j.groups + g + 1], count = r1 - r0;
     uint32_t *loaded = j.loaded + (int64_t)pair * j.groups;
+    if (skip) {
+      __syncthreads();  // (what to work on is read until here)
+      continue;
+    }
+    // (with all tokens before kept, and all of its own, they are in their places)
+    const bool moves = count > 0 && !(r0 == t0 && count == n_own), whole = count >= kWhole;
     unsigned char *const pages = static_cast<unsigned char *>(j.c.pages);
     // where a token's tile is, and the token in it; the page was seen to be there
     auto place = [&](int i, int64_t *tile, int64_t *total) {
@@ -457,56 +475,90 @@ __global__ void __launch_bounds__(kSlots) evict_move_kernel(const EvictJob j) {
       *total = (p * j.heads + head) * j.c.page_size + in;
       return in % kKvTile;
     };
-    if (moves) {
-      int64_t tile, total;
-      const int tok = place(src, &tile, &total);
-      const unsigned char *tp = pages + tile;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-#pragma unroll
-        for (int b = 0; b < D / 32; ++b) e_copy<16>(codes(v * (D / 32) + b), tp + kv_code_off(D, v, b, tok));
-        e_copy<C::kScale>(scales(v), tp + kv_scale_off(D, v, 0, tok));
-      }
-      e_copy<4>(my_total, j.totals + total);
-    }
-    // who loads from these slots: the groups of the ranks that their tokens have (kSlots at most)
-    int r0 = 0, r1 = 0;
-    if (warp == 0 && !skip) {
-      r0 = j.before[(int64_t)pair * j.groups + g];
-      r1 = j.before[(int64_t)pair * j.groups + g + 1];
-    }
-    int64_t tile = 0, total = 0;
-    int tok = 0;
-    if (moves || clears) tok = place(slot, &tile, &total);
-    asm volatile("cp.async.wait_all;" ::: "memory");  // (what has arrived has been read)
-    const bool work = __syncthreads_or(moves || clears);
-    // (a release: what the CTA's threads have read before the barrier, they have read before this)
-    if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(loaded + g), "r"(1u) : "memory");
-    if (!work) continue;
-    if (warp == 0) {
-      const int h = r0 / kSlots + lane;
-      if (r1 > r0 && h <= (r1 - 1) / kSlots && h < g && !wait_loaded(loaded + h)) s_ok = 0;
-    }
-    __syncthreads();
-    if (!s_ok) {
-      if (tid == 0 && j.c.status) atomicOr(j.c.status, MOE_KV_TIMED_OUT);
-      __syncthreads();
-      continue;
+    auto codes = [&](int piece) { return sm + ((size_t)piece * kSlots + tid) * 16; };
+    auto scales = [&](int v) { return sm + (size_t)kSlots * 16 * C::kPieces + ((size_t)v * kSlots + tid) * C::kScale; };
+    int64_t own_total = 0, tile = 0, total = 0;
+    int tok = 0, src = -1;
+    bool came = true;
+    const int to = r0 + tid;  // this thread's rank
+    if (tid < n_own) {
+      int64_t own_tile;
+      const int own_tok = place(t0 + tid, &own_tile, &own_total);
+      if (moves && whole && own_tok == 0) a_bulk_load(sm + tid / kKvTile * C::kTile, pages + own_tile, C::kTile, &bar);
+      s_total[tid] = j.totals[own_total];  // (in shared memory, so that it has arrived)
     }
     if (moves) {
-      unsigned char *tp = pages + tile;
+      if (whole && tid == 0) a_expect_tx(&bar, (uint32_t)((n_own + kKvTile - 1) / kKvTile * C::kTile));
+      if (tid < count) {
+        src = j.kept[(int64_t)pair * j.budget + to];
+        tok = place(to, &tile, &total);
+      }
+      // whose tokens are in the slots that are written: of two groups at most, which often have said so by now
+      if (warp == 1) {
+        const int h = r0 / kSlots + lane;
+        const bool wait = h <= (r1 - 1) / kSlots && h < g && !is_loaded(loaded + h);
+        if (const bool any = __any_sync(0xffffffffu, wait); lane == 0) s_wait = any;
+      }
+      if (whole) {
+        came = a_mbar_wait(&bar, phase);
+        phase ^= 1;
+      } else {
+        if (src > to) {
+          int64_t src_tile, unused;
+          const int src_tok = place(src, &src_tile, &unused);
+          const unsigned char *tp = pages + src_tile;
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
+          for (int v = 0; v < 2; ++v) {
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b)
-          *reinterpret_cast<uint4 *>(tp + kv_code_off(D, v, b, tok)) = *reinterpret_cast<const uint4 *>(codes(v * (D / 32) + b));
-        unsigned char *sp = tp + kv_scale_off(D, v, 0, tok);
-        if constexpr (C::kScale == 4) *reinterpret_cast<uint32_t *>(sp) = *reinterpret_cast<const uint32_t *>(scales(v));
-        else if constexpr (C::kScale == 8) *reinterpret_cast<uint2 *>(sp) = *reinterpret_cast<const uint2 *>(scales(v));
-        else *reinterpret_cast<uint4 *>(sp) = *reinterpret_cast<const uint4 *>(scales(v));
+            for (int b = 0; b < D / 32; ++b) e_copy<16>(codes(v * (D / 32) + b), tp + kv_code_off(D, v, b, src_tok));
+            e_copy<C::kScale>(scales(v), tp + kv_scale_off(D, v, 0, src_tok));
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
       }
     }
-    if (moves || clears) j.totals[total] = moves ? *my_total : 0.f;
+    if (!__syncthreads_and(came)) {
+      // a copy that never came: nothing is said to be loaded, nor written, any more
+      if (tid == 0) {
+        if (j.c.status) atomicOr(j.c.status, MOE_KV_TIMED_OUT);
+        (void)a_mbar_drain(&bar, phase ^ 1);
+      }
+      return;
+    }
+    // (A release: what the CTA's threads have read before the barrier, they have read before this.  It waits for the SM's
+    // writes on their way, so it is left out where nobody comes to write.)
+    if (tid == 0 && t0 < j.budget) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(loaded + g), "r"(1u) : "memory");
+    if (tid < n_own && t0 + tid >= j.budget) j.totals[own_total] = 0.f;
+    if (moves) {
+      if (s_wait) {
+        if (warp == 0) {
+          const int h = r0 / kSlots + lane;
+          if (h <= (r1 - 1) / kSlots && h < g && !wait_loaded(loaded + h)) s_ok = 0;
+        }
+        __syncthreads();
+      }
+      if (!s_ok) {
+        if (tid == 0 && j.c.status) atomicOr(j.c.status, MOE_KV_TIMED_OUT);
+      } else if (src > to) {
+        unsigned char *tp = pages + tile;
+        const int in = src - t0;
+        const unsigned char *from = sm + in / kKvTile * C::kTile;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+#pragma unroll
+          for (int b = 0; b < D / 32; ++b)
+            *reinterpret_cast<uint4 *>(tp + kv_code_off(D, v, b, tok)) = *reinterpret_cast<const uint4 *>(
+                whole ? from + kv_code_off(D, v, b, in % kKvTile) : codes(v * (D / 32) + b));
+          unsigned char *sp = tp + kv_scale_off(D, v, 0, tok);
+          const unsigned char *fp = whole ? from + kv_scale_off(D, v, 0, in % kKvTile) : scales(v);
+          if constexpr (C::kScale == 4) *reinterpret_cast<uint32_t *>(sp) = *reinterpret_cast<const uint32_t *>(fp);
+          else if constexpr (C::kScale == 8) *reinterpret_cast<uint2 *>(sp) = *reinterpret_cast<const uint2 *>(fp);
+          else *reinterpret_cast<uint4 *>(sp) = *reinterpret_cast<const uint4 *>(fp);
+        }
+        j.totals[total] = s_total[in];
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (before the next tiles come where these were read)
+    }
     __syncthreads();
   }
 }

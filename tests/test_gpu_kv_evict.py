@@ -123,6 +123,25 @@ def test_long_sequences_and_many_groups():
     assert torch.equal(kept[0, 0].cpu(), torch.arange(1, 30000, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("last", [0, 70])
+def test_groups_with_any_share_kept(d, last):
+    # of the i-th 128 tokens 4 i stay, then as many again of another order, then none
+    pages, table, totals = pool([10 * 1024 + last], 64, 2, d, 9)
+    stay = torch.zeros(2, 10 * 1024 + last)
+    g = torch.Generator().manual_seed(3)
+    for i in range(64):
+        k = 4 * i if i < 32 else 128 - 4 * (i - 32)
+        for h in range(2):
+            stay[h, 128 * i + torch.randperm(128, generator=g)[:k]] = 1.0 + i
+    tok = torch.arange(10 * 1024 + last)
+    totals[table[0][tok // 64].long(), :, tok % 64] = stay.T.contiguous()
+    budget = int((stay[0] > 0).sum())
+    assert budget == int((stay[1] > 0).sum())
+    for b in (budget, budget - 37, 36, 35, 1):
+        check([10 * 1024 + last], 64, 2, d, b, state=(pages, table, totals))
+
+
 def test_more_keys_than_shared_memory_holds():
     # 8 CTAs hold 49152 keys each: the rest is read again for every pass
     n = 8 * 49152 + 4321
