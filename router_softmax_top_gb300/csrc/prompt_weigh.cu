@@ -15,9 +15,9 @@
 //    that see any of them (causality: those from the keys on; a window: not far past them).
 //    Rows come by TMA, 128 / group tokens of all heads of the group at a time, two tiles
 //    ahead; two score buffers in tensor memory with a warpgroup each; two CTAs per SM (one for
-//    heads of 256), so that one's start and end hide behind the other.  8192 tokens: one
-//    warpgroup for both buffers 360 us, one stage and buffer and three CTAs per SM 269, one
-//    CTA with four buffers that stays and takes tile after tile 278, so 232.
+//    heads of 256), so that one's start and end hide behind the other.  8192 tokens: 232 us,
+//    with one stage and buffer and three CTAs per SM 269, with one CTA of four buffers that
+//    stays and takes tile after tile 278; one warpgroup for both buffers took 100 us more.
 //  * Tiles of keys are handed out in their order: earlier ones are seen by more rows, so the
 //    longest come first.  Where there are fewer tiles than room for CTAs, a cluster shares a
 //    tile's rows, and sums are joined in a fixed order: results do not depend on timing.
