@@ -11,7 +11,7 @@
 // are written in order, from counts per warp.
 //
 // Moving, in place: the token of rank r goes to slot r, which is never after its own.  A CTA
-// takes the 128 tokens of a group: it loads those that stay into shared memory, says so, waits
+// takes the 256 tokens of a group: it loads those that stay into shared memory, says so, waits
 // for the groups whose tokens are in the slots that these go to to have said so (at most two,
 // and none later than itself), and writes.  Groups are handed out in order, so whatever one
 // waits for has been begun by a CTA that is running, and loading waits for nothing.
@@ -22,7 +22,7 @@
 // few CTAs and the barriers between them.
 // Measured: one sequence of 131071 tokens on 8 heads of 128, half of them kept, 67 us: search
 // 23 (at the copy rate all bytes that DRAM has to move would take 35).  32 sequences of 3000 to
-// 12000 tokens on 4 heads of 256, 4096 kept, 95 us (search 14; DRAM 57).  One of 1100 tokens,
+// 12000 tokens on 4 heads of 256, 4096 kept, 89 us (search 14; DRAM 52).  One of 1100 tokens,
 // 1024 kept, 13 us.
 #include <algorithm>
 #include <cooperative_groups.h>
@@ -39,11 +39,14 @@ constexpr int kFew = 128;         // keys that are compared each with each
 constexpr int kMostHeld = 49152;  // keys that a CTA's shared memory holds (more are read again for every pass)
 constexpr int kMostHeldByTwo = 16384;  // of two CTAs on an SM
 constexpr int kSmallTokens = 4096;  // caches of so many tokens a sequence at most take a CTA of 256 threads
-constexpr int kSlots = 128;       // tokens of a group, a thread each
-// Kept tokens of a group from which on its tiles are loaded whole, by a bulk copy each, rather than the tokens' pieces: 32
-// sequences of 12000 tokens on 4 heads of 256 take 127 us whole and 122 in pieces with 26 of 128 kept, 133 and 137 with 38,
-// 173 and 186 with 96; heads of 64 alike.
-constexpr int kWhole = 36;
+constexpr int kSlots = 128;       // tokens of a step, four a lane
+// Tokens that a CTA moves, a thread each, two steps' worth: what it has loaded is announced once, and the announcement waits
+// for the SM's writes (32 sequences of 12000 tokens on 4 heads of 256, 3600 kept: 128 us by 128 tokens, 120 so; one of 1100
+// tokens 0.6 us more).
+constexpr int kGroup = 256, kSteps = kGroup / kSlots;
+// Kept tokens of a group from which on its tiles are loaded whole, by a bulk copy each, rather than the tokens' pieces: the
+// same sequences take 111 us whole and 115 in pieces with 51 of 256 kept, 120 and 131 with 77; with 26 pieces are 14% faster.
+constexpr int kWhole = 40;
 constexpr int kEvictSms = 152;
 constexpr int64_t kMostTokens = 1 << 30;  // that a row of the page table may hold (counts and steps stay within 32 bits)
 
@@ -53,8 +56,8 @@ struct EvictJob {
   float *totals;
   int budget, first, recent, heads;
   int32_t *new_lens, *kept;
-  // workspace: next group; per pair whether it stays as it is; per pair and group: the kept tokens before its slots, and
-  // whether what goes there has been loaded
+  // workspace: next group; per pair whether it stays as it is; per pair and step: the kept tokens before it; per pair and
+  // group: whether its tokens have been loaded
   uint32_t *ticket;
   int32_t *skip, *before;
   uint32_t *loaded;
@@ -390,18 +393,18 @@ struct MoveCfg {
   static constexpr int kScale = D / 16;         // bytes of a token's scales of keys, and of values
   static constexpr int kTile = 36 * D;
   // a group's tiles, or its kept tokens: of each a row of pieces over the threads, then of scales
-  static constexpr size_t kSmem = (size_t)kSlots / kKvTile * kTile;
-  static_assert(kSmem == (size_t)kSlots * (16 * kPieces + 2 * kScale), "the two ways of holding a group");
-  static constexpr int kCtas = D == 256 ? 6 : D == 128 ? 11 : 16;  // per SM, by shared memory and threads
+  static constexpr size_t kSmem = (size_t)kGroup / kKvTile * kTile;
+  static_assert(kSmem == (size_t)kGroup * (16 * kPieces + 2 * kScale), "the two ways of holding a group");
+  static constexpr int kCtas = D == 256 ? 3 : D == 128 ? 5 : 8;  // per SM, by shared memory and threads
 };
 
 template <int D>
-__global__ void __launch_bounds__(kSlots, MoveCfg<D>::kCtas) evict_move_kernel(const EvictJob j) {
+__global__ void __launch_bounds__(kGroup, MoveCfg<D>::kCtas) evict_move_kernel(const EvictJob j) {
   using C = MoveCfg<D>;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ uint64_t bar;
   __shared__ int s_seq, s_head, s_group, s_ok, s_wait;
-  __shared__ float s_total[kSlots];
+  __shared__ float s_total[kGroup];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (j.c.n_seqs + 31) / 32;
   uint32_t phase = 0;
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(kSlots, MoveCfg<D>::kCtas) evict_move_kernel(c
         const int s = lane * per + k;
         if (s >= j.c.n_seqs) break;
         const int n = __ldg(j.lens + s);
-        if (length_ok(j, n) && n > j.budget) mine += (int64_t)((n + kSlots - 1) / kSlots) * j.heads;
+        if (length_ok(j, n) && n > j.budget) mine += (int64_t)((n + kGroup - 1) / kGroup) * j.heads;
       }
       before = mine;
 #pragma unroll
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kSlots, MoveCfg<D>::kCtas) evict_move_kernel(c
         int64_t left = (int64_t)u - before;
         for (int k = 0; k < per; ++k) {
           const int s = lane * per + k, n = __ldg(j.lens + s);
-          const int64_t of = length_ok(j, n) && n > j.budget ? (int64_t)((n + kSlots - 1) / kSlots) * j.heads : 0;
+          const int64_t of = length_ok(j, n) && n > j.budget ? (int64_t)((n + kGroup - 1) / kGroup) * j.heads : 0;
           if (left < of) {
             s_seq = s;
             s_head = (int)(left % j.heads);
@@ -454,11 +457,12 @@ __global__ void __launch_bounds__(kSlots, MoveCfg<D>::kCtas) evict_move_kernel(c
     const int seq = s_seq, head = s_head, g = s_group;
     if (seq < 0) return;
     const int pair = seq * j.heads + head;
-    const int n = __ldg(j.lens + seq), t0 = g * kSlots, n_own = min(kSlots, n - t0);  // the group's tokens
+    const int n = __ldg(j.lens + seq), t0 = g * kGroup, n_own = min(kGroup, n - t0);  // the group's tokens
     const int32_t *row = j.c.page_table + (int64_t)seq * j.c.table_stride;
     const bool skip = j.skip[pair] != 0;
     // the ranks of those that stay: [r0, r1).  (Where the sequence is left as it is, neither is of use.)
-    const int r0 = j.before[(int64_t)pair * j.groups + g], r1 = j.before[(int64_t)pair * j.groups + g + 1], count = r1 - r0;
+    const int32_t *before = j.before + (int64_t)pair * j.groups;
+    const int r0 = before[g * kSteps], r1 = before[min((g + 1) * kSteps, (n + kSlots - 1) / kSlots)], count = r1 - r0;
     uint32_t *loaded = j.loaded + (int64_t)pair * j.groups;
     if (skip) {
       __syncthreads();  // (what to work on is read until here)
@@ -475,8 +479,8 @@ __global__ void __launch_bounds__(kSlots, MoveCfg<D>::kCtas) evict_move_kernel(c
       *total = (p * j.heads + head) * j.c.page_size + in;
       return in % kKvTile;
     };
-    auto codes = [&](int piece) { return sm + ((size_t)piece * kSlots + tid) * 16; };
-    auto scales = [&](int v) { return sm + (size_t)kSlots * 16 * C::kPieces + ((size_t)v * kSlots + tid) * C::kScale; };
+    auto codes = [&](int piece) { return sm + ((size_t)piece * kGroup + tid) * 16; };
+    auto scales = [&](int v) { return sm + (size_t)kGroup * 16 * C::kPieces + ((size_t)v * kGroup + tid) * C::kScale; };
     int64_t own_total = 0, tile = 0, total = 0;
     int tok = 0, src = -1;
     bool came = true;
@@ -495,8 +499,8 @@ __global__ void __launch_bounds__(kSlots, MoveCfg<D>::kCtas) evict_move_kernel(c
       }
       // whose tokens are in the slots that are written: of two groups at most, which often have said so by now
       if (warp == 1) {
-        const int h = r0 / kSlots + lane;
-        const bool wait = h <= (r1 - 1) / kSlots && h < g && !is_loaded(loaded + h);
+        const int h = r0 / kGroup + lane;
+        const bool wait = h <= (r1 - 1) / kGroup && h < g && !is_loaded(loaded + h);
         if (const bool any = __any_sync(0xffffffffu, wait); lane == 0) s_wait = any;
       }
       if (whole) {
@@ -532,8 +536,8 @@ __global__ void __launch_bounds__(kSlots, MoveCfg<D>::kCtas) evict_move_kernel(c
     if (moves) {
       if (s_wait) {
         if (warp == 0) {
-          const int h = r0 / kSlots + lane;
-          if (h <= (r1 - 1) / kSlots && h < g && !wait_loaded(loaded + h)) s_ok = 0;
+          const int h = r0 / kGroup + lane;
+          if (h <= (r1 - 1) / kGroup && h < g && !wait_loaded(loaded + h)) s_ok = 0;
         }
         __syncthreads();
       }
@@ -631,7 +635,7 @@ cudaError_t launch_move(const EvictJob &j, int64_t groups, cudaStream_t st) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  return launch_with(evict_move_kernel<D>, std::min<int64_t>(groups, (int64_t)kEvictSms * C::kCtas), kSlots, C::kSmem, attr, st, j);
+  return launch_with(evict_move_kernel<D>, std::min<int64_t>(groups, (int64_t)kEvictSms * C::kCtas), kGroup, C::kSmem, attr, st, j);
 }
 
 int64_t evict_groups(const moe_kv_cache *c) { return ((int64_t)c->table_width * c->page_size + kSlots - 1) / kSlots + 1; }
@@ -689,7 +693,7 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
                   : pairs <= kEvictSms || j.held > kMostHeldByTwo ? launch_select<1024, false>(j, pairs, 1, st)
                                                                        : launch_select<512, false>(j, pairs, 1, st);
   if (e == cudaSuccess && tokens > budget) {  // (else no sequence is over it)
-    const int64_t groups = pairs * (j.groups - 1);
+    const int64_t groups = pairs * ((j.groups - 1 + kSteps - 1) / kSteps);
     e = c->head_dim == 64    ? launch_move<64>(j, groups, st)
         : c->head_dim == 128 ? launch_move<128>(j, groups, st)
                              : launch_move<256>(j, groups, st);
