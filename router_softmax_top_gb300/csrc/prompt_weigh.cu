@@ -92,6 +92,9 @@ __device__ __forceinline__ void ld_wait32(float *v) {
                : "memory");
 }
 
+// Bits n and up, of 32.
+__device__ __forceinline__ uint32_t bits_from(int n) { return n >= 32 ? 0u : 0xffffffffu << max(n, 0); }
+
 // What one CTA works on: a tile of 128 keys of a sequence and key head.
 struct SumWork {
   int seq;               // -1: nothing
@@ -112,7 +115,6 @@ __global__ void __launch_bounds__(SumCfg<D, SHORT>::kThreads, SumCfg<D, SHORT>::
   __shared__ int s_fail;
   __shared__ SumWork s_work;
   __shared__ __align__(16) float s_lse[NB][2][kTileRows];
-  __shared__ __align__(16) int s_pos[NB][2][kTileRows];
   __shared__ float s_sum[NB][kTileRows];
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -307,28 +309,21 @@ __global__ void __launch_bounds__(SumCfg<D, SHORT>::kThreads, SumCfg<D, SHORT>::
     const int r_tok = r / j.group, r_head = w.head * j.group + r % j.group;
     bool ok = true;
     float total = 0.f;
-    // row r of a tile: its lse (infinity for a row that is none) and position
-    auto row_of = [&](int i, float *l, int *pos) {
+    // the lse of row r of a tile (infinity for a row that is none)
+    auto lse_of = [&](int i) {
       const int tok = first_token(i) + r_tok;
-      const bool live = r < live_rows && tok < w.row1;
-      *l = live ? __ldg(j.lse + (int64_t)(w.q0 + tok) * j.hq + r_head) : a_inf();
-      *pos = live ? off + tok : -1;
+      return r < live_rows && tok < w.row1 ? __ldg(j.lse + (int64_t)(w.q0 + tok) * j.hq + r_head) : a_inf();
     };
     // for the warpgroup: less the lse (of a row that is none: less infinity)
-    auto put_row = [&](int at, float l, int pos) {
+    auto put_lse = [&](int at, float l) {
       s_lse[buf][at][r] = -l;
-      s_pos[buf][at][r] = pos;
       asm volatile("bar.sync %0, 128;" ::"r"(1 + buf) : "memory");
     };
-    if (buf < n_tiles) {
-      float l;
-      int pos;
-      row_of(buf, &l, &pos);
-      put_row(0, l, pos);
-    }
+    if (buf < n_tiles) put_lse(0, lse_of(buf));
     const uint64_t scale2 = f2_pack(j.scale, j.scale), log2e2 = f2_pack(kLog2e, kLog2e);
-    // 32 columns' weights, added to sum.  (No branch within a tile: it would leave less to overlap.)
-    auto weigh = [&](const float *v, const float *ls, const int *ps, uint64_t (&sum)[2], auto is_masked) {
+    // 32 columns' weights, of those whose bit is set in `seen`, added to sum.  (No branch within a tile: it would leave less
+    // to overlap.)
+    auto weigh = [&](const float *v, const float *ls, uint32_t seen, uint64_t (&sum)[2], auto is_masked) {
 #pragma unroll
       for (int z = 0; z < 32; z += 4) {
         const float4 l4 = *reinterpret_cast<const float4 *>(ls + z);
@@ -336,18 +331,17 @@ __global__ void __launch_bounds__(SumCfg<D, SHORT>::kThreads, SumCfg<D, SHORT>::
         f2_unpack(f2_mul(f2_fma(f2_pack(v[z], v[z + 1]), scale2, f2_pack(l4.x, l4.y)), log2e2), a, b);
         f2_unpack(f2_mul(f2_fma(f2_pack(v[z + 2], v[z + 3]), scale2, f2_pack(l4.z, l4.w)), log2e2), c, d);
         if constexpr (decltype(is_masked)::value) {
-          const int4 p4 = *reinterpret_cast<const int4 *>(ps + z);
-          a = key <= p4.x && key > p4.x - back ? a : -a_inf();
-          b = key <= p4.y && key > p4.y - back ? b : -a_inf();
-          c = key <= p4.z && key > p4.z - back ? c : -a_inf();
-          d = key <= p4.w && key > p4.w - back ? d : -a_inf();
+          a = (seen >> z) & 1u ? a : -a_inf();
+          b = (seen >> (z + 1)) & 1u ? b : -a_inf();
+          c = (seen >> (z + 2)) & 1u ? c : -a_inf();
+          d = (seen >> (z + 3)) & 1u ? d : -a_inf();
         }
         sum[0] = f2_add(sum[0], f2_pack(a_exp2(a), a_exp2(b)));
         sum[1] = f2_add(sum[1], f2_pack(a_exp2(c), a_exp2(d)));
       }
     };
-    // A tile's 128 columns, the first `plain` 32s of them not masked.
-    auto tile = [&](const float *ls, const int *ps, uint64_t (&sum)[2], auto plain) {
+    // A tile's 128 columns, the first `plain` 32s of them not masked, of the others those of [c0, c1) seen.
+    auto tile = [&](const float *ls, int c0, int c1, uint64_t (&sum)[2], auto plain) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         float v[32];
@@ -359,14 +353,13 @@ __global__ void __launch_bounds__(SumCfg<D, SHORT>::kThreads, SumCfg<D, SHORT>::
           __syncwarp();
           if (lane == 0) a_mbar_arrive(&s_empty[buf]);
         }
-        if (x < decltype(plain)::value) weigh(v, ls + 32 * x, ps + 32 * x, sum, std::false_type());
-        else weigh(v, ls + 32 * x, ps + 32 * x, sum, std::true_type());
+        if (x < decltype(plain)::value) weigh(v, ls + 32 * x, 0u, sum, std::false_type());
+        else weigh(v, ls + 32 * x, bits_from(c0 - 32 * x) & ~bits_from(c1 - 32 * x), sum, std::true_type());
       }
     };
     for (int i = buf, n = 0; i < n_tiles; i += NB, ++n) {
       float l = 0.f;
-      int pos = -1;
-      if (i + NB < n_tiles) row_of(i + NB, &l, &pos);
+      if (i + NB < n_tiles) l = lse_of(i + NB);
       // (after a failure the warp goes on to the barrier, which counts all four)
       ok = ok && __all_sync(0xffffffffu, a_mbar_wait(&s_full[buf], (uint32_t)n & 1u, &s_fail)) != 0;
       if (!ok) s_fail = 1;
@@ -375,16 +368,18 @@ __global__ void __launch_bounds__(SumCfg<D, SHORT>::kThreads, SumCfg<D, SHORT>::
         const int t0 = first_token(i), t1 = min(w.row1, t0 + j.tile_tokens) - 1;  // the tile's tokens
         const bool whole = off + t0 >= last_key && (int64_t)off + t1 - back < w.key0 && t1 - t0 + 1 == j.tile_tokens;
         const float *ls = s_lse[buf][n & 1];
-        const int *ps = s_pos[buf][n & 1];
+        // the columns whose tokens see this thread's key: tokens stand in their order, `group` columns each
+        const int c0 = min(max(key - off - t0, 0), kTileRows) * j.group;
+        const int c1 = (int)min((int64_t)(t1 - t0 + 1), max((int64_t)0, (int64_t)key + back - off - t0)) * j.group;
         uint64_t sum[2] = {0, 0};
-        if (whole && live_rows == kTileRows) tile(ls, ps, sum, std::integral_constant<int, 4>());
-        else if (whole && live_rows >= 96) tile(ls, ps, sum, std::integral_constant<int, 3>());
-        else tile(ls, ps, sum, std::integral_constant<int, 0>());
+        if (whole && live_rows == kTileRows) tile(ls, c0, c1, sum, std::integral_constant<int, 4>());
+        else if (whole && live_rows >= 96) tile(ls, c0, c1, sum, std::integral_constant<int, 3>());
+        else tile(ls, c0, c1, sum, std::integral_constant<int, 0>());
         float a, b;
         f2_unpack(f2_add(sum[0], sum[1]), a, b);
         total += a + b;
       }
-      put_row((n + 1) & 1, l, pos);
+      put_lse((n + 1) & 1, l);
     }
     s_sum[buf][r] = ok ? total : a_nan();
   }
