@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(SumCfg<D, SHORT>::kThreads, SumCfg<D, SHORT>::
     };
     if (buf < n_tiles) put_lse(0, lse_of(buf));
     const uint64_t scale2 = f2_pack(j.scale, j.scale), log2e2 = f2_pack(kLog2e, kLog2e);
-    // 32 columns' weights, of those whose bit is set in `seen`, added to sum.  (No branch within a tile: it would leave less
-    // to overlap.)
+    // 32 columns' weights, of those whose bit is set in `seen`, added to sum.  (No other branch within a tile: it would leave
+    // less to overlap.)
     auto weigh = [&](const float *v, const float *ls, uint32_t seen, uint64_t (&sum)[2], auto is_masked) {
 #pragma unroll
       for (int z = 0; z < 32; z += 4) {
@@ -353,8 +353,13 @@ __global__ void __launch_bounds__(SumCfg<D, SHORT>::kThreads, SumCfg<D, SHORT>::
           __syncwarp();
           if (lane == 0) a_mbar_arrive(&s_empty[buf]);
         }
-        if (x < decltype(plain)::value) weigh(v, ls + 32 * x, 0u, sum, std::false_type());
-        else weigh(v, ls + 32 * x, bits_from(c0 - 32 * x) & ~bits_from(c1 - 32 * x), sum, std::true_type());
+        if (x < decltype(plain)::value) {
+          weigh(v, ls + 32 * x, 0u, sum, std::false_type());
+        } else {
+          const uint32_t seen = bits_from(c0 - 32 * x) & ~bits_from(c1 - 32 * x);
+          // (in tiles on the border there are 32s that none of the warp's keys is seen by)
+          if (decltype(plain)::value || __any_sync(0xffffffffu, seen != 0)) weigh(v, ls + 32 * x, seen, sum, std::true_type());
+        }
       }
     };
     for (int i = buf, n = 0; i < n_tiles; i += NB, ++n) {
