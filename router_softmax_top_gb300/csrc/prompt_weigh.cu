@@ -15,22 +15,24 @@
 //    that see any of them (causality: those from the keys on; a window: not far past them).
 //    Rows come by TMA, 128 / group tokens of all heads of the group at a time, two tiles
 //    ahead; two score buffers in tensor memory with a warpgroup each; two CTAs per SM (one for
-//    heads of 256), so that one's start and end hide behind the other.  8192 tokens: 232 us,
-//    with one stage and buffer and three CTAs per SM 269, with one CTA of four buffers that
-//    stays and takes tile after tile 278; one warpgroup for both buffers took 100 us more.
+//    heads of 256), so that one's start and end hide behind the other.  8192 tokens, when
+//    they took 232 us so: one stage and buffer and three CTAs per SM 269, one CTA of four
+//    buffers that stays and takes tile after tile 278; one warpgroup for both buffers took
+//    100 us more.
 //  * Tiles of keys are handed out in their order: earlier ones are seen by more rows, so the
 //    longest come first.  Where there are fewer tiles than room for CTAs, a cluster shares a
 //    tile's rows, and sums are joined in a fixed order: results do not depend on timing.
 //  * The score less lse is formed before the factor log2(e): of large weights, whose difference
 //    is small, only the score's own rounding is left.  (With that factor in the scale and in lse
-//    2% less time, and twice the error, from lse's rounding.)  Sums are fp32, of a tile's rows
+//    it took 2% less, with twice the error, from lse's rounding.)  Sums are fp32, of a tile's rows
 //    first.
-//  * Only tiles of rows that do not all see all keys are masked.  A row that a key does not
-//    see cannot reach it, whatever it holds.
-// Measured: 8192 tokens, 32 heads of 128 on 8: 232 us (0.61 of the measured bf16 rate), of the
-// pipes tensor 50%, exponentials 50%, shared memory busy for threads 62% and for the matrix
-// unit 49% of the time.  Twelve packed prompts of up to 1500 tokens, 24 heads of 64 on 8, fp16:
-// 46 us.  4 x 2048 tokens, 16 heads of 256 on 8: 69 us.
+//  * Only tiles of rows that do not all see all keys are masked: the rows that see a thread's
+//    key are a run of columns, a bit each (by positions per column the packed prompts took 46
+//    us instead of 37).  A row that a key does not see cannot reach it, whatever it holds.
+// Measured: 8192 tokens, 32 heads of 128 on 8: 223 us (0.63 of the measured bf16 rate), of the
+// pipes tensor 53%, exponentials 53%, shared memory busy for threads 64% and for the matrix
+// unit 51% of the time.  Twelve packed prompts of up to 1500 tokens, 24 heads of 64 on 8, fp16:
+// 37 us.  4 x 2048 tokens, 16 heads of 256 on 8: 67 us.
 // Every wait is bounded; when one gives up all roles stop, the tile's totals become NaN and the
 // status word says so.
 #include <algorithm>
@@ -61,11 +63,11 @@ struct SumJob {
 
 constexpr int kSumSms = 152;
 // CTAs that a call is to have at least, in those that run at once: with 1, 2, 4 and 8 of them 8192 tokens of 32 heads of
-// 128 on 8 take 249, 228, 243 and 286 us, twelve packed prompts with 24 heads of 64 on 8 44, 44, 58 and 84 us.
+// 128 on 8 take 247, 223, 240 and 280 us, twelve packed prompts with 24 heads of 64 on 8 37, 37, 50 and 73 us.
 constexpr int kSumShare = 2;
 
 // SHORT: of a call whose rows fit one tile, so that a CTA is a chain of waits: more of them, with one stage and buffer.  16
-// tokens of 32 heads on 60016 keys of 8 heads of 128 take 76 us with two of each and two CTAs per SM, and 57 us so.
+// tokens of 32 heads on 60016 keys of 8 heads of 128 take 65 us with two of each and two CTAs per SM, and 47 us so.
 template <int D, bool SHORT>
 struct SumCfg {
   static constexpr int kStages = SHORT ? 1 : 2;
