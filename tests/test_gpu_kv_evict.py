@@ -209,6 +209,30 @@ def test_bad_pages_and_lengths_leave_a_sequence_as_it_is():
         assert torch.equal(p, pages) and torch.equal(t, totals)
 
 
+def test_two_at_once():
+    # on streams of their own, each with its own cache, again and again
+    cases = []
+    for seed, (lens, d, budget) in enumerate((([5000, 3000, 9000], 128, 2500), ([20000], 64, 9000))):
+        pages, table, totals = pool(lens, 64, 2, d, 20 + seed)
+        want, after = expect(pages, table, totals, lens, budget, 4, 64, 64, 2, d)
+        cases.append((lens, d, budget, pages.cuda(), table.cuda(), totals.cuda(), i32(lens), want, after, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    done = []
+    for _ in range(6):
+        for lens, d, budget, pages, table, totals, n, want, after, stream in cases:
+            with torch.cuda.stream(stream):
+                p, t = pages.clone(), totals.clone()
+                new, kept = moe.kv_evict(p, table, n, budget, totals=t, page_size=64, n_kv_heads=2, head_dim=d, first=4, recent=64)
+                done.append((lens, d, table, want, after, p, t, kept))
+    torch.cuda.synchronize()
+    for lens, d, table, want, after, p, t, kept in done:
+        assert torch.equal(kept.cpu(), want)
+        for s, n in enumerate(lens):
+            tok, row = torch.arange(n), table[s].cpu()
+            assert torch.equal(rows(p.cpu(), row, n, 64, 2, d), after[s][0])
+            assert same(t.cpu()[row[tok // 64].long(), :, tok % 64], after[s][1])
+
+
 def test_streams_and_graphs():
     lens, ps = [500, 130, 700], 64
     pages, table, totals = pool(lens, ps, 2, 128, 12)
