@@ -12,12 +12,13 @@
 // Which experts are chosen must not depend on how p was rounded, as a border may lie
 // between two values.  Without a bias the order is that of the logits, exactly.  With
 // one (or with sums per group) values are formed in 32 bits with a bound on their error;
-// where two neighbours in the order are nearer than their bounds, and are not equal by
-// having the same logit and bias, the token is done again in 64 bits.
+// where two of the chosen that are neighbours in the order, or the last of them and any that
+// is not chosen, are nearer than their bounds, and are not equal by having the same logit and
+// bias, the few candidates, or the token, are done again in 64 bits.
 //
-// Measured: 16384 tokens of 256 experts in 8 groups, bf16, sigmoid, bias, 8 of 4 groups: 25 us,
+// Measured: 16384 tokens of 256 experts in 8 groups, bf16, sigmoid, bias, 8 of 4 groups: 26 us,
 // 940 instructions a token, of an SM's issue slots 69%; in 64 bits throughout it was 72 us.
-// 64 tokens 3.8 us, one of 128 experts 2.7 us.
+// 64 tokens 4.0 us, one of 128 experts 2.7 us.
 #include <math.h>
 
 #include <algorithm>
@@ -309,34 +310,37 @@ __device__ __forceinline__ bool choose_quick(const RouteJob &j, const T *row, co
     }
   }
   if (!sure || by_logit) return sure;
-  // Neighbours in the order, the one after the last among them, are further apart than their errors, or equal by having the
-  // same logit and bias.
+  // The chosen, neighbours in their order, are further apart than their errors, or equal by having the same logit and bias;
+  // and so is the last of them from all that are not chosen: from the largest of those by the largest error that any
+  // expert's value has (a smaller one may come from a larger score), or else from each.
   const float inv = quick_inverse(z);
   auto error_of = [&](float v, float c) {
     const float arg = j.sigmoid ? v : v - top;
     return (j.sigmoid ? quick_sigmoid(v) : quick_exp(arg) * inv) * score_error(j.sigmoid, arg) + kSumStep * fabsf(c) + kFloor;
   };
-  const int a = lane <= j.k ? pick.id[lane] : -1;  // (at -1 the logit and the bias are not looked at)
-  const float ca = pick.c[lane], va = r_float(row[max(a, 0)]), ba = __ldg(j.bias + max(a, 0)), ea = error_of(va, ca);
-  int e = __shfl_down_sync(0xffffffffu, a, 1);
-  float ce = __shfl_down_sync(0xffffffffu, ca, 1), ve = __shfl_down_sync(0xffffffffu, va, 1);
-  float be = __shfl_down_sync(0xffffffffu, ba, 1), ee = __shfl_down_sync(0xffffffffu, ea, 1);
-  if (j.k == 32) {  // lane 31's neighbour is no lane's
-    const int id = pick.id[32];
-    const float v = r_float(row[max(id, 0)]), c32 = pick.c[32], e32 = error_of(v, c32);
-    if (lane == 31) {
-      e = id;
-      ce = c32;
-      ve = v;
-      be = __ldg(j.bias + max(id, 0));
-      ee = e32;
-    }
-  }
-  const bool near = lane < j.k && e >= 0 && !(ca - ce > ea + ee) && !(va == ve && ba == be);
-  if (!__any_sync(0xffffffffu, near)) return true;
-  // Some are not: 64 bits for the few that may be chosen.
+  const int a = lane < j.k ? pick.id[lane] : 0;
+  const float ca = pick.c[lane], va = r_float(row[a]), ba = __ldg(j.bias + a), ea = error_of(va, ca);
+  const float ce = __shfl_down_sync(0xffffffffu, ca, 1), ve = __shfl_down_sync(0xffffffffu, va, 1);
+  const float be = __shfl_down_sync(0xffffffffu, ba, 1), ee = __shfl_down_sync(0xffffffffu, ea, 1);
+  const bool near = lane < j.k - 1 && !(ca - ce > ea + ee) && !(va == ve && ba == be);
   const float last = pick.c[j.k - 1];
   const float off = warp_max(most_p) * (j.sigmoid ? 8e-7f : 5e-6f) + 1e-7f + kSumStep * fabsf(last);
+  const bool crowded = pick.id[j.k] >= 0 && !(last - pick.c[j.k] > 2.1f * off);
+  if (!__any_sync(0xffffffffu, near)) {
+    if (!crowded) return true;
+    // each by its own error: of those equal to the last chosen one the lower experts were taken
+    const int last_id = pick.id[j.k - 1];
+    const float last_v = __shfl_sync(0xffffffffu, va, j.k - 1), last_b = __shfl_sync(0xffffffffu, ba, j.k - 1);
+    const float last_e = __shfl_sync(0xffffffffu, ea, j.k - 1);
+    const float from = last - 2.1f * off;
+    bool other = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (c[i] >= from && !(x[i] == last_v && b[i] == last_b) && (c[i] < last || (c[i] == last && e0 + i > last_id)))
+        other |= !(last - c[i] > last_e + error_of(x[i], c[i]));
+    if (!__any_sync(0xffffffffu, other)) return true;
+  }
+  // Some are not: 64 bits for the few that may be chosen.
   const int few = collect(last - 2.1f * off);
   if (few > 32) return false;
   uint64_t own = 0;
