@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, kRouteCtas<VPL>) route_kerne
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       w = sum > 0.f ? __fdividef(w, sum) : 0.f;
     } else if (j.sigmoid) {
-      w = 1.f / (1.f + expf(-v));
+      const float e = expf(-fabsf(v));  // (exp(-v) is past fp32 where p is among its smallest numbers)
+      w = (v < 0.f ? e : 1.f) / (1.f + e);
     } else {
       w = z > 0.f ? expf(v - top) / z : 0.f;
     }
