@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "dyn_smem.h"
+
 namespace moe {
 
 // ---------------------------------------------------------------- limits
@@ -115,13 +117,6 @@ inline SlotLayout make_slot_layout(int H, int F) {
   return s;
 }
 
-// The dynamic shared memory limit a kernel has been raised to, per device
-// (the attribute belongs to the kernel on each device).
-struct DynSmemLimit {
-  static constexpr int kDevices = 64;
-  std::atomic<size_t> bytes[kDevices] = {};
-};
-
 // Raise a kernel's dynamic shared memory limit on the current device to
 // `bytes` when needed (the limit plus the kernel's static shared memory must
 // stay within the opt-in maximum, so it is raised to what a launch needs, not
@@ -132,16 +127,8 @@ inline cudaError_t ensure_dyn_smem(Kern kernel, size_t bytes, DynSmemLimit &limi
   int dev = -1;
   const cudaError_t ge = cudaGetDevice(&dev);
   if (ge != cudaSuccess) return ge;
-  std::atomic<size_t> *cur = (dev >= 0 && dev < DynSmemLimit::kDevices) ? &limit.bytes[dev] : nullptr;
-  if (cur && bytes <= cur->load(std::memory_order_relaxed)) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess && cur) {
-    size_t seen = cur->load(std::memory_order_relaxed);
-    while (seen < bytes && !cur->compare_exchange_weak(seen, bytes, std::memory_order_relaxed)) {
-    }
-  }
-  return e;
+  return (cudaError_t)limit.raise(
+      dev, bytes, [&](size_t want) { return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)want); });
 }
 
 // ------------------------------------------------------------ launchers

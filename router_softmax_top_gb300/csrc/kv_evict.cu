@@ -580,11 +580,17 @@ cudaError_t launch_with(void (*kernel)(A...), int64_t grid, int threads, size_t 
 }
 
 template <int NT, bool CL>
-cudaError_t launch_select(const EvictJob &j, int64_t pairs, int ranks, cudaStream_t st) {
+DynSmemLimit &select_limit() {
   static DynSmemLimit limit;
+  return limit;
+}
+
+template <int NT, bool CL>
+cudaError_t launch_select(const EvictJob &j, int64_t pairs, int ranks, cudaStream_t st) {
   const size_t smem = (size_t)j.held * 4;
   // (raised from 16 KB on: the kernel's own arrays, 25 KB, count towards what needs no raising)
-  const cudaError_t e = ensure_dyn_smem(evict_select_kernel<NT, CL>, smem > 16 * 1024 ? std::max<size_t>(smem, 64 * 1024) : smem, limit);
+  const cudaError_t e = ensure_dyn_smem(evict_select_kernel<NT, CL>, smem > 16 * 1024 ? std::max<size_t>(smem, 64 * 1024) : smem,
+                                        select_limit<NT, CL>());
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -616,7 +622,7 @@ int wide_clusters() {
   int n = 0;
   const auto kernel = evict_select_kernel<1024, true>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4) != cudaSuccess ||
+      ensure_dyn_smem(kernel, cfg.dynamicSmemBytes, select_limit<1024, true>()) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
