@@ -190,7 +190,7 @@ int moe_prompt_attention_shared(const moe_tensor *q, int32_t n_q_tokens, int32_t
 /*
  * Totals: the attention weight that cached tokens have received, summed over queries
  * and over the query heads that share a key head; what moe_kv_evict goes by.  fp32
- * [n_pages][n_kv_heads][page_size] contiguous, of the same pages as the tokens.  A token
+ * [n_pages][n_kv_heads][page_size] contiguous, of the same pages as the tokens (NULL where there are none).  A token
  * that a call queries is new: its total begins at 0 with that call; those of the other
  * tokens that a row sees are added to, and the rest is left as it is.  With restart all
  * tokens of the sequences begin at 0 (a pool whose totals were never set).

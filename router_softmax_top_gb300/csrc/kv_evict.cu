@@ -661,7 +661,7 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
                          void *cuda_stream) {
   if (c && c->n_seqs == 0) return MOE_OK;
   if (const int rc = check_cache(c)) return rc;
-  if (!seq_lens || !totals || !new_lens || budget < 0 || first < 0 || recent < 0 || (int64_t)first + recent > budget ||
+  if (!seq_lens || (!totals && c->n_pages > 0) || !new_lens || budget < 0 || first < 0 || recent < 0 || (int64_t)first + recent > budget ||
       (!kept && budget > 0) || (uintptr_t)totals % 16 || (uintptr_t)kept % 4 || (uintptr_t)new_lens % 4)
     return MOE_ERR_INVALID_ARG;
   if (budget > kMostTokens || (int64_t)c->table_width * c->page_size > kMostTokens ||

@@ -460,7 +460,7 @@ MOE_API int moe_kv_weigh(const moe_kv_cache *c, const int32_t *seq_lens, const m
                          int32_t dtype, void *cuda_stream) {
   if (c && c->n_seqs == 0) return MOE_OK;
   if (const int rc = check_cache(c)) return rc;
-  if (!seq_lens || !lse || !totals || n_q_heads <= 0 || n_q_heads % c->n_kv_heads || q_tokens <= 0 || window < 0 ||
+  if (!seq_lens || !lse || (!totals && c->n_pages > 0) || n_q_heads <= 0 || n_q_heads % c->n_kv_heads || q_tokens <= 0 || window < 0 ||
       !(scale > 0.f && scale <= kMostScale) || (uintptr_t)lse % 4 || (uintptr_t)totals % 4)
     return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;

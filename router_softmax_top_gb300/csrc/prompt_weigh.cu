@@ -471,7 +471,7 @@ MOE_API int moe_prompt_weigh(const moe_tensor *q, int32_t n_q_tokens, int32_t n_
       n_q_tokens > (1 << 29) || n_k_tokens > (1 << 29) || (int64_t)table_width * page_size > (1 << 30))
     return MOE_ERR_UNSUPPORTED;
   if (n_seqs == 0 || n_k_tokens == 0) return MOE_OK;
-  if (!cu_q || !cu_k || !totals || (uintptr_t)totals % 4 || (uintptr_t)lse % 4 || (uintptr_t)status % 4 ||
+  if (!cu_q || !cu_k || (!totals && n_pages > 0) || (uintptr_t)totals % 4 || (uintptr_t)lse % 4 || (uintptr_t)status % 4 ||
       (n_q_tokens > 0 && !lse) || (table_width > 0 && (!page_table || table_stride < table_width)))
     return MOE_ERR_INVALID_ARG;
   if (n_q_tokens > 0)
