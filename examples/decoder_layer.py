@@ -13,6 +13,7 @@ line of torch each.
 `BoundedDecoderLayer` is the same with a cache of bounded size and grouped routing: what
 attention each cached token has received is summed as prompts and tokens go by, `bound`
 keeps the tokens with most of it, and the experts come from sigmoid scores with a bias.
+A prompt that follows (`chunk`) attends over what is still held.
 """
 import os
 import sys
@@ -128,7 +129,17 @@ class BoundedDecoderLayer(DecoderLayer):
         return self._rest(x, o)
 
     def chunk(self, x, cu, n_cached):
-        raise NotImplementedError("prompts enter in one piece")
+        """More of the prompts, or the next turn's, over the n_cached tokens that are still held (over all sequences)."""
+        q, _, _ = self._append(x, cu)
+        new = cu.diff()
+        cu_k = torch.cat([cu[:1], (self.lens + new).cumsum(0, dtype=torch.int32)])
+        k, v = moe.kv_read(self.pages, self.table, torch.zeros_like(self.lens), cu_k, n_cached + x.shape[0],
+                           page_size=self.page_size, n_kv_heads=self.hkv, head_dim=self.d, status=self.status)
+        o, lse = moe.prompt_attention(q, k, v, cu, cu_k, return_lse=True, status=self.status)
+        moe.prompt_weigh(q, k, lse, cu, cu_k, totals=self.totals, page_table=self.table, status=self.status)
+        self.lens += new
+        self.positions += new
+        return self._rest(x, o)
 
     def decode(self, x):
         q, _, _ = self._append(x, self.one_each)
@@ -184,6 +195,9 @@ def main():
         layer.bound()
         for _ in range(8):
             out = layer.decode(step)
+    # the next turn, over what is still held
+    layer.bound()
+    layer.chunk(torch.randn(25, hidden, device="cuda"), more, int(layer.lens.sum()))
     torch.cuda.synchronize()
     assert layer.experts.sync() == moe.MOE_OK
     print("bounded", tuple(out.shape), "cached", layer.lens.tolist(), "of", layer.positions.tolist(),
