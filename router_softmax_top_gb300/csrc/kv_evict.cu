@@ -38,14 +38,21 @@ constexpr int kBins = 2048;
 constexpr int kFew = 128;         // keys that are compared each with each
 constexpr int kMostHeld = 49152;  // keys that a CTA's shared memory holds (more are read again for every pass)
 constexpr int kMostHeldByTwo = 16384;  // of two CTAs on an SM
-constexpr int kSmallTokens = 4096;  // caches of so many tokens a sequence at most take a CTA of 256 threads
+// Caches of so many tokens a sequence at most take a CTA of 256 threads, of which several share an SM, rather than 1024 (1, 32
+// and 512 pairs of 1500 tokens: 13.6, 14.9 and 35.5 us by 256 threads, 12.9, 14.2 and 36.1 by more; of 2400 tokens 15.1, 17.7
+// and 52.5, and 13.1, 15.9 and 53.1).
+constexpr int kSmallTokens = 2048;
+// Tokens per CTA from which on a pair takes a cluster of twice as many (a sequence on 4 heads by one, two and four CTAs a
+// head: of 6000 tokens 15.0 and 16.5 us, of 12000 18.9, 20.0 and 18.8, of 16384 20.5, 20.2 and 19.0).
+constexpr int kClusterTokens = 8192;
 constexpr int kSlots = 128;       // tokens of a step, four a lane
 // Tokens that a CTA moves, a thread each, two steps' worth: what it has loaded is announced once, and the announcement waits
 // for the SM's writes (32 sequences of 12000 tokens on 4 heads of 256, 3600 kept: 128 us by 128 tokens, 120 so; one of 1100
 // tokens 0.6 us more).
 constexpr int kGroup = 256, kSteps = kGroup / kSlots;
-// Kept tokens of a group from which on its tiles are loaded whole, by a bulk copy each, rather than the tokens' pieces: the
-// same sequences take 111 us whole and 115 in pieces with 51 of 256 kept, 120 and 131 with 77; with 26 pieces are 14% faster.
+// Kept tokens of a group from which on its tiles are loaded whole, by a bulk copy each, rather than the tokens' pieces: 32
+// sequences of 12000 tokens on 4 heads of 64, 128 and 256 take 53, 73 and 111 us whole and 55, 76 and 115 in pieces with 51 of
+// 256 kept, 55, 79 and 121 and 60, 85 and 131 with 77, 50, 68 and 102 and 50, 65 and 95 with 26.
 constexpr int kWhole = 40;
 constexpr int kEvictSms = 152;
 constexpr int64_t kMostTokens = 1 << 30;  // that a row of the page table may hold (counts and steps stay within 32 bits)
@@ -687,11 +694,12 @@ MOE_API int moe_kv_evict(const moe_kv_cache *c, const int32_t *seq_lens, float *
   j.loaded = reinterpret_cast<uint32_t *>(j.before + pairs * j.groups);
   // A cluster per pair where pairs alone leave SMs idle and have many keys (32 sequences of 12000 tokens on 4 heads: 21 us
   // as clusters of two, 15 us so; one of 131071 on 8 heads 8 CTAs each).  A CTA of 1024 threads is alone on its SM, of 512
-  // two are.  Sixteen CTAs, if the GPU has room for such clusters, of more keys than fill half of what eight hold (one head
-  // by eight and by sixteen, both kernels: 131071 tokens 40 and 43 us, 180000 45 and 46, 290000 55 and 53, 600000 115 and 72).
+  // two are.  Sixteen CTAs, if the GPU has room for such clusters, of more keys than fill three quarters of what eight hold
+  // (one head by eight and by sixteen, both kernels, half of the tokens kept: 230000 tokens 41 and 45 us, 290000 45 and 47,
+  // 350000 54 and 53, 390000 60 and 56, 400000 82 and 58; four heads of 230000 71 and 73, of 350000 95 and 92).
   int ranks = 1;
-  while (ranks < 8 && pairs * ranks * 2 <= kEvictSms && tokens > 2 * kSmallTokens * (int64_t)ranks) ranks *= 2;
-  if (ranks == 8 && pairs * 16 <= kEvictSms && tokens > (int64_t)kMostHeld * 4 && wide_clusters() >= pairs) ranks = 16;
+  while (ranks < 8 && pairs * ranks * 2 <= kEvictSms && tokens > kClusterTokens * (int64_t)ranks) ranks *= 2;
+  if (ranks == 8 && pairs * 16 <= kEvictSms && tokens > (int64_t)kMostHeld * 6 && wide_clusters() >= pairs) ranks = 16;
   j.held = (int)std::min<int64_t>(kMostHeld, ((tokens + ranks - 1) / ranks + kSlots - 1) / kSlots * kSlots);
   cudaStream_t st = (cudaStream_t)cuda_stream;
   cudaError_t e = ranks > 1                                            ? launch_select<1024, true>(j, pairs, ranks, st)

@@ -62,8 +62,9 @@ struct SumJob {
 };
 
 constexpr int kSumSms = 152;
-// CTAs that a call is to have at least, in those that run at once: with 1, 2, 4 and 8 of them 8192 tokens of 32 heads of
-// 128 on 8 take 247, 223, 240 and 280 us, twelve packed prompts with 24 heads of 64 on 8 37, 37, 50 and 73 us.
+// CTAs that a call is to have at least, in those that run at once: with 1, 2 and 4 of them 8192 tokens of 32 heads of 128 on
+// 8 take 244, 223 and 239 us, twelve packed prompts with 24 heads of 64 on 8 37, 37 and 50, 4 x 2048 tokens of 16 heads of 256 on
+// 8 67, 67 and 89, 512 tokens after 8192 of 32 heads of 128 on 8 (where the first CTAs are not the longest) 38, 46 and 63.
 constexpr int kSumShare = 2;
 
 // SHORT: of a call whose rows fit one tile, so that a CTA is a chain of waits: more of them, with one stage and buffer.  16
