@@ -228,6 +228,7 @@ int moe_prompt_weigh(const moe_tensor *q, int32_t n_q_tokens, int32_t n_q_heads,
  * They move together, in place and in their order: keys, values and totals of the token
  * of rank r go to slot r.  What the slots from budget on hold is left as it is, but for
  * their totals, which become 0.  Positions are not kept: a key stays as it was rotated.
+ * From then on everything goes by places: a window of w tokens is the last w kept ones.
  * new_lens: device int32 [n_seqs], min(seq_lens, budget); not seq_lens itself.
  * kept: device int32 [n_seqs][n_kv_heads][budget], the slots that the kept tokens had;
  * of a sequence of n <= budget tokens 0..n-1, then -1.

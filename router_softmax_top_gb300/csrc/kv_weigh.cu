@@ -5,11 +5,14 @@
 // result: no maximum, no sum over keys, so tiles of keys have nothing to do with each other.
 //
 // Bound: the key half of the cache (18 D bytes per tile of 32 tokens and head), and the
-// totals, read and written; in fact the instructions that unpack it (about 470 per tile of
-// 128 wide heads, an SM issuing 70% of the time).  The 32-token tiles of all (sequence, key head) pairs in a row,
-// plus a few tiles' worth per pair for its set-up, are split evenly over all warps; a warp
-// copies its own tiles (the key half of a tile is contiguous: one bulk copy) into a ring of its
-// own, two to four ahead, and no barrier stands in the loop.
+// totals, read and written; in fact instructions: about 470 per tile of 128 wide heads, an SM
+// issuing 70% of the time.  By the source 144 of them unpack codes (9 per 8), some 120 are
+// products, scales and weights, of which four rows per key head leave half the columns
+// empty, and the rest the ring, waits, addresses and branches.  The 32-token tiles of all
+// (sequence, key head) pairs in a row, plus a few tiles' worth per pair for its set-up, are
+// split evenly over all warps; a warp copies its own tiles (the key half of a tile is
+// contiguous: one bulk copy) into a ring of its own, two to four ahead, and no barrier stands
+// in the loop.
 //  * Scores: K Q^T (m16n8k16), codes as the whole numbers q - 8 in fp16 (high nibbles times 16,
 //    which the query's share takes back): a nibble under the exponent of 1024 is one operation
 //    and one packed addition away from it.  The query is rounded to fp16 after a power-of-two
@@ -21,7 +24,8 @@
 //    lane that writes a token's total is the one that reads it, whatever the pass.
 // Measured, 32 heads of 128 on 8: 128 sequences of 64 to 8192 tokens 78 us (4.4 TB/s of what
 // it has to read and write; loads into registers instead of the rings 91), one of 131071
-// 25 us (31), one of 333 5.6 us.
+// 25 us (31), one of 333 5.6 us.  32 sequences of 64 to 8192 tokens, 4 query tokens, 32 heads on
+// 4 of 128 (32 rows a key head: four row tiles, 238 registers, one CTA per SM): 31 us.
 #include <algorithm>
 #include <type_traits>
 

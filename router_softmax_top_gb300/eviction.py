@@ -128,7 +128,7 @@ def kv_evict(pages, page_table, seq_lens, budget, *, totals, page_size, n_kv_hea
     Returns the new lengths int32 [n_seqs] and the slots that the kept tokens had, int32 [n_seqs, n_kv_heads, budget]
     (ascending; -1 past a shorter sequence's tokens).  pages and totals are written in place; the totals of the slots given
     free become 0.  A kept key stays as it was rotated: tokens appended from then on need ``positions`` of their own
-    (``kv_append``)."""
+    (``kv_append``).  A window counts places: of w tokens, the last w kept ones."""
     dev = _device(pages)
     c, n_seqs = _cache(pages, page_table, page_size, n_kv_heads, head_dim, status, dev)
     pl = _index(seq_lens, "seq_lens", n_seqs, dev)
